@@ -227,6 +227,61 @@ int verify_splitkv_paged_write_fwd(const vsk_tensor* q, const vsk_tensor* k_new,
                                    float v_scale, float sm_scale, void* workspace,
                                    size_t workspace_bytes, void* stream);
 
+/* Attention over whole prompts, causal, grouped heads, sequences of different
+ * lengths packed one after the other: the prompt's own pass, whose K / V rows
+ * then become the prefix of the verify calls above.  Sequence b owns the rows
+ * [qo_indptr[b], qo_indptr[b+1]) of q, k, v and o (any number of them, none
+ * included); its row i attends, under one softmax with scores
+ * sm_scale * <q, k>, to its rows t <= i.  Query head h reads KV head
+ * h / (h_q / h_kv).
+ *   q [N, h_q, D], k and v [N, h_kv, D], o [N, h_q, D]   bf16, D in {64, 128,
+ *              256}, h_q / h_kv <= 128; k and v rows 16-byte aligned (data
+ *              pointer and the byte strides of both leading dimensions), q and
+ *              o 4-byte aligned with even strides.  o must not overlap k or v.
+ *   qo_indptr  [B+1] int32.  Rows of o outside every sequence are left as they
+ *              were.  An entry pair that decreases or leaves [0, N] makes that
+ *              sequence empty and sets error bit 4.
+ *   workspace  256 bytes or more, 256-byte aligned (the error word is at its
+ *              start; the rules of verify_splitkv_fwd apply), or NULL for the
+ *              library-owned one.
+ * K and V values that a row must not see (later tokens, other sequences) never
+ * reach it, infinities and NaN included.  Returns 1 once the kernel is
+ * enqueued on `stream` (or there is no row), 0 with nothing enqueued
+ * otherwise (vsk_last_error() says why). */
+int prompt_attn_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* v,
+                    const vsk_tensor* o, const vsk_tensor* qo_indptr, float sm_scale,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* verify_splitkv_fwd for a batch whose sequences share a long prefix (a system
+ * prompt, a document): sequence b's prefix is the pool rows shared_indices[0 ..
+ * S), common to all, followed by its own kv_indices[kv_indptr[b] ..
+ * kv_indptr[b+1]).  The result is that of verify_splitkv_fwd on the
+ * concatenated indices; the shared K / V rows are read once per 256 packed
+ * rows of the whole batch (once per 128 at head_dim 256) instead of once per
+ * sequence.
+ *   shared_indices  [S] int32 or int64, S >= 0
+ *   other arguments, limits and device-side checks as verify_splitkv_fwd
+ *   (causal drafts), with head_dim == v_head_dim.
+ *   workspace       vsk_shared_workspace_size(max_bs, ...) bytes hold it for
+ *                   any B <= max_bs and any S; NULL selects the library-owned
+ *                   buffer.
+ * Up to three launches on `stream`: the own prefixes, the shared prefix, and
+ * the kernel that joins them with the drafts. */
+int verify_splitkv_shared_fwd(const vsk_tensor* q_extend, const vsk_tensor* k_extend,
+                              const vsk_tensor* v_extend, const vsk_tensor* o_extend,
+                              const vsk_tensor* k_buffer, const vsk_tensor* v_buffer,
+                              const vsk_tensor* qo_indptr, const vsk_tensor* kv_indptr,
+                              const vsk_tensor* kv_indices, const vsk_tensor* shared_indices,
+                              int64_t max_len_extend, float k_scale, float v_scale,
+                              float sm_scale, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Workspace bound of verify_splitkv_shared_fwd on the CURRENT device (0 when
+ * the shapes are unsupported or there is none); it also holds the calls that
+ * vsk_workspace_size(max_bs, ...) bounds. */
+size_t vsk_shared_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv,
+                                 int64_t head_dim, int64_t max_len_extend);
+
 /* Upper bound, in bytes, of the workspace verify_splitkv_fwd needs for any
  * batch of up to max_bs sequences with these head counts and sizes on the
  * CURRENT CUDA device (its SM count sets the number of persistent CTAs).

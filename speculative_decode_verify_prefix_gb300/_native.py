@@ -108,6 +108,14 @@ def _bind(lib):
     lib.verify_splitkv_paged_write_fwd.argtypes = [_P] * 8 + [ctypes.c_int64, ctypes.c_int64, ctypes.c_float,
                                                               ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
                                                               ctypes.c_size_t, ctypes.c_void_p]
+    lib.prompt_attn_fwd.restype = ctypes.c_int
+    lib.prompt_attn_fwd.argtypes = [_P] * 5 + [ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.verify_splitkv_shared_fwd.restype = ctypes.c_int
+    lib.verify_splitkv_shared_fwd.argtypes = [_P] * 10 + [ctypes.c_int64, ctypes.c_float, ctypes.c_float,
+                                                          ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t,
+                                                          ctypes.c_void_p]
+    lib.vsk_shared_workspace_size.restype = ctypes.c_size_t
+    lib.vsk_shared_workspace_size.argtypes = [ctypes.c_int64] * 5
     lib.vsk_workspace_size.restype = ctypes.c_size_t
     lib.vsk_workspace_size.argtypes = [ctypes.c_int64] * 6
     lib.vsk_workspace_size_for_sms.restype = ctypes.c_size_t

@@ -1,0 +1,157 @@
+// The last launch of verify_splitkv_shared_fwd: joins, for every draft row,
+// the partial softmaxes over the shared prefix (fa_kernel, one per key range),
+// those over the sequence's own prefix (the stream-only kernel, one per piece)
+// and the causal draft block.
+//
+// With (lse, o) of each partial in base 2 and m their largest lse, the joined
+// row is sum 2^(lse - m) o / sum 2^(lse - m); a draft key counts as a partial
+// of one key (lse = its score, o = its value).  All sums are 32-bit.
+//
+// One CTA per (sequence, KV head, 16-row tile, 32 output columns): thread t
+// owns row t / 8 of the tile and four columns.  The eight threads of a row
+// share its draft scores (an eighth of the head dimension each).  The
+// partials come from L2, where the launches before this one left them.
+#pragma once
+#include "flash_tc.cuh"
+
+namespace vsk {
+
+struct ScParams {
+  Params v;             // the flat call; its piece cut when has_own
+  int has_own;          // the stream-only kernel ran
+  int n_split, n_live;  // key ranges per row block, those that hold keys
+  int h_kv, tpb, nq;    // row blocks of fa_kernel: tokens per query tile, tiles per block
+  const float* splse;
+  const float* spo;
+};
+
+template <int D>
+__global__ void __launch_bounds__(128) shared_combine_kernel(const __grid_constant__ ScParams s) {
+  constexpr int kSlices = D / 32;
+  __shared__ long long scan[8];
+  const Params& p = s.v;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ch = static_cast<int>(blockIdx.x % kSlices);
+  const int tile = static_cast<int>((blockIdx.x / kSlices) % p.MT);
+  const int kvh = static_cast<int>((blockIdx.x / (kSlices * p.MT)) % s.h_kv);
+  const int b = static_cast<int>(blockIdx.x / (static_cast<long long>(kSlices) * p.MT * s.h_kv));
+  const float NEG_INF = -INFINITY;
+
+  const int fr = tid >> 3, fch = tid & 7;
+  const int row = 16 * tile + fr;
+  const bool live = row < p.R;
+  const int rr = live ? row : p.R - 1;
+  const int i = rr / p.gq, head = kvh * p.gq + rr % p.gq;
+  const int qa = __ldg(p.qo + b), qe = __ldg(p.qo + b + 1);
+  const bool ok = qa >= 0 && qe - qa == p.L && static_cast<long long>(qa) + p.L <= p.n_rows;
+  if (!ok && tid == 0 && ch == 0 && tile == 0 && kvh == 0) atomicOr(p.err, kErrBadQoIndptr);
+  const long long s_b = ok ? qa : static_cast<long long>(b) * p.L;
+
+  float m = NEG_INF, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  auto fold = [&](float x, const float4& v) {
+    if (x == NEG_INF) return;
+    if (x > m) {
+      const float a = exp2f(m - x);  // 0 while m is -inf
+      l *= a;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c] *= a;
+      m = x;
+    }
+    const float w = exp2f(x - m);
+    l += w;
+    acc[0] = fmaf(w, v.x, acc[0]);
+    acc[1] = fmaf(w, v.y, acc[1]);
+    acc[2] = fmaf(w, v.z, acc[2]);
+    acc[3] = fmaf(w, v.w, acc[3]);
+  };
+  const int col = 32 * ch + 4 * fch;
+
+  // ---- the shared prefix ----
+  {
+    const long long tok = s_b + i;
+    const int bt = s.nq * s.tpb;
+    const long long blk = tok / bt;
+    const int rem = static_cast<int>(tok - blk * bt);
+    const int in_block = (rem / s.tpb) * 128 + (rem % s.tpb) * p.gq + rr % p.gq;
+    const long long r0 = (blk * s.h_kv + kvh) * s.n_split * (128LL * s.nq) + in_block;
+#pragma unroll 4
+    for (int k = 0; k < s.n_live; ++k) {
+      const long long at = r0 + static_cast<long long>(k) * (128 * s.nq);
+      fold(__ldg(s.splse + at), __ldg(reinterpret_cast<const float4*>(s.spo + at * D + col)));
+    }
+  }
+
+  // ---- the sequence's own prefix: its pieces, cut as the stream cut them ----
+  if (s.has_own) {
+    long long tot = 0, bef = 0;
+    for (int bb = tid; bb < p.B; bb += 128) {
+      int P_;
+      long long k_;
+      seq_info(p, bb, P_, k_);
+      tot += max(P_, 1);
+      if (bb < b) bef += max(P_, 1);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      tot += __shfl_xor_sync(0xffffffffu, tot, o);
+      bef += __shfl_xor_sync(0xffffffffu, bef, o);
+    }
+    if (lane == 0) {
+      scan[warp] = tot;
+      scan[4 + warp] = bef;
+    }
+    __syncthreads();
+    tot = (scan[0] + scan[1] + scan[2] + scan[3]) * p.n_hg;
+    bef = scan[4] + scan[5] + scan[6] + scan[7];
+    int P;
+    long long kv0;
+    seq_info(p, b, P, kv0);
+    const int hg = kvh / p.HC, hc = kvh % p.HC, len = max(P, 1);
+    long long W = (tot + p.n_stream - 1) / p.n_stream;
+    if (W < p.w_min) W = p.w_min;
+    const long long off = bef * p.n_hg + static_cast<long long>(hg) * len;
+    const long long c0 = off / W, c1 = (off + len - 1) / W;
+    const long long slot0 = c0 + static_cast<long long>(b) * p.n_hg + hg;
+    const int RM = 16 * p.MT;
+#pragma unroll 4
+    for (long long k = 0; k <= c1 - c0; ++k) {
+      const long long at = ((slot0 + k) * p.HC + hc) * RM + rr;
+      fold(__ldg(p.plse + at), __ldg(reinterpret_cast<const float4*>(p.po + at * D + col)));
+    }
+  }
+
+  // ---- the drafts up to this row's own ----
+  {
+    constexpr int DE = D / 8;  // head dimensions of one thread's part of a score
+    const __nv_bfloat16* qr = p.q + (s_b + i) * p.q_s0 + static_cast<long long>(head) * p.q_s1 + fch * DE;
+    float2 qv[DE / 2];
+#pragma unroll
+    for (int u = 0; u < DE / 2; ++u) qv[u] = unpack_bf16(ld_u32(qr + 2 * u));
+    const int last = __reduce_max_sync(0xffffffffu, i);
+    for (int t = 0; t <= last; ++t) {
+      const __nv_bfloat16* kr = p.ke + (s_b + t) * p.ke_s0 + static_cast<long long>(kvh) * p.ke_s1 + fch * DE;
+      float x = 0.f;
+#pragma unroll
+      for (int u = 0; u < DE / 2; ++u) {
+        const float2 kv = unpack_bf16(ld_u32(kr + 2 * u));
+        x = fmaf(qv[u].x, kv.x, fmaf(qv[u].y, kv.y, x));
+      }
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      x += __shfl_xor_sync(0xffffffffu, x, 4);
+      if (t <= i) {
+        const __nv_bfloat16* vr = p.ve + (s_b + t) * p.ve_s0 + static_cast<long long>(kvh) * p.ve_s1 + col;
+        const float2 v0 = unpack_bf16(ld_u32(vr)), v1 = unpack_bf16(ld_u32(vr + 2));
+        fold(x * p.dscale2, make_float4(v0.x, v0.y, v1.x, v1.y));
+      }
+    }
+  }
+  if (live) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* op = p.o + (s_b + i) * p.o_s0 + static_cast<long long>(head) * p.o_s1 + col;
+    *reinterpret_cast<uint32_t*>(op) = pack_bf16(acc[0] * inv, acc[1] * inv);
+    *reinterpret_cast<uint32_t*>(op + 2) = pack_bf16(acc[2] * inv, acc[3] * inv);
+  }
+}
+
+}  // namespace vsk

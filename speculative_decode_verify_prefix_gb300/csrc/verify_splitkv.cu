@@ -17,6 +17,7 @@
 
 #include "../../include/verify_splitkv.h"
 #include "verify_kernel.cuh"
+#include "verify_host.cuh"
 #include "verify_tr.cuh"
 
 #define VSK_VERSION "verify_splitkv-gb300 0.2"
@@ -62,6 +63,8 @@ int fail(const char* fmt, ...) {
   return 0;
 }
 
+void clear_error() { g_err.clear(); }
+
 // process-wide tuning overrides (0 = default)
 int g_num_ctas = 0;
 long long g_min_tokens = 0;
@@ -76,13 +79,6 @@ int g_cl = 0;     // cluster form: 0 never (the default), 1 up to kClMaxWork, 2 
 int g_pipe = 1;   // head_dim 256 one-launch kernel over e4m3 pools with pipelined stages (1) or not (0)
 int g_pdl = 1;    // combine kernel as a programmatic dependent of the stream: 1 up to kPdlMaxWork, 2 always, 0 never
 
-struct Plan {
-  int gq, R, MT, MTW, HC, n_hg, nwc, threads, ek;
-  int stage_bytes, nst, ring_off, head_bytes, misc_off, misc_bytes;
-  size_t smem;
-  int ctas_per_sm;
-};
-
 int floor_pow2(int x) {
   int r = 1;
   while (r * 2 <= x) r *= 2;
@@ -94,7 +90,7 @@ int floor_pow2(int x) {
 // than one tile, so its K / V fragments feed both); ring depth from the
 // shared-memory budget.  DV: the value head_dim (0: the same as D).
 bool make_plan(long long h_q, long long h_kv, long long D, long long L, bool fp8, Plan& pl,
-               long long total_tokens, int tiles, long long DV = 0, int hc_cap = 0) {
+               long long total_tokens, int tiles, long long DV, int hc_cap) {
   if (DV == 0) DV = D;
   if (h_kv <= 0 || h_q % h_kv != 0) return fail("h_q (%lld) must be a positive multiple of h_kv (%lld)", h_q, h_kv);
   const long long R = (h_q / h_kv) * L;
@@ -309,10 +305,6 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // tickets' place is then the same for every call on a given buffer whatever
 // its shapes (up to 16,384 tickets), so the zero tickets a call leaves are the
 // ones the next call finds, and no call's partials reach them.
-struct WsLayout {
-  size_t lse_off, o_off, cnt_bytes, total;
-};
-
 WsLayout ws_layout(long long n_cta, long long B, const Plan& pl, long long DV) {
   WsLayout w;
   const long long segs = B * pl.n_hg;
@@ -972,16 +964,11 @@ static int launch_with_plan(Params& p, long long B, long long h_q, long long h_k
 // tree, fused store, allocation-free); cm / mi select tree verify (both null:
 // causal drafts), ocl the fused store.  Returns the static shapes the plan
 // needs.
-struct CallShape {
-  long long B, h_q, h_kv, D, DV, L, mean_len;
-  bool fp8;
-};
-
-static int prepare_verify(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tensor* ve, const vsk_tensor* o,
-                          const vsk_tensor* kb, const vsk_tensor* vb, const vsk_tensor* qo, const vsk_tensor* kvp,
-                          const vsk_tensor* kvi, int is_causal, int64_t max_len_extend, float k_scale, float v_scale,
-                          float sm_scale, const vsk_tensor* cm, const vsk_tensor* mi, const vsk_tensor* ocl, Params& p,
-                          CallShape& cs) {
+int prepare_verify(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tensor* ve, const vsk_tensor* o,
+                   const vsk_tensor* kb, const vsk_tensor* vb, const vsk_tensor* qo, const vsk_tensor* kvp,
+                   const vsk_tensor* kvi, int is_causal, int64_t max_len_extend, float k_scale, float v_scale,
+                   float sm_scale, const vsk_tensor* cm, const vsk_tensor* mi, const vsk_tensor* ocl, Params& p,
+                   CallShape& cs) {
   if (!gate(q, ke, ve, kb, vb, qo, kvp, kvi, is_causal, max_len_extend, -1, 0, 0.f, -1)) return 0;
   if (!check_3d(o, "o_extend")) return 0;
   if (o->dtype != VSK_DTYPE_BF16 || o->shape[0] != q->shape[0] || o->shape[1] != q->shape[1] ||
@@ -1068,6 +1055,41 @@ static int run_verify(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tenso
     return 0;
   return launch_with_plan(p, cs.B, cs.h_q, cs.h_kv, cs.D, cs.DV, cs.L, cs.fp8, workspace, workspace_bytes, stream,
                           cs.mean_len);
+}
+
+int plan_stream_only(const CallShape& cs, StreamOnly& so) {
+  const long long tokens = cs.mean_len * cs.B;
+  if (!make_plan(cs.h_q, cs.h_kv, cs.D, cs.L, cs.fp8, so.pl, tokens,
+                 g_tiles == 0 ? (tokens >= kSplitTwoTileMinTokens ? 2 : 1) : 0, cs.DV))
+    return 0;
+  so.fn = pick_so_kernel(static_cast<int>(cs.D), cs.fp8, so.pl.MTW);
+  if (!so.fn || !prepare_kernel(so.fn)) return fail("stream-only kernel for head_dim %lld unavailable", cs.D);
+  int dev = 0, occ = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail("cudaGetDevice: %s", cudaGetErrorString(e));
+  const int sms = device_sms(dev);
+  if (sms <= 0) return fail("cannot query the SM count of device %d", dev);
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, reinterpret_cast<const void*>(so.fn), so.pl.threads, so.pl.smem);
+  if (e != cudaSuccess || occ < 1) return fail("kernel does not fit an SM (%s)", cudaGetErrorString(e));
+  so.n_cta = g_num_ctas > 0 ? g_num_ctas : static_cast<long long>(sms) * std::min(occ, so.pl.ctas_per_sm);
+  so.wl = ws_layout(so.n_cta, cs.B, so.pl, cs.DV);
+  const long long wp = (cs.mean_len / kPiecesPerSegmentColSplit + kStageTokens - 1) / kStageTokens * kStageTokens;
+  so.w_min = g_min_tokens > 0 ? g_min_tokens : std::max(kDefaultMinTokens, wp);
+  return 1;
+}
+
+int launch_stream_only(Params& p, const CallShape& cs, const StreamOnly& so, unsigned char* ws, size_t ws_bytes,
+                       cudaStream_t st) {
+  CallPlan cp;
+  cp.pl = so.pl;
+  cp.fn = so.fn;
+  cp.threads = so.pl.threads;
+  cp.smem = so.pl.smem;
+  cp.n_cta = so.n_cta;
+  cp.w_min = so.w_min;
+  cp.wl = so.wl;
+  cp.D = static_cast<int>(cs.D);
+  return enqueue_call(p, cp, cs.B, cs.L, ws, ws_bytes, st);
 }
 
 bool check_2d(const vsk_tensor* t, const char* name) {

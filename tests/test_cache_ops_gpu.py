@@ -1,0 +1,295 @@
+"""GPU tests of the calls around the verify call against plain 64-bit forms.
+
+Tolerances, element by element.  Attention: the kernels round the softmax
+weights P to bf16 (each off by at most eps/2 = 2^-8 of itself) and the output
+to bf16 (2^-8 of itself); the sums are 32-bit.  With A = sum_j p_j |v_j| the
+output is therefore within 2^-8 (A + |o| (1 + 2^-8)) of the exact one, plus
+what 32-bit scores leave in the weights: D <= 256 products summed in 32 bits
+are off by at most D 2^-24 sum |q||k| sm_scale, for the N(0, 1) rows used here
+(sum |q||k| sm_scale <= 16) under 256 * 16 * 2^-24 = 2^-12, so 2^-12 A.
+Integers are equal.
+"""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F64 = torch.bfloat16, torch.float64
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def vsk():
+    import speculative_decode_verify_prefix_gb300 as m
+
+    m.build()
+    return m
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, *shape):
+    return torch.randn(*shape, generator=g, device=DEV, dtype=BF16)
+
+
+def indptr(lens):
+    return torch.tensor([0] + torch.tensor(lens).cumsum(0).tolist(), dtype=torch.int32, device=DEV)
+
+
+def attend64(q, k, v, visible, scale, v_abs=False):
+    """q [n, h, d], k and v [m, h_kv, d] in 64 bits, visible [n, m]: (o, A)."""
+    g = q.shape[1] // k.shape[1]
+    o, a = torch.empty_like(q), torch.empty_like(q)
+    for h in range(q.shape[1]):
+        x = (q[:, h] @ k[:, h // g].T) * scale
+        x = x.masked_fill(~visible, -math.inf)
+        p = torch.softmax(x, 1)
+        vh = v[:, h // g]
+        o[:, h] = p @ vh
+        a[:, h] = p @ vh.abs()
+    return o, a
+
+
+def check_attention(got, want, a):
+    got = got.to(F64)
+    tol = 2.0 ** -8 * (a + want.abs() * (1 + 2.0 ** -8)) + 2.0 ** -12 * a + 1e-30
+    bad = ~((got - want).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), float(((got - want).abs() / tol).nan_to_num(9e9).max()))
+
+
+# ---------------------------------------------------------------- prompts
+
+def prompt_case(lens, hq, hk, d, seed=0, extra=0, fused=False):
+    g = gen(seed)
+    n = sum(lens) + extra
+    if fused:
+        x = normal(g, n, hq + 2 * hk, d)
+        q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+    else:
+        q, k, v = normal(g, n, hq, d), normal(g, n, hk, d), normal(g, n, hk, d)
+    return q, k, v, indptr(lens)
+
+
+def prompt_want(q, k, v, lens, scale):
+    o, a, at = torch.zeros(q.shape, dtype=F64, device=DEV), torch.zeros(q.shape, dtype=F64, device=DEV), 0
+    for n in lens:
+        s = slice(at, at + n)
+        vis = torch.ones(n, n, dtype=torch.bool, device=DEV).tril()
+        o[s], a[s] = attend64(q[s].to(F64), k[s].to(F64), v[s].to(F64), vis, scale)
+        at += n
+    return o, a
+
+
+PROMPTS = [
+    # (lengths, h_q, h_kv, d)
+    ((1,), 1, 1, 64), ((1,), 32, 8, 128), ((1, 1, 1), 8, 1, 256), ((2, 0, 3), 4, 2, 128), ((0, 0, 5, 0), 3, 1, 64),
+    ((127, 128, 129), 2, 2, 128), ((63, 64, 65), 4, 1, 128), ((31, 32, 33, 255, 256, 257), 8, 2, 64),
+    ((200,), 5, 1, 128), ((333, 17), 14, 2, 256), ((77, 191), 6, 2, 64), ((129,), 16, 1, 128), ((40,), 128, 1, 64),
+    ((9, 70), 100, 1, 128), ((1025, 511), 16, 2, 256), ((4097,), 4, 1, 128), ((2300, 1, 700), 7, 7, 64),
+    (tuple(range(0, 90)), 4, 2, 128),
+]
+
+
+@pytest.mark.parametrize("case", PROMPTS, ids=lambda c: f"b{len(c[0])}n{sum(c[0])}h{c[1]}x{c[2]}d{c[3]}")
+def test_prompt_against_64_bits(vsk, case):
+    lens, hq, hk, d = case
+    q, k, v, ptr = prompt_case(lens, hq, hk, d, extra=5)
+    o = torch.full_like(q, 7.0)
+    vsk.prompt_attn_fwd(q, k, v, o, ptr)
+    n = sum(lens)
+    want, a = prompt_want(q, k, v, lens, d ** -0.5)
+    check_attention(o[:n], want[:n], a[:n])
+    assert bool((o[n:] == 7.0).all())  # rows behind the last sequence
+    assert vsk.read_error_flags() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompt_strided_rows_and_scale(vsk, d):
+    lens = (150, 3, 260)
+    q, k, v, ptr = prompt_case(lens, 6, 3, d, seed=3, fused=True)
+    big = torch.zeros(sum(lens), 8, d, dtype=BF16, device=DEV)
+    o = big[:, 1:7]
+    vsk.prompt_attn_fwd(q, k, v, o, ptr, sm_scale=0.3 * d ** -0.5)
+    want, a = prompt_want(q, k, v, lens, 0.3 * d ** -0.5)
+    check_attention(o, want, a)
+    assert bool((big[:, 0] == 0).all()) and bool((big[:, 7] == 0).all())
+
+
+def test_prompt_rows_of_four_byte_alignment(vsk):
+    lens, hq, d = (100, 45), 4, 128
+    g = gen(5)
+    flat = normal(g, sum(lens) * hq * d + 2)
+    q = flat[2:].view(sum(lens), hq, d)
+    oflat = torch.zeros_like(flat)
+    o = oflat[2:].view_as(q)
+    k, v = normal(g, sum(lens), 2, d), normal(g, sum(lens), 2, d)
+    vsk.prompt_attn_fwd(q, k, v, o, indptr(lens))
+    check_attention(o, *prompt_want(q, k, v, lens, d ** -0.5))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prompt_hidden_values_stay_hidden(vsk, d, bad):
+    """K and V of a later token, of the next sequence and of rows outside every sequence hold no number."""
+    lens = (170, 60)
+    q, k, v, ptr = prompt_case(lens, 4, 2, d, seed=11, extra=9)
+    want, a = prompt_want(q, k, v, lens, d ** -0.5)
+    k[230:], v[230:] = bad, bad
+    k[150], v[150, :, 3] = bad, bad        # seen by rows 150.. of the first sequence
+    k[170 + 59], v[170 + 59] = bad, bad    # seen by the last row of the second
+    o = torch.zeros_like(q)
+    vsk.prompt_attn_fwd(q, k, v, o, ptr)
+    keep = torch.ones(239, dtype=torch.bool, device=DEV)
+    keep[150:170] = False
+    keep[229:] = False
+    check_attention(o[keep], want[keep], a[keep])
+    assert not o[150:170].isfinite().any() and not o[229].isfinite().any()
+
+
+def test_prompt_values_not_finite_reach_the_rows_that_see_them(vsk):
+    lens, d = (300,), 128
+    q, k, v, ptr = prompt_case(lens, 4, 2, d, seed=12)
+    want, a = prompt_want(q, k, v, lens, d ** -0.5)
+    v[200, 0, 5] = float("inf")
+    v[290, 1, 7] = float("-inf")
+    o = torch.zeros_like(q)
+    vsk.prompt_attn_fwd(q, k, v, o, ptr)
+    seen = torch.zeros(o.shape, dtype=torch.bool, device=DEV)
+    seen[200:, :2, 5] = True
+    seen[290:, 2:, 7] = True
+    assert bool((o[200:, :2, 5] == math.inf).all()) and bool((o[290:, 2:, 7] == -math.inf).all())
+    check_attention(o[~seen], want[~seen], a[~seen])
+
+
+def test_prompt_large_scores_raise_the_reference(vsk):
+    """Scores that grow along the keys by far more than the headroom, so the running reference moves often."""
+    lens, d = (700,), 128
+    q, k, v, ptr = prompt_case(lens, 2, 1, d, seed=13)
+    k = (k.float() * torch.linspace(0.1, 6.0, 700, device=DEV)[:, None, None]).to(BF16)
+    o = torch.zeros_like(q)
+    vsk.prompt_attn_fwd(q, k, v, o, ptr)
+    want, a = prompt_want(q, k, v, lens, d ** -0.5)
+    # scores up to 6 times as large: 6 * 2^-12 A of the header's last term
+    check_attention(o, want, a * (1 + 6 * 2.0 ** -4))
+
+
+def test_prompt_bad_indptr_is_flagged(vsk):
+    q, k, v, _ = prompt_case((60,), 4, 2, 64, seed=14)
+    ptr = torch.tensor([0, 20, 10, 40, 99], dtype=torch.int32, device=DEV)  # the second and the last pair are wrong
+    o = torch.full_like(q, 7.0)
+    vsk.prompt_attn_fwd(q, k, v, o, ptr)
+    assert vsk.read_error_flags() == 4
+    want, a = prompt_want(q[:20], k[:20], v[:20], (20,), 0.125)
+    check_attention(o[:10], want[:10], a[:10])
+    assert bool((o[40:] == 7.0).all())
+
+
+# ---------------------------------------------------------------- a shared prefix
+
+def shared_case(s, own, l, hq, hk, d, pool="bf16", seed=0, extra=0):
+    g = gen(seed)
+    t, b = sum(own), len(own)
+    n = s + t + extra
+    dt = E4M3 if pool == "e4m3" else BF16
+    perm = torch.randperm(n, generator=g, device=DEV)
+    return {
+        "q": normal(g, b * l, hq, d), "ke": normal(g, b * l, hk, d), "ve": normal(g, b * l, hk, d),
+        "kb": normal(g, n, hk, d).to(dt), "vb": normal(g, n, hk, d).to(dt), "sh": perm[:s].clone(),
+        "kvi": perm[s:s + t].clone(), "kvp": indptr(own), "qo": indptr([l] * b), "l": l, "own": own,
+    }
+
+
+def rows64(pool, loc):
+    return pool.float()[loc].to(F64) if pool.dtype == E4M3 else pool[loc].to(F64)
+
+
+def shared_want(c, scale, ks=1.0, vs=1.0):
+    l, at = c["l"], 0
+    o, a = torch.empty(c["q"].shape, dtype=F64, device=DEV), torch.empty(c["q"].shape, dtype=F64, device=DEV)
+    for b, n in enumerate(c["own"]):
+        r = slice(b * l, (b + 1) * l)
+        loc = torch.cat([c["sh"], c["kvi"][at:at + n]]).long()
+        k = torch.cat([rows64(c["kb"], loc) * ks, c["ke"][r].to(F64)])
+        v = torch.cat([rows64(c["vb"], loc) * vs, c["ve"][r].to(F64)])
+        vis = torch.ones(l, len(loc) + l, dtype=torch.bool, device=DEV).tril(len(loc))
+        o[r], a[r] = attend64(c["q"][r].to(F64), k, v, vis, scale)
+        at += n
+    return o, a
+
+
+def run_shared(vsk, c, **kw):
+    o = torch.full_like(c["q"], float("nan"))
+    vsk.verify_splitkv_shared_fwd(c["q"], c["ke"], c["ve"], o, c["kb"], c["vb"], c["qo"], c["kvp"], c["kvi"], c["sh"],
+                                  c["l"], **kw)
+    return o
+
+
+SHARED = [
+    # (shared keys, own lengths, drafts, h_q, h_kv, d, pool)
+    (1, (0,), 1, 1, 1, 64, "bf16"), (0, (5, 70), 4, 4, 2, 64, "bf16"), (0, (0, 0), 3, 4, 2, 128, "bf16"),
+    (127, (1, 0, 33), 2, 6, 2, 128, "bf16"), (128, (64, 96), 4, 4, 1, 64, "bf16"), (129, (7,), 8, 16, 1, 128, "bf16"),
+    (1000, (0, 0, 0, 0, 0), 1, 8, 8, 128, "bf16"), (513, tuple(range(40)), 4, 16, 4, 128, "bf16"),
+    (5000, (300, 200), 5, 15, 3, 64, "bf16"), (3001, (17, 900, 0), 4, 16, 2, 256, "bf16"),
+    (700, (30,) * 9, 7, 14, 2, 256, "bf16"), (260, (0, 9), 128, 2, 2, 128, "bf16"), (260, (3, 9), 1, 128, 1, 64, "bf16"),
+    (1, (0, 2), 2, 4, 2, 256, "e4m3"), (385, (60, 0, 5), 4, 8, 2, 64, "e4m3"), (2049, (100, 33), 3, 9, 3, 128, "e4m3"),
+    (4000, (0, 512, 100), 4, 16, 2, 256, "e4m3"), (9000, (10,) * 70, 4, 8, 1, 128, "e4m3"),
+]
+
+
+@pytest.mark.parametrize("case", SHARED, ids=lambda c: f"s{c[0]}b{len(c[1])}l{c[2]}h{c[3]}x{c[4]}d{c[5]}{c[6]}")
+def test_shared_against_64_bits(vsk, case):
+    c = shared_case(*case, seed=21, extra=3)
+    unused = torch.ones(c["kb"].shape[0], dtype=torch.bool, device=DEV)
+    unused[c["sh"]] = False
+    unused[c["kvi"]] = False
+    for pool in (c["kb"], c["vb"]):  # rows no sequence refers to hold no number
+        pool.view(torch.uint8 if pool.dtype == E4M3 else torch.int16)[unused] = 0x7F if pool.dtype == E4M3 else 0x7FC0
+    o = run_shared(vsk, c)
+    check_attention(o, *shared_want(c, case[5] ** -0.5))
+    assert vsk.read_error_flags() == 0
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("ks,vs", [(0.5, 0.25), (-0.7, 2.0), (0.0, 1.0)])
+def test_shared_scales(vsk, pool, ks, vs):
+    c = shared_case(300, (20, 0, 150), 4, 8, 2, 128, pool, seed=22)
+    c["sh"], c["kvi"] = c["sh"].int(), c["kvi"].int()
+    o = run_shared(vsk, c, k_scale=ks, v_scale=vs, sm_scale=0.1)
+    check_attention(o, *shared_want(c, 0.1, ks, vs))
+
+
+def test_shared_equals_the_verify_call_on_joined_indices(vsk):
+    c = shared_case(777, (50, 0, 301), 4, 16, 4, 128, seed=23)
+    parts, at = [], 0
+    for n in c["own"]:
+        parts += [c["sh"], c["kvi"][at:at + n]]
+        at += n
+    o2 = torch.empty_like(c["q"])
+    assert vsk.verify_splitkv_fwd(c["q"], c["ke"], c["ve"], o2, c["kb"], c["vb"], c["qo"],
+                                  indptr([777 + n for n in c["own"]]), torch.cat(parts), None, True, None, c["l"], 1.0, 1.0)
+    _, a = shared_want(c, 128 ** -0.5)
+    # both are within the header's bound of the exact value
+    check_attention(run_shared(vsk, c), o2.to(F64), 2 * a)
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+def test_shared_bad_indices_are_left_out_and_flagged(vsk, pool):
+    c = shared_case(400, (30, 8), 4, 8, 2, 128, pool, seed=24)
+    good = dict(c)
+    keep = torch.ones(400, dtype=torch.bool, device=DEV)
+    keep[[3, 129, 399]] = False
+    good["sh"] = c["sh"][keep]
+    c["sh"][3], c["sh"][129], c["sh"][399] = -1, c["kb"].shape[0], 1 << 40
+    o = run_shared(vsk, c)
+    check_attention(o, *shared_want(good, 128 ** -0.5))
+    assert vsk.read_error_flags() == 1
+    c["sh"][:] = -5  # no shared key is left
+    good["sh"] = c["sh"][:0]
+    check_attention(run_shared(vsk, c), *shared_want(good, 128 ** -0.5))
+    assert vsk.read_error_flags() == 1

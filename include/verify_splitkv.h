@@ -42,7 +42,8 @@ enum {
   VSK_DTYPE_FP8E4M3 = 1,  /* float8 e4m3 "fn" (no infinities)           */
   VSK_DTYPE_I32 = 2,      /* int32                                      */
   VSK_DTYPE_I64 = 3,      /* int64                                      */
-  VSK_DTYPE_U8 = 4        /* uint8 (also used for bool masks)           */
+  VSK_DTYPE_U8 = 4,       /* uint8 (also used for bool masks)           */
+  VSK_DTYPE_F32 = 5       /* float32 (attention weights)                */
 };
 
 /* A strided view of device memory.  Strides and shape are in ELEMENTS.  For
@@ -51,7 +52,7 @@ enum {
 typedef struct vsk_tensor {
   const void* data;  /* device pointer (may be NULL only when the tensor is empty) */
   int32_t dtype;     /* one of VSK_DTYPE_*                                          */
-  int32_t ndim;      /* 1 or 3                                                      */
+  int32_t ndim;      /* 1, 2 or 3                                                   */
   int64_t shape[3];
   int64_t stride[3];
 } vsk_tensor;
@@ -282,6 +283,52 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q_extend, const vsk_tensor* k_ex
 size_t vsk_shared_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv,
                                  int64_t head_dim, int64_t max_len_extend);
 
+/* Attention weight of the cached keys: what every prefix key of a verify call
+ * receives from the call's draft rows, added to what it had.
+ *   mass[h][t] = mass_in[h][t] + sum over the rows (draft i, query head of KV
+ *                head h) of the softmax weight of the key of entry t
+ * for every entry t of kv_indices that belongs to a sequence (other columns
+ * are left as they were); the softmax is the one of verify_splitkv_fwd, over
+ * the sequence's prefix and its drafts up to i.  A key with a bad index gets
+ * weight 0 and sets error bit 1.
+ *   mass, mass_in   [h_kv, n] float32, n = kv_indices entries, rows contiguous;
+ *                   mass_in NULL counts as zeros and may be mass itself
+ *   other arguments and limits as verify_splitkv_fwd (head_dim in {64, 128,
+ *                   256}, (h_q/h_kv)*l_ext <= 128, or 64 at 256); workspace as
+ *                   prompt_attn_fwd.
+ * One launch on `stream`; the sums have a fixed order. */
+int verify_splitkv_mass(const vsk_tensor* q_extend, const vsk_tensor* k_extend,
+                        const vsk_tensor* k_buffer, const vsk_tensor* qo_indptr,
+                        const vsk_tensor* kv_indptr, const vsk_tensor* kv_indices,
+                        const vsk_tensor* mass_in, const vsk_tensor* mass,
+                        int64_t max_len_extend, float k_scale, float sm_scale,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Cuts every sequence's cache index down to a budget by accumulated attention
+ * weight.  A sequence of at most `budget` entries keeps them all; a longer one
+ * keeps its last `recent` entries and, of the others, the budget - recent of
+ * largest total[t] = mass[0][t] + mass[1][t] + ... (32-bit sums, heads in
+ * ascending order; equal totals: the earliest entries; NaN counts as the
+ * largest).  Kept entries stay in their order.
+ *   mass            [h_kv, n] float32 (as verify_splitkv_mass leaves it)
+ *   kv_indptr [B+1] int32, kv_indices [n] int32 or int64
+ *   budget >= 1, 0 <= recent <= budget
+ *   out_kv_indptr   [B+1] int32
+ *   out_kv_indices  [m] of kv_indices' type, out_mass [h_kv, m] float32: the
+ *                   kept entries and their weights, packed (m = min(n,
+ *                   B * budget) always suffices; what lies behind
+ *                   out_kv_indptr[B] is left as it was)
+ *   freed           of kv_indices' type: the other entries, sequence after
+ *                   sequence in their order (n entries always suffice): the
+ *                   pool rows that may be reused
+ * Outputs must not overlap inputs.  An output that is too short is filled and
+ * sets error bit 32.  Inconsistent kv_indptr entries give an empty sequence and
+ * set bit 2.  workspace as prompt_attn_fwd.  One launch on `stream`. */
+int kv_evict(const vsk_tensor* mass, const vsk_tensor* kv_indptr, const vsk_tensor* kv_indices,
+             int64_t budget, int64_t recent, const vsk_tensor* out_kv_indptr,
+             const vsk_tensor* out_kv_indices, const vsk_tensor* out_mass,
+             const vsk_tensor* freed, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Upper bound, in bytes, of the workspace verify_splitkv_fwd needs for any
  * batch of up to max_bs sequences with these head counts and sizes on the
  * CURRENT CUDA device (its SM count sets the number of persistent CTAs).
@@ -310,7 +357,8 @@ int vsk_workspace_init(void* workspace, size_t bytes, void* stream);
  * such waits: the CTA then stops streaming, frees its tensor memory and
  * exits, and that call's output is not valid; the default kernel has no
  * waits that can time out); 16 = a mask_indptr entry of
- * verify_splitkv_tree_fwd outside custom_mask.  Returns 1 on success, 0 on a
+ * verify_splitkv_tree_fwd outside custom_mask; 32 = an output of kv_evict too
+ * short for what is kept or freed.  Returns 1 on success, 0 on a
  * CUDA error.
  * Intended for tests and debugging: it blocks the host. */
 int vsk_read_error_flags(void* workspace, void* stream, uint32_t* flags);

@@ -8,11 +8,11 @@ from .api import (as_vsk, call_form, can_handle, get_workspace, launches_per_cal
                   set_tuning_tiles,
                   verify_splitkv_fwd, verify_splitkv_paged_fwd, verify_splitkv_paged_write_fwd,
                   verify_splitkv_write_fwd, version, workspace_size)
-from .cache_ops import prompt_attn_fwd, shared_workspace_size, verify_splitkv_shared_fwd
+from .cache_ops import kv_evict, prompt_attn_fwd, shared_workspace_size, verify_splitkv_mass, verify_splitkv_shared_fwd
 from ._native import build, last_error
 
-__all__ = ["as_vsk", "build", "call_form", "can_handle", "get_workspace", "last_error", "launches_per_call", "prompt_attn_fwd",
+__all__ = ["as_vsk", "build", "call_form", "can_handle", "get_workspace", "kv_evict", "last_error", "launches_per_call", "prompt_attn_fwd",
            "read_error_flags",
            "set_tuning", "set_tuning_cluster", "set_tuning_colsplit", "set_tuning_colsplit2", "set_tuning_pdl", "set_tuning_pipe", "set_tuning_shape", "set_tuning_split_launch", "set_tuning_tc",
            "set_tuning_tiles", "shared_workspace_size", "verify_splitkv_fwd", "verify_splitkv_paged_fwd", "verify_splitkv_paged_write_fwd",
-           "verify_splitkv_shared_fwd", "verify_splitkv_write_fwd", "version", "workspace_size"]
+           "verify_splitkv_mass", "verify_splitkv_shared_fwd", "verify_splitkv_write_fwd", "version", "workspace_size"]

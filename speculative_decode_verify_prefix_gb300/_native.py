@@ -79,7 +79,7 @@ class VskTensor(ctypes.Structure):
     ]
 
 
-DTYPE_BF16, DTYPE_FP8E4M3, DTYPE_I32, DTYPE_I64, DTYPE_U8 = 0, 1, 2, 3, 4
+DTYPE_BF16, DTYPE_FP8E4M3, DTYPE_I32, DTYPE_I64, DTYPE_U8, DTYPE_F32 = 0, 1, 2, 3, 4, 5
 
 _lib = None
 _lock = threading.Lock()
@@ -114,6 +114,12 @@ def _bind(lib):
     lib.verify_splitkv_shared_fwd.argtypes = [_P] * 10 + [ctypes.c_int64, ctypes.c_float, ctypes.c_float,
                                                           ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t,
                                                           ctypes.c_void_p]
+    lib.verify_splitkv_mass.restype = ctypes.c_int
+    lib.verify_splitkv_mass.argtypes = [_P] * 8 + [ctypes.c_int64, ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
+                                                   ctypes.c_size_t, ctypes.c_void_p]
+    lib.kv_evict.restype = ctypes.c_int
+    lib.kv_evict.argtypes = [_P] * 3 + [ctypes.c_int64, ctypes.c_int64] + [_P] * 4 + [
+        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.vsk_shared_workspace_size.restype = ctypes.c_size_t
     lib.vsk_shared_workspace_size.argtypes = [ctypes.c_int64] * 5
     lib.vsk_workspace_size.restype = ctypes.c_size_t

@@ -29,6 +29,7 @@ _DT = {
     torch.int64: _native.DTYPE_I64,
     torch.uint8: _native.DTYPE_U8,
     torch.bool: _native.DTYPE_U8,
+    torch.float32: _native.DTYPE_F32,
 }
 
 

@@ -1,5 +1,6 @@
 """Python binding of the calls around the verify call: attention over whole
-prompts and the verify call for a batch that shares a long prefix.
+prompts, the verify call for a batch that shares a long prefix, the attention
+weight of the cached keys and the eviction that goes by it.
 
 As in api.py: argument marshalling only, every step of the computation runs in
 the library's kernels, on the given stream (default: the current one of the
@@ -100,3 +101,36 @@ def verify_splitkv_shared_fwd(q_extend, k_extend, v_extend, o_extend, k_buffer, 
          _ref(q_extend), _ref(k_extend), _ref(v_extend), _ref(o_extend), _ref(k_buffer), _ref(v_buffer),
          _ref(qo_indptr), _ref(kv_indptr), _ref(kv_indices), _ref(shared_indices), mle, _coerce(k_scale),
          _coerce(v_scale), 0.0 if sm_scale is None else float(sm_scale))
+
+
+def verify_splitkv_mass(q_extend, k_extend, k_buffer, qo_indptr, kv_indptr, kv_indices, mass, max_len_extend,
+                        k_scale=1.0, sm_scale=None, mass_in=None, workspace=None, stream=None) -> None:
+    """Attention weight of the cached keys: writes to ``mass`` ([h_kv,
+    len(kv_indices)] float32) ``mass_in`` (None: zeros; may be ``mass`` itself)
+    plus, for every entry of ``kv_indices``, the sum over the draft rows and the
+    query heads of the KV head of the softmax weight its key has in
+    ``verify_splitkv_fwd`` (causal drafts)."""
+    named = dict(q_extend=q_extend, k_extend=k_extend, k_buffer=k_buffer, qo_indptr=qo_indptr, kv_indptr=kv_indptr,
+                 kv_indices=kv_indices, mass=mass)
+    if mass_in is not None:
+        named["mass_in"] = mass_in
+    dev = _device_of(**named)
+    _run("verify_splitkv_mass", dev, stream, workspace, lambda: 256, _ref(q_extend), _ref(k_extend), _ref(k_buffer),
+         _ref(qo_indptr), _ref(kv_indptr), _ref(kv_indices), None if mass_in is None else _ref(mass_in), _ref(mass),
+         int(max_len_extend), _coerce(k_scale), 0.0 if sm_scale is None else float(sm_scale))
+
+
+def kv_evict(mass, kv_indptr, kv_indices, budget, recent, out_kv_indptr, out_kv_indices, out_mass, freed,
+             workspace=None, stream=None) -> None:
+    """Cuts every sequence's cache index to ``budget`` entries: its last
+    ``recent`` ones and, of the others, those with the largest ``mass`` summed
+    over the KV heads, in their order.
+
+    Writes ``out_kv_indptr`` ([B+1] int32), the kept entries to
+    ``out_kv_indices`` and their weights to ``out_mass`` (both packed; min(n, B *
+    budget) columns always suffice) and the others, whose pool rows may be
+    reused, to ``freed`` (out_kv_indptr and kv_indptr tell how many)."""
+    dev = _device_of(mass=mass, kv_indptr=kv_indptr, kv_indices=kv_indices, out_kv_indptr=out_kv_indptr,
+                     out_kv_indices=out_kv_indices, out_mass=out_mass, freed=freed)
+    _run("kv_evict", dev, stream, workspace, lambda: 256, _ref(mass), _ref(kv_indptr), _ref(kv_indices), int(budget),
+         int(recent), _ref(out_kv_indptr), _ref(out_kv_indices), _ref(out_mass), _ref(freed))

@@ -1,12 +1,15 @@
 // Host side of the calls around the verify call: attention over whole prompts
-// (prompt_attn_fwd) and the verify call for a batch that shares a long prefix
-// (verify_splitkv_shared_fwd).
+// (prompt_attn_fwd), the verify call for a batch that shares a long prefix
+// (verify_splitkv_shared_fwd), the attention weight of the cached keys
+// (verify_splitkv_mass) and the eviction that goes by it (kv_evict).
 #include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstring>
 
 #include "flash_tc.cuh"
+#include "key_mass.cuh"
+#include "kv_evict.cuh"
 #include "shared_combine.cuh"
 #include "verify_host.cuh"
 
@@ -108,6 +111,60 @@ static size_t shared_workspace_for_sms(int sms, long long max_bs, long long h_q,
   if (own == 0 || h_q / h_kv > 128) return 0;
   const SharedCut c = shared_cut(max_bs * L, h_q / h_kv, h_kv, D, 1, sms);
   return own + shared_partial_bytes(std::max(c.units, 2LL * sms), c.nq, D);
+}
+
+// ---- one thread-block cluster per segment ----
+// Launches fn in clusters of c CTAs (at most 16; 8, then fewer, where so many
+// do not fit together on the GPU) over n_seg segments.
+static int launch_clusters(const void* fn, int c, long long n_seg, int threads, size_t smem, void** args,
+                           cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return fail("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  if (c > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+    cudaGetLastError();
+    c = 8;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  for (;; c /= 2) {
+    at[0].val.clusterDim.x = static_cast<unsigned>(c);
+    cfg.gridDim = dim3(static_cast<unsigned>(c));
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n >= 1) break;
+    cudaGetLastError();
+    if (c == 1) return fail("cluster of one CTA does not fit");
+  }
+  if (n_seg * c > INT_MAX) return fail("grid of %lld CTAs too large", n_seg * c);
+  cfg.gridDim = dim3(static_cast<unsigned>(n_seg * c));
+  e = cudaLaunchKernelExC(&cfg, fn, args);
+  if (e != cudaSuccess) return fail("kernel launch failed: %s", cudaGetErrorString(e));
+  return 1;
+}
+
+// A CTA's slice of a segment of the mean length holds at most `per` keys,
+// unless the cluster would pass 16 CTAs.
+static int cluster_size(long long mean_len, long long per) {
+  int c = 1;
+  while (c < 16 && mean_len > c * per) c *= 2;
+  return c;
+}
+constexpr long long kMassKeysPerCta = 256;
+constexpr long long kEvictKeysPerCta = 2048;
+
+static bool check_rows(const vsk_tensor* t, const char* name, long long rows) {
+  if (!check_2d(t, name)) return false;
+  if (t->dtype != VSK_DTYPE_F32) return fail("%s must be float32", name);
+  if (t->shape[0] != rows) return fail("%s must have one row per KV head (%lld)", name, rows);
+  if (!aligned(t->data, 4)) return fail("%s must be 4-byte aligned", name);
+  return true;
 }
 
 }  // namespace vsk
@@ -286,6 +343,129 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
   e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(128), args, 0, st);
   if (e != cudaSuccess) return fail("combine kernel launch failed: %s", cudaGetErrorString(e));
   return 1;
+}
+
+int verify_splitkv_mass(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tensor* kb, const vsk_tensor* qo,
+                        const vsk_tensor* kvp, const vsk_tensor* kvi, const vsk_tensor* mass_in,
+                        const vsk_tensor* mass, int64_t max_len_extend, float k_scale, float sm_scale, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  clear_error();
+  Params p;
+  CallShape cs;
+  // the values play no part: the keys stand in for them in the checks, the queries for the output
+  if (!prepare_verify(q, ke, ke, q, kb, kb, qo, kvp, kvi, 1, max_len_extend, k_scale, 1.f, sm_scale, nullptr, nullptr,
+                      nullptr, p, cs))
+    return 0;
+  const long long T = kvi->shape[0];
+  if (!check_rows(mass, "mass", cs.h_kv)) return 0;
+  if (mass->shape[1] != T) return fail("mass must have one column per kv_indices entry (%lld)", T);
+  if (mass_in) {
+    if (!check_rows(mass_in, "mass_in", cs.h_kv)) return 0;
+    if (mass_in->shape[1] != T) return fail("mass_in must have one column per kv_indices entry (%lld)", T);
+  }
+  if (T == 0) return 1;
+  km::MassParams m;
+  memset(&m, 0, sizeof m);
+  m.h_kv = static_cast<int>(cs.h_kv);
+  m.MT = static_cast<int>(((cs.h_q / cs.h_kv) * cs.L + 15) / 16);
+  const int rows = static_cast<int>((cs.h_q / cs.h_kv) * cs.L);
+  m.s_off = 16 * m.MT * static_cast<int>(cs.D) * 2;
+  m.cap = (km::kSmem - m.s_off) / (4 * rows) - 8;
+  m.cap = m.cap / 32 * 32;
+  m.pitch = m.cap + 8;  // 8 mod 32 floats: the four row groups of a fragment store meet different banks
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  size_t ws_bytes = 0;
+  unsigned char* ws = take_workspace(workspace, workspace_bytes, 256, st, &ws_bytes);
+  if (!ws) return 0;
+  p.B = static_cast<int>(cs.B);
+  p.L = static_cast<int>(cs.L);
+  p.gq = static_cast<int>(cs.h_q / cs.h_kv);
+  p.R = rows;
+  p.err = reinterpret_cast<unsigned*>(ws);
+  m.v = p;
+  m.in = mass_in ? static_cast<const float*>(mass_in->data) : nullptr;
+  m.in_s0 = mass_in ? mass_in->stride[0] : 0;
+  m.out = static_cast<float*>(const_cast<void*>(mass->data));
+  m.out_s0 = mass->stride[0];
+  void* args[] = {&m};
+  const size_t smem = m.s_off + static_cast<size_t>(m.pitch) * 4 * rows;
+  const km::MassFn fn = kernel_mass(static_cast<int>(cs.D), cs.fp8, m.MT == 1 && cs.D <= 128);
+  return launch_clusters(reinterpret_cast<const void*>(fn), cluster_size(cs.mean_len, kMassKeysPerCta),
+                         cs.B * cs.h_kv, km::kThreads, smem, args, st);
+}
+
+int kv_evict(const vsk_tensor* mass, const vsk_tensor* kvp, const vsk_tensor* kvi, int64_t budget, int64_t recent,
+             const vsk_tensor* out_kvp, const vsk_tensor* out_kvi, const vsk_tensor* out_mass,
+             const vsk_tensor* freed, void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  if (!check_1d(kvp, "kv_indptr") || !check_1d(kvi, "kv_indices") || !check_1d(out_kvp, "out_kv_indptr") ||
+      !check_1d(out_kvi, "out_kv_indices") || !check_1d(freed, "freed") || !check_2d(mass, "mass"))
+    return 0;
+  const long long B = kvp->shape[0] - 1, T = kvi->shape[0], h_kv = mass->shape[0];
+  if (B < 1) return fail("batch size must be >= 1");
+  if (kvp->dtype != VSK_DTYPE_I32 || out_kvp->dtype != VSK_DTYPE_I32) return fail("indptr arrays must be int32");
+  if (out_kvp->shape[0] != B + 1) return fail("out_kv_indptr must have B+1 entries");
+  if (kvi->dtype != VSK_DTYPE_I32 && kvi->dtype != VSK_DTYPE_I64) return fail("kv_indices must be int32 or int64");
+  if (out_kvi->dtype != kvi->dtype || freed->dtype != kvi->dtype)
+    return fail("out_kv_indices and freed must have the type of kv_indices");
+  const size_t ei = kvi->dtype == VSK_DTYPE_I64 ? 8 : 4;
+  if (!aligned(kvi->data, ei) || !aligned(out_kvi->data, ei) || !aligned(freed->data, ei) || !aligned(kvp->data, 4) ||
+      !aligned(out_kvp->data, 4))
+    return fail("index arrays must be aligned to their type");
+  if (h_kv < 1) return fail("mass must have one row per KV head");
+  if (!check_rows(mass, "mass", h_kv) || !check_rows(out_mass, "out_mass", h_kv)) return 0;
+  if (mass->shape[1] != T) return fail("mass must have one column per kv_indices entry (%lld)", T);
+  if (out_mass->shape[1] != out_kvi->shape[0]) return fail("out_mass must have one column per out_kv_indices entry");
+  if (budget < 1) return fail("budget must be >= 1");
+  if (recent < 0 || recent > budget) return fail("recent must be in [0, budget]");
+  // the kernel packs while it reads
+  struct Range { const vsk_tensor* t; const char* name; size_t bytes; };
+  auto span2 = [](const vsk_tensor* t) {
+    return t->shape[0] * t->shape[1] == 0 ? size_t{0}
+                                          : static_cast<size_t>(4 * ((t->shape[0] - 1) * t->stride[0] + t->shape[1]));
+  };
+  const Range ins[] = {{kvp, "kv_indptr", 4 * static_cast<size_t>(B + 1)}, {kvi, "kv_indices", ei * static_cast<size_t>(T)},
+                       {mass, "mass", span2(mass)}};
+  const Range outs[] = {{out_kvp, "out_kv_indptr", 4 * static_cast<size_t>(B + 1)},
+                        {out_kvi, "out_kv_indices", ei * static_cast<size_t>(out_kvi->shape[0])},
+                        {out_mass, "out_mass", span2(out_mass)},
+                        {freed, "freed", ei * static_cast<size_t>(freed->shape[0])}};
+  for (const Range& o : outs)
+    for (const Range& i : ins) {
+      const char *a = static_cast<const char*>(o.t->data), *c = static_cast<const char*>(i.t->data);
+      if (o.bytes > 0 && i.bytes > 0 && a < c + i.bytes && c < a + o.bytes)
+        return fail("%s overlaps %s", o.name, i.name);
+    }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  size_t ws_bytes = 0;
+  unsigned char* ws = take_workspace(workspace, workspace_bytes, 256, st, &ws_bytes);
+  if (!ws) return 0;
+  ev::EvictParams p;
+  memset(&p, 0, sizeof p);
+  p.mass = static_cast<const float*>(mass->data);
+  p.mass_s0 = mass->stride[0];
+  p.kvp = static_cast<const int*>(kvp->data);
+  p.kvi = kvi->data;
+  p.idx64 = kvi->dtype == VSK_DTYPE_I64;
+  p.h_kv = static_cast<int>(h_kv);
+  p.B = static_cast<int>(B);
+  p.n_idx = T;
+  p.budget = budget;
+  p.recent = recent;
+  p.out_ptr = static_cast<int*>(const_cast<void*>(out_kvp->data));
+  p.out_idx = const_cast<void*>(out_kvi->data);
+  p.out_mass = static_cast<float*>(const_cast<void*>(out_mass->data));
+  p.out_s0 = out_mass->stride[0];
+  p.freed = const_cast<void*>(freed->data);
+  p.out_cap = out_kvi->shape[0];
+  p.freed_cap = freed->shape[0];
+  p.err = reinterpret_cast<unsigned*>(ws);
+  const int c = cluster_size(T / B, kEvictKeysPerCta);
+  // slices of up to twice the mean stay in shared memory
+  p.cap = static_cast<int>(std::min(24576LL, std::max(4096LL, 2 * (T / B / c + 1))));
+  void* args[] = {&p};
+  return launch_clusters(reinterpret_cast<const void*>(evict_kernel), c, B, ev::kThreads,
+                         4 * static_cast<size_t>(p.cap), args, st);
 }
 
 }  // extern "C"

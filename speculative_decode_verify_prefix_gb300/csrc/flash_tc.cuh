@@ -445,6 +445,10 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
     }
     // ---- epilogue ----
     if (my_tiles > 0) {
+      // one query tile: the last scores are issued before the PV of the tile
+      // before, so that phase has to be seen to complete first
+      if (NQ == 1 && my_tiles > 1)
+        tr::wait_warp(bar(kBOFull + t), static_cast<uint32_t>((my_tiles - 2) & 1), abort_flag, p.err);
       tr::wait_warp(bar(kBOFull + t), static_cast<uint32_t>((my_tiles - 1) & 1), abort_flag, p.err);
       tc_fence_after();
     }

@@ -238,7 +238,8 @@ SHARED = [
     (5000, (300, 200), 5, 15, 3, 64, "bf16"), (3001, (17, 900, 0), 4, 16, 2, 256, "bf16"),
     (700, (30,) * 9, 7, 14, 2, 256, "bf16"), (260, (0, 9), 128, 2, 2, 128, "bf16"), (260, (3, 9), 1, 128, 1, 64, "bf16"),
     (1, (0, 2), 2, 4, 2, 256, "e4m3"), (385, (60, 0, 5), 4, 8, 2, 64, "e4m3"), (2049, (100, 33), 3, 9, 3, 128, "e4m3"),
-    (4000, (0, 512, 100), 4, 16, 2, 256, "e4m3"), (9000, (10,) * 70, 4, 8, 1, 128, "e4m3"),
+    (4000, (0, 512, 100), 4, 16, 2, 256, "e4m3"), (8192, (0, 100, 512, 3, 40, 500, 10, 0), 4, 16, 2, 256, "e4m3"),
+    (40000, (0, 7, 0), 4, 16, 2, 256, "e4m3"), (40000, (0, 7, 0), 4, 16, 2, 256, "bf16"), (40000, (9,), 4, 16, 2, 128, "e4m3"), (9000, (10,) * 70, 4, 8, 1, 128, "e4m3"),
 ]
 
 

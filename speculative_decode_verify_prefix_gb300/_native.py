@@ -85,6 +85,7 @@ _lib = None
 _lock = threading.Lock()
 
 _P = ctypes.POINTER(VskTensor)
+_V = ctypes.c_void_p  # a VskTensor by address
 
 
 def _bind(lib):
@@ -109,16 +110,16 @@ def _bind(lib):
                                                               ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
                                                               ctypes.c_size_t, ctypes.c_void_p]
     lib.prompt_attn_fwd.restype = ctypes.c_int
-    lib.prompt_attn_fwd.argtypes = [_P] * 5 + [ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.prompt_attn_fwd.argtypes = [_V] * 5 + [ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.verify_splitkv_shared_fwd.restype = ctypes.c_int
-    lib.verify_splitkv_shared_fwd.argtypes = [_P] * 10 + [ctypes.c_int64, ctypes.c_float, ctypes.c_float,
+    lib.verify_splitkv_shared_fwd.argtypes = [_V] * 10 + [ctypes.c_int64, ctypes.c_float, ctypes.c_float,
                                                           ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t,
                                                           ctypes.c_void_p]
     lib.verify_splitkv_mass.restype = ctypes.c_int
-    lib.verify_splitkv_mass.argtypes = [_P] * 8 + [ctypes.c_int64, ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
+    lib.verify_splitkv_mass.argtypes = [_V] * 8 + [ctypes.c_int64, ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
                                                    ctypes.c_size_t, ctypes.c_void_p]
     lib.kv_evict.restype = ctypes.c_int
-    lib.kv_evict.argtypes = [_P] * 3 + [ctypes.c_int64, ctypes.c_int64] + [_P] * 4 + [
+    lib.kv_evict.argtypes = [_V] * 3 + [ctypes.c_int64, ctypes.c_int64] + [_V] * 4 + [
         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.vsk_shared_workspace_size.restype = ctypes.c_size_t
     lib.vsk_shared_workspace_size.argtypes = [ctypes.c_int64] * 5

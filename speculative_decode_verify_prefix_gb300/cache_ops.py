@@ -10,52 +10,87 @@ raises ValueError with its message and launches nothing.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
 from . import _native
-from .api import _WS, _WS_LOCK, _coerce, _ref
+from .api import _DT, _WS, _WS_LOCK, _coerce
+
+# A vsk_tensor: data, dtype, ndim, shape[3], stride[3].  The views of a call are
+# packed into one buffer: about a third of the time of filling a ctypes
+# structure per tensor (a call of ten tensors 57 -> 24 us on the host).
+_VIEW = struct.Struct("Pii6q")
+assert _VIEW.size == ctypes.sizeof(_native.VskTensor)
 
 
-def _device_of(**tensors) -> torch.device:
-    """The CUDA device of a call's tensors; they must all be on one."""
-    dev = None
-    for name, t in tensors.items():
+def _views(device, named):
+    """The packed views of a call's tensors (None stays None) and their
+    addresses; all tensors must be on one CUDA device, which is returned."""
+    buf = (ctypes.c_char * (_VIEW.size * len(named)))()
+    at, args, off = ctypes.addressof(buf), [], 0
+    for name, t in named:
+        if t is None:
+            args.append(None)
+            continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
-        dev = t.device
-    return dev
+        dev = t.get_device()
+        if device is None:
+            device = dev
+        elif dev != device:
+            raise ValueError(f"{name} is on cuda:{dev}, the call's other tensors on cuda:{device}")
+        shape, stride = t.shape, t.stride()
+        n = len(shape)
+        if n < 3:
+            shape, stride = (*shape, 0, 0, 0)[:3], (*stride, 0, 0, 0)[:3]
+        _VIEW.pack_into(buf, off, t.data_ptr() if t.numel() else 0, _DT.get(t.dtype, -1), n, *shape[:3], *stride[:3])
+        args.append(at + off)
+        off += _VIEW.size
+    return device, buf, args
 
 
-def _workspace_of(device, stream, need):
+def _workspace_of(device, stream, raw_stream, need):
     """The cached workspace of (device, stream), grown to ``need`` bytes.  Not
     while the stream is captured: growing it later would free the buffer that
     the graph keeps using."""
-    with torch.cuda.stream(stream):
-        if torch.cuda.is_current_stream_capturing():
-            raise ValueError("pass workspace= to a call that is captured into a graph")
-        key = (device, int(stream.cuda_stream))
-        with _WS_LOCK:
+    if stream is None:
+        capturing = torch.cuda.is_current_stream_capturing()
+    else:
+        with torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+    if capturing:
+        raise ValueError("pass workspace= to a call that is captured into a graph")
+    key = (torch.device("cuda", device), raw_stream)
+    ws = _WS.get(key)
+    if ws is None or ws.numel() < need:
+        with torch.cuda.stream(stream), _WS_LOCK:  # zeroed in the order of the stream that uses it
             ws = _WS.get(key)
             if ws is None or ws.numel() < need:
-                ws = torch.zeros(need, dtype=torch.uint8, device=device)
+                ws = torch.zeros(need, dtype=torch.uint8, device=key[0])
                 _WS[key] = ws
     return ws
 
 
-def _run(name, device, stream, workspace, need, *args) -> None:
-    """Calls a library entry point whose last arguments are workspace, its
-    bytes and the stream, with ``device`` current."""
-    with torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        if workspace is None:
-            workspace = _workspace_of(device, stream, need())
-        ok = getattr(_native.lib(), name)(*args, ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                          ctypes.c_void_p(stream.cuda_stream))
-    if not ok:
+def _run(name, named, scalars, stream, workspace, need=None) -> None:
+    """Calls a library entry point: the tensors' views, the scalars, then
+    workspace, its bytes and the stream, with the tensors' device current.
+    ``named``: (name, tensor) in the order of the C arguments, a scalar in
+    between as (None, value).  ``need``: workspace bytes (None: the error word)."""
+    device, buf, args = _views(None, [x for x in named if x[0] is not None])
+    if any(x[0] is None for x in named):
+        it = iter(args)
+        args = [next(it) if n is not None else v for n, v in named]
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _run(name, named, scalars, stream, workspace, need)
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if workspace is None:
+        workspace = _workspace_of(device, stream, raw, 256 if need is None else need())
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
+    if not getattr(_native.lib(), name)(*args, *scalars, workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), raw):
         raise ValueError(f"{name}: {_native.last_error()}")
 
 
@@ -67,9 +102,11 @@ def prompt_attn_fwd(q, k, v, o, qo_indptr, sm_scale=None, workspace=None, stream
     qo_indptr[b] .. qo_indptr[b+1] - 1, of any lengths.  Row i of a sequence
     attends to its rows t <= i.  Rows of ``o`` outside every sequence are left
     as they were.  ``workspace``: 256 bytes or more (the error word)."""
-    dev = _device_of(q=q, k=k, v=v, o=o, qo_indptr=qo_indptr)
-    _run("prompt_attn_fwd", dev, stream, workspace, lambda: 256, _ref(q), _ref(k), _ref(v), _ref(o), _ref(qo_indptr),
-         0.0 if sm_scale is None else float(sm_scale))
+    _run("prompt_attn_fwd", (("q", q), ("k", k), ("v", v), ("o", o), ("qo_indptr", qo_indptr)),
+         (0.0 if sm_scale is None else float(sm_scale),), stream, workspace)
+
+
+_SIZES = {}  # (device, max_bs, h_q, h_kv, head_dim, l_ext) -> bytes
 
 
 def shared_workspace_size(max_bs, h_q, h_kv, head_dim, l_ext) -> int:
@@ -85,9 +122,6 @@ def verify_splitkv_shared_fwd(q_extend, k_extend, v_extend, o_extend, k_buffer, 
     a prefix: every sequence's prefix is the pool rows ``shared_indices``
     ([S] int32 or int64) followed by its own ``kv_indices`` rows.  The shared
     rows are read for the whole batch at once, not per sequence."""
-    dev = _device_of(q_extend=q_extend, k_extend=k_extend, v_extend=v_extend, o_extend=o_extend, k_buffer=k_buffer,
-                     v_buffer=v_buffer, qo_indptr=qo_indptr, kv_indptr=kv_indptr, kv_indices=kv_indices,
-                     shared_indices=shared_indices)
     mle = int(max_len_extend)
 
     def need():
@@ -95,12 +129,18 @@ def verify_splitkv_shared_fwd(q_extend, k_extend, v_extend, o_extend, k_buffer, 
             return 256  # the library names what is wrong
         bs = qo_indptr.shape[0] - 1
         mb = bs if (max_bs is None or max_bs < bs) else int(max_bs)
-        return shared_workspace_size(mb, q_extend.shape[1], k_extend.shape[1], q_extend.shape[2], mle) or 256
+        key = (q_extend.get_device(), mb, q_extend.shape[1], k_extend.shape[1], q_extend.shape[2], mle)
+        n = _SIZES.get(key)
+        if n is None:
+            n = _SIZES[key] = shared_workspace_size(*key[1:]) or 256
+        return n
 
-    _run("verify_splitkv_shared_fwd", dev, stream, workspace, need,
-         _ref(q_extend), _ref(k_extend), _ref(v_extend), _ref(o_extend), _ref(k_buffer), _ref(v_buffer),
-         _ref(qo_indptr), _ref(kv_indptr), _ref(kv_indices), _ref(shared_indices), mle, _coerce(k_scale),
-         _coerce(v_scale), 0.0 if sm_scale is None else float(sm_scale))
+    _run("verify_splitkv_shared_fwd",
+         (("q_extend", q_extend), ("k_extend", k_extend), ("v_extend", v_extend), ("o_extend", o_extend),
+          ("k_buffer", k_buffer), ("v_buffer", v_buffer), ("qo_indptr", qo_indptr), ("kv_indptr", kv_indptr),
+          ("kv_indices", kv_indices), ("shared_indices", shared_indices)),
+         (mle, _coerce(k_scale), _coerce(v_scale), 0.0 if sm_scale is None else float(sm_scale)), stream, workspace,
+         need)
 
 
 def verify_splitkv_mass(q_extend, k_extend, k_buffer, qo_indptr, kv_indptr, kv_indices, mass, max_len_extend,
@@ -110,14 +150,10 @@ def verify_splitkv_mass(q_extend, k_extend, k_buffer, qo_indptr, kv_indptr, kv_i
     plus, for every entry of ``kv_indices``, the sum over the draft rows and the
     query heads of the KV head of the softmax weight its key has in
     ``verify_splitkv_fwd`` (causal drafts)."""
-    named = dict(q_extend=q_extend, k_extend=k_extend, k_buffer=k_buffer, qo_indptr=qo_indptr, kv_indptr=kv_indptr,
-                 kv_indices=kv_indices, mass=mass)
-    if mass_in is not None:
-        named["mass_in"] = mass_in
-    dev = _device_of(**named)
-    _run("verify_splitkv_mass", dev, stream, workspace, lambda: 256, _ref(q_extend), _ref(k_extend), _ref(k_buffer),
-         _ref(qo_indptr), _ref(kv_indptr), _ref(kv_indices), None if mass_in is None else _ref(mass_in), _ref(mass),
-         int(max_len_extend), _coerce(k_scale), 0.0 if sm_scale is None else float(sm_scale))
+    _run("verify_splitkv_mass",
+         (("q_extend", q_extend), ("k_extend", k_extend), ("k_buffer", k_buffer), ("qo_indptr", qo_indptr),
+          ("kv_indptr", kv_indptr), ("kv_indices", kv_indices), ("mass_in", mass_in), ("mass", mass)),
+         (int(max_len_extend), _coerce(k_scale), 0.0 if sm_scale is None else float(sm_scale)), stream, workspace)
 
 
 def kv_evict(mass, kv_indptr, kv_indices, budget, recent, out_kv_indptr, out_kv_indices, out_mass, freed,
@@ -130,7 +166,7 @@ def kv_evict(mass, kv_indptr, kv_indices, budget, recent, out_kv_indptr, out_kv_
     ``out_kv_indices`` and their weights to ``out_mass`` (both packed; min(n, B *
     budget) columns always suffice) and the others, whose pool rows may be
     reused, to ``freed`` (out_kv_indptr and kv_indptr tell how many)."""
-    dev = _device_of(mass=mass, kv_indptr=kv_indptr, kv_indices=kv_indices, out_kv_indptr=out_kv_indptr,
-                     out_kv_indices=out_kv_indices, out_mass=out_mass, freed=freed)
-    _run("kv_evict", dev, stream, workspace, lambda: 256, _ref(mass), _ref(kv_indptr), _ref(kv_indices), int(budget),
-         int(recent), _ref(out_kv_indptr), _ref(out_kv_indices), _ref(out_mass), _ref(freed))
+    _run("kv_evict",
+         (("mass", mass), ("kv_indptr", kv_indptr), ("kv_indices", kv_indices), (None, int(budget)),
+          (None, int(recent)), ("out_kv_indptr", out_kv_indptr), ("out_kv_indices", out_kv_indices),
+          ("out_mass", out_mass), ("freed", freed)), (), stream, workspace)

@@ -6,6 +6,9 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <map>
+#include <mutex>
+#include <tuple>
 
 #include "flash_tc.cuh"
 #include "key_mass.cuh"
@@ -114,11 +117,18 @@ static size_t shared_workspace_for_sms(int sms, long long max_bs, long long h_q,
 }
 
 // ---- one thread-block cluster per segment ----
-// Launches fn in clusters of c CTAs (at most 16; 8, then fewer, where so many
-// do not fit together on the GPU) over n_seg segments.
-static int launch_clusters(const void* fn, int c, long long n_seg, int threads, size_t smem, void** args,
-                           cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+// The largest cluster of at most c CTAs (c, then 8 or fewer by halves) of which
+// one fits on the current device; asked from the runtime once per shape (the
+// query costs several microseconds).  0: none fits.
+static int cluster_fit(const void* fn, int c, int threads, size_t smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail("no CUDA device");
+  static std::mutex mu;
+  static std::map<std::tuple<int, const void*, int, int, size_t>, int> known;
+  std::lock_guard<std::mutex> lk(mu);
+  int& fit = known[{dev, fn, c, threads, smem}];
+  if (fit > 0) return fit;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerCTAMax - 4096);
   if (e != cudaSuccess) return fail("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   if (c > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
     cudaGetLastError();
@@ -131,20 +141,36 @@ static int launch_clusters(const void* fn, int c, long long n_seg, int threads, 
   at[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  for (;; c /= 2) {
+  for (; c >= 1; c /= 2) {
     at[0].val.clusterDim.x = static_cast<unsigned>(c);
     cfg.gridDim = dim3(static_cast<unsigned>(c));
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n >= 1) break;
-    cudaGetLastError();
-    if (c == 1) return fail("cluster of one CTA does not fit");
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n >= 1) return fit = c;
+    cudaGetLastError();  // clear the error the query left
   }
+  return fail("a cluster of one CTA does not fit");
+}
+
+static int launch_clusters(const void* fn, int c, long long n_seg, int threads, size_t smem, void** args,
+                           cudaStream_t st) {
+  c = cluster_fit(fn, c, threads, smem);
+  if (c == 0) return 0;
   if (n_seg * c > INT_MAX) return fail("grid of %lld CTAs too large", n_seg * c);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(c);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(n_seg * c));
-  e = cudaLaunchKernelExC(&cfg, fn, args);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
   if (e != cudaSuccess) return fail("kernel launch failed: %s", cudaGetErrorString(e));
   return 1;
 }

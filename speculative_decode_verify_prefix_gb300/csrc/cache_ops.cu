@@ -389,15 +389,18 @@ int verify_splitkv_mass(const vsk_tensor* q, const vsk_tensor* ke, const vsk_ten
     if (!check_rows(mass_in, "mass_in", cs.h_kv)) return 0;
     if (mass_in->shape[1] != T) return fail("mass_in must have one column per kv_indices entry (%lld)", T);
   }
+  if (kb->shape[0] >= 0xFFFFFFFFLL) return fail("a pool of %lld rows is too large", static_cast<long long>(kb->shape[0]));
   if (T == 0) return 1;
   km::MassParams m;
   memset(&m, 0, sizeof m);
   m.h_kv = static_cast<int>(cs.h_kv);
   m.MT = static_cast<int>(((cs.h_q / cs.h_kv) * cs.L + 15) / 16);
   const int rows = static_cast<int>((cs.h_q / cs.h_kv) * cs.L);
-  m.s_off = 16 * m.MT * static_cast<int>(cs.D) * 2;
-  m.cap = (km::kSmem - m.s_off) / (4 * rows) - 8;
+  m.x_off = 16 * m.MT * static_cast<int>(cs.D) * 2;
+  m.i_off = m.x_off + (16 * rows * 8 + 127) / 128 * 128;
+  m.cap = (km::kSmem - m.i_off) / (4 * rows + 4) - 8;
   m.cap = m.cap / 32 * 32;
+  m.s_off = m.i_off + 4 * m.cap;
   m.pitch = m.cap + 8;  // 8 mod 32 floats: the four row groups of a fragment store meet different banks
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   size_t ws_bytes = 0;

@@ -38,13 +38,14 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRows = 128;
 constexpr int kSmem = 110 * 1024;  // two CTAs per SM
+constexpr unsigned kNoRow = 0xFFFFFFFFu;
 
 struct MassParams {
   Params v;                 // the flat call: q, ke, kb, qo, kvp, kvi, scales
   const float* in; long long in_s0;
   float* out;      long long out_s0;
   int h_kv, MT, cap, pitch;  // keys of a chunk (a multiple of 32), floats between score rows
-  int q_off, s_off;          // shared memory: queries, scores
+  int x_off, i_off, s_off;   // shared memory: the CTAs' row sums, pool rows, scores (queries at 0)
 };
 using MassFn = void (*)(const MassParams);
 
@@ -59,11 +60,20 @@ struct Geo {
   static constexpr int QCH = D / 8;                         // 16-byte chunks of a query row in shared memory
 };
 
-__device__ __forceinline__ uint4 ld_stream(const void* a) {
+// 16 bytes of a key row; the lanes of a row take its 64-byte pieces one after
+// the other, so L2 is asked for all of it (ROWB bytes or 256) at the first, and
+// L1 keeps what the first brought (bypassing it measured 30 % slower)
+template <int ROWB>
+__device__ __forceinline__ uint4 ld_row(const void* a) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(a));
+  if constexpr (ROWB >= 256)
+    asm volatile("ld.global.nc.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(a));
+  else
+    asm volatile("ld.global.nc.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(a));
   return v;
 }
 
@@ -96,13 +106,14 @@ __global__ void __launch_bounds__(km::kThreads, 2) mass_kernel(const __grid_cons
     if (!q_ok) atomicOr(p.err, kErrBadQoIndptr);
   }
   if (P == 0) return;  // the whole cluster: no key, nothing to write
+  cluster.barrier_arrive();  // completes once every CTA runs: its shared memory may then be written
   const long long s_b = q_ok ? qa : static_cast<long long>(b) * p.L;
   const int per = (P + C * 32 - 1) / (C * 32) * 32;
   const int lo = static_cast<int>(min(static_cast<long long>(P), static_cast<long long>(rank) * per));
   const int hi = min(P, lo + per);
 
   // ---- queries into shared memory, 16-byte chunk c of row r at chunk c ^ (r & 7) ----
-  unsigned char* qs = smem + mp.q_off;
+  unsigned char* qs = smem;
   float* sc = reinterpret_cast<float*>(smem + mp.s_off);
   if (tid == 0) q_max = 0u;
   __syncthreads();
@@ -222,31 +233,21 @@ __global__ void __launch_bounds__(km::kThreads, 2) mass_kernel(const __grid_cons
     uint4 k[G::NB][G::NL];
     unsigned ok;  // bit n: key g of group n is in the chunk and its index in the pool
   };
-  // pool row of key g of group n of the stage at key0 (-2: past the chunk)
-  auto load_loc = [&](int key0, int end, long long (&loc)[G::NB]) {
-#pragma unroll
-    for (int n = 0; n < G::NB; ++n) {
-      const int key = key0 + 8 * n + g;
-      loc[n] = -2;
-      if (key < end)
-        loc[n] = p.idx64 ? __ldg(static_cast<const long long*>(p.kvi) + kv0 + key)
-                         : static_cast<long long>(__ldg(static_cast<const int*>(p.kvi) + kv0 + key));
-    }
-  };
-  auto load_k = [&](const long long (&loc)[G::NB], Stage& s) {
+  unsigned* idx = reinterpret_cast<unsigned*>(smem + mp.i_off);  // pool rows of the chunk's keys, kNoRow: none
+  auto load_k = [&](int at, Stage& s) {
     s.ok = 0u;
 #pragma unroll
     for (int n = 0; n < G::NB; ++n) {
-      const bool ok = loc[n] >= 0 && loc[n] < p.pool;
-      if (!ok && loc[n] != -2) atomicOr(p.err, kErrBadIndex);
+      const unsigned loc = idx[at + 8 * n + g];
+      const bool ok = loc != kNoRow;
       s.ok |= ok ? 1u << n : 0u;
-      const unsigned char* src = kbase + (ok ? loc[n] : 0) * p.kb_s0 + 16 * j4;
+      const unsigned char* src = kbase + static_cast<long long>(ok ? loc : 0u) * p.kb_s0 + 16 * j4;
 #pragma unroll
-      for (int i = 0; i < G::NL; ++i) s.k[n][i] = ok ? ld_stream(src + 64 * i) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < G::NL; ++i) s.k[n][i] = ok ? ld_row<G::ROWB>(src + 64 * i) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
-  // scores of one stage into sc[row][key - c0]
-  auto multiply = [&](const Stage& s, int key0, int c0) {
+  // scores of one stage into sc[row][key of the chunk]
+  auto multiply = [&](const Stage& s, int at0) {
 #pragma unroll 1
     for (int mt = 0; mt < (QREG ? 1 : mp.MT); ++mt) {
       float acc[G::NB][4];
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(km::kThreads, 2) mass_kernel(const __grid_cons
         // columns 2 j4 and 2 j4 + 1 of the group: their keys' validity sits in lanes 8 j4 and 8 j4 + 4
         const bool v0 = (__shfl_sync(0xffffffffu, s.ok, 8 * j4) >> n) & 1u;
         const bool v1 = (__shfl_sync(0xffffffffu, s.ok, 8 * j4 + 4) >> n) & 1u;
-        const int at = key0 - c0 + 8 * n + 2 * j4;
+        const int at = at0 + 8 * n + 2 * j4;
         const int r = 16 * mt + g;
         if (r < p.R)
           *reinterpret_cast<float2*>(sc + r * mp.pitch + at) =
@@ -290,44 +291,69 @@ __global__ void __launch_bounds__(km::kThreads, 2) mass_kernel(const __grid_cons
       }
     }
   };
-  // scores of keys [c0, c1): stages dealt to the warps in turn, two in flight
-  auto chunk = [&](int c0, int c1) {
+  // scores of the chunk of n keys at c0: stages dealt to the warps in turn, one
+  // loading while the other is multiplied
+  auto chunk = [&](int c0, int n) {
     constexpr int STEP = kWarps * G::KEYS;
-    int key = c0 + warp * G::KEYS;
-    if (key >= c1) return;
-    long long loc[G::NB];
-    Stage s0, s1;
-    load_loc(key, c1, loc);
-    load_k(loc, s0);
-    load_loc(key + STEP, c1, loc);
-#pragma unroll 1
-    while (true) {
-      load_k(loc, s1);
-      load_loc(key + 2 * STEP, c1, loc);
-      multiply(s0, key, c0);
-      key += STEP;
-      if (key >= c1) break;
-      load_k(loc, s0);
-      load_loc(key + 2 * STEP, c1, loc);
-      multiply(s1, key, c0);
-      key += STEP;
-      if (key >= c1) break;
+    const int end = (n + G::KEYS - 1) / G::KEYS * G::KEYS;
+    for (int i = tid; i < end; i += kThreads) {
+      unsigned row = kNoRow;
+      if (i < n) {
+        const long long at = kv0 + c0 + i;
+        const long long loc = p.idx64 ? __ldg(static_cast<const long long*>(p.kvi) + at)
+                                      : static_cast<long long>(__ldg(static_cast<const int*>(p.kvi) + at));
+        if (loc >= 0 && loc < p.pool)
+          row = static_cast<unsigned>(loc);
+        else
+          atomicOr(p.err, kErrBadIndex);
+      }
+      idx[i] = row;
     }
-  };
-  const int n_chunks = (hi - lo + mp.cap - 1) / mp.cap;
-  for (int k = 0; k < n_chunks; ++k) {
-    const int c0 = lo + k * mp.cap, n = min(mp.cap, hi - c0);
-    __syncthreads();  // the scores of the chunk before are done with
-    chunk(c0, c0 + n);
     __syncthreads();
+    int at = warp * G::KEYS;
+    if (at < end) {
+      Stage s0, s1;
+      load_k(at, s0);
+#pragma unroll 1
+      while (true) {
+        if (at + STEP < end) load_k(at + STEP, s1);
+        multiply(s0, at);
+        at += STEP;
+        if (at >= end) break;
+        if (at + STEP < end) load_k(at + STEP, s0);
+        multiply(s1, at);
+        at += STEP;
+        if (at >= end) break;
+      }
+    }
+    __syncthreads();
+  };
+  // chunks of cap keys behind a first one of the rest, so that the scores kept
+  // at the end are as many as fit
+  const int n_chunks = (hi - lo + mp.cap - 1) / mp.cap;
+  const int rest = hi - lo - (n_chunks - 1) * mp.cap;
+  auto chunk_at = [&](int k) { return k == 0 ? lo : lo + rest + (k - 1) * mp.cap; };
+  auto chunk_keys = [&](int k) { return k == 0 ? rest : mp.cap; };
+  for (int k = 0; k < n_chunks; ++k) {
+    const int n = chunk_keys(k);
+    chunk(chunk_at(k), n);
     for (int r = warp; r < p.R; r += kWarps) {
-      const float* x = sc + r * mp.pitch;
+      // keys past n, up to a multiple of 4, hold -inf
+      const float4* x = reinterpret_cast<const float4*>(sc + r * mp.pitch);
       float m = NEG_INF, l = 0.f;
-      for (int i = lane; i < n; i += 32) m = fmaxf(m, x[i]);
+#pragma unroll 2
+      for (int i = lane; 4 * i < n; i += 32) {
+        const float4 v = x[i];
+        const float mn = fmaxf(fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)), m), ms = mn == NEG_INF ? 0.f : mn;
+        l = l * fast_exp2(m - ms) + ((fast_exp2(v.x - ms) + fast_exp2(v.y - ms)) + (fast_exp2(v.z - ms) + fast_exp2(v.w - ms)));
+        m = mn;
+      }
+      const float old = row_m[r];
+      float mn = fmaxf(m, old);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float old = row_m[r], mn = fmaxf(m, old), ms = mn == NEG_INF ? 0.f : mn;
-      for (int i = lane; i < n; i += 32) l += fast_exp2(x[i] - ms);
+      for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      const float ms = mn == NEG_INF ? 0.f : mn;
+      l *= fast_exp2(m - ms);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       __syncwarp();
@@ -336,35 +362,39 @@ __global__ void __launch_bounds__(km::kThreads, 2) mass_kernel(const __grid_cons
         row_m[r] = mn;
       }
     }
+    __syncthreads();  // the scores are done with
   }
 
-  // ---- the rows' sums over the whole cluster ----
+  // ---- the rows' sums over the whole cluster: every CTA hands its own to all ----
+  __syncthreads();
+  cluster.barrier_wait();
+  float2* xch = reinterpret_cast<float2*>(smem + mp.x_off);  // [C][R] (m, l)
+  for (int i = tid; i < C * p.R; i += kThreads) {
+    const int c = i / p.R, r = i % p.R;
+    *cluster.map_shared_rank(xch + rank * p.R + r, c) = make_float2(row_m[r], row_l[r]);
+  }
   cluster.sync();
   for (int r = tid; r < p.R; r += kThreads) {
-    float m = NEG_INF;
-    for (int c = 0; c < C; ++c) m = fmaxf(m, *cluster.map_shared_rank(row_m + r, c));
+    float m = NEG_INF, l = 0.f;
+    for (int c = 0; c < C; ++c) m = fmaxf(m, xch[c * p.R + r].x);
     const float ms = m == NEG_INF ? 0.f : m;
-    float l = 0.f;
-    for (int c = 0; c < C; ++c) {
-      const float mc = *cluster.map_shared_rank(row_m + r, c);
-      l += *cluster.map_shared_rank(row_l + r, c) * (mc == NEG_INF ? 0.f : exp2f(mc - ms));
-    }
+    for (int c = 0; c < C; ++c) l += xch[c * p.R + r].y * exp2f(xch[c * p.R + r].x - ms);
     row_lse[r] = l == 0.f ? INFINITY : ms + log2f(l);  // a row with nothing visible gives no weight
   }
-  cluster.sync();  // the others have read this CTA's sums; row_lse is complete
+  __syncthreads();
 
   // ---- weights: the last chunk from the kept scores, the others computed again ----
   const float* in = mp.in ? mp.in + h * mp.in_s0 + kv0 : nullptr;
   float* out = mp.out + h * mp.out_s0 + kv0;
   for (int k = n_chunks - 1; k >= 0; --k) {
-    const int c0 = lo + k * mp.cap, n = min(mp.cap, hi - c0);
+    const int c0 = chunk_at(k), n = chunk_keys(k);
     if (k < n_chunks - 1) {
       __syncthreads();
-      chunk(c0, c0 + n);
-      __syncthreads();
+      chunk(c0, n);
     }
     for (int i = tid; i < n; i += kThreads) {
       float w = 0.f;
+#pragma unroll 8
       for (int r = 0; r < p.R; ++r) w += fast_exp2(sc[r * mp.pitch + i] - row_lse[r]);
       out[c0 + i] = (in ? in[c0 + i] : 0.f) + w;
     }

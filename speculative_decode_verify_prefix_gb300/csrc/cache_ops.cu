@@ -183,7 +183,7 @@ static int cluster_size(long long mean_len, long long per) {
   return c;
 }
 constexpr long long kMassKeysPerCta = 256;
-constexpr long long kEvictKeysPerCta = 2048;
+constexpr long long kEvictKeysPerCta = 4096;
 
 static bool check_rows(const vsk_tensor* t, const char* name, long long rows) {
   if (!check_2d(t, name)) return false;

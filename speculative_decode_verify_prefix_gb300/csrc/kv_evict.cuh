@@ -13,12 +13,14 @@
 // one by counting.  One thread-block cluster owns a sequence; each CTA keeps its
 // slice's integers in shared memory (mass is read once; what does not fit is
 // summed again), counts into a 256-bin histogram and reads the others' through
-// distributed shared memory, so a pass costs one cluster barrier.  A second
-// walk over the slice packs the output: positions come from ballots and a scan
-// over the block, no atomics, so the result is exact and in order.
+// distributed shared memory, so a pass costs one cluster barrier.  To pack the
+// output every warp counts what it keeps of its part of the slice, the counts
+// are summed over the block and the cluster, and each warp then writes its part
+// with positions from ballots: no atomics on the output, so the result is
+// exact and in order.
 //
 // Bound by the mass rows (4 h_kv bytes a key) and, for short sequences, by the
-// seven cluster barriers.
+// five cluster barriers.
 #pragma once
 #include <cooperative_groups.h>
 
@@ -29,6 +31,7 @@ namespace ev {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 16;
 constexpr unsigned kErrNoRoom = 32u;  // an output is shorter than what is written to it
 
 struct EvictParams {
@@ -52,10 +55,19 @@ __device__ __forceinline__ int seq_len(const EvictParams& p, int b, bool& ok) {
   return ok ? e - a : 0;
 }
 
-// total of key j as an unsigned integer of the same order (+0 and -0 alike, NaN largest)
+// total of key j as an unsigned integer of the same order (+0 and -0 alike, NaN
+// largest); eight heads' loads at a time are in flight
 __device__ __forceinline__ unsigned order_key(const EvictParams& p, long long j) {
-  float t = __ldg(p.mass + j);
-  for (int h = 1; h < p.h_kv; ++h) t = __fadd_rn(t, __ldg(p.mass + h * p.mass_s0 + j));
+  float t = 0.f;
+  for (int h0 = 0; h0 < p.h_kv; h0 += 8) {
+    float x[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h0 + h < p.h_kv) x[h] = __ldg(p.mass + (h0 + h) * p.mass_s0 + j);
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+      if (h0 + h < p.h_kv) t = h0 + h == 0 ? x[h] : __fadd_rn(t, x[h]);
+  }
   if (t != t) return 0xFFFFFFFFu;
   const unsigned u = __float_as_uint(t + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
@@ -81,13 +93,14 @@ __global__ void __launch_bounds__(ev::kThreads) evict_kernel(const __grid_consta
   namespace cg = cooperative_groups;
   extern __shared__ unsigned keys[];
   __shared__ int hist[2][256];
-  __shared__ int counts[2];             // this CTA's keys above the threshold, and at it
+  __shared__ int2 counts[kMaxCluster];  // per CTA of the cluster: keys surely kept, keys at the threshold
   __shared__ long long scan[2][kWarps];
   __shared__ int sel_bin, sel_left, wsum[2][kWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = static_cast<int>(blockIdx.x / C);
+  cluster.barrier_arrive();  // completes once every CTA runs: its shared memory may then be written
 
   // ---- where this sequence's output starts ----
   long long kept_before = 0, gone_before = 0;
@@ -144,11 +157,14 @@ __global__ void __launch_bounds__(ev::kThreads) evict_kernel(const __grid_consta
         const unsigned u = key_at(j);
         if ((u & mask) == prefix) atomicAdd(hs + ((u >> shift) & 255u), 1);
       }
+      if (pass == 0) cluster.barrier_wait();
       cluster.sync();
       if (warp < 8) {
         // bin 255 - tid: how many keys lie in the bins above it
         int n = 0;
-        for (int c = 0; c < C; ++c) n += *cluster.map_shared_rank(hs + 255 - tid, c);
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < C) n += *cluster.map_shared_rank(hs + 255 - tid, c);
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -170,87 +186,89 @@ __global__ void __launch_bounds__(ev::kThreads) evict_kernel(const __grid_consta
     }
     thr = prefix;
     eq_left = k;
-    // ---- keys above and at the threshold in the slices before this one ----
-    int gt = 0, eq = 0;
-    for (int j = lo_o + tid; j < hi_o; j += kThreads) {
-      const unsigned u = key_at(j);
-      gt += u > thr;
-      eq += u == thr;
-    }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (tid == 0) counts[0] = counts[1] = 0;
-    __syncthreads();
-    if (lane == 0) {
-      atomicAdd(counts, gt);
-      atomicAdd(counts + 1, eq);
-    }
-    cluster.sync();
-    int gt_b = 0, eq_b = 0;
-    for (int c = 0; c < rank; ++c) {
-      gt_b += *cluster.map_shared_rank(counts, c);
-      eq_b += *cluster.map_shared_rank(counts + 1, c);
-    }
-    const int eq_k = min(eq_left, eq_b);
-    const int kept_o = gt_b + eq_k;
-    kept_before += kept_o + (lo - lo_o);
-    gone_before += lo_o - kept_o;
-    eq_left -= eq_k;
-    cluster.sync();  // the counts have been read
-  } else {
-    // nothing of [0, old) is kept
-    kept_before += lo - lo_o;
-    gone_before += lo_o;
   }
 
-  // ---- pack the slice ----
-  for (int j0 = lo; j0 < hi; j0 += kThreads) {
-    const int j = j0 + tid;
-    bool sure = false, tie = false;
-    if (j < hi) {
-      if (j >= old) {
-        sure = true;
-      } else if (want > 0) {
-        const unsigned u = key_at(j);
-        sure = u > thr;
-        tie = u == thr;
-      }
+  // ---- what each warp keeps: its part [w_lo, w_hi) of the slice, whole 32s ----
+  const int part = ((hi - lo + kWarps - 1) / kWarps + 31) / 32 * 32;
+  const int w_lo = min(hi, lo + warp * part), w_hi = min(hi, w_lo + part);
+  auto classify = [&](int j, bool& sure, bool& tie) {
+    sure = tie = false;
+    if (j >= w_hi) return;
+    if (j >= old) {
+      sure = true;
+    } else if (want > 0) {
+      const unsigned u = key_at(j);
+      sure = u > thr;
+      tie = u == thr;
     }
-    const unsigned ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
-    __syncthreads();  // the sums of the round before have been read
+  };
+  {
+    int ns = 0, nt = 0;
+    for (int j0 = w_lo; j0 < w_hi; j0 += 32) {
+      bool sure, tie;
+      classify(j0 + lane, sure, tie);
+      ns += __popc(__ballot_sync(0xffffffffu, sure));
+      nt += __popc(__ballot_sync(0xffffffffu, tie));
+    }
     if (lane == 0) {
-      wsum[0][warp] = __popc(ms);
-      wsum[1][warp] = __popc(mt);
+      wsum[0][warp] = ns;
+      wsum[1][warp] = nt;
     }
-    __syncthreads();
+  }
+  __syncthreads();
+  int sure_all = 0, tie_all = 0, sure_b = 0, tie_b = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    sure_b += w < warp ? wsum[0][w] : 0;
+    tie_b += w < warp ? wsum[1][w] : 0;
+    sure_all += wsum[0][w];
+    tie_all += wsum[1][w];
+  }
+  // every CTA hands its counts to all
+  if (want <= 0) cluster.barrier_wait();
+  if (tid < C) *cluster.map_shared_rank(counts + rank, tid) = make_int2(sure_all, tie_all);
+  cluster.sync();
+  for (int c = 0; c < rank; ++c) {
+    sure_b += counts[c].x;
+    tie_b += counts[c].y;
+  }
+
+  // ---- pack ----
+  int w_kept = sure_b + min(tie_b, eq_left);  // kept of the sequence before this warp's part
+  int left = eq_left - min(tie_b, eq_left);
+  kept_before += w_kept;
+  gone_before += w_lo - w_kept;
+  for (int j0 = w_lo; j0 < w_hi; j0 += 32) {
+    const int j = j0 + lane;
+    bool sure, tie;
+    classify(j, sure, tie);
+    const unsigned ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
     const unsigned below = (1u << lane) - 1u;
-    int s_b = __popc(ms & below), t_b = __popc(mt & below), s_all = 0, t_all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) {
-        s_b += wsum[0][w];
-        t_b += wsum[1][w];
-      }
-      s_all += wsum[0][w];
-      t_all += wsum[1][w];
-    }
-    const bool keep = sure || (tie && t_b < eq_left);
-    const int before = s_b + min(t_b, eq_left);  // kept keys before j in this round
-    if (j < hi) {
-      if (keep) {
+    const int t_b = __popc(mt & below), before = __popc(ms & below) + min(t_b, left);
+    if (j < w_hi) {
+      if (sure || (tie && t_b < left)) {
         const long long at = kept_before + before;
         if (at < p.out_cap) {
           copy_index(p, p.out_idx, at, kv0 + j);
-          for (int h = 0; h < p.h_kv; ++h) p.out_mass[h * p.out_s0 + at] = __ldg(p.mass + h * p.mass_s0 + kv0 + j);
+          for (int h0 = 0; h0 < p.h_kv; h0 += 8) {
+            float x[8];
+#pragma unroll
+            for (int h = 0; h < 8; ++h)
+              if (h0 + h < p.h_kv) x[h] = __ldg(p.mass + (h0 + h) * p.mass_s0 + kv0 + j);
+#pragma unroll
+            for (int h = 0; h < 8; ++h)
+              if (h0 + h < p.h_kv) p.out_mass[(h0 + h) * p.out_s0 + at] = x[h];
+          }
         }
       } else {
-        const long long at = gone_before + tid - before;
+        const long long at = gone_before + lane - before;
         if (at < p.freed_cap) copy_index(p, p.freed, at, kv0 + j);
       }
     }
-    const int n = min(kThreads, hi - j0), k = s_all + min(t_all, eq_left);
+    const int n_t = __popc(mt), k = __popc(ms) + min(n_t, left);
     kept_before += k;
-    gone_before += n - k;
-    eq_left -= min(t_all, eq_left);
+    gone_before += min(32, w_hi - j0) - k;
+    left -= min(n_t, left);
   }
 }
 

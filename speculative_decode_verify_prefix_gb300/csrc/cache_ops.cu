@@ -183,7 +183,7 @@ static int cluster_size(long long mean_len, long long per) {
   return c;
 }
 constexpr long long kMassKeysPerCta = 256;
-constexpr long long kEvictKeysPerCta = 4096;
+constexpr long long kEvictKeysPerCta = 8192;
 
 static bool check_rows(const vsk_tensor* t, const char* name, long long rows) {
   if (!check_2d(t, name)) return false;
@@ -494,7 +494,7 @@ int kv_evict(const vsk_tensor* mass, const vsk_tensor* kvp, const vsk_tensor* kv
   p.cap = static_cast<int>(std::min(24576LL, std::max(4096LL, 2 * (T / B / c + 1))));
   void* args[] = {&p};
   return launch_clusters(reinterpret_cast<const void*>(evict_kernel), c, B, ev::kThreads,
-                         4 * static_cast<size_t>(p.cap), args, st);
+                         8 * static_cast<size_t>(p.cap), args, st);
 }
 
 }  // extern "C"

@@ -14,10 +14,11 @@
 // slice's integers in shared memory (mass is read once; what does not fit is
 // summed again), counts into a 256-bin histogram and reads the others' through
 // distributed shared memory, so a pass costs one cluster barrier.  To pack the
-// output every warp counts what it keeps of its part of the slice, the counts
-// are summed over the block and the cluster, and each warp then writes its part
-// with positions from ballots: no atomics on the output, so the result is
-// exact and in order.
+// output every warp counts what it keeps of its part of the slice and the
+// counts are summed over the block and the cluster; positions from ballots
+// then sort the slice into a list (kept, others), which the block copies with
+// neighbouring threads on neighbouring outputs.  No atomics on the output, so
+// the result is exact and in order.
 //
 // Bound by the mass rows (4 h_kv bytes a key) and, for short sequences, by the
 // five cluster barriers.
@@ -45,7 +46,7 @@ struct EvictParams {
   float* out_mass; long long out_s0;
   void* freed;     // of kvi's type
   long long out_cap, freed_cap;
-  int cap;         // integers of a slice kept in shared memory
+  int cap;         // keys of a slice kept in shared memory (their integers; as many list entries)
   unsigned* err;
 };
 
@@ -188,12 +189,10 @@ __global__ void __launch_bounds__(ev::kThreads) evict_kernel(const __grid_consta
     eq_left = k;
   }
 
-  // ---- what each warp keeps: its part [w_lo, w_hi) of the slice, whole 32s ----
-  const int part = ((hi - lo + kWarps - 1) / kWarps + 31) / 32 * 32;
-  const int w_lo = min(hi, lo + warp * part), w_hi = min(hi, w_lo + part);
-  auto classify = [&](int j, bool& sure, bool& tie) {
+  // ---- how many keys of the slice are surely kept, and how many tie ----
+  auto classify = [&](int j, int end, bool& sure, bool& tie) {
     sure = tie = false;
-    if (j >= w_hi) return;
+    if (j >= end) return;
     if (j >= old) {
       sure = true;
     } else if (want > 0) {
@@ -202,11 +201,17 @@ __global__ void __launch_bounds__(ev::kThreads) evict_kernel(const __grid_consta
       tie = u == thr;
     }
   };
-  {
+  // counts of keys [c0, c1): of this warp's part [w_lo, w_hi) (whole 32s) in
+  // wsum, and summed over the parts before it and over all
+  int w_lo, w_hi, sure_b, tie_b, sure_all, tie_all;
+  auto count = [&](int c0, int c1) {
+    const int part = ((c1 - c0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+    w_lo = min(c1, c0 + warp * part);
+    w_hi = min(c1, w_lo + part);
     int ns = 0, nt = 0;
     for (int j0 = w_lo; j0 < w_hi; j0 += 32) {
       bool sure, tie;
-      classify(j0 + lane, sure, tie);
+      classify(j0 + lane, w_hi, sure, tie);
       ns += __popc(__ballot_sync(0xffffffffu, sure));
       nt += __popc(__ballot_sync(0xffffffffu, tie));
     }
@@ -214,61 +219,78 @@ __global__ void __launch_bounds__(ev::kThreads) evict_kernel(const __grid_consta
       wsum[0][warp] = ns;
       wsum[1][warp] = nt;
     }
-  }
-  __syncthreads();
-  int sure_all = 0, tie_all = 0, sure_b = 0, tie_b = 0;
+    __syncthreads();
+    sure_b = tie_b = sure_all = tie_all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    sure_b += w < warp ? wsum[0][w] : 0;
-    tie_b += w < warp ? wsum[1][w] : 0;
-    sure_all += wsum[0][w];
-    tie_all += wsum[1][w];
-  }
+    for (int w = 0; w < kWarps; ++w) {
+      sure_b += w < warp ? wsum[0][w] : 0;
+      tie_b += w < warp ? wsum[1][w] : 0;
+      sure_all += wsum[0][w];
+      tie_all += wsum[1][w];
+    }
+  };
+  count(lo, hi);
   // every CTA hands its counts to all
   if (want <= 0) cluster.barrier_wait();
   if (tid < C) *cluster.map_shared_rank(counts + rank, tid) = make_int2(sure_all, tie_all);
   cluster.sync();
-  for (int c = 0; c < rank; ++c) {
-    sure_b += counts[c].x;
-    tie_b += counts[c].y;
+  {
+    int s = 0, t = 0;
+    for (int c = 0; c < rank; ++c) {
+      s += counts[c].x;
+      t += counts[c].y;
+    }
+    const int k = s + min(t, eq_left);  // kept of the sequence before this slice
+    kept_before += k;
+    gone_before += lo - k;
+    eq_left -= min(t, eq_left);
   }
 
-  // ---- pack ----
-  int w_kept = sure_b + min(tie_b, eq_left);  // kept of the sequence before this warp's part
-  int left = eq_left - min(tie_b, eq_left);
-  kept_before += w_kept;
-  gone_before += w_lo - w_kept;
-  for (int j0 = w_lo; j0 < w_hi; j0 += 32) {
-    const int j = j0 + lane;
-    bool sure, tie;
-    classify(j, sure, tie);
-    const unsigned ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
-    const unsigned below = (1u << lane) - 1u;
-    const int t_b = __popc(mt & below), before = __popc(ms & below) + min(t_b, left);
-    if (j < w_hi) {
-      if (sure || (tie && t_b < left)) {
-        const long long at = kept_before + before;
-        if (at < p.out_cap) {
-          copy_index(p, p.out_idx, at, kv0 + j);
-          for (int h0 = 0; h0 < p.h_kv; h0 += 8) {
-            float x[8];
+  // ---- pack, cap keys at a time: positions into a list (the kept ones, then
+  // the others), which the whole block then copies, neighbours by neighbours ----
+  unsigned* list = keys + p.cap;
+  for (int c0 = lo; c0 < hi; c0 += p.cap) {
+    const int n = min(p.cap, hi - c0);
+    if (n < hi - lo) {  // (a single chunk was counted above)
+      __syncthreads();
+      count(c0, c0 + n);
+    }
+    const int kept_n = sure_all + min(tie_all, eq_left);
+    int k0 = sure_b + min(tie_b, eq_left), left = eq_left - min(tie_b, eq_left);
+    for (int j0 = w_lo; j0 < w_hi; j0 += 32) {
+      const int j = j0 + lane;
+      bool sure, tie;
+      classify(j, w_hi, sure, tie);
+      const unsigned ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
+      const unsigned below = (1u << lane) - 1u;
+      const int t_b = __popc(mt & below), at = k0 + __popc(ms & below) + min(t_b, left);
+      if (j < w_hi) list[(sure || (tie && t_b < left)) ? at : kept_n + (j - c0) - at] = static_cast<unsigned>(j);
+      k0 += __popc(ms) + min(__popc(mt), left);
+      left -= min(__popc(mt), left);
+    }
+    __syncthreads();
+#pragma unroll 2
+    for (int i = tid; i < n; i += kThreads) {
+      const bool keep = i < kept_n;
+      const long long from = kv0 + list[i], to = keep ? kept_before + i : gone_before + i - kept_n;
+      if (to < (keep ? p.out_cap : p.freed_cap)) copy_index(p, keep ? p.out_idx : p.freed, to, from);
+    }
+    for (int i = tid; i < kept_n; i += kThreads) {
+      const long long from = kv0 + list[i], to = kept_before + i;
+      if (to >= p.out_cap) break;
+      for (int h0 = 0; h0 < p.h_kv; h0 += 8) {
+        float x[8];
 #pragma unroll
-            for (int h = 0; h < 8; ++h)
-              if (h0 + h < p.h_kv) x[h] = __ldg(p.mass + (h0 + h) * p.mass_s0 + kv0 + j);
+        for (int h = 0; h < 8; ++h)
+          if (h0 + h < p.h_kv) x[h] = __ldg(p.mass + (h0 + h) * p.mass_s0 + from);
 #pragma unroll
-            for (int h = 0; h < 8; ++h)
-              if (h0 + h < p.h_kv) p.out_mass[(h0 + h) * p.out_s0 + at] = x[h];
-          }
-        }
-      } else {
-        const long long at = gone_before + lane - before;
-        if (at < p.freed_cap) copy_index(p, p.freed, at, kv0 + j);
+        for (int h = 0; h < 8; ++h)
+          if (h0 + h < p.h_kv) p.out_mass[(h0 + h) * p.out_s0 + to] = x[h];
       }
     }
-    const int n_t = __popc(mt), k = __popc(ms) + min(n_t, left);
-    kept_before += k;
-    gone_before += min(32, w_hi - j0) - k;
-    left -= min(n_t, left);
+    kept_before += kept_n;
+    gone_before += n - kept_n;
+    eq_left -= min(tie_all, eq_left);
   }
 }
 

@@ -30,7 +30,7 @@
 //   warps 0-3, 4-7   softmax of query tile 0 / 1 (thread = row; at head_dim 256
 //                    warps 4-7 are idle): scores from tensor memory, P back
 //                    over them (bf16, half the columns), rescale, epilogue
-//   warp 8           one thread issues the MMAs: S = Q K^T (both operands in
+//   warp 8           issues the MMAs (one elected lane): S = Q K^T (both operands in
 //                    shared memory), O += P V (P in tensor memory)
 //   warps 12-15      copy K / V rows into a ring of 128-key entries (128 head
 //                    dimensions each, K then V of a tile) with 16-byte
@@ -134,6 +134,15 @@ struct FaParams {
 
 using FaFn = void (*)(const FaParams);
 
+// The MMA warp runs its loop converged; one elected lane issues each group of
+// MMAs.  Addresses and descriptors are then the same for the whole warp and stay
+// in uniform registers (in a branch of one lane around the whole loop every MMA
+// first moves them there: 140 cycles an MMA instead of 64).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void mma_f16_ts(uint32_t tmem, uint32_t a, uint64_t b, uint32_t id, bool acc) {
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
@@ -197,7 +206,8 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
   constexpr int NQ = G::NQ, NH = G::NH, NE = G::NE, ENT = G::ENT;
   constexpr bool PROMPT = MODE == kPrompt;
   extern __shared__ __align__(1024) unsigned char smem[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const float NEG_INF = -INFINITY;
 
   // ---- this CTA's work: row block (tokens [tok0, tok0 + NQ tpb) of rows [row0, row0 + n)), KV head, key tiles ----
@@ -515,14 +525,14 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp >= kWarpMma) {
-      if (warp == kWarpMma && lane == 0) {
+      if (warp == kWarpMma) {
         // ============================ MMA issue ============================
         constexpr uint32_t idS = idesc(1, 1, 0, 0, 128, KT);
         constexpr uint32_t idPV = idesc(1, 1, 0, 1, 128, G::ED);
         const uint64_t dq0 = sdesc(q_s, 16, 1024), dk0 = sdesc(ring_s, 16, 1024), dv0 = sdesc(ring_s, KT * 128, 1024);
         // entry of (tile j, K / V, half h): (2 j + kv) NH + h
         auto wait_full = [&](int e) {
-          tr::wait(bar(kBFull + e % NE), static_cast<uint32_t>((e / NE) & 1), abort_flag, p.err);
+          tr::wait_warp(bar(kBFull + e % NE), static_cast<uint32_t>((e / NE) & 1), abort_flag, p.err);
         };
         auto qk = [&](int t, int j) {
           const uint32_t dc = tmem + (NQ == 2 ? t : (j & 1)) * KT;
@@ -531,13 +541,15 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
             const int slot = (2 * j * NH + h) % NE;
             const uint64_t qd = dq0 + static_cast<uint64_t>((t * G::QT + h * 2 * (128 * 128)) >> 4);
             const uint64_t kd = dk0 + static_cast<uint64_t>((slot * ENT) >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < G::ED / 16; ++ks) {
-              const uint64_t off = static_cast<uint64_t>(((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4);
-              mma_f16_ss(dc, qd + off, kd + off, idS, h > 0 || ks > 0);
+              for (int ks = 0; ks < G::ED / 16; ++ks) {
+                const uint64_t off = static_cast<uint64_t>(((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4);
+                mma_f16_ss(dc, qd + off, kd + off, idS, h > 0 || ks > 0);
+              }
             }
           }
-          mma_commit(bar(kBSFull + (NQ == 2 ? t : (j & 1))));
+          if (elect_one()) mma_commit(bar(kBSFull + (NQ == 2 ? t : (j & 1))));
         };
         auto pv = [&](int t, int j) {
           const uint32_t a = tmem + (NQ == 2 ? t : (j & 1)) * KT;
@@ -545,12 +557,14 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
           for (int h = 0; h < NH; ++h) {
             const int slot = ((2 * j + 1) * NH + h) % NE;
             const uint64_t vd = dv0 + static_cast<uint64_t>((slot * ENT) >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < KT / 16; ++ks)
-              mma_f16_ts(tmem + G::col_o + t * D + h * G::ED, a + ks * 8, vd + static_cast<uint64_t>(ks * 128), idPV,
-                         j > 0 || ks > 0);
+              for (int ks = 0; ks < KT / 16; ++ks)
+                mma_f16_ts(tmem + G::col_o + t * D + h * G::ED, a + ks * 8, vd + static_cast<uint64_t>(ks * 128), idPV,
+                           j > 0 || ks > 0);
+            }
           }
-          mma_commit(bar(kBOFull + t));
+          if (elect_one()) mma_commit(bar(kBOFull + t));
         };
         auto acquire = [&](int j, int kv) {
 #pragma unroll
@@ -560,16 +574,17 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
         };
         auto release = [&](int j, int kv) {
 #pragma unroll
-          for (int h = 0; h < NH; ++h) mma_commit(bar(kBEmpty + ((2 * j + kv) * NH + h) % NE));
+          for (int h = 0; h < NH; ++h)
+            if (elect_one()) mma_commit(bar(kBEmpty + ((2 * j + kv) * NH + h) % NE));
         };
         auto wait_p = [&](int t, int j) {
           const int buf = NQ == 2 ? t : (j & 1);
-          tr::wait(bar(kBPFull + buf), static_cast<uint32_t>(NQ == 2 ? (j & 1) : ((j >> 1) & 1)), abort_flag, p.err);
+          tr::wait_warp(bar(kBPFull + buf), static_cast<uint32_t>(NQ == 2 ? (j & 1) : ((j >> 1) & 1)), abort_flag, p.err);
           tc_fence_after();
         };
         if (nt > 0) {
 #pragma unroll
-          for (int t = 0; t < NQ; ++t) tr::wait(bar(kBQFull + t), 0u, abort_flag, p.err);
+          for (int t = 0; t < NQ; ++t) tr::wait_warp(bar(kBQFull + t), 0u, abort_flag, p.err);
           acquire(0, 0);
 #pragma unroll
           for (int t = 0; t < NQ; ++t)
@@ -602,8 +617,8 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
             }
           }
         }
-        mma_commit(bar(kBDone));
-        tr::wait(bar(kBDone), 0u, abort_flag, p.err);  // no arrival is pending when the CTA exits
+        if (elect_one()) mma_commit(bar(kBDone));
+        tr::wait_warp(bar(kBDone), 0u, abort_flag, p.err);  // no arrival is pending when the CTA exits
       } else if (warp >= kWarpLoad) {
         // ================================ loaders ================================
         const int lw = warp - kWarpLoad;

@@ -10,6 +10,8 @@
 #include <mutex>
 #include <tuple>
 
+#include <cudaTypedefs.h>
+
 #include "flash_tc.cuh"
 #include "key_mass.cuh"
 #include "kv_evict.cuh"
@@ -25,14 +27,43 @@ fa::FaFn kernel_fa(int D, int mode) {
 static int fa_smem(int D) { return D == 64 ? fa::Geo<64>::smem : D == 128 ? fa::Geo<128>::smem : fa::Geo<256>::smem; }
 static int fa_nq(int D) { return D == 256 ? 1 : 2; }
 
-static int launch_fa(const fa::FaParams& p, int D, int mode, long long grid, cudaStream_t st) {
+// Tensor map of K or V rows [rows][h_kv][D] for [32 rows][64 columns] boxes in
+// the 128-byte swizzle.  False where the strides are none that a map takes
+// (rows then go by cp.async).
+static bool rows_map(const vsk_tensor* t, CUtensorMap* map) {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+        r == cudaDriverEntryPointSuccess)
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    cudaGetLastError();
+  });
+  // a dimension of one element has any stride
+  const long long n = t->shape[0], h = t->shape[1], d = t->shape[2];
+  const long long s1 = h > 1 ? t->stride[1] : d, s0 = n > 1 ? t->stride[0] : h * s1;
+  if (!encode || s1 < d || s0 < d || s0 >= (1LL << 38) || s1 >= (1LL << 38)) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(h), static_cast<cuuint64_t>(n)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * s1), static_cast<cuuint64_t>(2 * s0)};
+  const cuuint32_t box[3] = {64, 1, 32}, unit[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(t->data), dims, strides, box, unit,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static int launch_fa(const fa::FaParams& p, const CUtensorMap* maps, int D, int mode, long long grid, cudaStream_t st) {
   fa::FaFn fn = kernel_fa(D, mode);
   if (grid > INT_MAX) return fail("grid of %lld CTAs too large", grid);
   cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        fa_smem(D));
   if (e != cudaSuccess) return fail("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   fa::FaParams a = p;
-  void* args[] = {&a};
+  CUtensorMap m[2];
+  memset(m, 0, sizeof m);
+  if (maps) memcpy(m, maps, sizeof m);
+  void* args[] = {&a, &m[0], &m[1]};
   e = cudaLaunchKernel(reinterpret_cast<const void*>(fn), dim3(static_cast<unsigned>(grid)), dim3(fa::kThreads), args,
                        fa_smem(D), st);
   if (e != cudaSuccess) return fail("kernel launch failed: %s", cudaGetErrorString(e));
@@ -255,7 +286,9 @@ int prompt_attn_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* 
   p.err = reinterpret_cast<unsigned*>(ws);
   // every sequence adds at most one row block to its share of N / block
   const long long blocks = N / (fa_nq(static_cast<int>(D)) * p.tpb) + B;
-  return launch_fa(p, static_cast<int>(D), fa::kPrompt, blocks * h_kv, st);
+  CUtensorMap maps[2];
+  p.tma = rows_map(k, &maps[0]) && rows_map(v, &maps[1]);
+  return launch_fa(p, p.tma ? maps : nullptr, static_cast<int>(D), fa::kPrompt, blocks * h_kv, st);
 }
 
 size_t vsk_shared_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv, int64_t head_dim, int64_t max_len_extend) {
@@ -342,7 +375,7 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
     f.err = reinterpret_cast<unsigned*>(ws);
     f.plse = reinterpret_cast<float*>(ws + base);
     f.po = reinterpret_cast<float*>(ws + sh_o);
-    if (!launch_fa(f, D, cs.fp8 ? fa::kSharedE4m3 : fa::kSharedBf16, items, st)) return 0;
+    if (!launch_fa(f, nullptr, D, cs.fp8 ? fa::kSharedE4m3 : fa::kSharedBf16, items, st)) return 0;
   }
   p.B = static_cast<int>(cs.B);
   p.L = static_cast<int>(cs.L);

@@ -32,9 +32,10 @@
 //                    over them (bf16, half the columns), rescale, epilogue
 //   warp 8           issues the MMAs (one elected lane): S = Q K^T (both operands in
 //                    shared memory), O += P V (P in tensor memory)
-//   warps 12-15      copy K / V rows into a ring of 128-key entries (128 head
-//                    dimensions each, K then V of a tile) with 16-byte
-//                    cp.async; e4m3 rows are widened to bf16 (exact) in registers
+//   warps 12-15      bring K / V rows into a ring of 128-key entries (128 head
+//                    dimensions each, K then V of a tile): contiguous rows by
+//                    TMA, gathered ones with 16-byte cp.async; e4m3 rows are
+//                    widened to bf16 (exact) in registers
 // S of the next tile is issued behind PV of this one: the issuing order makes
 // the overwrite of P by S safe.
 //
@@ -51,6 +52,8 @@
 // Every mbarrier wait is bounded (one second): a wait that gives up sets error
 // bit 8 and the CTA drains, frees its tensor memory and exits.
 #pragma once
+#include <cuda.h>
+
 #include "verify_kernel.cuh"
 #include "verify_tr.cuh"
 
@@ -126,13 +129,14 @@ struct FaParams {
   float scale2;           // > 0
   int qmode;              // queries enter as they are (0), negated (1) or as zeros (2): the sign of the scale
   int q16, o16;           // 16-byte accesses allowed
+  int tma;                // prompt: K / V tiles come through the tensor maps
   float v_scale;
   unsigned* err;
   float* plse;            // shared: partials, one row block of NQ * 128 rows per CTA
   float* po;
 };
 
-using FaFn = void (*)(const FaParams);
+using FaFn = void (*)(const FaParams, const CUtensorMap, const CUtensorMap);
 
 // The MMA warp runs its loop converged; one elected lane issues each group of
 // MMAs.  Addresses and descriptors are then the same for the whole warp and stay
@@ -190,6 +194,21 @@ __device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, bool
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 
+// One [32 rows][64 head dimensions] box of a K / V tensor map into shared memory.
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int head, int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          dst),
+      "l"(map), "r"(bar), "r"(x), "r"(head), "r"(row)
+      : "memory");
+}
+// A warp's 32 arrivals by one lane: 31, and one that also announces the bytes
+// its copies will bring.
+__device__ __forceinline__ void mbar_arrive_warp_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 31;" ::"r"(bar) : "memory");
+}
+
 // bf16 pair with infinities and NaN replaced by 0; bad: whether there were any
 __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, bool& bad) {
   const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
@@ -200,7 +219,9 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, bool& bad) {
 }  // namespace fa
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_constant__ fa::FaParams p) {
+__global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_constant__ fa::FaParams p,
+                                                             const __grid_constant__ CUtensorMap kmap,
+                                                             const __grid_constant__ CUtensorMap vmap) {
   using namespace fa;
   using G = fa::Geo<D>;
   constexpr int NQ = G::NQ, NH = G::NH, NE = G::NE, ENT = G::ENT;
@@ -695,6 +716,18 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
                 }
                 fence_proxy_async();
                 mbar_arrive(bar(kBFull + e % NE));
+              } else if (PROMPT && p.tma && (kv == 0 || j < j_edge)) {
+                // keys past the sequence may come along: their scores are masked,
+                // and V tiles that hold any take the next branch
+                if (lane == 0) {
+                  const uint32_t d0 = smem_u32(ent) + 32 * lw * 128, fb = bar(kBFull + e % NE);
+                  mbar_arrive_warp_tx(fb, 32 * G::ED * 2);
+#pragma unroll
+                  for (int cb = 0; cb < G::ED / 64; ++cb)
+                    tma_load_box(d0 + cb * (KT * 128), kv ? &vmap : &kmap, fb, h * G::ED + cb * 64, head,
+                                 static_cast<int>(row0) + j * KT + 32 * lw);
+                }
+                __syncwarp();
               } else if (PROMPT && kv == 1 && j >= j_edge) {
                 // V on the diagonal: values that are not finite become 0 here
                 // and are added by the epilogue to the rows that see them

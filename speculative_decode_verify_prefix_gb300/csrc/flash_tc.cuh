@@ -94,7 +94,7 @@ constexpr int kMaskOff = 1024;   // [kMaskRing][4] key-validity words
 constexpr int kDataOff = 2048;
 // barriers
 constexpr int kBFull = 0, kBEmpty = kMaxNE, kBQFull = 2 * kMaxNE, kBSFull = kBQFull + 2, kBPFull = kBSFull + 2,
-              kBOFull = kBPFull + 2, kBMask = kBOFull + 2, kBDone = kBMask + kMaskRing, kNumBars = kBDone + 1;
+              kBOFull = kBPFull + 4, kBMask = kBOFull + 2, kBDone = kBMask + kMaskRing, kNumBars = kBDone + 1;
 static_assert(kBarOff + 8 * kNumBars <= kTmemOff, "barriers overlap");
 
 template <int D>
@@ -192,6 +192,28 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
 // 16-byte global -> shared copy through L2 only, zeros when !valid
 __device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+
+// Two 32-bit operations in one instruction; the larger of three.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 d, a, b;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // One [32 rows][64 head dimensions] box of a K / V tensor map into shared memory.
@@ -338,7 +360,8 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(kBQFull + t), 4);
       mbar_init(bar(kBSFull + t), 1);
-      mbar_init(bar(kBPFull + t), 4);
+      mbar_init(bar(kBPFull + 2 * t), 4);
+      mbar_init(bar(kBPFull + 2 * t + 1), 4);
       mbar_init(bar(kBOFull + t), 1);
     }
     for (int i = 0; i < kMaskRing; ++i) mbar_init(bar(kBMask + i), 4);
@@ -405,35 +428,51 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
       const uint32_t t_s = t_lane + buf * KT;
       tr::wait_warp(bar(kBSFull + buf), par, abort_flag, p.err);
       tc_fence_after();
+      // Scores, then P, in halves of 64 keys: the second half is on its way
+      // while the first one's maximum is taken, and the first half of P is
+      // handed to the MMAs while the second is computed.
       uint32_t s[KT];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32_nw(t_s + 32 * c, s + 32 * c);
-      tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_pass(s + 32 * c);
-      // ---- masked keys: -inf ----
+      bool masked;
+      unsigned mw[4];
       if constexpr (PROMPT) {
-        if ((j + 1) * KT - 1 > first) {
-          const int lim = tok - j * KT;  // keys c <= lim are visible
+        masked = (j + 1) * KT - 1 > first;
+        const int lim = tok - j * KT;  // keys c <= lim are visible
 #pragma unroll
-          for (int c = 0; c < KT; ++c) s[c] = c <= lim ? s[c] : __float_as_uint(NEG_INF);
+        for (int u = 0; u < 4; ++u) {
+          const int n_vis = min(32, max(0, lim + 1 - 32 * u));
+          mw[u] = n_vis == 32 ? 0xFFFFFFFFu : (1u << n_vis) - 1u;
         }
       } else {
         const int jm = j % kMaskRing;
         tr::wait_warp(bar(kBMask + jm), static_cast<uint32_t>((j / kMaskRing) & 1), abort_flag, p.err);
-        const unsigned m0 = maskw[4 * jm], m1 = maskw[4 * jm + 1], m2 = maskw[4 * jm + 2], m3 = maskw[4 * jm + 3];
-        if ((m0 & m1 & m2 & m3) != 0xFFFFFFFFu) {
 #pragma unroll
-          for (int c = 0; c < KT; ++c) {
-            const unsigned mw = c < 32 ? m0 : c < 64 ? m1 : c < 96 ? m2 : m3;
-            s[c] = ((mw >> (c & 31)) & 1u) ? s[c] : __float_as_uint(NEG_INF);
-          }
-        }
+        for (int u = 0; u < 4; ++u) mw[u] = maskw[4 * jm + u];
+        masked = (mw[0] & mw[1] & mw[2] & mw[3]) != 0xFFFFFFFFu;
       }
-      // ---- the tile's maximum; raise the reference when it is passed by more than kThr ----
       float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-      for (int c = 0; c < KT; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+      for (int h = 0; h < 2; ++h) {
+        if (h == 0) {
+          tmem_ld32_nw(t_s, s);
+          tmem_ld32_nw(t_s + 32, s + 32);
+        }
+        tmem_wait_ld();
+        tmem_pass(s + 64 * h);
+        tmem_pass(s + 64 * h + 32);
+        if (h == 0) {
+          tmem_ld32_nw(t_s + 64, s + 64);
+          tmem_ld32_nw(t_s + 96, s + 96);
+        }
+        if (masked) {  // -inf for masked keys
+#pragma unroll
+          for (int c = 64 * h; c < 64 * h + 64; ++c)
+            s[c] = ((mw[c >> 5] >> (c & 31)) & 1u) ? s[c] : __float_as_uint(NEG_INF);
+        }
+#pragma unroll
+        for (int c = 64 * h; c < 64 * h + 64; c += 2)
+          mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+      }
+      // ---- raise the reference when the tile's maximum passes it by more than kThr ----
       const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
       if (__any_sync(0xffffffffu, mt > mrun + kThr)) {
         const float mn = fmaxf(mrun, mt);
@@ -455,24 +494,32 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
       }
       const float mref = mrun == NEG_INF ? 0.f : mrun;
       // ---- P over the scores' columns ----
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2 sc2 = make_float2(sc, sc), mn2 = make_float2(-mref, -mref);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t pk[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float p0 = fast_exp2(fmaf(__uint_as_float(s[64 * h + 2 * i]), sc, -mref));
-          const float p1 = fast_exp2(fmaf(__uint_as_float(s[64 * h + 2 * i + 1]), sc, -mref));
-          l4[i & 3] += p0 + p1;
+          const int c = 64 * h + 2 * i;
+          const float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, mn2);
+          const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
           pk[i] = pack_bf16(p0, p1);
+          s[c] = __float_as_uint(p0);
+          s[c + 1] = __float_as_uint(p1);
         }
         tmem_st32(t_s + 32 * h, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBPFull + 2 * buf + h));
       }
-      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBPFull + buf));
+      // ---- the row's sum, off the MMAs' way ----
+      float2 l4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+      for (int i = 0; i < KT / 2; ++i)
+        l4[i & 3] = add2(l4[i & 3], make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])));
+      l4[0] = add2(add2(l4[0], l4[1]), add2(l4[2], l4[3]));
+      l += l4[0].x + l4[0].y;
     }
     // ---- epilogue ----
     if (my_tiles > 0) {
@@ -573,16 +620,23 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
           if (elect_one()) mma_commit(bar(kBSFull + (NQ == 2 ? t : (j & 1))));
         };
         auto pv = [&](int t, int j) {
-          const uint32_t a = tmem + (NQ == 2 ? t : (j & 1)) * KT;
+          const int buf = NQ == 2 ? t : (j & 1);
+          const uint32_t par = static_cast<uint32_t>(NQ == 2 ? (j & 1) : ((j >> 1) & 1));
+          const uint32_t a = tmem + buf * KT;
 #pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const int slot = ((2 * j + 1) * NH + h) % NE;
-            const uint64_t vd = dv0 + static_cast<uint64_t>((slot * ENT) >> 4);
-            if (elect_one()) {
+          for (int half = 0; half < 2; ++half) {
+            tr::wait_warp(bar(kBPFull + 2 * buf + half), par, abort_flag, p.err);
+            tc_fence_after();
 #pragma unroll
-              for (int ks = 0; ks < KT / 16; ++ks)
-                mma_f16_ts(tmem + G::col_o + t * D + h * G::ED, a + ks * 8, vd + static_cast<uint64_t>(ks * 128), idPV,
-                           j > 0 || ks > 0);
+            for (int h = 0; h < NH; ++h) {
+              const int slot = ((2 * j + 1) * NH + h) % NE;
+              const uint64_t vd = dv0 + static_cast<uint64_t>((slot * ENT) >> 4);
+              if (elect_one()) {
+#pragma unroll
+                for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                  mma_f16_ts(tmem + G::col_o + t * D + h * G::ED, a + ks * 8, vd + static_cast<uint64_t>(ks * 128),
+                             idPV, j > 0 || ks > 0);
+              }
             }
           }
           if (elect_one()) mma_commit(bar(kBOFull + t));
@@ -590,18 +644,14 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
         auto acquire = [&](int j, int kv) {
 #pragma unroll
           for (int h = 0; h < NH; ++h) wait_full((2 * j + kv) * NH + h);
-          fence_proxy_async();
+          // rows that came by cp.async (stores and TMA need none here)
+          if (MODE == kSharedBf16 || (PROMPT && !p.tma)) fence_proxy_async();
           tc_fence_after();
         };
         auto release = [&](int j, int kv) {
 #pragma unroll
           for (int h = 0; h < NH; ++h)
             if (elect_one()) mma_commit(bar(kBEmpty + ((2 * j + kv) * NH + h) % NE));
-        };
-        auto wait_p = [&](int t, int j) {
-          const int buf = NQ == 2 ? t : (j & 1);
-          tr::wait_warp(bar(kBPFull + buf), static_cast<uint32_t>(NQ == 2 ? (j & 1) : ((j >> 1) & 1)), abort_flag, p.err);
-          tc_fence_after();
         };
         if (nt > 0) {
 #pragma unroll
@@ -619,17 +669,13 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
                 release(j + 1, 0);
               }
               acquire(j, 1);
-              wait_p(0, j);
               pv(0, j);
               release(j, 1);
             } else {
               acquire(j, 1);
 #pragma unroll
               for (int t = 0; t < NQ; ++t) {
-                if (j < n_tiles[t]) {
-                  wait_p(t, j);
-                  pv(t, j);
-                }
+                if (j < n_tiles[t]) pv(t, j);
                 if (t == NQ - 1) release(j, 1);
                 if (j + 1 < nt && t == 0) acquire(j + 1, 0);
                 if (j + 1 < n_tiles[t]) qk(t, j + 1);

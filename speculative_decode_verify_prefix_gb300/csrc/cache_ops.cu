@@ -25,12 +25,14 @@ fa::FaFn kernel_fa(int D, int mode) {
 }
 
 static int fa_smem(int D) { return D == 64 ? fa::Geo<64>::smem : D == 128 ? fa::Geo<128>::smem : fa::Geo<256>::smem; }
+constexpr size_t kSchedOff = 64;  // fa_kernel's counters, between the error word and the partials
 static int fa_nq(int D) { return D == 256 ? 1 : 2; }
 
-// Tensor map of K or V rows [rows][h_kv][D] for [32 rows][64 columns] boxes in
-// the 128-byte swizzle.  False where the strides are none that a map takes
-// (rows then go by cp.async).
-static bool rows_map(const vsk_tensor* t, CUtensorMap* map) {
+// Tensor map of bf16 rows [rows][heads][D] for boxes of [n_rows][n_heads][64
+// columns] in the 128-byte swizzle.  False where base or strides are none that
+// a map takes (the rows are then copied without one).
+static bool rows16(const vsk_tensor* t, int e);
+static bool rows_map(const vsk_tensor* t, int n_rows, int n_heads, CUtensorMap* map) {
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   std::call_once(once, [] {
@@ -44,28 +46,36 @@ static bool rows_map(const vsk_tensor* t, CUtensorMap* map) {
   // a dimension of one element has any stride
   const long long n = t->shape[0], h = t->shape[1], d = t->shape[2];
   const long long s1 = h > 1 ? t->stride[1] : d, s0 = n > 1 ? t->stride[0] : h * s1;
-  if (!encode || s1 < d || s0 < d || s0 >= (1LL << 38) || s1 >= (1LL << 38)) return false;
+  if (!encode || !rows16(t, 2) || s1 < d || s0 < d || s0 >= (1LL << 38) || s1 >= (1LL << 38)) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(h), static_cast<cuuint64_t>(n)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * s1), static_cast<cuuint64_t>(2 * s0)};
-  const cuuint32_t box[3] = {64, 1, 32}, unit[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(n_heads), static_cast<cuuint32_t>(n_rows)}, unit[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(t->data), dims, strides, box, unit,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static int launch_fa(const fa::FaParams& p, const CUtensorMap* maps, int D, int mode, long long grid, cudaStream_t st) {
+// One CTA per SM at most, which draw the items; maps: queries, K, V.
+static int launch_fa(const fa::FaParams& p, const CUtensorMap* maps, int D, int mode, long long n_items, void* ws,
+                     cudaStream_t st) {
   fa::FaFn fn = kernel_fa(D, mode);
-  if (grid > INT_MAX) return fail("grid of %lld CTAs too large", grid);
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       fa_smem(D));
+  if (n_items > INT_MAX / 2) return fail("%lld row blocks are too many", n_items);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail("cudaGetDevice: %s", cudaGetErrorString(e));
+  const int sms = device_sms(dev);
+  if (sms <= 0) return fail("cannot query the SM count of device %d", dev);
+  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, fa_smem(D));
   if (e != cudaSuccess) return fail("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   fa::FaParams a = p;
-  CUtensorMap m[2];
-  memset(m, 0, sizeof m);
-  if (maps) memcpy(m, maps, sizeof m);
-  void* args[] = {&a, &m[0], &m[1]};
-  e = cudaLaunchKernel(reinterpret_cast<const void*>(fn), dim3(static_cast<unsigned>(grid)), dim3(fa::kThreads), args,
-                       fa_smem(D), st);
+  a.n_items = static_cast<int>(n_items);
+  a.err = static_cast<unsigned*>(ws);
+  a.sched = reinterpret_cast<int*>(static_cast<unsigned char*>(ws) + kSchedOff);
+  CUtensorMap m[3];
+  memcpy(m, maps, sizeof m);
+  void* args[] = {&a, &m[0], &m[1], &m[2]};
+  e = cudaLaunchKernel(reinterpret_cast<const void*>(fn), dim3(static_cast<unsigned>(std::min<long long>(n_items, sms))),
+                       dim3(fa::kThreads), args, fa_smem(D), st);
   if (e != cudaSuccess) return fail("kernel launch failed: %s", cudaGetErrorString(e));
   return 1;
 }
@@ -283,12 +293,13 @@ int prompt_attn_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* 
   p.q16 = rows16(q, 2);
   p.o16 = rows16(o, 2);
   p.v_scale = 1.f;
-  p.err = reinterpret_cast<unsigned*>(ws);
   // every sequence adds at most one row block to its share of N / block
   const long long blocks = N / (fa_nq(static_cast<int>(D)) * p.tpb) + B;
-  CUtensorMap maps[2];
-  p.tma = rows_map(k, &maps[0]) && rows_map(v, &maps[1]);
-  return launch_fa(p, p.tma ? maps : nullptr, static_cast<int>(D), fa::kPrompt, blocks * h_kv, st);
+  CUtensorMap maps[3];
+  memset(maps, 0, sizeof maps);
+  p.qtma = rows_map(q, p.tpb, p.gq, &maps[0]);
+  p.tma = rows_map(k, 32, 1, &maps[1]) && rows_map(v, 32, 1, &maps[2]);
+  return launch_fa(p, maps, static_cast<int>(D), fa::kPrompt, blocks * h_kv, ws, st);
 }
 
 size_t vsk_shared_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv, int64_t head_dim, int64_t max_len_extend) {
@@ -372,10 +383,12 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
     f.scale2 = scale2 == 0.f ? 1.f : std::fabs(scale2);
     f.q16 = rows16(q, 2);
     f.v_scale = v_scale;
-    f.err = reinterpret_cast<unsigned*>(ws);
     f.plse = reinterpret_cast<float*>(ws + base);
     f.po = reinterpret_cast<float*>(ws + sh_o);
-    if (!launch_fa(f, nullptr, D, cs.fp8 ? fa::kSharedE4m3 : fa::kSharedBf16, items, st)) return 0;
+    CUtensorMap maps[3];
+    memset(maps, 0, sizeof maps);
+    f.qtma = f.qmode == 0 && rows_map(q, f.tpb, f.gq, &maps[0]);
+    if (!launch_fa(f, maps, D, cs.fp8 ? fa::kSharedE4m3 : fa::kSharedBf16, items, ws, st)) return 0;
   }
   p.B = static_cast<int>(cs.B);
   p.L = static_cast<int>(cs.L);

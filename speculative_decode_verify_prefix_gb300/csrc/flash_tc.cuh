@@ -16,8 +16,8 @@
 //
 // Rows.  The g = h_q / h_kv query heads of a KV head share its keys, so the
 // packed row r of a query tile is (token r / g, head r % g): a 128-row tile
-// holds 128 / g tokens (rounded down; spare rows are zero and never stored).  A
-// CTA owns one block of NQ tiles of one KV head: two at head_dim 64 / 128
+// holds 128 / g tokens (rounded down; spare rows are never stored).  An item of
+// work is one block of NQ tiles of one KV head: two at head_dim 64 / 128
 // (every K / V tile in shared memory feeds both, and the tensor core works on
 // one tile while the softmax of the other runs), one at 256, whose O takes
 // half of the 512 tensor-memory columns and whose scores are double-buffered
@@ -32,6 +32,8 @@
 //                    over them (bf16, half the columns), rescale, epilogue
 //   warp 8           issues the MMAs (one elected lane): S = Q K^T (both operands in
 //                    shared memory), O += P V (P in tensor memory)
+//   warp 9           draws the items; the CTAs (one per SM) stay, so that the
+//                    next item's loads run under the end of this one
 //   warps 12-15      bring K / V rows into a ring of 128-key entries (128 head
 //                    dimensions each, K then V of a tile): contiguous rows by
 //                    TMA, gathered ones with 16-byte cp.async; e4m3 rows are
@@ -77,6 +79,7 @@ using tc::tmem_wait_st;
 constexpr int KT = 128;          // keys per tile
 constexpr int kThreads = 512;
 constexpr int kWarpMma = 8;
+constexpr int kWarpSched = 9;
 constexpr int kWarpLoad = 12;    // loader warps 12-15
 constexpr int kLoadThreads = 128;
 constexpr int kRegsSoftmax = 184, kRegsOther = 72;
@@ -89,13 +92,26 @@ enum Mode { kPrompt = 0, kSharedBf16 = 1, kSharedE4m3 = 2 };
 
 // shared-memory map
 constexpr int kBarOff = 0;
-constexpr int kTmemOff = 512, kAbortOff = 516, kBadVOff = 520, kWorkOff = 528;  // kWorkOff: 4 x i32
+constexpr int kTmemOff = 512, kAbortOff = 516;
+constexpr int kWorkOff = 576;    // [2] Work
 constexpr int kMaskOff = 1024;   // [kMaskRing][4] key-validity words
 constexpr int kDataOff = 2048;
 // barriers
-constexpr int kBFull = 0, kBEmpty = kMaxNE, kBQFull = 2 * kMaxNE, kBSFull = kBQFull + 2, kBPFull = kBSFull + 2,
-              kBOFull = kBPFull + 4, kBMask = kBOFull + 2, kBDone = kBMask + kMaskRing, kNumBars = kBDone + 1;
+constexpr int kBFull = 0, kBEmpty = kMaxNE, kBQFull = 2 * kMaxNE, kBQEmpty = kBQFull + 2, kBSFull = kBQEmpty + 2,
+              kBPFull = kBSFull + 2, kBOFull = kBPFull + 4, kBOEmpty = kBOFull + 2, kBWFull = kBOEmpty + 2,
+              kBWEmpty = kBWFull + 2, kBEdge = kBWEmpty + 2, kBMask = kBEdge + 2, kBDone = kBMask + kMaskRing,
+              kNumBars = kBDone + 1;
 static_assert(kBarOff + 8 * kNumBars <= kTmemOff, "barriers overlap");
+
+// One item: a row block (query tiles of tokens [tok0, tok0 + NQ tpb) of the
+// rows [row0, row0 + n)), a KV head and key tiles [j_first, j_first + nt).
+struct Work {
+  int n_tiles[2];   // key tiles of query tile 0 / 1 (-1: no more items)
+  int head, tok0, n, j_first, j_edge;
+  int bad_v;        // prompt: a V value on the diagonal was not finite
+  long long row0, item;
+};
+static_assert(kWorkOff + 2 * sizeof(Work) <= kMaskOff, "work slots overlap");
 
 template <int D>
 struct Geo {
@@ -125,18 +141,20 @@ struct FaParams {
   int idx64;
   long long n_keys, pool;
   int h_kv, gq, tpb;      // tpb: tokens per query tile
+  int n_items;            // items at most
+  int* sched;             // next ticket beyond the grid's, CTAs done (both zero between calls)
   int n_split, split_tiles;  // shared: key ranges per row block, key tiles of one
   float scale2;           // > 0
   int qmode;              // queries enter as they are (0), negated (1) or as zeros (2): the sign of the scale
   int q16, o16;           // 16-byte accesses allowed
-  int tma;                // prompt: K / V tiles come through the tensor maps
+  int tma, qtma;          // K / V tiles (prompt), query tiles come through the tensor maps
   float v_scale;
   unsigned* err;
   float* plse;            // shared: partials, one row block of NQ * 128 rows per CTA
   float* po;
 };
 
-using FaFn = void (*)(const FaParams, const CUtensorMap, const CUtensorMap);
+using FaFn = void (*)(const FaParams, const CUtensorMap, const CUtensorMap, const CUtensorMap);
 
 // The MMA warp runs its loop converged; one elected lane issues each group of
 // MMAs.  Addresses and descriptors are then the same for the whole warp and stay
@@ -216,7 +234,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// One [32 rows][64 head dimensions] box of a K / V tensor map into shared memory.
+// One box of a [rows][heads][head_dim] tensor map into shared memory ([32 rows]
+// [64 head dimensions] of a K / V head, [tpb rows][g heads][64] of the queries).
 __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int head, int row) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
@@ -242,6 +261,7 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, bool& bad) {
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_constant__ fa::FaParams p,
+                                                             const __grid_constant__ CUtensorMap qmap,
                                                              const __grid_constant__ CUtensorMap kmap,
                                                              const __grid_constant__ CUtensorMap vmap) {
   using namespace fa;
@@ -252,117 +272,35 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const float NEG_INF = -INFINITY;
-
-  // ---- this CTA's work: row block (tokens [tok0, tok0 + NQ tpb) of rows [row0, row0 + n)), KV head, key tiles ----
-  int* work = reinterpret_cast<int*>(smem + kWorkOff);
   const int bt = NQ * p.tpb;
-  int head, split = 0;
-  if constexpr (PROMPT) {
-    head = static_cast<int>(blockIdx.x % p.h_kv);
-    if (warp == 0) {
-      // the sequence that holds row block blockIdx.x / h_kv: blocks are
-      // numbered sequence by sequence, the last block of a sequence (its
-      // longest key range) first
-      long long want = blockIdx.x / p.h_kv;
-      int found = -1, n_f = 0, a_f = 0, blk_f = 0;
-      for (int b0 = 0; b0 < p.B && found < 0; b0 += 32) {
-        const int b = b0 + lane;
-        int a = 0, n = 0;
-        if (b < p.B) {
-          a = __ldg(p.qo + b);
-          const int e = __ldg(p.qo + b + 1);
-          n = (a >= 0 && e >= a && e <= p.n_rows) ? e - a : 0;
-        }
-        const int nb = n / bt + (n % bt != 0);
-        int incl = nb;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, incl, off);
-          if (lane >= off) incl += y;
-        }
-        const bool here = want >= incl - nb && want < incl;
-        const unsigned m = __ballot_sync(0xffffffffu, here);
-        if (m) {
-          const int src = __ffs(m) - 1;
-          found = b0 + src;
-          n_f = __shfl_sync(0xffffffffu, n, src);
-          a_f = __shfl_sync(0xffffffffu, a, src);
-          const int last = __shfl_sync(0xffffffffu, incl, src) - 1;
-          blk_f = last - static_cast<int>(want);
-        } else {
-          want -= __shfl_sync(0xffffffffu, incl, 31);
-        }
-      }
-      if (lane == 0) {
-        work[0] = found;
-        work[1] = a_f;
-        work[2] = n_f;
-        work[3] = blk_f;
-      }
-    }
-    if (blockIdx.x == 0 && warp == 1) {
-      for (int b = lane; b < p.B; b += 32) {
-        const int a = __ldg(p.qo + b), e = __ldg(p.qo + b + 1);
-        if (!(a >= 0 && e >= a && e <= p.n_rows)) atomicOr(p.err, kErrBadQoIndptr);
-      }
-    }
-    __syncthreads();
-    if (work[0] < 0) return;  // uniform: the grid is an upper bound
-  }
-  long long row0;
-  int n, tok0, j_first, n_tiles[2];
-  if constexpr (PROMPT) {
-    row0 = work[1];
-    n = work[2];
-    tok0 = work[3] * bt;
-    j_first = 0;
-  } else {
-    split = static_cast<int>(blockIdx.x % p.n_split);
-    const int u = static_cast<int>(blockIdx.x / p.n_split);
-    head = u % p.h_kv;
-    row0 = 0;
-    n = static_cast<int>(p.n_rows);
-    tok0 = (u / p.h_kv) * bt;
-    j_first = split * p.split_tiles;
-  }
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int first = tok0 + t * p.tpb;
-    if (t >= NQ || first >= n) {
-      n_tiles[t] = 0;
-    } else if constexpr (PROMPT) {
-      n_tiles[t] = (min(first + p.tpb, n) + KT - 1) / KT;
-    } else {
-      const long long tiles = (p.n_keys + KT - 1) / KT;
-      n_tiles[t] = static_cast<int>(max(0LL, min(static_cast<long long>(p.split_tiles), tiles - j_first)));
-    }
-  }
-  const int nt = max(n_tiles[0], n_tiles[1]);
-  const int j_edge = PROMPT ? tok0 / KT : 0;  // prompt: first tile that holds keys some row of the block must not see
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
   auto bar = [&](int i) -> uint32_t { return smem_u32(bars + i); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kAbortOff);
-  volatile int* bad_v = reinterpret_cast<volatile int*>(smem + kBadVOff);
   volatile unsigned* maskw = reinterpret_cast<volatile unsigned*>(smem + kMaskOff);
+  Work* work = reinterpret_cast<Work*>(smem + kWorkOff);
   const uint32_t q_s = smem_u32(smem + G::q_off), ring_s = smem_u32(smem + G::ring_off);
-  if ((smem_u32(smem) & 1023u) != 0u) {  // the swizzled layouts need it; uniform
+  if ((smem_u32(smem) & 1023u) != 0u) {  // the swizzled layouts need it; uniform over the grid
     if (tid == 0) atomicOr(p.err, kErrTimeout);
     return;
   }
   if (tid == 0) {
     *abort_flag = 0;
-    *bad_v = 0;
     for (int i = 0; i < NE; ++i) {
       mbar_init(bar(kBFull + i), kLoadThreads);
       mbar_init(bar(kBEmpty + i), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(kBQFull + t), 4);
+      mbar_init(bar(kBQFull + t), p.qtma ? 1 : 4);
+      mbar_init(bar(kBQEmpty + t), 1);
       mbar_init(bar(kBSFull + t), 1);
       mbar_init(bar(kBPFull + 2 * t), 4);
       mbar_init(bar(kBPFull + 2 * t + 1), 4);
       mbar_init(bar(kBOFull + t), 1);
+      mbar_init(bar(kBOEmpty + t), 4);
+      mbar_init(bar(kBWFull + t), 1);
+      mbar_init(bar(kBWEmpty + t), 4 * NQ + 1 + 4);
+      mbar_init(bar(kBEdge + t), 4);
     }
     for (int i = 0; i < kMaskRing; ++i) mbar_init(bar(kBMask + i), 4);
     mbar_init(bar(kBDone), 1);
@@ -374,331 +312,514 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (p.qtma && p.tpb * p.gq < 128) {
+    // rows of the query tiles that no box fills
+    const int rows = 128 - p.tpb * p.gq;
+    for (int i = tid; i < NQ * (D / 64) * rows * 8; i += kThreads)
+      *reinterpret_cast<uint4*>(smem + G::q_off + (i / (rows * 8)) * (128 * 128) + (128 - rows) * 128 +
+                                (i % (rows * 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async();
+  }
+  if (PROMPT && blockIdx.x == 0 && warp == kWarpSched) {
+    for (int b = lane; b < p.B; b += 32) {
+      const int a = __ldg(p.qo + b), e = __ldg(p.qo + b + 1);
+      if (!(a >= 0 && e >= a && e <= p.n_rows)) atomicOr(p.err, kErrBadQoIndptr);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTmemOff);
 
+  // The item of round `it` for a role's warp: false when there is none left.
+  auto take = [&](int it, const Work*& w) -> bool {
+    tr::wait_warp(bar(kBWFull + (it & 1)), static_cast<uint32_t>((it >> 1) & 1), abort_flag, p.err);
+    w = work + (it & 1);
+    const int first = *const_cast<const volatile int*>(&w->n_tiles[0]);
+    return !__any_sync(0xffffffffu, *abort_flag != 0) && first >= 0;
+  };
+  auto give_back = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBWEmpty + (it & 1)));
+  };
+
   if (warp < 4 * NQ) {
     // ================================ softmax ================================
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = warp >> 2, w = warp & 3, tw = tid & 127;
-    const int first = tok0 + t * p.tpb;  // first token of the tile
-    const int my_tiles = n_tiles[t];
-    // ---- queries of the tile into shared memory ----
-    {
-      constexpr int CPR = D / 8;  // 16-byte chunks of a row
-      unsigned char* qs = smem + G::q_off + t * G::QT;
-#pragma unroll 4
-      for (int i = 0; i < CPR; ++i) {
-        const int ci = tw + 128 * i, r = ci / CPR, c = ci % CPR;
-        const int tok = first + r / p.gq, g = r % p.gq;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.tpb * p.gq && tok < n && p.qmode != 2) {
-          const __nv_bfloat16* src =
-              p.q + (row0 + tok) * p.q_s0 + static_cast<long long>(head * p.gq + g) * p.q_s1 + c * 8;
-          if (p.q16)
-            x = __ldg(reinterpret_cast<const uint4*>(src));
-          else
-            x = make_uint4(ld_u32(src), ld_u32(src + 2), ld_u32(src + 4), ld_u32(src + 6));
-          if (p.qmode == 1) {
-            x.x ^= 0x80008000u;
-            x.y ^= 0x80008000u;
-            x.z ^= 0x80008000u;
-            x.w ^= 0x80008000u;
-          }
-        }
-        *reinterpret_cast<uint4*>(qs + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBQFull + t));
-    }
-    const int r = 32 * w + lane;  // this thread's packed row
-    const int tok = min(first + r / p.gq, n - 1);
-    const bool real = r < p.tpb * p.gq && first + r / p.gq < n;
+    const int r = 32 * w + lane;  // this thread's packed row of the tile
+    const int r_tok = r / p.gq, r_head = r % p.gq;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(32 * w) << 16);
     const uint32_t t_o = t_lane + G::col_o + t * D;
     const float sc = p.scale2;
-    float mrun = NEG_INF, l = 0.f;
+    uint32_t g = 0;   // key tiles of this query tile so far
+    uint32_t gm = 0;  // key tiles of the CTA so far (shared prefix: the mask ring's position)
 #pragma unroll 1
-    for (int j = 0; j < my_tiles; ++j) {
-      const int buf = NQ == 2 ? t : (j & 1);
-      const uint32_t par = NQ == 2 ? (j & 1) : ((j >> 1) & 1);
-      const uint32_t t_s = t_lane + buf * KT;
-      tr::wait_warp(bar(kBSFull + buf), par, abort_flag, p.err);
-      tc_fence_after();
-      // Scores, then P, in halves of 64 keys: the second half is on its way
-      // while the first one's maximum is taken, and the first half of P is
-      // handed to the MMAs while the second is computed.
-      uint32_t s[KT];
-      bool masked;
-      unsigned mw[4];
-      if constexpr (PROMPT) {
-        masked = (j + 1) * KT - 1 > first;
-        const int lim = tok - j * KT;  // keys c <= lim are visible
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int n_vis = min(32, max(0, lim + 1 - 32 * u));
-          mw[u] = n_vis == 32 ? 0xFFFFFFFFu : (1u << n_vis) - 1u;
+    for (int it = 0;; ++it) {
+      const Work* wk;
+      if (!take(it, wk)) break;
+      const int my_tiles = wk->n_tiles[t], n = wk->n, head = wk->head;
+      const int first = wk->tok0 + t * p.tpb;  // first token of the tile
+      const long long row0 = wk->row0;
+      // ---- queries of the tile into shared memory (where no tensor map takes them) ----
+      if (!p.qtma) {
+        tr::wait_warp(bar(kBQEmpty + t), static_cast<uint32_t>((it & 1) ^ 1), abort_flag, p.err);
+        constexpr int CPR = D / 8;  // 16-byte chunks of a row
+        unsigned char* qs = smem + G::q_off + t * G::QT;
+#pragma unroll 8
+        for (int i = 0; i < CPR; ++i) {
+          const int ci = tw + 128 * i, qr = ci / CPR, c = ci % CPR;
+          const int qt = first + qr / p.gq, qh = qr % p.gq;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (qr < p.tpb * p.gq && qt < n && p.qmode != 2) {
+            const __nv_bfloat16* src =
+                p.q + (row0 + qt) * p.q_s0 + static_cast<long long>(head * p.gq + qh) * p.q_s1 + c * 8;
+            if (p.q16)
+              x = __ldg(reinterpret_cast<const uint4*>(src));
+            else
+              x = make_uint4(ld_u32(src), ld_u32(src + 2), ld_u32(src + 4), ld_u32(src + 6));
+            if (p.qmode == 1) {
+              x.x ^= 0x80008000u;
+              x.y ^= 0x80008000u;
+              x.z ^= 0x80008000u;
+              x.w ^= 0x80008000u;
+            }
+          }
+          *reinterpret_cast<uint4*>(qs + (c >> 3) * (128 * 128) + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) = x;
         }
-      } else {
-        const int jm = j % kMaskRing;
-        tr::wait_warp(bar(kBMask + jm), static_cast<uint32_t>((j / kMaskRing) & 1), abort_flag, p.err);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) mw[u] = maskw[4 * jm + u];
-        masked = (mw[0] & mw[1] & mw[2] & mw[3]) != 0xFFFFFFFFu;
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBQFull + t));
       }
-      float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+      const int tok = min(first + r_tok, n - 1);
+      const bool real = r < p.tpb * p.gq && first + r_tok < n;
+      float mrun = NEG_INF, l = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < my_tiles; ++j, ++g) {
+        const int buf = NQ == 2 ? t : (g & 1);
+        const uint32_t par = NQ == 2 ? (g & 1) : ((g >> 1) & 1);
+        const uint32_t t_s = t_lane + buf * KT;
+        tr::wait_warp(bar(kBSFull + buf), par, abort_flag, p.err);
+        tc_fence_after();
+        // Scores, then P, in halves of 64 keys.  The first half's P is computed
+        // against the reference that the tiles before left, while the second
+        // half's scores arrive and the tile's maximum is taken; only where that
+        // maximum passes the reference by more than kThr is it done again.
+        uint32_t s[KT];
+        bool masked;
+        unsigned mw[4];
+        if constexpr (PROMPT) {
+          masked = (j + 1) * KT - 1 > first;
+          const int lim = tok - j * KT;  // keys c <= lim are visible
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h == 0) {
-          tmem_ld32_nw(t_s, s);
-          tmem_ld32_nw(t_s + 32, s + 32);
+          for (int u = 0; u < 4; ++u) {
+            const int n_vis = min(32, max(0, lim + 1 - 32 * u));
+            mw[u] = n_vis == 32 ? 0xFFFFFFFFu : (1u << n_vis) - 1u;
+          }
+        } else {
+          const uint32_t jm = (gm + j) % kMaskRing;
+          tr::wait_warp(bar(kBMask + jm), ((gm + j) / kMaskRing) & 1, abort_flag, p.err);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mw[u] = maskw[4 * jm + u];
+          masked = (mw[0] & mw[1] & mw[2] & mw[3]) != 0xFFFFFFFFu;
         }
-        tmem_wait_ld();
-        tmem_pass(s + 64 * h);
-        tmem_pass(s + 64 * h + 32);
-        if (h == 0) {
-          tmem_ld32_nw(t_s + 64, s + 64);
-          tmem_ld32_nw(t_s + 96, s + 96);
-        }
-        if (masked) {  // -inf for masked keys
+        float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+        const float2 sc2 = make_float2(sc, sc);
+        uint32_t pk[32];
+        float2 l2[2];
+        auto probs = [&](int h, float mref) {  // pk and the sum of half h
+          const float2 mn2 = make_float2(-mref, -mref);
+          l2[0] = l2[1] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int c = 64 * h + 2 * i;
+            float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, mn2);
+            x.x = fast_exp2(x.x);
+            x.y = fast_exp2(x.y);
+            l2[i & 1] = add2(l2[i & 1], x);
+            pk[i] = pack_bf16(x.x, x.y);
+          }
+        };
+        auto hide = [&](int h) {  // -inf for masked keys
 #pragma unroll
           for (int c = 64 * h; c < 64 * h + 64; ++c)
             s[c] = ((mw[c >> 5] >> (c & 31)) & 1u) ? s[c] : __float_as_uint(NEG_INF);
-        }
+        };
+        auto top = [&](int h) {
 #pragma unroll
-        for (int c = 64 * h; c < 64 * h + 64; c += 2)
-          mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-      }
-      // ---- raise the reference when the tile's maximum passes it by more than kThr ----
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-      if (__any_sync(0xffffffffu, mt > mrun + kThr)) {
-        const float mn = fmaxf(mrun, mt);
-        const float al = mn == NEG_INF ? 1.f : fast_exp2(mrun - mn);
-        if (j > 0) {
-          tr::wait_warp(bar(kBOFull + t), static_cast<uint32_t>((j - 1) & 1), abort_flag, p.err);
-          tc_fence_after();
+          for (int c = 64 * h; c < 64 * h + 64; c += 2)
+            mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        };
+        tmem_ld32_nw(t_s, s);
+        tmem_ld32_nw(t_s + 32, s + 32);
+        tmem_wait_ld();
+        tmem_pass(s);
+        tmem_pass(s + 32);
+        tmem_ld32_nw(t_s + 64, s + 64);
+        tmem_ld32_nw(t_s + 96, s + 96);
+        if (masked) hide(0);
+        probs(0, mrun == NEG_INF ? 0.f : mrun);
+        top(0);
+        tmem_wait_ld();
+        tmem_pass(s + 64);
+        tmem_pass(s + 96);
+        if (masked) hide(1);
+        top(1);
+        // ---- raise the reference when the tile's maximum passes it by more than kThr ----
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        if (__any_sync(0xffffffffu, mt > mrun + kThr)) {
+          const float mn = fmaxf(mrun, mt);
+          const float al = mn == NEG_INF ? 1.f : fast_exp2(mrun - mn);
+          if (j > 0) {
+            tr::wait_warp(bar(kBOFull + t), (g - 1) & 1, abort_flag, p.err);
+            tc_fence_after();
 #pragma unroll 1
-          for (int cb = 0; cb < D / 8; ++cb) {
-            float o[8];
-            tmem_ld<8>(t_o + 8 * cb, o);
+            for (int cb = 0; cb < D / 8; ++cb) {
+              float o[8];
+              tmem_ld<8>(t_o + 8 * cb, o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] *= al;
-            tmem_st<8>(t_o + 8 * cb, o);
+              for (int i = 0; i < 8; ++i) o[i] *= al;
+              tmem_st<8>(t_o + 8 * cb, o);
+            }
+          }
+          l *= al;
+          mrun = mn;
+          probs(0, mrun == NEG_INF ? 0.f : mrun);
+        }
+        // ---- P over the scores' columns, half by half ----
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1) probs(1, mrun == NEG_INF ? 0.f : mrun);
+          tmem_st32(t_s + 32 * h, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBPFull + 2 * buf + h));
+          l2[0] = add2(l2[0], l2[1]);
+          l += l2[0].x + l2[0].y;
+        }
+      }
+      gm += max(wk->n_tiles[0], wk->n_tiles[1]);
+      // ---- epilogue ----
+      if (my_tiles > 0) {
+        // one query tile: the last scores are issued before the PV of the tile
+        // before, so that phase has to be seen to complete first
+        if (NQ == 1 && my_tiles > 1) tr::wait_warp(bar(kBOFull + t), (g - 2) & 1, abort_flag, p.err);
+        tr::wait_warp(bar(kBOFull + t), (g - 1) & 1, abort_flag, p.err);
+        tc_fence_after();
+      }
+      if constexpr (PROMPT) {
+        // the item's diagonal V tiles have been looked at
+        tr::wait_warp(bar(kBEdge + (it & 1)), static_cast<uint32_t>((it >> 1) & 1), abort_flag, p.err);
+        if (my_tiles > 0) {
+          const float inv = 1.f / l;
+          const bool fix = *const_cast<const volatile int*>(&wk->bad_v) != 0;
+          const int key0 = wk->j_edge * KT;
+          __nv_bfloat16* orow =
+              p.o + (row0 + tok) * p.o_s0 + static_cast<long long>(head * p.gq + r_head) * p.o_s1;
+#pragma unroll 1
+          for (int cb = 0; cb < D / 32; ++cb) {
+            float o[32];
+            tmem_ld<32>(t_o + 32 * cb, o);
+            if (!real) continue;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= inv;
+            if (fix) {
+              // values the loaders zeroed, for the rows that see them
+              for (int key = key0; key <= tok; ++key) {
+                const uint32_t* vr =
+                    reinterpret_cast<const uint32_t*>(p.v + (row0 + key) * p.v_s0 + head * p.v_s1 + cb * 64);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const uint32_t x = __ldg(vr + i);
+                  const float2 f = unpack_bf16(x);
+                  if ((x & 0x7F80u) == 0x7F80u) o[2 * i] += f.x;
+                  if ((x & 0x7F800000u) == 0x7F800000u) o[2 * i + 1] += f.y;
+                }
+              }
+            }
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
+            uint32_t* dst = reinterpret_cast<uint32_t*>(orow + 32 * cb);
+            if (p.o16) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4*>(dst)[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) dst[i] = y[i];
+            }
           }
         }
-        l *= al;
-        mrun = mn;
-      }
-      const float mref = mrun == NEG_INF ? 0.f : mrun;
-      // ---- P over the scores' columns ----
-      const float2 sc2 = make_float2(sc, sc), mn2 = make_float2(-mref, -mref);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int c = 64 * h + 2 * i;
-          const float2 x = fma2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, mn2);
-          const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-          pk[i] = pack_bf16(p0, p1);
-          s[c] = __float_as_uint(p0);
-          s[c + 1] = __float_as_uint(p1);
-        }
-        tmem_st32(t_s + 32 * h, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBPFull + 2 * buf + h));
-      }
-      // ---- the row's sum, off the MMAs' way ----
-      float2 l4[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-      for (int i = 0; i < KT / 2; ++i)
-        l4[i & 3] = add2(l4[i & 3], make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])));
-      l4[0] = add2(add2(l4[0], l4[1]), add2(l4[2], l4[3]));
-      l += l4[0].x + l4[0].y;
-    }
-    // ---- epilogue ----
-    if (my_tiles > 0) {
-      // one query tile: the last scores are issued before the PV of the tile
-      // before, so that phase has to be seen to complete first
-      if (NQ == 1 && my_tiles > 1)
-        tr::wait_warp(bar(kBOFull + t), static_cast<uint32_t>((my_tiles - 2) & 1), abort_flag, p.err);
-      tr::wait_warp(bar(kBOFull + t), static_cast<uint32_t>((my_tiles - 1) & 1), abort_flag, p.err);
-      tc_fence_after();
-    }
-    if constexpr (PROMPT) {
-      named_bar_sync(1, kLoadThreads + 128 * NQ);  // the loaders are done: bad_v is final
-      if (my_tiles > 0) {
-        const float inv = 1.f / l;
-        const bool fix = *bad_v != 0;
-        __nv_bfloat16* orow =
-            p.o + (row0 + tok) * p.o_s0 + static_cast<long long>(head * p.gq + r % p.gq) * p.o_s1;
+      } else if (my_tiles > 0) {
+        // partial of this key range: o v_scale / l and m + log2 l, -inf and 0 where no key was valid
+        const long long prow = wk->item * (NQ * 128) + t * 128 + r;
+        const float inv = l > 0.f ? p.v_scale / l : 0.f;
+        if (real) p.plse[prow] = l > 0.f ? mrun + log2f(l) : (l == 0.f ? NEG_INF : l);
+        float* orow = p.po + prow * D;
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {
           float o[32];
           tmem_ld<32>(t_o + 32 * cb, o);
           if (!real) continue;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= inv;
-          if (fix) {
-            // values the loaders zeroed, for the rows that see them
-            for (int key = j_edge * KT; key <= tok; ++key) {
-              const uint32_t* vr = reinterpret_cast<const uint32_t*>(
-                  p.v + (row0 + key) * p.v_s0 + head * p.v_s1 + cb * 64);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const uint32_t x = __ldg(vr + i);
-                const float2 f = unpack_bf16(x);
-                if ((x & 0x7F80u) == 0x7F80u) o[2 * i] += f.x;
-                if ((x & 0x7F800000u) == 0x7F800000u) o[2 * i + 1] += f.y;
-              }
-            }
-          }
-          uint32_t y[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
-          uint32_t* dst = reinterpret_cast<uint32_t*>(orow + 32 * cb);
-          if (p.o16) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              reinterpret_cast<uint4*>(dst)[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dst[i] = y[i];
-          }
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(orow + 32 * cb + 4 * i) =
+                make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
         }
       }
-    } else if (my_tiles > 0) {
-      // partial of this key range: o v_scale / l and m + log2 l, -inf and 0 where no key was valid
-      const long long prow = static_cast<long long>(blockIdx.x) * (NQ * 128) + t * 128 + r;
-      const float inv = l > 0.f ? p.v_scale / l : 0.f;
-      if (real) p.plse[prow] = l > 0.f ? mrun + log2f(l) : (l == 0.f ? NEG_INF : l);
-      float* orow = p.po + prow * D;
-#pragma unroll 1
-      for (int cb = 0; cb < D / 32; ++cb) {
-        float o[32];
-        tmem_ld<32>(t_o + 32 * cb, o);
-        if (!real) continue;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(orow + 32 * cb + 4 * i) =
-              make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
-      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && my_tiles > 0) mbar_arrive(bar(kBOEmpty + t));
+      give_back(it);
     }
-    tc_fence_before();
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp >= kWarpMma) {
-      if (warp == kWarpMma) {
-        // ============================ MMA issue ============================
-        constexpr uint32_t idS = idesc(1, 1, 0, 0, 128, KT);
-        constexpr uint32_t idPV = idesc(1, 1, 0, 1, 128, G::ED);
-        const uint64_t dq0 = sdesc(q_s, 16, 1024), dk0 = sdesc(ring_s, 16, 1024), dv0 = sdesc(ring_s, KT * 128, 1024);
-        // entry of (tile j, K / V, half h): (2 j + kv) NH + h
-        auto wait_full = [&](int e) {
-          tr::wait_warp(bar(kBFull + e % NE), static_cast<uint32_t>((e / NE) & 1), abort_flag, p.err);
-        };
-        auto qk = [&](int t, int j) {
-          const uint32_t dc = tmem + (NQ == 2 ? t : (j & 1)) * KT;
+    if (warp == kWarpSched) {
+      // ============================ items of this CTA ============================
+      // The first is the CTA's number, the others are drawn from a counter, so
+      // that long and short items even out; a sequence's row blocks come last
+      // (longest key range) first.
+#pragma unroll 1
+      for (int it = 0;; ++it) {
+        int ticket = static_cast<int>(blockIdx.x);
+        if (it > 0) {
+          if (lane == 0) ticket = static_cast<int>(gridDim.x) + atomicAdd(p.sched, 1);
+          ticket = __shfl_sync(0xffffffffu, ticket, 0);
+        }
+        Work x;
+        x.n_tiles[0] = x.n_tiles[1] = -1;
+        x.bad_v = 0;
+        x.item = ticket;
+        if (ticket < p.n_items) {
+          bool found = true;
+          if constexpr (PROMPT) {
+            x.head = ticket % p.h_kv;
+            x.j_first = 0;
+            long long want = ticket / p.h_kv;
+            found = false;
+            for (int b0 = 0; b0 < p.B && !found; b0 += 32) {
+              const int b = b0 + lane;
+              int a = 0, n = 0;
+              if (b < p.B) {
+                a = __ldg(p.qo + b);
+                const int e = __ldg(p.qo + b + 1);
+                n = (a >= 0 && e >= a && e <= p.n_rows) ? e - a : 0;
+              }
+              const int nb = n / bt + (n % bt != 0);
+              int incl = nb;
 #pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const int slot = (2 * j * NH + h) % NE;
-            const uint64_t qd = dq0 + static_cast<uint64_t>((t * G::QT + h * 2 * (128 * 128)) >> 4);
-            const uint64_t kd = dk0 + static_cast<uint64_t>((slot * ENT) >> 4);
-            if (elect_one()) {
-#pragma unroll
-              for (int ks = 0; ks < G::ED / 16; ++ks) {
-                const uint64_t off = static_cast<uint64_t>(((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4);
-                mma_f16_ss(dc, qd + off, kd + off, idS, h > 0 || ks > 0);
+              for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += y;
+              }
+              const unsigned m = __ballot_sync(0xffffffffu, want >= incl - nb && want < incl);
+              if (m) {
+                const int src = __ffs(m) - 1;
+                found = true;
+                x.n = __shfl_sync(0xffffffffu, n, src);
+                x.row0 = __shfl_sync(0xffffffffu, a, src);
+                x.tok0 = (__shfl_sync(0xffffffffu, incl, src) - 1 - static_cast<int>(want)) * bt;
+              } else {
+                want -= __shfl_sync(0xffffffffu, incl, 31);
               }
             }
+          } else {
+            const int u = ticket / p.n_split;
+            x.head = u % p.h_kv;
+            x.row0 = 0;
+            x.n = static_cast<int>(p.n_rows);
+            x.tok0 = (u / p.h_kv) * bt;
+            x.j_first = (ticket % p.n_split) * p.split_tiles;
           }
-          if (elect_one()) mma_commit(bar(kBSFull + (NQ == 2 ? t : (j & 1))));
-        };
-        auto pv = [&](int t, int j) {
-          const int buf = NQ == 2 ? t : (j & 1);
-          const uint32_t par = static_cast<uint32_t>(NQ == 2 ? (j & 1) : ((j >> 1) & 1));
-          const uint32_t a = tmem + buf * KT;
+          if (found) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            tr::wait_warp(bar(kBPFull + 2 * buf + half), par, abort_flag, p.err);
-            tc_fence_after();
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-              const int slot = ((2 * j + 1) * NH + h) % NE;
-              const uint64_t vd = dv0 + static_cast<uint64_t>((slot * ENT) >> 4);
-              if (elect_one()) {
-#pragma unroll
-                for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                  mma_f16_ts(tmem + G::col_o + t * D + h * G::ED, a + ks * 8, vd + static_cast<uint64_t>(ks * 128),
-                             idPV, j > 0 || ks > 0);
+            for (int t = 0; t < 2; ++t) {
+              const int first = x.tok0 + t * p.tpb;
+              if (t >= NQ || first >= x.n) {
+                x.n_tiles[t] = 0;
+              } else if constexpr (PROMPT) {
+                x.n_tiles[t] = (min(first + p.tpb, x.n) + KT - 1) / KT;
+              } else {
+                const long long tiles = (p.n_keys + KT - 1) / KT;
+                x.n_tiles[t] = static_cast<int>(max(0LL, min(static_cast<long long>(p.split_tiles), tiles - x.j_first)));
               }
             }
+            x.j_edge = PROMPT ? x.tok0 / KT : 0;  // first tile with keys that some row of the block must not see
           }
-          if (elect_one()) mma_commit(bar(kBOFull + t));
-        };
-        auto acquire = [&](int j, int kv) {
+        }
+        tr::wait_warp(bar(kBWEmpty + (it & 1)), static_cast<uint32_t>(((it >> 1) & 1) ^ 1), abort_flag, p.err);
+        if (lane == 0) {
+          work[it & 1] = x;
+          mbar_arrive(bar(kBWFull + (it & 1)));
+        }
+        __syncwarp();
+        if (x.n_tiles[0] < 0 || __any_sync(0xffffffffu, *abort_flag != 0)) break;
+      }
+    } else if (warp == kWarpMma) {
+      // ============================ MMA issue ============================
+      constexpr uint32_t idS = idesc(1, 1, 0, 0, 128, KT);
+      constexpr uint32_t idPV = idesc(1, 1, 0, 1, 128, G::ED);
+      const uint64_t dq0 = sdesc(q_s, 16, 1024), dk0 = sdesc(ring_s, 16, 1024), dv0 = sdesc(ring_s, KT * 128, 1024);
+      uint32_t e0 = 0;             // ring entries of the items before
+      uint32_t g[2] = {0u, 0u};    // key tiles per query tile of the items before
+      uint32_t n_o[2] = {0u, 0u};  // items that gave the query tile any
+      // entry of (tile j, K / V, half h): e0 + (2 j + kv) NH + h
+      auto entry = [&](int j, int kv, int h) -> uint32_t { return e0 + static_cast<uint32_t>((2 * j + kv) * NH + h); };
+      auto qk = [&](int t, int j) {
+        const uint32_t buf = NQ == 2 ? t : ((g[t] + j) & 1);
+        const uint32_t dc = tmem + buf * KT;
 #pragma unroll
-          for (int h = 0; h < NH; ++h) wait_full((2 * j + kv) * NH + h);
-          // rows that came by cp.async (stores and TMA need none here)
-          if (MODE == kSharedBf16 || (PROMPT && !p.tma)) fence_proxy_async();
-          tc_fence_after();
-        };
-        auto release = [&](int j, int kv) {
+        for (int h = 0; h < NH; ++h) {
+          const uint32_t slot = entry(j, 0, h) % NE;
+          const uint64_t qd = dq0 + static_cast<uint64_t>((t * G::QT + h * 2 * (128 * 128)) >> 4);
+          const uint64_t kd = dk0 + static_cast<uint64_t>((slot * ENT) >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int h = 0; h < NH; ++h)
-            if (elect_one()) mma_commit(bar(kBEmpty + ((2 * j + kv) * NH + h) % NE));
-        };
-        if (nt > 0) {
-#pragma unroll
-          for (int t = 0; t < NQ; ++t) tr::wait_warp(bar(kBQFull + t), 0u, abort_flag, p.err);
-          acquire(0, 0);
-#pragma unroll
-          for (int t = 0; t < NQ; ++t)
-            if (n_tiles[t] > 0) qk(t, 0);
-          release(0, 0);
-          for (int j = 0; j < nt; ++j) {
-            if constexpr (NQ == 1) {
-              if (j + 1 < nt) {
-                acquire(j + 1, 0);
-                qk(0, j + 1);
-                release(j + 1, 0);
-              }
-              acquire(j, 1);
-              pv(0, j);
-              release(j, 1);
-            } else {
-              acquire(j, 1);
-#pragma unroll
-              for (int t = 0; t < NQ; ++t) {
-                if (j < n_tiles[t]) pv(t, j);
-                if (t == NQ - 1) release(j, 1);
-                if (j + 1 < nt && t == 0) acquire(j + 1, 0);
-                if (j + 1 < n_tiles[t]) qk(t, j + 1);
-                if (t == NQ - 1 && j + 1 < nt) release(j + 1, 0);
-              }
+            for (int ks = 0; ks < G::ED / 16; ++ks) {
+              const uint64_t off = static_cast<uint64_t>(((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4);
+              mma_f16_ss(dc, qd + off, kd + off, idS, h > 0 || ks > 0);
             }
           }
         }
-        if (elect_one()) mma_commit(bar(kBDone));
-        tr::wait_warp(bar(kBDone), 0u, abort_flag, p.err);  // no arrival is pending when the CTA exits
-      } else if (warp >= kWarpLoad) {
-        // ================================ loaders ================================
-        const int lw = warp - kWarpLoad;
-        constexpr int CPK = G::ED / 8;        // 16-byte chunks of an entry's bf16 row
-        constexpr int RPP = 32 / CPK;         // rows of a warp's pass
-        constexpr int NP = 32 / RPP;          // passes over a warp's 32 rows
-        const int cc = lane % CPK, rr = lane / CPK;
-        auto slot_wait = [&](int e) {
-          tr::wait_warp(bar(kBEmpty + e % NE), static_cast<uint32_t>(((e / NE) & 1) ^ 1), abort_flag, p.err);
+        if (elect_one()) mma_commit(bar(kBSFull + buf));
+      };
+      auto pv = [&](int t, int j) {
+        const uint32_t gt = g[t] + j;
+        const uint32_t buf = NQ == 2 ? t : (gt & 1), par = NQ == 2 ? (gt & 1) : ((gt >> 1) & 1);
+        const uint32_t a = tmem + buf * KT;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          tr::wait_warp(bar(kBPFull + 2 * buf + half), par, abort_flag, p.err);
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const uint32_t slot = entry(j, 1, h) % NE;
+            const uint64_t vd = dv0 + static_cast<uint64_t>((slot * ENT) >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                mma_f16_ts(tmem + G::col_o + t * D + h * G::ED, a + ks * 8, vd + static_cast<uint64_t>(ks * 128), idPV,
+                           j > 0 || ks > 0);
+            }
+          }
+        }
+        if (elect_one()) mma_commit(bar(kBOFull + t));
+      };
+      auto acquire = [&](int j, int kv) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const uint32_t e = entry(j, kv, h);
+          tr::wait_warp(bar(kBFull + e % NE), (e / NE) & 1, abort_flag, p.err);
+        }
+        // rows that came by cp.async (stores are fenced by their writers, TMA needs none)
+        if (MODE == kSharedBf16 || (PROMPT && !p.tma)) fence_proxy_async();
+        tc_fence_after();
+      };
+      auto release = [&](int j, int kv) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+          if (elect_one()) mma_commit(bar(kBEmpty + entry(j, kv, h) % NE));
+      };
+#pragma unroll 1
+      for (int it = 0;; ++it) {
+        const Work* wk;
+        if (!take(it, wk)) break;
+        const int n_tiles[2] = {wk->n_tiles[0], wk->n_tiles[1]};
+        give_back(it);
+        const int nt = max(n_tiles[0], n_tiles[1]);
+        // the queries; after its last scores a tile's are free again
+        auto q_done = [&](int t) {
+          if (elect_one()) mma_commit(bar(kBQEmpty + t));
         };
-        auto dst_off = [&](int key, int c) -> uint32_t {
-          return static_cast<uint32_t>((c >> 3) * (KT * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4));
-        };
+#pragma unroll
+        for (int t = 0; t < NQ; ++t)
+          tr::wait_warp(bar(kBQFull + t), static_cast<uint32_t>(it & 1), abort_flag, p.err);
+        tc_fence_after();
+        if (nt > 0) acquire(0, 0);
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) {
+          if (n_tiles[t] > 0) qk(t, 0);
+          if (n_tiles[t] <= 1) q_done(t);
+        }
+        if (nt > 0) release(0, 0);
+        // the rows of O of the item before have been read (a query tile without
+        // keys has none, and its softmax warps say nothing)
+#pragma unroll
+        for (int t = 0; t < NQ; ++t)
+          if (n_tiles[t] > 0) tr::wait_warp(bar(kBOEmpty + t), (n_o[t]++ & 1) ^ 1, abort_flag, p.err);
+        tc_fence_after();
+#pragma unroll 1
+        for (int j = 0; j < nt; ++j) {
+          if constexpr (NQ == 1) {
+            if (j + 1 < nt) {
+              acquire(j + 1, 0);
+              qk(0, j + 1);
+              release(j + 1, 0);
+              if (j + 2 == nt) q_done(0);
+            }
+            acquire(j, 1);
+            pv(0, j);
+            release(j, 1);
+          } else {
+            acquire(j, 1);
+#pragma unroll
+            for (int t = 0; t < NQ; ++t) {
+              if (j < n_tiles[t]) pv(t, j);
+              if (t == NQ - 1) release(j, 1);
+              if (j + 1 < nt && t == 0) acquire(j + 1, 0);
+              if (j + 1 < n_tiles[t]) {
+                qk(t, j + 1);
+                if (j + 2 == n_tiles[t]) q_done(t);
+              }
+              if (t == NQ - 1 && j + 1 < nt) release(j + 1, 0);
+            }
+          }
+        }
+        e0 += static_cast<uint32_t>(2 * nt * NH);
+        g[0] += n_tiles[0];
+        g[1] += n_tiles[1];
+      }
+      if (elect_one()) mma_commit(bar(kBDone));
+      tr::wait_warp(bar(kBDone), 0u, abort_flag, p.err);  // no arrival is pending when the CTA exits
+    } else if (warp >= kWarpLoad) {
+      // ================================ loaders ================================
+      const int lw = warp - kWarpLoad;
+      constexpr int CPK = G::ED / 8;        // 16-byte chunks of an entry's bf16 row
+      constexpr int RPP = 32 / CPK;         // rows of a warp's pass
+      constexpr int NP = 32 / RPP;          // passes over a warp's 32 rows
+      const int cc = lane % CPK, rr = lane / CPK;
+      auto slot_wait = [&](uint32_t e) {
+        tr::wait_warp(bar(kBEmpty + e % NE), ((e / NE) & 1) ^ 1, abort_flag, p.err);
+      };
+      auto dst_off = [&](int key, int c) -> uint32_t {
+        return static_cast<uint32_t>((c >> 3) * (KT * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+      };
+      uint32_t e = 0;   // ring entry
+      uint32_t gm = 0;  // key tiles so far
+#pragma unroll 1
+      for (int it = 0;; ++it) {
+        const Work* wk;
+        if (!take(it, wk)) break;
+        const int nt = max(wk->n_tiles[0], wk->n_tiles[1]);
+        const int head = wk->head, n = wk->n, j_first = wk->j_first, j_edge = wk->j_edge;
+        const long long row0 = wk->row0;
+        if (p.qtma && lw < NQ) {
+          // query tile lw (rows past the sequence may come along: they are never stored)
+          tr::wait_warp(bar(kBQEmpty + lw), static_cast<uint32_t>((it & 1) ^ 1), abort_flag, p.err);
+          if (lane == 0) {
+            const uint32_t fb = bar(kBQFull + lw);
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(fb),
+                         "r"(p.tpb * p.gq * D * 2)
+                         : "memory");
+#pragma unroll 1
+            for (int cb = 0; cb < D / 64; ++cb)
+              tma_load_box(q_s + lw * G::QT + cb * (128 * 128), &qmap, fb, cb * 64, head * p.gq,
+                           static_cast<int>(row0) + wk->tok0 + lw * p.tpb);
+          }
+          __syncwarp();
+        }
         auto load_idx = [&](int j) -> long long {
           const long long at = static_cast<long long>(j_first + j) * KT + 32 * lw + lane;
           if (j >= nt || at >= p.n_keys) return -2;
@@ -708,7 +829,7 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
         long long loc_next = 0;
         if constexpr (!PROMPT) loc_next = load_idx(0);
 #pragma unroll 1
-        for (int j = 0; j < nt; ++j) {
+        for (int j = 0; j < nt; ++j, ++gm) {
           long long loc = 0;
           unsigned ok_mask = 0u;
           if constexpr (PROMPT) {
@@ -726,16 +847,11 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
             const unsigned char* base = kv ? p.v + head * p.v_s1 : p.k + head * p.k_s1;
             const long long s0 = kv ? p.v_s0 : p.k_s0;
 #pragma unroll 1
-            for (int h = 0; h < NH; ++h) {
-              const int e = (2 * j + kv) * NH + h;
+            for (int h = 0; h < NH; ++h, ++e) {
               unsigned char* ent = smem + G::ring_off + (e % NE) * ENT;
-              slot_wait(e);
-              if (!PROMPT && kv == 0 && h == 0 && lane == 0) {
-                maskw[4 * (j % kMaskRing) + lw] = ok_mask;
-                mbar_arrive(bar(kBMask + j % kMaskRing));
-              }
               if constexpr (MODE == kSharedE4m3) {
-                // 16 e4m3 values a lane, two 16-byte bf16 chunks
+                // 16 e4m3 values a lane, two 16-byte bf16 chunks; the rows are
+                // under way before the slot is free
                 constexpr int LPR = CPK / 2, RP8 = 32 / LPR, NP8 = 32 / RP8;
                 const int c8 = lane % LPR, r8 = lane / LPR;
                 uint4 x[NP8];
@@ -746,6 +862,11 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
                   x[i] = ((ok_mask >> kl) & 1u)
                              ? __ldg(reinterpret_cast<const uint4*>(base + lc * s0 + h * G::ED + c8 * 16))
                              : make_uint4(0u, 0u, 0u, 0u);
+                }
+                slot_wait(e);
+                if (kv == 0 && h == 0 && lane == 0) {
+                  maskw[4 * (gm % kMaskRing) + lw] = ok_mask;
+                  mbar_arrive(bar(kBMask + gm % kMaskRing));
                 }
 #pragma unroll
                 for (int i = 0; i < NP8; ++i) {
@@ -765,6 +886,7 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
               } else if (PROMPT && p.tma && (kv == 0 || j < j_edge)) {
                 // keys past the sequence may come along: their scores are masked,
                 // and V tiles that hold any take the next branch
+                slot_wait(e);
                 if (lane == 0) {
                   const uint32_t d0 = smem_u32(ent) + 32 * lw * 128, fb = bar(kBFull + e % NE);
                   mbar_arrive_warp_tx(fb, 32 * G::ED * 2);
@@ -779,18 +901,19 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
                 // and are added by the epilogue to the rows that see them
                 bool bad = false;
 #pragma unroll 1
-                for (int i0 = 0; i0 < NP; i0 += 4) {
-                  uint4 x[4];
+                for (int i0 = 0; i0 < NP; i0 += 8) {
+                  uint4 x[8];
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
+                  for (int i = 0; i < 8; ++i) {
                     const int kl = (i0 + i) * RPP + rr;
                     const long long lc = __shfl_sync(0xffffffffu, loc, kl);
                     x[i] = ((ok_mask >> kl) & 1u)
                                ? __ldg(reinterpret_cast<const uint4*>(base + lc * s0 + h * G::ED * 2 + cc * 16))
                                : make_uint4(0u, 0u, 0u, 0u);
                   }
+                  if (i0 == 0) slot_wait(e);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
+                  for (int i = 0; i < 8; ++i) {
                     const int key = 32 * lw + (i0 + i) * RPP + rr;
                     x[i].x = finite_bf16x2(x[i].x, bad);
                     x[i].y = finite_bf16x2(x[i].y, bad);
@@ -799,10 +922,15 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
                     *reinterpret_cast<uint4*>(ent + dst_off(key, cc)) = x[i];
                   }
                 }
-                if (bad) *bad_v = 1;
+                if (bad) *const_cast<volatile int*>(&work[it & 1].bad_v) = 1;
                 fence_proxy_async();
                 mbar_arrive(bar(kBFull + e % NE));
               } else {
+                slot_wait(e);
+                if (!PROMPT && kv == 0 && h == 0 && lane == 0) {
+                  maskw[4 * (gm % kMaskRing) + lw] = ok_mask;
+                  mbar_arrive(bar(kBMask + gm % kMaskRing));
+                }
                 const uint32_t d0 = smem_u32(ent);
 #pragma unroll 4
                 for (int i = 0; i < NP; ++i) {
@@ -817,18 +945,30 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
             }
           }
         }
-        cp_async_wait<0>();
-        if constexpr (PROMPT)
-          asm volatile("bar.arrive %0, %1;" ::"r"(1), "r"(kLoadThreads + 128 * NQ) : "memory");
+        if constexpr (PROMPT) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBEdge + (it & 1)));  // bad_v is final
+        }
+        give_back(it);
       }
-      __syncwarp();
+      cp_async_wait<0>();
     }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+  // the last CTA leaves the counters at zero for the next call
+  if (tid == 0) {
+    __threadfence();
+    if (atomicAdd(p.sched + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+      p.sched[0] = 0;
+      p.sched[1] = 0;
+      __threadfence();
+    }
   }
 }
 

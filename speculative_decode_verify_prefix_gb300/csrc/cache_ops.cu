@@ -28,11 +28,7 @@ static int fa_smem(int D) { return D == 64 ? fa::Geo<64>::smem : D == 128 ? fa::
 constexpr size_t kSchedOff = 64;  // fa_kernel's counters, between the error word and the partials
 static int fa_nq(int D) { return D == 256 ? 1 : 2; }
 
-// Tensor map of bf16 rows [rows][heads][D] for boxes of [n_rows][n_heads][64
-// columns] in the 128-byte swizzle.  False where base or strides are none that
-// a map takes (the rows are then copied without one).
-static bool rows16(const vsk_tensor* t, int e);
-static bool rows_map(const vsk_tensor* t, int n_rows, int n_heads, CUtensorMap* map) {
+static PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   std::call_once(once, [] {
@@ -43,6 +39,15 @@ static bool rows_map(const vsk_tensor* t, int n_rows, int n_heads, CUtensorMap* 
       encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     cudaGetLastError();
   });
+  return encode;
+}
+
+// Tensor map of bf16 rows [rows][heads][D] for boxes of [n_rows][n_heads][64
+// columns] in the 128-byte swizzle.  False where base or strides are none that
+// a map takes (the rows are then copied without one).
+static bool rows16(const vsk_tensor* t, int e);
+static bool rows_map(const vsk_tensor* t, int n_rows, int n_heads, CUtensorMap* map) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
   // a dimension of one element has any stride
   const long long n = t->shape[0], h = t->shape[1], d = t->shape[2];
   const long long s1 = h > 1 ? t->stride[1] : d, s0 = n > 1 ? t->stride[0] : h * s1;
@@ -51,6 +56,21 @@ static bool rows_map(const vsk_tensor* t, int n_rows, int n_heads, CUtensorMap* 
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * s1), static_cast<cuuint64_t>(2 * s0)};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(n_heads), static_cast<cuuint32_t>(n_rows)}, unit[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(t->data), dims, strides, box, unit,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same for gathers of four pool rows of 64 columns at a time: a pool row
+// (all its heads) is a row of the map.
+static bool pool_map(const vsk_tensor* t, CUtensorMap* map) {
+  const long long n = t->shape[0], h = t->shape[1], d = t->shape[2];
+  const long long row = (h > 1 ? (h - 1) * t->stride[1] : 0) + d, s0 = n > 1 ? t->stride[0] : row;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
+  if (!encode || n > INT_MAX || row > INT_MAX || s0 < row || s0 >= (1LL << 38)) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(n)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(2 * s0)};
+  const cuuint32_t box[2] = {64, 1}, unit[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(t->data), dims, strides, box, unit,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -388,6 +408,7 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
     CUtensorMap maps[3];
     memset(maps, 0, sizeof maps);
     f.qtma = f.qmode == 0 && rows_map(q, f.tpb, f.gq, &maps[0]);
+    f.tma = !cs.fp8 && pool_map(kb, &maps[1]) && pool_map(vb, &maps[2]);
     if (!launch_fa(f, maps, D, cs.fp8 ? fa::kSharedE4m3 : fa::kSharedBf16, items, ws, st)) return 0;
   }
   p.B = static_cast<int>(cs.B);

@@ -121,6 +121,7 @@ struct Geo {
   static constexpr int ENT = KT * ED * 2;
   static constexpr int QT = 128 * D * 2;           // one query tile
   static constexpr int NE = D == 64 ? 8 : 5;
+  static constexpr int NLG = D == 256 ? 2 : 1;     // groups of four loader warps (12-15, then 4-7)
   static constexpr int q_off = kDataOff;
   static constexpr int ring_off = q_off + NQ * QT;
   static constexpr int smem = ring_off + NE * ENT;
@@ -147,7 +148,7 @@ struct FaParams {
   float scale2;           // > 0
   int qmode;              // queries enter as they are (0), negated (1) or as zeros (2): the sign of the scale
   int q16, o16;           // 16-byte accesses allowed
-  int tma, qtma;          // K / V tiles (prompt), query tiles come through the tensor maps
+  int tma, qtma;          // K / V tiles (bf16), query tiles come through the tensor maps
   float v_scale;
   unsigned* err;
   float* plse;            // shared: partials, one row block of NQ * 128 rows per CTA
@@ -243,6 +244,15 @@ __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* ma
       "l"(map), "r"(bar), "r"(x), "r"(head), "r"(row)
       : "memory");
 }
+// Four rows of 64 elements, gathered by row number, into four consecutive 128-byte rows.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int r0, int r1,
+                                            int r2, int r3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
+      "%6, %7}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+      : "memory");
+}
 // A warp's 32 arrivals by one lane: 31, and one that also announces the bytes
 // its copies will bring.
 __device__ __forceinline__ void mbar_arrive_warp_tx(uint32_t bar, uint32_t bytes) {
@@ -299,8 +309,8 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
       mbar_init(bar(kBOFull + t), 1);
       mbar_init(bar(kBOEmpty + t), 4);
       mbar_init(bar(kBWFull + t), 1);
-      mbar_init(bar(kBWEmpty + t), 4 * NQ + 1 + 4);
-      mbar_init(bar(kBEdge + t), 4);
+      mbar_init(bar(kBWEmpty + t), 4 * NQ + 1 + 4 * G::NLG);
+      mbar_init(bar(kBEdge + t), 4 * G::NLG);
     }
     for (int i = 0; i < kMaskRing; ++i) mbar_init(bar(kBMask + i), 4);
     mbar_init(bar(kBDone), 1);
@@ -783,9 +793,10 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
       }
       if (elect_one()) mma_commit(bar(kBDone));
       tr::wait_warp(bar(kBDone), 0u, abort_flag, p.err);  // no arrival is pending when the CTA exits
-    } else if (warp >= kWarpLoad) {
+    } else if (warp >= kWarpLoad || (G::NLG == 2 && warp < kWarpMma)) {
       // ================================ loaders ================================
-      const int lw = warp - kWarpLoad;
+      // (head_dim 256: two groups of four warps, each every other entry)
+      const int lw = warp & 3, grp_l = warp < 8 ? 1 : 0;
       constexpr int CPK = G::ED / 8;        // 16-byte chunks of an entry's bf16 row
       constexpr int RPP = 32 / CPK;         // rows of a warp's pass
       constexpr int NP = 32 / RPP;          // passes over a warp's 32 rows
@@ -805,7 +816,7 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
         const int nt = max(wk->n_tiles[0], wk->n_tiles[1]);
         const int head = wk->head, n = wk->n, j_first = wk->j_first, j_edge = wk->j_edge;
         const long long row0 = wk->row0;
-        if (p.qtma && lw < NQ) {
+        if (p.qtma && grp_l == 0 && lw < NQ) {
           // query tile lw (rows past the sequence may come along: they are never stored)
           tr::wait_warp(bar(kBQEmpty + lw), static_cast<uint32_t>((it & 1) ^ 1), abort_flag, p.err);
           if (lane == 0) {
@@ -848,6 +859,7 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
             const long long s0 = kv ? p.v_s0 : p.k_s0;
 #pragma unroll 1
             for (int h = 0; h < NH; ++h, ++e) {
+              if (G::NLG == 2 && (e & 1u) != static_cast<uint32_t>(grp_l)) continue;
               unsigned char* ent = smem + G::ring_off + (e % NE) * ENT;
               if constexpr (MODE == kSharedE4m3) {
                 // 16 e4m3 values a lane, two 16-byte bf16 chunks; the rows are
@@ -925,6 +937,29 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
                 if (bad) *const_cast<volatile int*>(&work[it & 1].bad_v) = 1;
                 fence_proxy_async();
                 mbar_arrive(bar(kBFull + e % NE));
+              } else if (MODE == kSharedBf16 && p.tma && ok_mask == 0xFFFFFFFFu) {
+                // 8 groups of 4 rows x ED / 64 column blocks, one gather a lane
+                constexpr int NB = G::ED / 64;
+                int r[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  r[i] = __shfl_sync(0xffffffffu, static_cast<int>(loc), (4 * (lane / NB) + i) & 31);
+                slot_wait(e);
+                if (lane == 0) {
+                  if (kv == 0 && h == 0) {
+                    maskw[4 * (gm % kMaskRing) + lw] = ok_mask;
+                    mbar_arrive(bar(kBMask + gm % kMaskRing));
+                  }
+                  mbar_arrive_warp_tx(bar(kBFull + e % NE), 32 * G::ED * 2);
+                }
+                __syncwarp();
+                if (lane < 8 * NB) {
+                  const int grp = lane / NB, cb = lane % NB;
+                  tma_gather4(smem_u32(ent) + cb * (KT * 128) + (32 * lw + 4 * grp) * 128, kv ? &vmap : &kmap,
+                              bar(kBFull + e % NE), head * static_cast<int>((kv ? p.v_s1 : p.k_s1) / 2) + h * G::ED + cb * 64,
+                              r[0], r[1], r[2], r[3]);
+                }
+                __syncwarp();
               } else {
                 slot_wait(e);
                 if (!PROMPT && kv == 0 && h == 0 && lane == 0) {

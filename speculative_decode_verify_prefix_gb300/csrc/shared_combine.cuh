@@ -64,6 +64,24 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const __grid_consta
     acc[2] = fmaf(w, v.z, acc[2]);
     acc[3] = fmaf(w, v.w, acc[3]);
   };
+  // n partials, `step` rows apart, eight at a time under way
+  auto fold_all = [&](int n, const float* lse, const float* o, long long step) {
+    for (int k0 = 0; k0 < n; k0 += 8) {
+      float x[8];
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[k] = NEG_INF;
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + k < n) {
+          x[k] = __ldg(lse + (k0 + k) * step);
+          v[k] = __ldg(reinterpret_cast<const float4*>(o + (k0 + k) * step * D));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) fold(x[k], v[k]);
+    }
+  };
   const int col = 32 * ch + 4 * fch;
 
   // ---- the shared prefix ----
@@ -74,11 +92,7 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const __grid_consta
     const int rem = static_cast<int>(tok - blk * bt);
     const int in_block = (rem / s.tpb) * 128 + (rem % s.tpb) * p.gq + rr % p.gq;
     const long long r0 = (blk * s.h_kv + kvh) * s.n_split * (128LL * s.nq) + in_block;
-#pragma unroll 4
-    for (int k = 0; k < s.n_live; ++k) {
-      const long long at = r0 + static_cast<long long>(k) * (128 * s.nq);
-      fold(__ldg(s.splse + at), __ldg(reinterpret_cast<const float4*>(s.spo + at * D + col)));
-    }
+    fold_all(s.n_live, s.splse + r0, s.spo + r0 * D + col, 128 * s.nq);
   }
 
   // ---- the sequence's own prefix: its pieces, cut as the stream cut them ----
@@ -113,11 +127,8 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const __grid_consta
     const long long c0 = off / W, c1 = (off + len - 1) / W;
     const long long slot0 = c0 + static_cast<long long>(b) * p.n_hg + hg;
     const int RM = 16 * p.MT;
-#pragma unroll 4
-    for (long long k = 0; k <= c1 - c0; ++k) {
-      const long long at = ((slot0 + k) * p.HC + hc) * RM + rr;
-      fold(__ldg(p.plse + at), __ldg(reinterpret_cast<const float4*>(p.po + at * D + col)));
-    }
+    const long long at = (slot0 * p.HC + hc) * RM + rr;
+    fold_all(static_cast<int>(c1 - c0 + 1), p.plse + at, p.po + at * D + col, static_cast<long long>(p.HC) * RM);
   }
 
   // ---- the drafts up to this row's own ----

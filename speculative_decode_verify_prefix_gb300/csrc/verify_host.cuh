@@ -45,11 +45,13 @@ int prepare_verify(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tensor* 
                    const vsk_tensor* kvi, int is_causal, int64_t max_len_extend, float k_scale, float v_scale,
                    float sm_scale, const vsk_tensor* cm, const vsk_tensor* mi, const vsk_tensor* ocl, Params& p,
                    CallShape& cs);
-// The stream-only form of the prefix stream (no draft block, partials left in
-// the workspace): its plan, and the launch.
+// A prefix stream alone (no draft block, partials left in the workspace): its
+// plan, and the launch.
 struct StreamOnly {
   Plan pl;
   KernelFn fn;
+  int threads;
+  size_t smem;
   long long n_cta, w_min;
   WsLayout wl;
 };

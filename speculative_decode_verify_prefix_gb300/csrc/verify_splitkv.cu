@@ -1059,21 +1059,39 @@ static int run_verify(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tenso
 
 int plan_stream_only(const CallShape& cs, StreamOnly& so) {
   const long long tokens = cs.mean_len * cs.B;
-  if (!make_plan(cs.h_q, cs.h_kv, cs.D, cs.L, cs.fp8, so.pl, tokens,
-                 g_tiles == 0 ? (tokens >= kSplitTwoTileMinTokens ? 2 : 1) : 0, cs.DV))
-    return 0;
-  so.fn = pick_so_kernel(static_cast<int>(cs.D), cs.fp8, so.pl.MTW);
-  if (!so.fn || !prepare_kernel(so.fn)) return fail("stream-only kernel for head_dim %lld unavailable", cs.D);
   int dev = 0, occ = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail("cudaGetDevice: %s", cudaGetErrorString(e));
   const int sms = device_sms(dev);
   if (sms <= 0) return fail("cannot query the SM count of device %d", dev);
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, reinterpret_cast<const void*>(so.fn), so.pl.threads, so.pl.smem);
+  // the rows-on-M tensor-memory stream where the verify call takes it, else
+  // the stream-only mma.sync kernel; both leave the same partials
+  const bool rows_m = cs.D == cs.DV && g_tc != 1 && tc_eligible(cs.h_q, cs.h_kv, cs.D, cs.L, tokens, cs.fp8);
+  int per_sm = 1;
+  if (rows_m) {
+    if (!make_tc_plan(cs.h_q, cs.h_kv, cs.D, cs.L, cs.fp8, so.pl)) return 0;
+    so.fn = kernel_tr(cs.fp8, 16 * so.pl.MT);
+    int ne = 0;
+    cs.fp8 ? tr_smem<true>(ne, so.smem) : tr_smem<false>(ne, so.smem);
+    if (ne < (cs.fp8 ? 2 : 4)) return fail("tensor-memory ring of %d entries is too shallow", ne);
+    so.pl.nst = ne;
+    so.threads = tr::kThreads;
+  } else {
+    if (!make_plan(cs.h_q, cs.h_kv, cs.D, cs.L, cs.fp8, so.pl, tokens,
+                   g_tiles == 0 ? (tokens >= kSplitTwoTileMinTokens ? 2 : 1) : 0, cs.DV))
+      return 0;
+    so.fn = pick_so_kernel(static_cast<int>(cs.D), cs.fp8, so.pl.MTW);
+    so.smem = so.pl.smem;
+    so.threads = so.pl.threads;
+    per_sm = so.pl.ctas_per_sm;
+  }
+  if (!so.fn || !prepare_kernel(so.fn)) return fail("stream kernel for head_dim %lld unavailable", cs.D);
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, reinterpret_cast<const void*>(so.fn), so.threads, so.smem);
   if (e != cudaSuccess || occ < 1) return fail("kernel does not fit an SM (%s)", cudaGetErrorString(e));
-  so.n_cta = g_num_ctas > 0 ? g_num_ctas : static_cast<long long>(sms) * std::min(occ, so.pl.ctas_per_sm);
+  so.n_cta = g_num_ctas > 0 ? g_num_ctas : static_cast<long long>(sms) * std::min(occ, per_sm);
   so.wl = ws_layout(so.n_cta, cs.B, so.pl, cs.DV);
-  const long long wp = (cs.mean_len / kPiecesPerSegmentColSplit + kStageTokens - 1) / kStageTokens * kStageTokens;
+  const long long per = rows_m ? kPiecesPerSegment : kPiecesPerSegmentColSplit;
+  const long long wp = (cs.mean_len / per + kStageTokens - 1) / kStageTokens * kStageTokens;
   so.w_min = g_min_tokens > 0 ? g_min_tokens : std::max(kDefaultMinTokens, wp);
   return 1;
 }
@@ -1083,8 +1101,8 @@ int launch_stream_only(Params& p, const CallShape& cs, const StreamOnly& so, uns
   CallPlan cp;
   cp.pl = so.pl;
   cp.fn = so.fn;
-  cp.threads = so.pl.threads;
-  cp.smem = so.pl.smem;
+  cp.threads = so.threads;
+  cp.smem = so.smem;
   cp.n_cta = so.n_cta;
   cp.w_min = so.w_min;
   cp.wl = so.wl;

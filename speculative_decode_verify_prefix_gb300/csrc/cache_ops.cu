@@ -75,9 +75,11 @@ static bool pool_map(const vsk_tensor* t, CUtensorMap* map) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// One CTA per SM at most, which draw the items; maps: queries, K, V.
+// One CTA per SM at most; maps: queries, K, V.  beside: the grid may start while
+// the kernel before it on the stream runs (it needs nothing of that kernel, and
+// completes after it).
 static int launch_fa(const fa::FaParams& p, const CUtensorMap* maps, int D, int mode, long long n_items, void* ws,
-                     cudaStream_t st) {
+                     bool beside, cudaStream_t st) {
   fa::FaFn fn = kernel_fa(D, mode);
   if (n_items > INT_MAX / 2) return fail("%lld row blocks are too many", n_items);
   int dev = 0;
@@ -94,8 +96,17 @@ static int launch_fa(const fa::FaParams& p, const CUtensorMap* maps, int D, int 
   CUtensorMap m[3];
   memcpy(m, maps, sizeof m);
   void* args[] = {&a, &m[0], &m[1], &m[2]};
-  e = cudaLaunchKernel(reinterpret_cast<const void*>(fn), dim3(static_cast<unsigned>(std::min<long long>(n_items, sms))),
-                       dim3(fa::kThreads), args, fa_smem(D), st);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(n_items, sms)));
+  cfg.blockDim = dim3(D == 256 || mode != fa::kPrompt ? fa::Cfg<256, 0>::threads : fa::Cfg<128, 0>::threads);
+  cfg.dynamicSmemBytes = fa_smem(D);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = beside ? 1 : 0;
+  e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(fn), args);
   if (e != cudaSuccess) return fail("kernel launch failed: %s", cudaGetErrorString(e));
   return 1;
 }
@@ -135,38 +146,30 @@ static double softmax_scale(float sm_scale, long long D) {
 }
 constexpr double kLog2e = 1.4426950408889634;
 
-// ---- shared prefix: how its keys are cut ----
-// Row blocks x KV heads of work, each cut into key ranges of whole tiles.  An
-// item costs its tiles plus about kItemTiles tiles' time to start and drain,
-// and the items run in waves of one per SM: the cut with the least waves x
-// cost is taken.
-constexpr long long kItemTiles = 4;
+// ---- shared prefix: how the work is cut ----
+// The key tiles of the units (row blocks x KV heads) are laid end to end and
+// every CTA (one per SM) takes the same number of them, at least kMinShare: a
+// shorter piece costs more to start, write and join than its tiles.  Piece of
+// CTA c and unit u: partial c + u.
+constexpr long long kMinShare = 2;
 struct SharedCut {
   int tpb, nq;
-  long long blocks, units, tiles, n_split, split_tiles;
+  long long units, tiles, share, n_cta, pieces;
 };
 static SharedCut shared_cut(long long n_rows, long long gq, long long h_kv, long long D, long long n_keys, int sms) {
   SharedCut c;
   c.tpb = static_cast<int>(128 / gq);
   c.nq = fa_nq(static_cast<int>(D));
-  c.blocks = (n_rows + c.nq * c.tpb - 1) / (c.nq * c.tpb);
-  c.units = c.blocks * h_kv;
+  c.units = (n_rows + c.nq * c.tpb - 1) / (c.nq * c.tpb) * h_kv;
   c.tiles = (n_keys + fa::KT - 1) / fa::KT;
-  c.n_split = 1;
-  long long best = LLONG_MAX;
-  for (long long ns = 1; ns <= std::max(1LL, std::min(c.tiles, 2LL * sms / std::max(1LL, c.units))); ++ns) {
-    const long long per = (c.tiles + ns - 1) / ns;
-    const long long cost = (c.units * ns + sms - 1) / sms * (per + kItemTiles);
-    if (cost < best) {
-      best = cost;
-      c.n_split = ns;
-    }
-  }
-  c.split_tiles = (c.tiles + c.n_split - 1) / c.n_split;
+  const long long total = c.units * c.tiles;
+  c.share = std::max(kMinShare, (total + sms - 1) / sms);
+  c.n_cta = (total + c.share - 1) / c.share;
+  c.pieces = c.n_cta + c.units;
   return c;
 }
-static size_t shared_partial_bytes(long long items, int nq, long long D) {
-  return align256(4 * static_cast<size_t>(items) * 128 * nq) + align256(4 * static_cast<size_t>(items) * 128 * nq * D);
+static size_t shared_partial_bytes(long long pieces, int nq, long long D) {
+  return align256(4 * static_cast<size_t>(pieces) * 128 * nq) + align256(4 * static_cast<size_t>(pieces) * 128 * nq * D);
 }
 
 static size_t shared_workspace_for_sms(int sms, long long max_bs, long long h_q, long long h_kv, long long D,
@@ -174,7 +177,7 @@ static size_t shared_workspace_for_sms(int sms, long long max_bs, long long h_q,
   const size_t own = vsk_workspace_size_for_sms(sms, max_bs, h_q, h_kv, D, D, L);
   if (own == 0 || h_q / h_kv > 128) return 0;
   const SharedCut c = shared_cut(max_bs * L, h_q / h_kv, h_kv, D, 1, sms);
-  return own + shared_partial_bytes(std::max(c.units, 2LL * sms), c.nq, D);
+  return own + shared_partial_bytes(c.units + sms, c.nq, D);
 }
 
 // ---- one thread-block cluster per segment ----
@@ -319,7 +322,7 @@ int prompt_attn_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* 
   memset(maps, 0, sizeof maps);
   p.qtma = rows_map(q, p.tpb, p.gq, &maps[0]);
   p.tma = rows_map(k, 32, 1, &maps[1]) && rows_map(v, 32, 1, &maps[2]);
-  return launch_fa(p, maps, static_cast<int>(D), fa::kPrompt, blocks * h_kv, ws, st);
+  return launch_fa(p, maps, static_cast<int>(D), fa::kPrompt, blocks * h_kv, ws, false, st);
 }
 
 size_t vsk_shared_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv, int64_t head_dim, int64_t max_len_extend) {
@@ -361,10 +364,9 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
   const SharedCut c = shared_cut(cs.B * cs.L, gq, cs.h_kv, cs.D, shi->shape[0], sms);
   // the own pieces as the stream lays them out, the shared partials behind
   // them, the tickets of other calls at the end of the buffer
-  const long long items = c.units * c.n_split;
   const size_t base = so.wl.total - so.wl.cnt_bytes;
-  const size_t sh_o = base + align256(4 * static_cast<size_t>(items) * 128 * c.nq);
-  const size_t need = base + shared_partial_bytes(items, c.nq, cs.D) + so.wl.cnt_bytes;
+  const size_t sh_o = base + align256(4 * static_cast<size_t>(c.pieces) * 128 * c.nq);
+  const size_t need = base + shared_partial_bytes(c.pieces, c.nq, cs.D) + so.wl.cnt_bytes;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   size_t ws_bytes = 0;
   unsigned char* ws = take_workspace(workspace, workspace_bytes, need, st, &ws_bytes);
@@ -395,8 +397,8 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
     f.h_kv = static_cast<int>(cs.h_kv);
     f.gq = static_cast<int>(gq);
     f.tpb = c.tpb;
-    f.n_split = static_cast<int>(c.n_split);
-    f.split_tiles = static_cast<int>(c.split_tiles);
+    f.n_units = c.units;
+    f.share = c.share;
     // the kernel takes the maximum of the unscaled scores: a negative scale
     // goes into the queries' signs, a zero one makes them zero
     f.qmode = scale2 > 0.f ? 0 : scale2 < 0.f ? 1 : 2;
@@ -409,7 +411,7 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
     memset(maps, 0, sizeof maps);
     f.qtma = f.qmode == 0 && rows_map(q, f.tpb, f.gq, &maps[0]);
     f.tma = !cs.fp8 && pool_map(kb, &maps[1]) && pool_map(vb, &maps[2]);
-    if (!launch_fa(f, maps, D, cs.fp8 ? fa::kSharedE4m3 : fa::kSharedBf16, items, ws, st)) return 0;
+    if (!launch_fa(f, maps, D, cs.fp8 ? fa::kSharedE4m3 : fa::kSharedBf16, c.n_cta, ws, has_own, st)) return 0;
   }
   p.B = static_cast<int>(cs.B);
   p.L = static_cast<int>(cs.L);
@@ -420,8 +422,8 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
   p.n_hg = so.pl.n_hg;
   p.err = reinterpret_cast<unsigned*>(ws);
   s.v = p;
-  s.n_split = static_cast<int>(c.n_split);
-  s.n_live = has_shared ? static_cast<int>((c.tiles + c.split_tiles - 1) / c.split_tiles) : 0;
+  s.tiles = has_shared ? c.tiles : 0;
+  s.share = c.share;
   s.h_kv = static_cast<int>(cs.h_kv);
   s.tpb = c.tpb;
   s.nq = c.nq;

@@ -77,18 +77,31 @@ using tc::tmem_st;
 using tc::tmem_wait_st;
 
 constexpr int KT = 128;          // keys per tile
-constexpr int kThreads = 512;
 constexpr int kWarpMma = 8;
 constexpr int kWarpSched = 9;
-constexpr int kWarpLoad = 12;    // loader warps 12-15
-constexpr int kLoadThreads = 128;
-constexpr int kRegsSoftmax = 184, kRegsOther = 72;
-static_assert(8 * 32 * (kRegsSoftmax + kRegsOther) <= 65536, "register shares exceed the launch's");
+constexpr int kLoadArrivals = 128;  // of a ring entry: one per key
 constexpr float kThr = 8.f;      // log2 headroom before the running reference is raised
 constexpr int kMaxNE = 8;        // ring entries at most
 constexpr int kMaskRing = 8;     // > the tiles loaders can run ahead of the softmax
 
 enum Mode { kPrompt = 0, kSharedBf16 = 1, kSharedE4m3 = 2 };
+
+// Warps and registers.  The softmax warps hold a row of 128 scores and half a
+// row of P, so they get what the launch's registers allow; where two warps
+// suffice to load (TMA), the CTA is one warpgroup smaller.
+template <int D, int MODE>
+struct Cfg {
+  static constexpr bool kWide = D == 256 || MODE != kPrompt;
+  static constexpr int threads = kWide ? 512 : 384;
+  static constexpr int warp_load = kWide ? 12 : 10;  // first loader warp
+  static constexpr int n_load = kWide ? 4 : 2;       // loader warps (of a group), 4 / n_load 32-key groups of a tile each
+  static constexpr int groups = D == 256 ? 2 : 1;    // groups of loader warps (head_dim 256: warps 4-7 too)
+  static constexpr int regs_softmax = D == 256 ? 232 : kWide ? 184 : 216;
+  static constexpr int regs_other = 72;
+  static constexpr int regs_launch = 65536 / threads / 8 * 8;
+  static_assert((D == 256 ? regs_softmax + 3 * regs_other : 2 * regs_softmax + (threads / 128 - 2) * regs_other) <=
+                    threads / 128 * regs_launch, "register shares exceed the launch's");
+};
 
 // shared-memory map
 constexpr int kBarOff = 0;
@@ -121,7 +134,6 @@ struct Geo {
   static constexpr int ENT = KT * ED * 2;
   static constexpr int QT = 128 * D * 2;           // one query tile
   static constexpr int NE = D == 64 ? 8 : 5;
-  static constexpr int NLG = D == 256 ? 2 : 1;     // groups of four loader warps (12-15, then 4-7)
   static constexpr int q_off = kDataOff;
   static constexpr int ring_off = q_off + NQ * QT;
   static constexpr int smem = ring_off + NE * ENT;
@@ -144,14 +156,14 @@ struct FaParams {
   int h_kv, gq, tpb;      // tpb: tokens per query tile
   int n_items;            // items at most
   int* sched;             // next ticket beyond the grid's, CTAs done (both zero between calls)
-  int n_split, split_tiles;  // shared: key ranges per row block, key tiles of one
+  long long n_units, share;  // shared: row blocks x KV heads, key tiles per CTA
   float scale2;           // > 0
   int qmode;              // queries enter as they are (0), negated (1) or as zeros (2): the sign of the scale
   int q16, o16;           // 16-byte accesses allowed
   int tma, qtma;          // K / V tiles (bf16), query tiles come through the tensor maps
   float v_scale;
   unsigned* err;
-  float* plse;            // shared: partials, one row block of NQ * 128 rows per CTA
+  float* plse;            // shared: partials; piece of CTA c, unit u: NQ * 128 rows at (c + u)
   float* po;
 };
 
@@ -235,6 +247,33 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Wait of a whole warp for a phase, one second at most (a wait that gives up
+// sets the abort flag and the error bit).  Every lane looks, and looks again at
+// once: a suspended warp (try_wait) wakes some hundred cycles late, which the
+// chain of scores, softmax and product pays several times a tile (long prompts
+// 1129 us suspended, 847 us so); the clock is read only after many looks.
+__device__ __forceinline__ void wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+  unsigned long long t0 = 0;
+  for (int looks = 0; !__all_sync(0xffffffffu, tr::test(bar, parity)); ++looks) {
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return;
+    if (looks == 65536) t0 = tc::global_ns();
+    if (looks > 65536 && (looks & 1023) == 0 && __all_sync(0xffffffffu, tc::global_ns() - t0 > 1000000000ull)) {
+      *abort_flag = 1;
+      if ((threadIdx.x & 31) == 0) atomicOr(err, kErrTimeout);
+      return;
+    }
+  }
+}
+// Position in the ring: slot and the parity of its lap.
+template <int NE>
+struct Pos {
+  uint32_t slot, par;
+  __device__ __forceinline__ Pos ahead(uint32_t n) const {
+    const uint32_t x = slot + n;
+    return x >= NE ? Pos{x - NE, par ^ 1u} : Pos{x, par};
+  }
+};
+
 // One box of a [rows][heads][head_dim] tensor map into shared memory ([32 rows]
 // [64 head dimensions] of a K / V head, [tpb rows][g heads][64] of the queries).
 __device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int head, int row) {
@@ -270,12 +309,13 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, bool& bad) {
 }  // namespace fa
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_constant__ fa::FaParams p,
+__global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const __grid_constant__ fa::FaParams p,
                                                              const __grid_constant__ CUtensorMap qmap,
                                                              const __grid_constant__ CUtensorMap kmap,
                                                              const __grid_constant__ CUtensorMap vmap) {
   using namespace fa;
   using G = fa::Geo<D>;
+  using C = fa::Cfg<D, MODE>;
   constexpr int NQ = G::NQ, NH = G::NH, NE = G::NE, ENT = G::ENT;
   constexpr bool PROMPT = MODE == kPrompt;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -297,7 +337,7 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
   if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < NE; ++i) {
-      mbar_init(bar(kBFull + i), kLoadThreads);
+      mbar_init(bar(kBFull + i), kLoadArrivals);
       mbar_init(bar(kBEmpty + i), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -309,8 +349,8 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
       mbar_init(bar(kBOFull + t), 1);
       mbar_init(bar(kBOEmpty + t), 4);
       mbar_init(bar(kBWFull + t), 1);
-      mbar_init(bar(kBWEmpty + t), 4 * NQ + 1 + 4 * G::NLG);
-      mbar_init(bar(kBEdge + t), 4 * G::NLG);
+      mbar_init(bar(kBWEmpty + t), 4 * NQ + 1 + C::n_load * C::groups);
+      mbar_init(bar(kBEdge + t), C::n_load * C::groups);
     }
     for (int i = 0; i < kMaskRing; ++i) mbar_init(bar(kBMask + i), 4);
     mbar_init(bar(kBDone), 1);
@@ -325,7 +365,7 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
   if (p.qtma && p.tpb * p.gq < 128) {
     // rows of the query tiles that no box fills
     const int rows = 128 - p.tpb * p.gq;
-    for (int i = tid; i < NQ * (D / 64) * rows * 8; i += kThreads)
+    for (int i = tid; i < NQ * (D / 64) * rows * 8; i += C::threads)
       *reinterpret_cast<uint4*>(smem + G::q_off + (i / (rows * 8)) * (128 * 128) + (128 - rows) * 128 +
                                 (i % (rows * 8)) * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async();
@@ -343,7 +383,7 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
 
   // The item of round `it` for a role's warp: false when there is none left.
   auto take = [&](int it, const Work*& w) -> bool {
-    tr::wait_warp(bar(kBWFull + (it & 1)), static_cast<uint32_t>((it >> 1) & 1), abort_flag, p.err);
+    wait_all(bar(kBWFull + (it & 1)), static_cast<uint32_t>((it >> 1) & 1), abort_flag, p.err);
     w = work + (it & 1);
     const int first = *const_cast<const volatile int*>(&w->n_tiles[0]);
     return !__any_sync(0xffffffffu, *abort_flag != 0) && first >= 0;
@@ -355,7 +395,7 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
 
   if (warp < 4 * NQ) {
     // ================================ softmax ================================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::regs_softmax));
     const int t = warp >> 2, w = warp & 3, tw = tid & 127;
     const int r = 32 * w + lane;  // this thread's packed row of the tile
     const int r_tok = r / p.gq, r_head = r % p.gq;
@@ -373,7 +413,7 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
       const long long row0 = wk->row0;
       // ---- queries of the tile into shared memory (where no tensor map takes them) ----
       if (!p.qtma) {
-        tr::wait_warp(bar(kBQEmpty + t), static_cast<uint32_t>((it & 1) ^ 1), abort_flag, p.err);
+        wait_all(bar(kBQEmpty + t), static_cast<uint32_t>((it & 1) ^ 1), abort_flag, p.err);
         constexpr int CPR = D / 8;  // 16-byte chunks of a row
         unsigned char* qs = smem + G::q_off + t * G::QT;
 #pragma unroll 8
@@ -409,7 +449,7 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
         const int buf = NQ == 2 ? t : (g & 1);
         const uint32_t par = NQ == 2 ? (g & 1) : ((g >> 1) & 1);
         const uint32_t t_s = t_lane + buf * KT;
-        tr::wait_warp(bar(kBSFull + buf), par, abort_flag, p.err);
+        wait_all(bar(kBSFull + buf), par, abort_flag, p.err);
         tc_fence_after();
         // Scores, then P, in halves of 64 keys.  The first half's P is computed
         // against the reference that the tiles before left, while the second
@@ -420,15 +460,17 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
         unsigned mw[4];
         if constexpr (PROMPT) {
           masked = (j + 1) * KT - 1 > first;
-          const int lim = tok - j * KT;  // keys c <= lim are visible
+          if (masked) {
+            const int lim = tok - j * KT;  // keys c <= lim are visible
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int n_vis = min(32, max(0, lim + 1 - 32 * u));
-            mw[u] = n_vis == 32 ? 0xFFFFFFFFu : (1u << n_vis) - 1u;
+            for (int u = 0; u < 4; ++u) {
+              const int n_vis = min(32, max(0, lim + 1 - 32 * u));
+              mw[u] = n_vis == 32 ? 0xFFFFFFFFu : (1u << n_vis) - 1u;
+            }
           }
         } else {
           const uint32_t jm = (gm + j) % kMaskRing;
-          tr::wait_warp(bar(kBMask + jm), ((gm + j) / kMaskRing) & 1, abort_flag, p.err);
+          wait_all(bar(kBMask + jm), ((gm + j) / kMaskRing) & 1, abort_flag, p.err);
 #pragma unroll
           for (int u = 0; u < 4; ++u) mw[u] = maskw[4 * jm + u];
           masked = (mw[0] & mw[1] & mw[2] & mw[3]) != 0xFFFFFFFFu;
@@ -467,21 +509,21 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
         tmem_pass(s + 32);
         tmem_ld32_nw(t_s + 64, s + 64);
         tmem_ld32_nw(t_s + 96, s + 96);
-        if (masked) hide(0);
+        if (__builtin_expect(masked, 0)) hide(0);
         probs(0, mrun == NEG_INF ? 0.f : mrun);
         top(0);
         tmem_wait_ld();
         tmem_pass(s + 64);
         tmem_pass(s + 96);
-        if (masked) hide(1);
+        if (__builtin_expect(masked, 0)) hide(1);
         top(1);
         // ---- raise the reference when the tile's maximum passes it by more than kThr ----
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-        if (__any_sync(0xffffffffu, mt > mrun + kThr)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, mt > mrun + kThr), 0)) {
           const float mn = fmaxf(mrun, mt);
           const float al = mn == NEG_INF ? 1.f : fast_exp2(mrun - mn);
           if (j > 0) {
-            tr::wait_warp(bar(kBOFull + t), (g - 1) & 1, abort_flag, p.err);
+            wait_all(bar(kBOFull + t), (g - 1) & 1, abort_flag, p.err);
             tc_fence_after();
 #pragma unroll 1
             for (int cb = 0; cb < D / 8; ++cb) {
@@ -514,13 +556,13 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
       if (my_tiles > 0) {
         // one query tile: the last scores are issued before the PV of the tile
         // before, so that phase has to be seen to complete first
-        if (NQ == 1 && my_tiles > 1) tr::wait_warp(bar(kBOFull + t), (g - 2) & 1, abort_flag, p.err);
-        tr::wait_warp(bar(kBOFull + t), (g - 1) & 1, abort_flag, p.err);
+        if (NQ == 1 && my_tiles > 1) wait_all(bar(kBOFull + t), (g - 2) & 1, abort_flag, p.err);
+        wait_all(bar(kBOFull + t), (g - 1) & 1, abort_flag, p.err);
         tc_fence_after();
       }
       if constexpr (PROMPT) {
         // the item's diagonal V tiles have been looked at
-        tr::wait_warp(bar(kBEdge + (it & 1)), static_cast<uint32_t>((it >> 1) & 1), abort_flag, p.err);
+        wait_all(bar(kBEdge + (it & 1)), static_cast<uint32_t>((it >> 1) & 1), abort_flag, p.err);
         if (my_tiles > 0) {
           const float inv = 1.f / l;
           const bool fix = *const_cast<const volatile int*>(&wk->bad_v) != 0;
@@ -585,16 +627,19 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
       give_back(it);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::regs_other));
     if (warp == kWarpSched) {
       // ============================ items of this CTA ============================
-      // The first is the CTA's number, the others are drawn from a counter, so
-      // that long and short items even out; a sequence's row blocks come last
-      // (longest key range) first.
+      // Prompts: the first is the CTA's number, the others are drawn from a
+      // counter, so that long and short items even out; a sequence's row blocks
+      // come last (longest key range) first.  Shared prefix: every CTA has the
+      // same number of key tiles, cut where a row block's keys end.
+      long long at = static_cast<long long>(blockIdx.x) * p.share;  // shared prefix: next tile of this CTA's share
+      int n_piece = 0;
 #pragma unroll 1
       for (int it = 0;; ++it) {
         int ticket = static_cast<int>(blockIdx.x);
-        if (it > 0) {
+        if (PROMPT && it > 0) {
           if (lane == 0) ticket = static_cast<int>(gridDim.x) + atomicAdd(p.sched, 1);
           ticket = __shfl_sync(0xffffffffu, ticket, 0);
         }
@@ -636,12 +681,19 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
               }
             }
           } else {
-            const int u = ticket / p.n_split;
+            // piece `it` of this CTA's share of the row blocks' key tiles, laid end to end
+            const long long tiles = (p.n_keys + KT - 1) / KT;
+            const long long end = min(tiles * p.n_units, static_cast<long long>(blockIdx.x + 1) * p.share);
+            found = at < end;
+            const int u = static_cast<int>(at / tiles);
             x.head = u % p.h_kv;
             x.row0 = 0;
             x.n = static_cast<int>(p.n_rows);
             x.tok0 = (u / p.h_kv) * bt;
-            x.j_first = (ticket % p.n_split) * p.split_tiles;
+            x.j_first = static_cast<int>(at - u * tiles);
+            x.item = static_cast<long long>(blockIdx.x) + u;
+            n_piece = static_cast<int>(min(tiles - x.j_first, end - at));
+            at += n_piece;
           }
           if (found) {
 #pragma unroll
@@ -652,14 +704,13 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
               } else if constexpr (PROMPT) {
                 x.n_tiles[t] = (min(first + p.tpb, x.n) + KT - 1) / KT;
               } else {
-                const long long tiles = (p.n_keys + KT - 1) / KT;
-                x.n_tiles[t] = static_cast<int>(max(0LL, min(static_cast<long long>(p.split_tiles), tiles - x.j_first)));
+                x.n_tiles[t] = n_piece;
               }
             }
             x.j_edge = PROMPT ? x.tok0 / KT : 0;  // first tile with keys that some row of the block must not see
           }
         }
-        tr::wait_warp(bar(kBWEmpty + (it & 1)), static_cast<uint32_t>(((it >> 1) & 1) ^ 1), abort_flag, p.err);
+        wait_all(bar(kBWEmpty + (it & 1)), static_cast<uint32_t>(((it >> 1) & 1) ^ 1), abort_flag, p.err);
         if (lane == 0) {
           work[it & 1] = x;
           mbar_arrive(bar(kBWFull + (it & 1)));
@@ -669,140 +720,142 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
       }
     } else if (warp == kWarpMma) {
       // ============================ MMA issue ============================
+      const uint32_t tmem_u = __reduce_max_sync(0xffffffffu, tmem);
       constexpr uint32_t idS = idesc(1, 1, 0, 0, 128, KT);
       constexpr uint32_t idPV = idesc(1, 1, 0, 1, 128, G::ED);
       const uint64_t dq0 = sdesc(q_s, 16, 1024), dk0 = sdesc(ring_s, 16, 1024), dv0 = sdesc(ring_s, KT * 128, 1024);
-      uint32_t e0 = 0;             // ring entries of the items before
-      uint32_t g[2] = {0u, 0u};    // key tiles per query tile of the items before
+      using RP = Pos<NE>;
+      RP kp{0u, 0u}, vp{NH, 0u};   // ring entries of the next K / V tile (NH each)
+      uint32_t g[2] = {0u, 0u};    // key tiles per query tile so far
       uint32_t n_o[2] = {0u, 0u};  // items that gave the query tile any
-      // entry of (tile j, K / V, half h): e0 + (2 j + kv) NH + h
-      auto entry = [&](int j, int kv, int h) -> uint32_t { return e0 + static_cast<uint32_t>((2 * j + kv) * NH + h); };
-      auto qk = [&](int t, int j) {
-        const uint32_t buf = NQ == 2 ? t : ((g[t] + j) & 1);
-        const uint32_t dc = tmem + buf * KT;
+      // S of query tile t against the K tile at kp; last: the K tile's entries
+      // are free afterwards; q_free: the queries are
+      auto qk = [&](int t, uint32_t gt, bool last, bool q_free) {
+        const uint32_t buf = NQ == 2 ? t : (gt & 1);
+        const uint32_t dc = tmem_u + buf * KT;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          const uint32_t slot = entry(j, 0, h) % NE;
+          const uint32_t slot = kp.ahead(h).slot;
           const uint64_t qd = dq0 + static_cast<uint64_t>((t * G::QT + h * 2 * (128 * 128)) >> 4);
-          const uint64_t kd = dk0 + static_cast<uint64_t>((slot * ENT) >> 4);
+          const uint64_t kd = dk0 + static_cast<uint64_t>(slot * (ENT >> 4));
           if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < G::ED / 16; ++ks) {
               const uint64_t off = static_cast<uint64_t>(((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4);
               mma_f16_ss(dc, qd + off, kd + off, idS, h > 0 || ks > 0);
             }
+            if (h == NH - 1) mma_commit(bar(kBSFull + buf));
+            if (last) mma_commit(bar(kBEmpty + slot));
+            if (h == NH - 1 && q_free) mma_commit(bar(kBQEmpty + t));
           }
         }
-        if (elect_one()) mma_commit(bar(kBSFull + buf));
       };
-      auto pv = [&](int t, int j) {
-        const uint32_t gt = g[t] + j;
+      // O += P V of query tile t with the V tile at vp
+      auto pv = [&](int t, uint32_t gt, bool first, bool last) {
         const uint32_t buf = NQ == 2 ? t : (gt & 1), par = NQ == 2 ? (gt & 1) : ((gt >> 1) & 1);
-        const uint32_t a = tmem + buf * KT;
+        const uint32_t a = tmem_u + buf * KT;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          tr::wait_warp(bar(kBPFull + 2 * buf + half), par, abort_flag, p.err);
+          wait_all(bar(kBPFull + 2 * buf + half), par, abort_flag, p.err);
           tc_fence_after();
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
-            const uint32_t slot = entry(j, 1, h) % NE;
-            const uint64_t vd = dv0 + static_cast<uint64_t>((slot * ENT) >> 4);
+            const uint32_t slot = vp.ahead(h).slot;
+            const uint64_t vd = dv0 + static_cast<uint64_t>(slot * (ENT >> 4));
             if (elect_one()) {
 #pragma unroll
               for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                mma_f16_ts(tmem + G::col_o + t * D + h * G::ED, a + ks * 8, vd + static_cast<uint64_t>(ks * 128), idPV,
-                           j > 0 || ks > 0);
+                mma_f16_ts(tmem_u + G::col_o + t * D + h * G::ED, a + ks * 8, vd + static_cast<uint64_t>(ks * 128), idPV,
+                           !first || ks > 0);
+              if (half == 1 && h == NH - 1) mma_commit(bar(kBOFull + t));
+              if (half == 1 && last) mma_commit(bar(kBEmpty + slot));
             }
           }
         }
-        if (elect_one()) mma_commit(bar(kBOFull + t));
       };
-      auto acquire = [&](int j, int kv) {
+      auto acquire = [&](const RP& x) {
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          const uint32_t e = entry(j, kv, h);
-          tr::wait_warp(bar(kBFull + e % NE), (e / NE) & 1, abort_flag, p.err);
+          const RP y = x.ahead(h);
+          wait_all(bar(kBFull + y.slot), y.par, abort_flag, p.err);
         }
         // rows that came by cp.async (stores are fenced by their writers, TMA needs none)
         if (MODE == kSharedBf16 || (PROMPT && !p.tma)) fence_proxy_async();
         tc_fence_after();
       };
-      auto release = [&](int j, int kv) {
-#pragma unroll
-        for (int h = 0; h < NH; ++h)
-          if (elect_one()) mma_commit(bar(kBEmpty + entry(j, kv, h) % NE));
-      };
 #pragma unroll 1
       for (int it = 0;; ++it) {
         const Work* wk;
         if (!take(it, wk)) break;
-        const int n_tiles[2] = {wk->n_tiles[0], wk->n_tiles[1]};
+        // (through a warp reduction, whose result is a uniform register: the loop
+        // and with it the descriptors' arithmetic are then uniform, too)
+        const int n0 = __reduce_max_sync(0xffffffffu, wk->n_tiles[0]);
+        const int n1 = __reduce_max_sync(0xffffffffu, wk->n_tiles[1]);
         give_back(it);
-        const int nt = max(n_tiles[0], n_tiles[1]);
-        // the queries; after its last scores a tile's are free again
-        auto q_done = [&](int t) {
-          if (elect_one()) mma_commit(bar(kBQEmpty + t));
-        };
+        const int nt = max(n0, n1);
 #pragma unroll
-        for (int t = 0; t < NQ; ++t)
-          tr::wait_warp(bar(kBQFull + t), static_cast<uint32_t>(it & 1), abort_flag, p.err);
+        for (int t = 0; t < NQ; ++t) wait_all(bar(kBQFull + t), static_cast<uint32_t>(it & 1), abort_flag, p.err);
         tc_fence_after();
-        if (nt > 0) acquire(0, 0);
-#pragma unroll
-        for (int t = 0; t < NQ; ++t) {
-          if (n_tiles[t] > 0) qk(t, 0);
-          if (n_tiles[t] <= 1) q_done(t);
+        if (nt > 0) {
+          acquire(kp);
+          if (n0 > 0) qk(0, g[0], NQ == 1 || n1 == 0, n0 == 1);
+          if (NQ == 2 && n1 > 0) qk(1, g[1], true, n1 == 1);
+          kp = kp.ahead(2 * NH);
         }
-        if (nt > 0) release(0, 0);
+        if (elect_one()) {
+          if (n0 == 0) mma_commit(bar(kBQEmpty));
+          if (NQ == 2 && n1 == 0) mma_commit(bar(kBQEmpty + 1));
+        }
         // the rows of O of the item before have been read (a query tile without
         // keys has none, and its softmax warps say nothing)
-#pragma unroll
-        for (int t = 0; t < NQ; ++t)
-          if (n_tiles[t] > 0) tr::wait_warp(bar(kBOEmpty + t), (n_o[t]++ & 1) ^ 1, abort_flag, p.err);
+        if (n0 > 0) wait_all(bar(kBOEmpty), (n_o[0]++ & 1) ^ 1, abort_flag, p.err);
+        if (NQ == 2 && n1 > 0) wait_all(bar(kBOEmpty + 1), (n_o[1]++ & 1) ^ 1, abort_flag, p.err);
         tc_fence_after();
 #pragma unroll 1
         for (int j = 0; j < nt; ++j) {
+          const bool more = j + 1 < nt;
           if constexpr (NQ == 1) {
-            if (j + 1 < nt) {
-              acquire(j + 1, 0);
-              qk(0, j + 1);
-              release(j + 1, 0);
-              if (j + 2 == nt) q_done(0);
+            if (more) {
+              acquire(kp);
+              qk(0, g[0] + 1, true, j + 2 == nt);
+              kp = kp.ahead(2 * NH);
             }
-            acquire(j, 1);
-            pv(0, j);
-            release(j, 1);
+            acquire(vp);
+            pv(0, g[0], j == 0, true);
+            ++g[0];
           } else {
-            acquire(j, 1);
-#pragma unroll
-            for (int t = 0; t < NQ; ++t) {
-              if (j < n_tiles[t]) pv(t, j);
-              if (t == NQ - 1) release(j, 1);
-              if (j + 1 < nt && t == 0) acquire(j + 1, 0);
-              if (j + 1 < n_tiles[t]) {
-                qk(t, j + 1);
-                if (j + 2 == n_tiles[t]) q_done(t);
-              }
-              if (t == NQ - 1 && j + 1 < nt) release(j + 1, 0);
+            // (the tiles of a block have as many keys or the second one more)
+            acquire(vp);
+            if (j < n0) {
+              pv(0, g[0], j == 0, j >= n1);
+              ++g[0];
             }
+            if (more) acquire(kp);
+            if (j + 1 < n0) qk(0, g[0], j + 1 >= n1, j + 2 == n0);
+            if (j < n1) {
+              pv(1, g[1], j == 0, true);
+              ++g[1];
+            }
+            if (j + 1 < n1) qk(1, g[1], true, j + 2 == n1);
+            if (more) kp = kp.ahead(2 * NH);
           }
+          vp = vp.ahead(2 * NH);
         }
-        e0 += static_cast<uint32_t>(2 * nt * NH);
-        g[0] += n_tiles[0];
-        g[1] += n_tiles[1];
       }
       if (elect_one()) mma_commit(bar(kBDone));
-      tr::wait_warp(bar(kBDone), 0u, abort_flag, p.err);  // no arrival is pending when the CTA exits
-    } else if (warp >= kWarpLoad || (G::NLG == 2 && warp < kWarpMma)) {
+      wait_all(bar(kBDone), 0u, abort_flag, p.err);  // no arrival is pending when the CTA exits
+    } else if (warp >= C::warp_load || (C::groups == 2 && warp < kWarpMma)) {
       // ================================ loaders ================================
-      // (head_dim 256: two groups of four warps, each every other entry)
-      const int lw = warp & 3, grp_l = warp < 8 ? 1 : 0;
+      // A warp has NS of the four 32-key groups of every entry (with two groups
+      // of loader warps: of every other entry).
+      constexpr int NS = 4 / C::n_load;
+      const int lw = warp >= C::warp_load ? warp - C::warp_load : warp & 3, lgrp = warp < kWarpMma ? 1 : 0;
       constexpr int CPK = G::ED / 8;        // 16-byte chunks of an entry's bf16 row
       constexpr int RPP = 32 / CPK;         // rows of a warp's pass
-      constexpr int NP = 32 / RPP;          // passes over a warp's 32 rows
+      constexpr int NP = 32 / RPP;          // passes over 32 rows
       const int cc = lane % CPK, rr = lane / CPK;
       auto slot_wait = [&](uint32_t e) {
-        tr::wait_warp(bar(kBEmpty + e % NE), ((e / NE) & 1) ^ 1, abort_flag, p.err);
+        wait_all(bar(kBEmpty + e % NE), ((e / NE) & 1) ^ 1, abort_flag, p.err);
       };
       auto dst_off = [&](int key, int c) -> uint32_t {
         return static_cast<uint32_t>((c >> 3) * (KT * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4));
@@ -816,9 +869,9 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
         const int nt = max(wk->n_tiles[0], wk->n_tiles[1]);
         const int head = wk->head, n = wk->n, j_first = wk->j_first, j_edge = wk->j_edge;
         const long long row0 = wk->row0;
-        if (p.qtma && grp_l == 0 && lw < NQ) {
+        if (p.qtma && lgrp == 0 && lw < NQ) {
           // query tile lw (rows past the sequence may come along: they are never stored)
-          tr::wait_warp(bar(kBQEmpty + lw), static_cast<uint32_t>((it & 1) ^ 1), abort_flag, p.err);
+          wait_all(bar(kBQEmpty + lw), static_cast<uint32_t>((it & 1) ^ 1), abort_flag, p.err);
           if (lane == 0) {
             const uint32_t fb = bar(kBQFull + lw);
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(fb),
@@ -831,27 +884,34 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
           }
           __syncwarp();
         }
-        auto load_idx = [&](int j) -> long long {
-          const long long at = static_cast<long long>(j_first + j) * KT + 32 * lw + lane;
+        auto load_idx = [&](int j, int kg) -> long long {
+          const long long at = static_cast<long long>(j_first + j) * KT + 32 * kg + lane;
           if (j >= nt || at >= p.n_keys) return -2;
           return p.idx64 ? __ldg(static_cast<const long long*>(p.idx) + at)
                          : static_cast<long long>(__ldg(static_cast<const int*>(p.idx) + at));
         };
-        long long loc_next = 0;
-        if constexpr (!PROMPT) loc_next = load_idx(0);
+        long long loc_next[NS];
+        if constexpr (!PROMPT) {
+#pragma unroll
+          for (int u = 0; u < NS; ++u) loc_next[u] = load_idx(0, lw * NS + u);
+        }
 #pragma unroll 1
         for (int j = 0; j < nt; ++j, ++gm) {
-          long long loc = 0;
-          unsigned ok_mask = 0u;
-          if constexpr (PROMPT) {
-            loc = row0 + static_cast<long long>(j) * KT + 32 * lw + lane;
-            ok_mask = __ballot_sync(0xffffffffu, j * KT + 32 * lw + lane < n);
-          } else {
-            loc = loc_next;
-            loc_next = load_idx(j + 1);
-            const bool ok = loc >= 0 && loc < p.pool;
-            if (!ok && loc != -2) atomicOr(p.err, kErrBadIndex);
-            ok_mask = __ballot_sync(0xffffffffu, ok);
+          long long loc[NS];
+          unsigned ok_mask[NS];
+#pragma unroll
+          for (int u = 0; u < NS; ++u) {
+            const int kg = lw * NS + u;
+            if constexpr (PROMPT) {
+              loc[u] = row0 + static_cast<long long>(j) * KT + 32 * kg + lane;
+              ok_mask[u] = __ballot_sync(0xffffffffu, j * KT + 32 * kg + lane < n);
+            } else {
+              loc[u] = loc_next[u];
+              loc_next[u] = load_idx(j + 1, kg);
+              const bool ok = loc[u] >= 0 && loc[u] < p.pool;
+              if (!ok && loc[u] != -2) atomicOr(p.err, kErrBadIndex);
+              ok_mask[u] = __ballot_sync(0xffffffffu, ok);
+            }
           }
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
@@ -859,8 +919,15 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
             const long long s0 = kv ? p.v_s0 : p.k_s0;
 #pragma unroll 1
             for (int h = 0; h < NH; ++h, ++e) {
-              if (G::NLG == 2 && (e & 1u) != static_cast<uint32_t>(grp_l)) continue;
+              if (C::groups == 2 && (e & 1u) != static_cast<uint32_t>(lgrp)) continue;
               unsigned char* ent = smem + G::ring_off + (e % NE) * ENT;
+              const uint32_t fb = bar(kBFull + e % NE);
+              auto publish_mask = [&](int u) {  // which keys of the group count, with a tile's first entry
+                if (!PROMPT && kv == 0 && h == 0 && lane == 0) {
+                  maskw[4 * (gm % kMaskRing) + lw * NS + u] = ok_mask[u];
+                  mbar_arrive(bar(kBMask + gm % kMaskRing));
+                }
+              };
               if constexpr (MODE == kSharedE4m3) {
                 // 16 e4m3 values a lane, two 16-byte bf16 chunks; the rows are
                 // under way before the slot is free
@@ -870,16 +937,13 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
 #pragma unroll
                 for (int i = 0; i < NP8; ++i) {
                   const int kl = i * RP8 + r8;
-                  const long long lc = __shfl_sync(0xffffffffu, loc, kl);
-                  x[i] = ((ok_mask >> kl) & 1u)
+                  const long long lc = __shfl_sync(0xffffffffu, loc[0], kl);
+                  x[i] = ((ok_mask[0] >> kl) & 1u)
                              ? __ldg(reinterpret_cast<const uint4*>(base + lc * s0 + h * G::ED + c8 * 16))
                              : make_uint4(0u, 0u, 0u, 0u);
                 }
                 slot_wait(e);
-                if (kv == 0 && h == 0 && lane == 0) {
-                  maskw[4 * (gm % kMaskRing) + lw] = ok_mask;
-                  mbar_arrive(bar(kBMask + gm % kMaskRing));
-                }
+                publish_mask(0);
 #pragma unroll
                 for (int i = 0; i < NP8; ++i) {
                   const int key = 32 * lw + i * RP8 + r8;
@@ -894,88 +958,84 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
                   *reinterpret_cast<uint4*>(ent + dst_off(key, 2 * c8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
                 }
                 fence_proxy_async();
-                mbar_arrive(bar(kBFull + e % NE));
-              } else if (PROMPT && p.tma && (kv == 0 || j < j_edge)) {
-                // keys past the sequence may come along: their scores are masked,
-                // and V tiles that hold any take the next branch
-                slot_wait(e);
-                if (lane == 0) {
-                  const uint32_t d0 = smem_u32(ent) + 32 * lw * 128, fb = bar(kBFull + e % NE);
-                  mbar_arrive_warp_tx(fb, 32 * G::ED * 2);
-#pragma unroll
-                  for (int cb = 0; cb < G::ED / 64; ++cb)
-                    tma_load_box(d0 + cb * (KT * 128), kv ? &vmap : &kmap, fb, h * G::ED + cb * 64, head,
-                                 static_cast<int>(row0) + j * KT + 32 * lw);
-                }
-                __syncwarp();
-              } else if (PROMPT && kv == 1 && j >= j_edge) {
-                // V on the diagonal: values that are not finite become 0 here
-                // and are added by the epilogue to the rows that see them
-                bool bad = false;
-#pragma unroll 1
-                for (int i0 = 0; i0 < NP; i0 += 8) {
-                  uint4 x[8];
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    const int kl = (i0 + i) * RPP + rr;
-                    const long long lc = __shfl_sync(0xffffffffu, loc, kl);
-                    x[i] = ((ok_mask >> kl) & 1u)
-                               ? __ldg(reinterpret_cast<const uint4*>(base + lc * s0 + h * G::ED * 2 + cc * 16))
-                               : make_uint4(0u, 0u, 0u, 0u);
-                  }
-                  if (i0 == 0) slot_wait(e);
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    const int key = 32 * lw + (i0 + i) * RPP + rr;
-                    x[i].x = finite_bf16x2(x[i].x, bad);
-                    x[i].y = finite_bf16x2(x[i].y, bad);
-                    x[i].z = finite_bf16x2(x[i].z, bad);
-                    x[i].w = finite_bf16x2(x[i].w, bad);
-                    *reinterpret_cast<uint4*>(ent + dst_off(key, cc)) = x[i];
-                  }
-                }
-                if (bad) *const_cast<volatile int*>(&work[it & 1].bad_v) = 1;
-                fence_proxy_async();
-                mbar_arrive(bar(kBFull + e % NE));
-              } else if (MODE == kSharedBf16 && p.tma && ok_mask == 0xFFFFFFFFu) {
-                // 8 groups of 4 rows x ED / 64 column blocks, one gather a lane
-                constexpr int NB = G::ED / 64;
-                int r[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  r[i] = __shfl_sync(0xffffffffu, static_cast<int>(loc), (4 * (lane / NB) + i) & 31);
-                slot_wait(e);
-                if (lane == 0) {
-                  if (kv == 0 && h == 0) {
-                    maskw[4 * (gm % kMaskRing) + lw] = ok_mask;
-                    mbar_arrive(bar(kBMask + gm % kMaskRing));
-                  }
-                  mbar_arrive_warp_tx(bar(kBFull + e % NE), 32 * G::ED * 2);
-                }
-                __syncwarp();
-                if (lane < 8 * NB) {
-                  const int grp = lane / NB, cb = lane % NB;
-                  tma_gather4(smem_u32(ent) + cb * (KT * 128) + (32 * lw + 4 * grp) * 128, kv ? &vmap : &kmap,
-                              bar(kBFull + e % NE), head * static_cast<int>((kv ? p.v_s1 : p.k_s1) / 2) + h * G::ED + cb * 64,
-                              r[0], r[1], r[2], r[3]);
-                }
-                __syncwarp();
+                mbar_arrive(fb);
               } else {
                 slot_wait(e);
-                if (!PROMPT && kv == 0 && h == 0 && lane == 0) {
-                  maskw[4 * (gm % kMaskRing) + lw] = ok_mask;
-                  mbar_arrive(bar(kBMask + gm % kMaskRing));
-                }
-                const uint32_t d0 = smem_u32(ent);
+#pragma unroll 1
+                for (int u = 0; u < NS; ++u) {
+                  const int key0 = 32 * (lw * NS + u);  // first key of the group in the tile
+                  const long long my_loc = loc[u];
+                  const unsigned my_ok = ok_mask[u];
+                  publish_mask(u);
+                  if (PROMPT && p.tma && (kv == 0 || j < j_edge)) {
+                    // keys past the sequence may come along: their scores are
+                    // masked, and V tiles that hold any take the next branch
+                    if (lane == 0) {
+                      const uint32_t d0 = smem_u32(ent) + key0 * 128;
+                      mbar_arrive_warp_tx(fb, 32 * G::ED * 2);
+#pragma unroll
+                      for (int cb = 0; cb < G::ED / 64; ++cb)
+                        tma_load_box(d0 + cb * (KT * 128), kv ? &vmap : &kmap, fb, h * G::ED + cb * 64, head,
+                                     static_cast<int>(row0) + j * KT + key0);
+                    }
+                    __syncwarp();
+                  } else if (PROMPT && kv == 1 && j >= j_edge) {
+                    // V on the diagonal: values that are not finite become 0 here
+                    // and are added by the epilogue to the rows that see them
+                    bool bad = false;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < NP; i0 += 8) {
+                      uint4 x[8];
+#pragma unroll
+                      for (int i = 0; i < 8; ++i) {
+                        const int kl = (i0 + i) * RPP + rr;
+                        const long long lc = __shfl_sync(0xffffffffu, my_loc, kl);
+                        x[i] = ((my_ok >> kl) & 1u)
+                                   ? __ldg(reinterpret_cast<const uint4*>(base + lc * s0 + h * G::ED * 2 + cc * 16))
+                                   : make_uint4(0u, 0u, 0u, 0u);
+                      }
+#pragma unroll
+                      for (int i = 0; i < 8; ++i) {
+                        const int key = key0 + (i0 + i) * RPP + rr;
+                        x[i].x = finite_bf16x2(x[i].x, bad);
+                        x[i].y = finite_bf16x2(x[i].y, bad);
+                        x[i].z = finite_bf16x2(x[i].z, bad);
+                        x[i].w = finite_bf16x2(x[i].w, bad);
+                        *reinterpret_cast<uint4*>(ent + dst_off(key, cc)) = x[i];
+                      }
+                    }
+                    if (bad) *const_cast<volatile int*>(&work[it & 1].bad_v) = 1;
+                    fence_proxy_async();
+                    mbar_arrive(fb);
+                  } else if (MODE == kSharedBf16 && p.tma && my_ok == 0xFFFFFFFFu) {
+                    // 8 groups of 4 rows x ED / 64 column blocks, one gather a lane
+                    constexpr int NB = G::ED / 64;
+                    int r[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                      r[i] = __shfl_sync(0xffffffffu, static_cast<int>(my_loc), (4 * (lane / NB) + i) & 31);
+                    if (lane == 0) mbar_arrive_warp_tx(fb, 32 * G::ED * 2);
+                    __syncwarp();
+                    if (lane < 8 * NB) {
+                      const int grp = lane / NB, cb = lane % NB;
+                      tma_gather4(smem_u32(ent) + cb * (KT * 128) + (key0 + 4 * grp) * 128, kv ? &vmap : &kmap, fb,
+                                  head * static_cast<int>((kv ? p.v_s1 : p.k_s1) / 2) + h * G::ED + cb * 64, r[0], r[1],
+                                  r[2], r[3]);
+                    }
+                    __syncwarp();
+                  } else {
+                    const uint32_t d0 = smem_u32(ent);
 #pragma unroll 4
-                for (int i = 0; i < NP; ++i) {
-                  const int kl = i * RPP + rr;
-                  const long long lc = __shfl_sync(0xffffffffu, loc, kl);
-                  const bool ok = (ok_mask >> kl) & 1u;
-                  const unsigned char* src = ok ? base + lc * s0 + h * G::ED * 2 + cc * 16 : base;
-                  cp_async_16z(d0 + dst_off(32 * lw + kl, cc), src, ok);
+                    for (int i = 0; i < NP; ++i) {
+                      const int kl = i * RPP + rr;
+                      const long long lc = __shfl_sync(0xffffffffu, my_loc, kl);
+                      const bool ok = (my_ok >> kl) & 1u;
+                      const unsigned char* src = ok ? base + lc * s0 + h * G::ED * 2 + cc * 16 : base;
+                      cp_async_16z(d0 + dst_off(key0 + kl, cc), src, ok);
+                    }
+                    cp_async_arrive_noinc(fb);
+                  }
                 }
-                cp_async_arrive_noinc(bar(kBFull + e % NE));
               }
             }
           }
@@ -996,8 +1056,11 @@ __global__ void __launch_bounds__(fa::kThreads, 1) fa_kernel(const __grid_consta
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
+  // the own prefixes' stream, of which this launch may be a programmatic
+  // dependent (it reads nothing of it), is complete before this grid is
+  if (!PROMPT && tid == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   // the last CTA leaves the counters at zero for the next call
-  if (tid == 0) {
+  if (PROMPT && tid == 0) {
     __threadfence();
     if (atomicAdd(p.sched + 1, 1) == static_cast<int>(gridDim.x) - 1) {
       p.sched[0] = 0;

@@ -1,5 +1,5 @@
 // The last launch of verify_splitkv_shared_fwd: joins, for every draft row,
-// the partial softmaxes over the shared prefix (fa_kernel, one per key range),
+// the partial softmaxes over the shared prefix (fa_kernel, one per piece),
 // those over the sequence's own prefix (the stream-only kernel, one per piece)
 // and the causal draft block.
 //
@@ -19,8 +19,8 @@ namespace vsk {
 struct ScParams {
   Params v;             // the flat call; its piece cut when has_own
   int has_own;          // the stream-only kernel ran
-  int n_split, n_live;  // key ranges per row block, those that hold keys
-  int h_kv, tpb, nq;    // row blocks of fa_kernel: tokens per query tile, tiles per block
+  long long tiles, share;  // key tiles of the shared prefix (0: none), of one CTA of fa_kernel
+  int h_kv, tpb, nq;       // row blocks of fa_kernel: tokens per query tile, tiles per block
   const float* splse;
   const float* spo;
 };
@@ -84,15 +84,17 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const __grid_consta
   };
   const int col = 32 * ch + 4 * fch;
 
-  // ---- the shared prefix ----
-  {
+  // ---- the shared prefix: the pieces that fa_kernel's CTAs left of this row's block ----
+  if (s.tiles > 0) {
     const long long tok = s_b + i;
     const int bt = s.nq * s.tpb;
     const long long blk = tok / bt;
     const int rem = static_cast<int>(tok - blk * bt);
     const int in_block = (rem / s.tpb) * 128 + (rem % s.tpb) * p.gq + rr % p.gq;
-    const long long r0 = (blk * s.h_kv + kvh) * s.n_split * (128LL * s.nq) + in_block;
-    fold_all(s.n_live, s.splse + r0, s.spo + r0 * D + col, 128 * s.nq);
+    const long long u = blk * s.h_kv + kvh;
+    const long long c0 = u * s.tiles / s.share, c1 = ((u + 1) * s.tiles - 1) / s.share;
+    const long long r0 = (c0 + u) * (128LL * s.nq) + in_block;
+    fold_all(static_cast<int>(c1 - c0 + 1), s.splse + r0, s.spo + r0 * D + col, 128 * s.nq);
   }
 
   // ---- the sequence's own prefix: its pieces, cut as the stream cut them ----

@@ -1050,6 +1050,8 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
     }
     __syncwarp();
   }
+  // the kernel that joins the partials may start its CTAs where SMs are free
+  if (!PROMPT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {

@@ -9,8 +9,9 @@
 //
 // One CTA per (sequence, KV head, 16-row tile, 32 output columns): thread t
 // owns row t / 8 of the tile and four columns.  The eight threads of a row
-// share its draft scores (an eighth of the head dimension each).  The
-// partials come from L2, where the launches before this one left them.
+// share its draft scores (an eighth of the head dimension each).  The drafts
+// come first: this kernel is a programmatic dependent of the launch before it,
+// and they need nothing of it.  The partials then come from L2.
 #pragma once
 #include "flash_tc.cuh"
 
@@ -74,8 +75,8 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const __grid_consta
         x[k] = NEG_INF;
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k0 + k < n) {
-          x[k] = __ldg(lse + (k0 + k) * step);
-          v[k] = __ldg(reinterpret_cast<const float4*>(o + (k0 + k) * step * D));
+          x[k] = __ldcg(lse + (k0 + k) * step);
+          v[k] = __ldcg(reinterpret_cast<const float4*>(o + (k0 + k) * step * D));
         }
       }
 #pragma unroll
@@ -84,20 +85,9 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const __grid_consta
   };
   const int col = 32 * ch + 4 * fch;
 
-  // ---- the shared prefix: the pieces that fa_kernel's CTAs left of this row's block ----
-  if (s.tiles > 0) {
-    const long long tok = s_b + i;
-    const int bt = s.nq * s.tpb;
-    const long long blk = tok / bt;
-    const int rem = static_cast<int>(tok - blk * bt);
-    const int in_block = (rem / s.tpb) * 128 + (rem % s.tpb) * p.gq + rr % p.gq;
-    const long long u = blk * s.h_kv + kvh;
-    const long long c0 = u * s.tiles / s.share, c1 = ((u + 1) * s.tiles - 1) / s.share;
-    const long long r0 = (c0 + u) * (128LL * s.nq) + in_block;
-    fold_all(static_cast<int>(c1 - c0 + 1), s.splse + r0, s.spo + r0 * D + col, 128 * s.nq);
-  }
-
-  // ---- the sequence's own prefix: its pieces, cut as the stream cut them ----
+  // ---- where the pieces of the sequence's own prefix lie, cut as the stream cut them ----
+  long long own_at = 0;
+  int own_n = 0;
   if (s.has_own) {
     long long tot = 0, bef = 0;
     for (int bb = tid; bb < p.B; bb += 128) {
@@ -129,36 +119,69 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const __grid_consta
     const long long c0 = off / W, c1 = (off + len - 1) / W;
     const long long slot0 = c0 + static_cast<long long>(b) * p.n_hg + hg;
     const int RM = 16 * p.MT;
-    const long long at = (slot0 * p.HC + hc) * RM + rr;
-    fold_all(static_cast<int>(c1 - c0 + 1), p.plse + at, p.po + at * D + col, static_cast<long long>(p.HC) * RM);
+    own_at = (slot0 * p.HC + hc) * RM + rr;
+    own_n = static_cast<int>(c1 - c0 + 1);
   }
 
-  // ---- the drafts up to this row's own ----
+  // ---- the drafts up to this row's own, four at a time ----
   {
     constexpr int DE = D / 8;  // head dimensions of one thread's part of a score
     const __nv_bfloat16* qr = p.q + (s_b + i) * p.q_s0 + static_cast<long long>(head) * p.q_s1 + fch * DE;
-    float2 qv[DE / 2];
+    const __nv_bfloat16* kr0 = p.ke + s_b * p.ke_s0 + static_cast<long long>(kvh) * p.ke_s1 + fch * DE;
+    const __nv_bfloat16* vr0 = p.ve + s_b * p.ve_s0 + static_cast<long long>(kvh) * p.ve_s1 + col;
+    uint32_t qv[DE / 2];
 #pragma unroll
-    for (int u = 0; u < DE / 2; ++u) qv[u] = unpack_bf16(ld_u32(qr + 2 * u));
+    for (int u = 0; u < DE / 2; ++u) qv[u] = ld_u32(qr + 2 * u);
     const int last = __reduce_max_sync(0xffffffffu, i);
-    for (int t = 0; t <= last; ++t) {
-      const __nv_bfloat16* kr = p.ke + (s_b + t) * p.ke_s0 + static_cast<long long>(kvh) * p.ke_s1 + fch * DE;
-      float x = 0.f;
+    for (int t0 = 0; t0 <= last; t0 += 4) {
+      float x[4];
+      uint32_t vv[4][2];
 #pragma unroll
-      for (int u = 0; u < DE / 2; ++u) {
-        const float2 kv = unpack_bf16(ld_u32(kr + 2 * u));
-        x = fmaf(qv[u].x, kv.x, fmaf(qv[u].y, kv.y, x));
+      for (int k = 0; k < 4; ++k) {
+        x[k] = 0.f;
+        vv[k][0] = vv[k][1] = 0u;
+        const int t = min(t0 + k, last);
+        const __nv_bfloat16* kr = kr0 + t * p.ke_s0;
+#pragma unroll
+        for (int u = 0; u < DE / 2; ++u) {
+          const float2 qf = unpack_bf16(qv[u]), kf = unpack_bf16(ld_u32(kr + 2 * u));
+          x[k] = fmaf(qf.x, kf.x, fmaf(qf.y, kf.y, x[k]));
+        }
+        if (t0 + k <= i) {
+          vv[k][0] = ld_u32(vr0 + t * p.ve_s0);
+          vv[k][1] = ld_u32(vr0 + t * p.ve_s0 + 2);
+        }
       }
-      x += __shfl_xor_sync(0xffffffffu, x, 1);
-      x += __shfl_xor_sync(0xffffffffu, x, 2);
-      x += __shfl_xor_sync(0xffffffffu, x, 4);
-      if (t <= i) {
-        const __nv_bfloat16* vr = p.ve + (s_b + t) * p.ve_s0 + static_cast<long long>(kvh) * p.ve_s1 + col;
-        const float2 v0 = unpack_bf16(ld_u32(vr)), v1 = unpack_bf16(ld_u32(vr + 2));
-        fold(x * p.dscale2, make_float4(v0.x, v0.y, v1.x, v1.y));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[k] += __shfl_xor_sync(0xffffffffu, x[k], 1);
+        x[k] += __shfl_xor_sync(0xffffffffu, x[k], 2);
+        x[k] += __shfl_xor_sync(0xffffffffu, x[k], 4);
+        if (t0 + k <= i) {
+          const float2 v0 = unpack_bf16(vv[k][0]), v1 = unpack_bf16(vv[k][1]);
+          fold(x[k] * p.dscale2, make_float4(v0.x, v0.y, v1.x, v1.y));
+        }
       }
     }
   }
+
+  // Everything above reads the call's inputs only; the partials are complete
+  // once the launches before this one are (fa_kernel completes after the stream).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // ---- the shared prefix: the pieces that fa_kernel's CTAs left of this row's block ----
+  if (s.tiles > 0) {
+    const long long tok = s_b + i;
+    const int bt = s.nq * s.tpb;
+    const long long blk = tok / bt;
+    const int rem = static_cast<int>(tok - blk * bt);
+    const int in_block = (rem / s.tpb) * 128 + (rem % s.tpb) * p.gq + rr % p.gq;
+    const long long u = blk * s.h_kv + kvh;
+    const long long c0 = u * s.tiles / s.share, c1 = ((u + 1) * s.tiles - 1) / s.share;
+    const long long r0 = (c0 + u) * (128LL * s.nq) + in_block;
+    fold_all(static_cast<int>(c1 - c0 + 1), s.splse + r0, s.spo + r0 * D + col, 128 * s.nq);
+  }
+
+  if (s.has_own) fold_all(own_n, p.plse + own_at, p.po + own_at * D + col, static_cast<long long>(p.HC) * 16 * p.MT);
   if (live) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
     __nv_bfloat16* op = p.o + (s_b + i) * p.o_s0 + static_cast<long long>(head) * p.o_s1 + col;

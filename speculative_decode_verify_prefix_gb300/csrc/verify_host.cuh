@@ -52,6 +52,7 @@ struct StreamOnly {
   KernelFn fn;
   int threads;
   size_t smem;
+  bool rows_m;  // the rows-on-M tensor-memory stream
   long long n_cta, w_min;
   WsLayout wl;
 };

@@ -1066,7 +1066,7 @@ int plan_stream_only(const CallShape& cs, StreamOnly& so) {
   if (sms <= 0) return fail("cannot query the SM count of device %d", dev);
   // the rows-on-M tensor-memory stream where the verify call takes it, else
   // the stream-only mma.sync kernel; both leave the same partials
-  const bool rows_m = cs.D == cs.DV && g_tc != 1 && tc_eligible(cs.h_q, cs.h_kv, cs.D, cs.L, tokens, cs.fp8);
+  const bool rows_m = so.rows_m = cs.D == cs.DV && g_tc != 1 && tc_eligible(cs.h_q, cs.h_kv, cs.D, cs.L, tokens, cs.fp8);
   int per_sm = 1;
   if (rows_m) {
     if (!make_tc_plan(cs.h_q, cs.h_kv, cs.D, cs.L, cs.fp8, so.pl)) return 0;

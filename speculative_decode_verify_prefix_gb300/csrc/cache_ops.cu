@@ -472,6 +472,7 @@ int verify_splitkv_mass(const vsk_tensor* q, const vsk_tensor* ke, const vsk_ten
   }
   if (kb->shape[0] >= 0xFFFFFFFFLL) return fail("a pool of %lld rows is too large", static_cast<long long>(kb->shape[0]));
   if (T == 0) return 1;
+  if (kb->shape[0] == 0) return fail("k_buffer has no rows");
   km::MassParams m;
   memset(&m, 0, sizeof m);
   m.h_kv = static_cast<int>(cs.h_kv);

@@ -19,8 +19,8 @@
 // g's elements at four positions of every 16-wide k step, and which positions
 // those are is free as long as the queries use the same ones, so the lane
 // takes 16 consecutive bytes (4 lanes: 64 bytes of a row) and no shuffle,
-// ldmatrix or staging buffer is needed.  The next group's loads are in flight
-// while one is multiplied.  e4m3 keys are widened to f16 (exact) and meet
+// ldmatrix or staging buffer is needed.  The loads of the next two or three
+// stages are in flight while one is multiplied.  e4m3 keys are widened to f16 (exact) and meet
 // queries scaled by a power of two so that the largest lies in [2^14, 2^15)
 // (elements more than 2^29 smaller than it lose bits).
 //
@@ -49,13 +49,16 @@ struct MassParams {
 };
 using MassFn = void (*)(const MassParams);
 
-// 8-key groups of a stage, 16-byte loads of a lane per key row
+// 8-key groups of a stage, 16-byte loads of a lane per key row, stages in flight.
+// A stage takes 16 registers a lane (32 at 512-byte rows); DEPTH - 1 of them are
+// loading while one is multiplied.
 template <int D, bool FP8>
 struct Geo {
   static constexpr int ROWB = D * (FP8 ? 1 : 2);
   static constexpr int NL = ROWB / 64;                      // loads per key row
-  static constexpr int NB = NL >= 8 ? 1 : NL == 4 ? 2 : 4;  // groups per stage
+  static constexpr int NB = NL >= 4 ? 1 : 4 / NL;           // groups per stage
   static constexpr int KEYS = 8 * NB;
+  static constexpr int DEPTH = 2;
   static constexpr int KS = D / 16;                         // k steps
   static constexpr int QCH = D / 8;                         // 16-byte chunks of a query row in shared memory
 };
@@ -234,6 +237,8 @@ __global__ void __launch_bounds__(km::kThreads, 2) mass_kernel(const __grid_cons
     unsigned ok;  // bit n: key g of group n is in the chunk and its index in the pool
   };
   unsigned* idx = reinterpret_cast<unsigned*>(smem + mp.i_off);  // pool rows of the chunk's keys, kNoRow: none
+  // (a key without a row loads row 0, and its scores become -inf: a load under a
+  // condition would be waited for where the two cases meet)
   auto load_k = [&](int at, Stage& s) {
     s.ok = 0u;
 #pragma unroll
@@ -243,16 +248,18 @@ __global__ void __launch_bounds__(km::kThreads, 2) mass_kernel(const __grid_cons
       s.ok |= ok ? 1u << n : 0u;
       const unsigned char* src = kbase + static_cast<long long>(ok ? loc : 0u) * p.kb_s0 + 16 * j4;
 #pragma unroll
-      for (int i = 0; i < G::NL; ++i) s.k[n][i] = ok ? ld_row<G::ROWB>(src + 64 * i) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < G::NL; ++i) s.k[n][i] = ld_row<G::ROWB>(src + 64 * i);
     }
   };
   // scores of one stage into sc[row][key of the chunk]
   auto multiply = [&](const Stage& s, int at0) {
 #pragma unroll 1
     for (int mt = 0; mt < (QREG ? 1 : mp.MT); ++mt) {
-      float acc[G::NB][4];
+      // (two chains of products where the stage is one group)
+      constexpr int NC = G::NB == 1 ? 2 : 1;
+      float acc[G::NB * NC][4];
 #pragma unroll
-      for (int n = 0; n < G::NB; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+      for (int n = 0; n < G::NB * NC; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < G::KS; ++ks) {
         uint32_t a[4];
@@ -267,13 +274,17 @@ __global__ void __launch_bounds__(km::kThreads, 2) mass_kernel(const __grid_cons
           if constexpr (FP8) {
             const uint4& w = s.k[n][ks >> 2];
             const uint32_t x = (ks & 3) == 0 ? w.x : (ks & 3) == 1 ? w.y : (ks & 3) == 2 ? w.z : w.w;
-            mma_f16(acc[n], a, e4m3x2_to_f16x2(static_cast<unsigned short>(x & 0xFFFFu)),
+            mma_f16(acc[n * NC + ks % NC], a, e4m3x2_to_f16x2(static_cast<unsigned short>(x & 0xFFFFu)),
                     e4m3x2_to_f16x2(static_cast<unsigned short>(x >> 16)));
           } else {
             const uint4& w = s.k[n][ks >> 1];
-            mma_bf16(acc[n], a, (ks & 1) ? w.z : w.x, (ks & 1) ? w.w : w.y);
+            mma_bf16(acc[n * NC + ks % NC], a, (ks & 1) ? w.z : w.x, (ks & 1) ? w.w : w.y);
           }
         }
+      }
+      if constexpr (NC == 2) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[0][u] += acc[1][u];
       }
 #pragma unroll
       for (int n = 0; n < G::NB; ++n) {
@@ -291,8 +302,7 @@ __global__ void __launch_bounds__(km::kThreads, 2) mass_kernel(const __grid_cons
       }
     }
   };
-  // scores of the chunk of n keys at c0: stages dealt to the warps in turn, one
-  // loading while the other is multiplied
+  // scores of the chunk of n keys at c0: stages dealt to the warps in turn
   auto chunk = [&](int c0, int n) {
     constexpr int STEP = kWarps * G::KEYS;
     const int end = (n + G::KEYS - 1) / G::KEYS * G::KEYS;
@@ -312,18 +322,20 @@ __global__ void __launch_bounds__(km::kThreads, 2) mass_kernel(const __grid_cons
     __syncthreads();
     int at = warp * G::KEYS;
     if (at < end) {
-      Stage s0, s1;
-      load_k(at, s0);
+      Stage s[G::DEPTH];
+#pragma unroll
+      for (int u = 0; u < G::DEPTH - 1; ++u)
+        if (at + u * STEP < end) load_k(at + u * STEP, s[u]);
 #pragma unroll 1
-      while (true) {
-        if (at + STEP < end) load_k(at + STEP, s1);
-        multiply(s0, at);
-        at += STEP;
-        if (at >= end) break;
-        if (at + STEP < end) load_k(at + STEP, s0);
-        multiply(s1, at);
-        at += STEP;
-        if (at >= end) break;
+      while (at < end) {
+#pragma unroll
+        for (int u = 0; u < G::DEPTH; ++u) {
+          if (at < end) {
+            if (at + (G::DEPTH - 1) * STEP < end) load_k(at + (G::DEPTH - 1) * STEP, s[(u + G::DEPTH - 1) % G::DEPTH]);
+            multiply(s[u], at);
+            at += STEP;
+          }
+        }
       }
     }
     __syncthreads();

@@ -10,6 +10,7 @@ raises ValueError with its message and launches nothing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
@@ -18,36 +19,54 @@ from . import _native
 from .api import _DT, _WS, _WS_LOCK, _coerce
 
 # A vsk_tensor: data, dtype, ndim, shape[3], stride[3].  The views of a call are
-# packed into one buffer: about a third of the time of filling a ctypes
-# structure per tensor (a call of ten tensors 57 -> 24 us on the host).
+# packed into one buffer: a fraction of the time of filling a ctypes structure
+# per tensor.
 _VIEW = struct.Struct("Pii6q")
 assert _VIEW.size == ctypes.sizeof(_native.VskTensor)
 
 
-def _views(device, named):
+_ARENA = {n: ctypes.c_char * (_VIEW.size * n) for n in range(1, 16)}
+_pack, _SIZE, _code = _VIEW.pack_into, _VIEW.size, _DT.get
+
+
+def _views(names, tensors):
     """The packed views of a call's tensors (None stays None) and their
     addresses; all tensors must be on one CUDA device, which is returned."""
-    buf = (ctypes.c_char * (_VIEW.size * len(named)))()
-    at, args, off = ctypes.addressof(buf), [], 0
-    for name, t in named:
+    buf = _ARENA[len(tensors)]()
+    at = ctypes.addressof(buf)
+    device, args, off = -1, [], 0
+    for t in tensors:
         if t is None:
             args.append(None)
             continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        dev = t.get_device()
-        if device is None:
+        try:
+            dev, shape, stride = t.get_device(), t.shape, t.stride()
+        except AttributeError:
+            dev = -1
+        if dev != device:
+            name = names[len(args)]
+            if dev < 0:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if device >= 0:
+                raise ValueError(f"{name} is on cuda:{dev}, the call's other tensors on cuda:{device}")
             device = dev
-        elif dev != device:
-            raise ValueError(f"{name} is on cuda:{dev}, the call's other tensors on cuda:{device}")
-        shape, stride = t.shape, t.stride()
         n = len(shape)
-        if n < 3:
-            shape, stride = (*shape, 0, 0, 0)[:3], (*stride, 0, 0, 0)[:3]
-        _VIEW.pack_into(buf, off, t.data_ptr() if t.numel() else 0, _DT.get(t.dtype, -1), n, *shape[:3], *stride[:3])
+        if n == 3:
+            _pack(buf, off, t.data_ptr(), _code(t.dtype, -1), 3, *shape, *stride)
+        elif n == 1:
+            _pack(buf, off, t.data_ptr(), _code(t.dtype, -1), 1, shape[0], 0, 0, stride[0], 0, 0)
+        else:
+            _pack(buf, off, t.data_ptr(), _code(t.dtype, -1), n, *(*shape, 0, 0, 0)[:3], *(*stride, 0, 0, 0)[:3])
         args.append(at + off)
-        off += _VIEW.size
+        off += _SIZE
+    if device < 0:
+        raise ValueError(f"{names[0]} must be a CUDA tensor")
     return device, buf, args
+
+
+@functools.lru_cache(maxsize=None)
+def _device(index):
+    return torch.device("cuda", index)
 
 
 def _workspace_of(device, stream, raw_stream, need):
@@ -61,7 +80,7 @@ def _workspace_of(device, stream, raw_stream, need):
             capturing = torch.cuda.is_current_stream_capturing()
     if capturing:
         raise ValueError("pass workspace= to a call that is captured into a graph")
-    key = (torch.device("cuda", device), raw_stream)
+    key = (_device(device), raw_stream)
     ws = _WS.get(key)
     if ws is None or ws.numel() < need:
         with torch.cuda.stream(stream), _WS_LOCK:  # zeroed in the order of the stream that uses it
@@ -72,25 +91,22 @@ def _workspace_of(device, stream, raw_stream, need):
     return ws
 
 
-def _run(name, named, scalars, stream, workspace, need=None) -> None:
-    """Calls a library entry point: the tensors' views, the scalars, then
-    workspace, its bytes and the stream, with the tensors' device current.
-    ``named``: (name, tensor) in the order of the C arguments, a scalar in
-    between as (None, value).  ``need``: workspace bytes (None: the error word)."""
-    device, buf, args = _views(None, [x for x in named if x[0] is not None])
-    if any(x[0] is None for x in named):
-        it = iter(args)
-        args = [next(it) if n is not None else v for n, v in named]
+def _run(name, names, tensors, scalars, stream, workspace, need=None, scalars_at=None) -> None:
+    """Calls a library entry point: the tensors' views, the scalars (after
+    ``scalars_at`` tensors; None: after all), then workspace, its bytes and the
+    stream, with the tensors' device current.  ``need``: workspace bytes (None:
+    the error word)."""
+    device, buf, args = _views(names, tensors)
     if device != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return _run(name, named, scalars, stream, workspace, need)
+            return _run(name, names, tensors, scalars, stream, workspace, need, scalars_at)
     raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
     if workspace is None:
         workspace = _workspace_of(device, stream, raw, 256 if need is None else need())
     elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
-    if not getattr(_native.lib(), name)(*args, *scalars, workspace.data_ptr(),
-                                        workspace.numel() * workspace.element_size(), raw):
+    k = len(args) if scalars_at is None else scalars_at
+    if not getattr(_native.lib(), name)(*args[:k], *scalars, *args[k:], workspace.data_ptr(), workspace.nbytes, raw):
         raise ValueError(f"{name}: {_native.last_error()}")
 
 
@@ -102,7 +118,7 @@ def prompt_attn_fwd(q, k, v, o, qo_indptr, sm_scale=None, workspace=None, stream
     qo_indptr[b] .. qo_indptr[b+1] - 1, of any lengths.  Row i of a sequence
     attends to its rows t <= i.  Rows of ``o`` outside every sequence are left
     as they were.  ``workspace``: 256 bytes or more (the error word)."""
-    _run("prompt_attn_fwd", (("q", q), ("k", k), ("v", v), ("o", o), ("qo_indptr", qo_indptr)),
+    _run("prompt_attn_fwd", ("q", "k", "v", "o", "qo_indptr"), (q, k, v, o, qo_indptr),
          (0.0 if sm_scale is None else float(sm_scale),), stream, workspace)
 
 
@@ -136,9 +152,10 @@ def verify_splitkv_shared_fwd(q_extend, k_extend, v_extend, o_extend, k_buffer, 
         return n
 
     _run("verify_splitkv_shared_fwd",
-         (("q_extend", q_extend), ("k_extend", k_extend), ("v_extend", v_extend), ("o_extend", o_extend),
-          ("k_buffer", k_buffer), ("v_buffer", v_buffer), ("qo_indptr", qo_indptr), ("kv_indptr", kv_indptr),
-          ("kv_indices", kv_indices), ("shared_indices", shared_indices)),
+         ("q_extend", "k_extend", "v_extend", "o_extend", "k_buffer", "v_buffer", "qo_indptr", "kv_indptr",
+          "kv_indices", "shared_indices"),
+         (q_extend, k_extend, v_extend, o_extend, k_buffer, v_buffer, qo_indptr, kv_indptr, kv_indices,
+          shared_indices),
          (mle, _coerce(k_scale), _coerce(v_scale), 0.0 if sm_scale is None else float(sm_scale)), stream, workspace,
          need)
 
@@ -151,8 +168,8 @@ def verify_splitkv_mass(q_extend, k_extend, k_buffer, qo_indptr, kv_indptr, kv_i
     query heads of the KV head of the softmax weight its key has in
     ``verify_splitkv_fwd`` (causal drafts)."""
     _run("verify_splitkv_mass",
-         (("q_extend", q_extend), ("k_extend", k_extend), ("k_buffer", k_buffer), ("qo_indptr", qo_indptr),
-          ("kv_indptr", kv_indptr), ("kv_indices", kv_indices), ("mass_in", mass_in), ("mass", mass)),
+         ("q_extend", "k_extend", "k_buffer", "qo_indptr", "kv_indptr", "kv_indices", "mass_in", "mass"),
+         (q_extend, k_extend, k_buffer, qo_indptr, kv_indptr, kv_indices, mass_in, mass),
          (int(max_len_extend), _coerce(k_scale), 0.0 if sm_scale is None else float(sm_scale)), stream, workspace)
 
 
@@ -167,6 +184,6 @@ def kv_evict(mass, kv_indptr, kv_indices, budget, recent, out_kv_indptr, out_kv_
     budget) columns always suffice) and the others, whose pool rows may be
     reused, to ``freed`` (out_kv_indptr and kv_indptr tell how many)."""
     _run("kv_evict",
-         (("mass", mass), ("kv_indptr", kv_indptr), ("kv_indices", kv_indices), (None, int(budget)),
-          (None, int(recent)), ("out_kv_indptr", out_kv_indptr), ("out_kv_indices", out_kv_indices),
-          ("out_mass", out_mass), ("freed", freed)), (), stream, workspace)
+         ("mass", "kv_indptr", "kv_indices", "out_kv_indptr", "out_kv_indices", "out_mass", "freed"),
+         (mass, kv_indptr, kv_indices, out_kv_indptr, out_kv_indices, out_mass, freed), (int(budget), int(recent)),
+         stream, workspace, scalars_at=3)

@@ -8,6 +8,7 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <set>
 #include <tuple>
 
 #include <cudaTypedefs.h>
@@ -87,8 +88,17 @@ static int launch_fa(const fa::FaParams& p, const CUtensorMap* maps, int D, int 
   if (e != cudaSuccess) return fail("cudaGetDevice: %s", cudaGetErrorString(e));
   const int sms = device_sms(dev);
   if (sms <= 0) return fail("cannot query the SM count of device %d", dev);
-  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize, fa_smem(D));
-  if (e != cudaSuccess) return fail("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  {
+    static std::mutex mu;
+    static std::set<std::pair<int, const void*>> done;  // (device, kernel) whose attribute is set
+    std::lock_guard<std::mutex> lk(mu);
+    const std::pair<int, const void*> key{dev, reinterpret_cast<const void*>(fn)};
+    if (!done.count(key)) {
+      e = cudaFuncSetAttribute(key.second, cudaFuncAttributeMaxDynamicSharedMemorySize, fa_smem(D));
+      if (e != cudaSuccess) return fail("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      done.insert(key);
+    }
+  }
   fa::FaParams a = p;
   a.n_items = static_cast<int>(n_items);
   a.err = static_cast<unsigned*>(ws);

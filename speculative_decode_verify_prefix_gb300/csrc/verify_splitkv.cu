@@ -11,8 +11,10 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <map>
 #include <mutex>
 #include <string>
+#include <tuple>
 #include <vector>
 
 #include "../../include/verify_splitkv.h"
@@ -1085,9 +1087,23 @@ int plan_stream_only(const CallShape& cs, StreamOnly& so) {
     so.threads = so.pl.threads;
     per_sm = so.pl.ctas_per_sm;
   }
-  if (!so.fn || !prepare_kernel(so.fn)) return fail("stream kernel for head_dim %lld unavailable", cs.D);
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, reinterpret_cast<const void*>(so.fn), so.threads, so.smem);
-  if (e != cudaSuccess || occ < 1) return fail("kernel does not fit an SM (%s)", cudaGetErrorString(e));
+  if (!so.fn) return fail("stream kernel for head_dim %lld unavailable", cs.D);
+  {
+    // CTAs per SM, asked from the runtime once per device and shape
+    static std::mutex mu;
+    static std::map<std::tuple<int, KernelFn, int, size_t>, int> known;
+    std::lock_guard<std::mutex> lk(mu);
+    int& n = known[{dev, so.fn, so.threads, so.smem}];
+    if (n == 0) {
+      if (!prepare_kernel(so.fn)) return fail("stream kernel for head_dim %lld unavailable", cs.D);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, reinterpret_cast<const void*>(so.fn), so.threads, so.smem);
+      if (e != cudaSuccess || n < 1) {
+        n = 0;
+        return fail("kernel does not fit an SM (%s)", cudaGetErrorString(e));
+      }
+    }
+    occ = n;
+  }
   so.n_cta = g_num_ctas > 0 ? g_num_ctas : static_cast<long long>(sms) * std::min(occ, per_sm);
   so.wl = ws_layout(so.n_cta, cs.B, so.pl, cs.DV);
   const long long per = rows_m ? kPiecesPerSegment : kPiecesPerSegmentColSplit;

@@ -217,7 +217,7 @@ static int cluster_fit(const void* fn, int c, int threads, size_t smem) {
   cfg.dynamicSmemBytes = smem;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  for (; c >= 1; c /= 2) {
+  for (; c >= 1; c = c > 8 ? 8 : c / 2) {
     at[0].val.clusterDim.x = static_cast<unsigned>(c);
     cfg.gridDim = dim3(static_cast<unsigned>(c));
     int n = 0;
@@ -256,7 +256,19 @@ static int cluster_size(long long mean_len, long long per) {
   while (c < 16 && mean_len > c * per) c *= 2;
   return c;
 }
-constexpr long long kMassKeysPerCta = 256;
+// Key weights: the smallest cluster whose CTAs keep the scores of a mean
+// segment (or nearly: what does not fit is computed again), since a CTA costs
+// some 9 us beside its keys and larger clusters leave more SMs without a place
+// (128 sequences of 8,000 keys: 8 CTAs 760 us, 12 915, 16 1203; the serving
+// batch, mean 21,400: 8 1120, 12 1072, 14 1373, 16 1213); but more, down to 256
+// keys each, while the GPU is not full.
+static int mass_cluster(long long mean_len, long long cap, long long n_seg, int sms) {
+  constexpr int kSizes[] = {1, 2, 4, 6, 8, 12, 16};
+  size_t i = 0;
+  while (kSizes[i] < 16 && 10 * mean_len > 12 * kSizes[i] * cap) ++i;
+  while (kSizes[i] < 16 && n_seg * kSizes[i] < 2LL * sms && mean_len > 256LL * kSizes[i]) ++i;
+  return kSizes[i];
+}
 constexpr long long kEvictKeysPerCta = 8192;
 
 static bool check_rows(const vsk_tensor* t, const char* name, long long rows) {
@@ -510,8 +522,12 @@ int verify_splitkv_mass(const vsk_tensor* q, const vsk_tensor* ke, const vsk_ten
   m.out_s0 = mass->stride[0];
   void* args[] = {&m};
   const size_t smem = m.s_off + static_cast<size_t>(m.pitch) * 4 * rows;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail("no CUDA device");
+  const int sms = device_sms(dev);
+  if (sms <= 0) return fail("cannot query the SM count of device %d", dev);
   const km::MassFn fn = kernel_mass(static_cast<int>(cs.D), cs.fp8, m.MT == 1 && cs.D <= 128);
-  return launch_clusters(reinterpret_cast<const void*>(fn), cluster_size(cs.mean_len, kMassKeysPerCta),
+  return launch_clusters(reinterpret_cast<const void*>(fn), mass_cluster(cs.mean_len, m.cap, cs.B * cs.h_kv, sms),
                          cs.B * cs.h_kv, km::kThreads, smem, args, st);
 }
 

@@ -292,7 +292,8 @@ size_t vsk_shared_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv,
  * the sequence's prefix and its drafts up to i.  A key with a bad index gets
  * weight 0 and sets error bit 1.
  *   mass, mass_in   [h_kv, n] float32, n = kv_indices entries, rows contiguous;
- *                   mass_in NULL counts as zeros and may be mass itself
+ *                   mass_in NULL counts as zeros; it may be mass itself and must
+                   not overlap it otherwise
  *   other arguments and limits as verify_splitkv_fwd (head_dim in {64, 128,
  *                   256}, (h_q/h_kv)*l_ext <= 128, or 64 at 256); workspace as
  *                   prompt_attn_fwd.
@@ -321,7 +322,7 @@ int verify_splitkv_mass(const vsk_tensor* q_extend, const vsk_tensor* k_extend,
  *   freed           of kv_indices' type: the other entries, sequence after
  *                   sequence in their order (n entries always suffice): the
  *                   pool rows that may be reused
- * Outputs must not overlap inputs.  An output that is too short is filled and
+ * Outputs must not overlap inputs (refused) nor each other.  An output that is too short is filled and
  * sets error bit 32.  Inconsistent kv_indptr entries give an empty sequence and
  * set bit 2.  workspace as prompt_attn_fwd.  One launch on `stream`. */
 int kv_evict(const vsk_tensor* mass, const vsk_tensor* kv_indptr, const vsk_tensor* kv_indices,

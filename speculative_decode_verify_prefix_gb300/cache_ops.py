@@ -43,7 +43,7 @@ def _views(names, tensors):
             dev, shape, stride = t.get_device(), t.shape, t.stride()
         except AttributeError:
             dev = -1
-        if dev != device:
+        if dev != device or dev < 0:
             name = names[len(args)]
             if dev < 0:
                 raise ValueError(f"{name} must be a CUDA tensor")

@@ -304,10 +304,11 @@ int prompt_attn_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* 
     return fail("k and v must be [%lld, h_kv, %lld]", N, D);
   if (o->shape[0] != N || o->shape[1] != h_q || o->shape[2] != D) return fail("o must have the shape of q");
   if (h_q / h_kv > 128) return fail("h_q / h_kv = %lld exceeds 128", h_q / h_kv);
-  if (N > INT_MAX) return fail("%lld rows exceed 2^31 - 1", N);
+  if (N > INT_MAX - 1024) return fail("%lld rows are too many (2^31 - 1025 at most)", N);
   if (!rows16(k, 2) || !rows16(v, 2)) return fail("k and v rows must be 16-byte aligned");
   if (!rows4(q) || !rows4(o)) return fail("q and o must be 4-byte aligned with even strides");
   if (!aligned(qo_indptr->data, 4)) return fail("qo_indptr must be 4-byte aligned");
+  if (!std::isfinite(static_cast<float>(softmax_scale(sm_scale, D) * kLog2e))) return fail("sm_scale is too large");
   if (workspace && workspace_bytes < 256) return fail("workspace of %zu bytes is smaller than 256", workspace_bytes);
   if (N == 0) return 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -335,6 +336,10 @@ int prompt_attn_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* 
   p.gq = static_cast<int>(h_q / h_kv);
   p.tpb = 128 / p.gq;
   p.scale2 = static_cast<float>(softmax_scale(sm_scale, D) * kLog2e);
+  if (p.scale2 == 0.f) {  // below the smallest float: all scores alike
+    p.qmode = 2;
+    p.scale2 = 1.f;
+  }
   p.q16 = rows16(q, 2);
   p.o16 = rows16(o, 2);
   p.v_scale = 1.f;
@@ -342,7 +347,7 @@ int prompt_attn_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* 
   const long long blocks = N / (fa_nq(static_cast<int>(D)) * p.tpb) + B;
   CUtensorMap maps[3];
   memset(maps, 0, sizeof maps);
-  p.qtma = rows_map(q, p.tpb, p.gq, &maps[0]);
+  p.qtma = p.qmode == 0 && rows_map(q, p.tpb, p.gq, &maps[0]);
   p.tma = rows_map(k, 32, 1, &maps[1]) && rows_map(v, 32, 1, &maps[2]);
   return launch_fa(p, maps, static_cast<int>(D), fa::kPrompt, blocks * h_kv, ws, false, st);
 }
@@ -372,7 +377,8 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
   if (!check_1d(shi, "shared_indices")) return 0;
   if (shi->dtype != VSK_DTYPE_I32 && shi->dtype != VSK_DTYPE_I64) return fail("shared_indices must be int32 or int64");
   if (!aligned(shi->data, shi->dtype == VSK_DTYPE_I64 ? 8 : 4)) return fail("shared_indices must be aligned to its type");
-  if (cs.B * cs.L > INT_MAX) return fail("%lld rows exceed 2^31 - 1", cs.B * cs.L);
+  if (cs.B * cs.L > INT_MAX - 1024) return fail("%lld rows are too many (2^31 - 1025 at most)", cs.B * cs.L);
+  if (!std::isfinite(p.scale2)) return fail("sm_scale * k_scale is too large");
   const int D = static_cast<int>(cs.D);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -636,6 +636,10 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
       // same number of key tiles, cut where a row block's keys end.
       long long at = static_cast<long long>(blockIdx.x) * p.share;  // shared prefix: next tile of this CTA's share
       int n_piece = 0;
+      // prompts: sequences [0, b_scan) have `before` row blocks, all behind this
+      // CTA's tickets (they only grow)
+      int b_scan = 0;
+      long long before = 0;
 #pragma unroll 1
       for (int it = 0;; ++it) {
         int ticket = static_cast<int>(blockIdx.x);
@@ -652,10 +656,10 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
           if constexpr (PROMPT) {
             x.head = ticket % p.h_kv;
             x.j_first = 0;
-            long long want = ticket / p.h_kv;
             found = false;
-            for (int b0 = 0; b0 < p.B && !found; b0 += 32) {
-              const int b = b0 + lane;
+            while (b_scan < p.B && !found) {
+              const long long want = ticket / p.h_kv - before;
+              const int b = b_scan + lane;
               int a = 0, n = 0;
               if (b < p.B) {
                 a = __ldg(p.qo + b);
@@ -677,7 +681,8 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
                 x.row0 = __shfl_sync(0xffffffffu, a, src);
                 x.tok0 = (__shfl_sync(0xffffffffu, incl, src) - 1 - static_cast<int>(want)) * bt;
               } else {
-                want -= __shfl_sync(0xffffffffu, incl, 31);
+                before += __shfl_sync(0xffffffffu, incl, 31);
+                b_scan += 32;
               }
             }
           } else {

@@ -121,6 +121,37 @@ def test_prompt_strided_rows_and_scale(vsk, d):
     assert bool((big[:, 0] == 0).all()) and bool((big[:, 7] == 0).all())
 
 
+@pytest.mark.parametrize("d", [64, 256])
+def test_prompt_head_major_and_single_head_layouts(vsk, d):
+    lens = (140, 33)
+    g = gen(4)
+    q, k, v = (normal(g, h, sum(lens), d).transpose(0, 1) for h in (4, 2, 2))
+    o = torch.zeros(4, sum(lens), d, dtype=BF16, device=DEV).transpose(0, 1)
+    vsk.prompt_attn_fwd(q, k, v, o, indptr(lens))
+    check_attention(o, *prompt_want(q, k, v, lens, d ** -0.5))
+    # one KV head behind every query head: an expanded view
+    k1, v1 = k[:, :1].expand(-1, 2, -1), v[:, :1].expand(-1, 2, -1)
+    vsk.prompt_attn_fwd(q, k1, v1, o, indptr(lens))
+    check_attention(o, *prompt_want(q, k1, v1, lens, d ** -0.5))
+
+
+def test_prompt_many_sequences_and_a_vanishing_scale(vsk):
+    lens = (3, 0, 1, 2) * 700
+    q, k, v, ptr = prompt_case(lens, 4, 2, 64, seed=6)
+    o = torch.zeros_like(q)
+    vsk.prompt_attn_fwd(q, k, v, o, ptr, sm_scale=1e-45)  # all scores alike: means
+    want, a = prompt_want(q, k, v, lens, 0.0)
+    check_attention(o, want, a)
+    vsk.prompt_attn_fwd(q, k, v, o, ptr)
+    check_attention(o, *prompt_want(q, k, v, lens, 0.125))
+
+
+def test_shared_head_major_pool(vsk):
+    c = shared_case(700, (40, 0, 99), 4, 8, 2, 128, seed=25)
+    c["kb"], c["vb"] = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (c["kb"], c["vb"]))
+    check_attention(run_shared(vsk, c), *shared_want(c, 128 ** -0.5))
+
+
 def test_prompt_rows_of_four_byte_alignment(vsk):
     lens, hq, d = (100, 45), 4, 128
     g = gen(5)

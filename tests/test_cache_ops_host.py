@@ -56,6 +56,11 @@ def test_prompt_refusals(change, msg):
     refused(msg, call("prompt_attn_fwd", [a["q"], a["k"], a["v"], a["o"], a["p"]], 0.0))
 
 
+def test_scales_beyond_a_float_are_refused():
+    refused("too large", call("prompt_attn_fwd", PROMPT.values(), 3.2e38, ws=(None, 0)))
+    refused("too large", call("verify_splitkv_shared_fwd", shared_args(), 4, 100.0, 1.0, 3e38))
+
+
 def test_prompt_workspace_too_small():
     refused("smaller than 256", call("prompt_attn_fwd", PROMPT.values(), 0.0, ws=(256, 255)))
 

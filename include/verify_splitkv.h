@@ -293,7 +293,7 @@ size_t vsk_shared_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv,
  * weight 0 and sets error bit 1.
  *   mass, mass_in   [h_kv, n] float32, n = kv_indices entries, rows contiguous;
  *                   mass_in NULL counts as zeros; it may be mass itself and must
-                   not overlap it otherwise
+ *                   not overlap it otherwise
  *   other arguments and limits as verify_splitkv_fwd (head_dim in {64, 128,
  *                   256}, (h_q/h_kv)*l_ext <= 128, or 64 at 256); workspace as
  *                   prompt_attn_fwd.
@@ -322,9 +322,9 @@ int verify_splitkv_mass(const vsk_tensor* q_extend, const vsk_tensor* k_extend,
  *   freed           of kv_indices' type: the other entries, sequence after
  *                   sequence in their order (n entries always suffice): the
  *                   pool rows that may be reused
- * Outputs must not overlap inputs (refused) nor each other.  An output that is too short is filled and
- * sets error bit 32.  Inconsistent kv_indptr entries give an empty sequence and
- * set bit 2.  workspace as prompt_attn_fwd.  One launch on `stream`. */
+ * Outputs must not overlap inputs (refused) nor each other.  An output that is
+ * too short is filled and sets error bit 32.  Inconsistent kv_indptr entries
+ * give an empty sequence and set bit 2.  workspace as prompt_attn_fwd.  One launch on `stream`. */
 int kv_evict(const vsk_tensor* mass, const vsk_tensor* kv_indptr, const vsk_tensor* kv_indices,
              int64_t budget, int64_t recent, const vsk_tensor* out_kv_indptr,
              const vsk_tensor* out_kv_indices, const vsk_tensor* out_mass,
@@ -354,10 +354,10 @@ int vsk_workspace_init(void* workspace, size_t bytes, void* stream);
  * word holds the flags of the most recent such call there).  Bits: 1 = a kv_indices value outside [0, pool); 2 = kv_indptr
  * not non-decreasing or beyond kv_indices; 4 = qo_indptr inconsistent with
  * l_ext; 8 = a pipeline wait that gave up after one second (only the
- * tensor-memory forms of the stream, selected by vsk_set_tuning_tc(1 or 2), have
- * such waits: the CTA then stops streaming, frees its tensor memory and
- * exits, and that call's output is not valid; the default kernel has no
- * waits that can time out); 16 = a mask_indptr entry of
+ * tensor-memory forms of the stream, see vsk_set_tuning_tc, and of
+ * prompt_attn_fwd and verify_splitkv_shared_fwd have such waits: the CTA then
+ * stops streaming, frees its tensor memory and exits, and that call's output
+ * is not valid; the other kernels have no waits that can time out); 16 = a mask_indptr entry of
  * verify_splitkv_tree_fwd outside custom_mask; 32 = an output of kv_evict too
  * short for what is kept or freed.  Returns 1 on success, 0 on a
  * CUDA error.

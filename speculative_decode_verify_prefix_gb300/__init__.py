@@ -1,4 +1,5 @@
-"""Split-KV verify attention for EAGLE target-verify (topk = 1) on GB300.
+"""Split-KV verify attention for EAGLE target-verify (topk = 1) on GB300,
+with the calls around it: prompts, shared prefixes, eviction from the cache.
 
 The computation runs in the CUDA library built from ``csrc/*.cu``
 (C ABI: ``include/verify_splitkv.h``); this package is its Python binding.

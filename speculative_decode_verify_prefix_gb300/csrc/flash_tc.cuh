@@ -11,7 +11,7 @@
 // exceeds it by more than 8: until then P stays below 2^8, far from any
 // limit of the 32-bit sums, and O in tensor memory need not be touched.
 // Scores, m, l and O are 32-bit; P is rounded to bf16 because both operands of
-// an MMA have one type and V is bf16 (relative error 2^-9, of the order of the
+// an MMA have one type and V is bf16 (relative error 2^-8 at most, that of the
 // output's own rounding; l sums the unrounded P).
 //
 // Rows.  The g = h_q / h_kv query heads of a KV head share its keys, so the
@@ -24,20 +24,35 @@
 // instead.
 //
 // What bounds it: per 128-key tile and query tile 2 MMAs of 128 x 128 x D
-// against 16,384 exponentials; both pipes are busy at once.
+// against 16,384 exponentials; both pipes are busy at once, and each waits for
+// the other at a tile's hand-overs.  Measured: four prompts, 21,716 tokens,
+// 32/8 heads of 128, 674 us = 0.79 of the library matrix product's rate; three
+// documents, 2,296 tokens, 16/2 heads of 256, 40 us (too few items to fill the
+// SMs evenly); a prefix of 32,768 rows shared by 64 sequences of 4 drafts, 32/8
+// of 128, 126 us at 45 % of the tensor pipe (each of the four row blocks of a KV
+// head gathers the rows again, 4.2 TB/s in all).
 //
-// Roles (16 warps; registers redistributed with setmaxnreg):
-//   warps 0-3, 4-7   softmax of query tile 0 / 1 (thread = row; at head_dim 256
-//                    warps 4-7 are idle): scores from tensor memory, P back
-//                    over them (bf16, half the columns), rescale, epilogue
-//   warp 8           issues the MMAs (one elected lane): S = Q K^T (both operands in
-//                    shared memory), O += P V (P in tensor memory)
-//   warp 9           draws the items; the CTAs (one per SM) stay, so that the
-//                    next item's loads run under the end of this one
-//   warps 12-15      bring K / V rows into a ring of 128-key entries (128 head
+// Items.  The CTAs (one per SM) stay, so that the next item's loads run under
+// the end of this one.  Prompts: an item is a block of query tiles over all its
+// keys; items are drawn from a counter, longest first, as their lengths differ.
+// Shared prefix: every block reads all keys, so each CTA takes an equal share of
+// the (block, key tile) pairs, in order; the pieces of a block are joined by the
+// launch behind.
+//
+// Roles (registers redistributed with setmaxnreg):
+//   warps 0-3, 4-7   softmax of query tile 0 / 1 (thread = row): scores from
+//                    tensor memory, P back over them (bf16, half the columns),
+//                    rescale, epilogue; at head_dim 256 warps 4-7 load instead
+//   warp 8           issues the MMAs: S = Q K^T (both operands in shared memory),
+//                    O += P V (P in tensor memory)
+//   warp 9           draws the items
+//   from 10 (prompts at head_dim 64 / 128, two warps) or 12 (four) on
+//                    bring K / V rows into a ring of 128-key entries (128 head
 //                    dimensions each, K then V of a tile): contiguous rows by
-//                    TMA, gathered ones with 16-byte cp.async; e4m3 rows are
-//                    widened to bf16 (exact) in registers
+//                    TMA boxes, gathered bf16 rows by TMA gathers of four rows,
+//                    either with 16-byte cp.async where base, strides or row
+//                    numbers do not fit a tensor map; e4m3 rows are widened to
+//                    bf16 (exact) in registers
 // S of the next tile is issued behind PV of this one: the issuing order makes
 // the overwrite of P by S safe.
 //
@@ -171,8 +186,8 @@ using FaFn = void (*)(const FaParams, const CUtensorMap, const CUtensorMap, cons
 
 // The MMA warp runs its loop converged; one elected lane issues each group of
 // MMAs.  Addresses and descriptors are then the same for the whole warp and stay
-// in uniform registers (in a branch of one lane around the whole loop every MMA
-// first moves them there: 140 cycles an MMA instead of 64).
+// in uniform registers (with one lane in a branch around the whole loop long
+// prompts took 1155 us, so 1020).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n.reg .pred q;\nelect.sync _|q, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
@@ -251,7 +266,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // sets the abort flag and the error bit).  Every lane looks, and looks again at
 // once: a suspended warp (try_wait) wakes some hundred cycles late, which the
 // chain of scores, softmax and product pays several times a tile (long prompts
-// 1129 us suspended, 847 us so); the clock is read only after many looks.
+// 1129 us suspended, 676 us so); the clock is read only after many looks.
 __device__ __forceinline__ void wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
   unsigned long long t0 = 0;
   for (int looks = 0; !__all_sync(0xffffffffu, tr::test(bar, parity)); ++looks) {

@@ -19,10 +19,15 @@
 // g's elements at four positions of every 16-wide k step, and which positions
 // those are is free as long as the queries use the same ones, so the lane
 // takes 16 consecutive bytes (4 lanes: 64 bytes of a row) and no shuffle,
-// ldmatrix or staging buffer is needed.  The loads of the next two or three
-// stages are in flight while one is multiplied.  e4m3 keys are widened to f16 (exact) and meet
-// queries scaled by a power of two so that the largest lies in [2^14, 2^15)
+// ldmatrix or staging buffer is needed.  The next stage's loads are in flight
+// while one is multiplied (deeper queues cost registers: the serving batch
+// 1354 us with three stages, 1213 with two; a ring filled by cp.async 1211
+// against 1072).  e4m3 keys are widened to f16 (exact) and meet queries scaled by a power of two so that the largest lies in [2^14, 2^15)
 // (elements more than 2^29 smaller than it lose bits).
+//
+// Measured: 64 sequences of 8,192 to 32,768 keys, 32/8 heads of 128, 4 drafts,
+// bf16: 1,064 us, 2.7 TB/s over the call and about 4 while keys load; exchange,
+// weights and the wait for a whole cluster's place on the GPU take the rest.
 //
 // The sum over a head's rows runs in row order and every key has one writer:
 // the result does not depend on scheduling.

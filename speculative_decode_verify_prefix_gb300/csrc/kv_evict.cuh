@@ -21,7 +21,9 @@
 // the result is exact and in order.
 //
 // Bound by the mass rows (4 h_kv bytes a key) and, for short sequences, by the
-// five cluster barriers.
+// five cluster barriers.  Measured: 64 sequences of 8,192 to 32,768 keys cut to
+// 4,096, 8 heads: 46 us against 11 us of traffic (each pass waits for the
+// cluster's slowest CTA); 4 sequences of 800 to 960 keys cut to 256: 10 us.
 #pragma once
 #include <cooperative_groups.h>
 

@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
       constexpr uint32_t idPV = idesc(1, 1, 0, 1, 128, G::ED);
       const uint64_t dq0 = sdesc(q_s, 16, 1024), dk0 = sdesc(ring_s, 16, 1024), dv0 = sdesc(ring_s, KT * 128, 1024);
       using RP = Pos<NE>;
-      RP kp{0u, 0u}, vp{NH, 0u};   // ring entries of the next K / V tile (NH each)
+      RP kp{0u, 0u}, vp{NH, 0u};   // ring entries of the next K / V tile (NH each; at NQ = 1 of the next tile)
       uint32_t g[2] = {0u, 0u};    // key tiles per query tile so far
       uint32_t n_o[2] = {0u, 0u};  // items that gave the query tile any
       // S of query tile t against the K tile at kp; last: the K tile's entries
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
           acquire(kp);
           if (n0 > 0) qk(0, g[0], NQ == 1 || n1 == 0, n0 == 1);
           if (NQ == 2 && n1 > 0) qk(1, g[1], true, n1 == 1);
-          kp = kp.ahead(2 * NH);
+          kp = kp.ahead(NQ == 1 ? NH : 2 * NH);
         }
         if (elect_one()) {
           if (n0 == 0) mma_commit(bar(kBQEmpty));
@@ -838,10 +838,12 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
             if (more) {
               acquire(kp);
               qk(0, g[0] + 1, true, j + 2 == nt);
-              kp = kp.ahead(2 * NH);
+              kp = kp.ahead(NH);
             }
+            vp = kp;
             acquire(vp);
             pv(0, g[0], j == 0, true);
+            kp = kp.ahead(NH);
             ++g[0];
           } else {
             // (the tiles of a block have as many keys or the second one more)
@@ -858,8 +860,8 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
             }
             if (j + 1 < n1) qk(1, g[1], true, j + 2 == n1);
             if (more) kp = kp.ahead(2 * NH);
+            vp = vp.ahead(2 * NH);
           }
-          vp = vp.ahead(2 * NH);
         }
       }
       if (elect_one()) mma_commit(bar(kBDone));
@@ -910,15 +912,135 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
           return p.idx64 ? __ldg(static_cast<const long long*>(p.idx) + at)
                          : static_cast<long long>(__ldg(static_cast<const int*>(p.idx) + at));
         };
-        long long loc_next[NS];
-        if constexpr (!PROMPT) {
-#pragma unroll
-          for (int u = 0; u < NS; ++u) loc_next[u] = load_idx(0, lw * NS + u);
-        }
+        // the entries of K (kv = 0) or V tile j, of rows loc (a lane's key of each group)
+        auto load = [&](int kv, int j, const long long (&loc)[NS], const unsigned (&ok_mask)[NS]) {
+          const unsigned char* base = kv ? p.v + head * p.v_s1 : p.k + head * p.k_s1;
+          const long long s0 = kv ? p.v_s0 : p.k_s0;
 #pragma unroll 1
-        for (int j = 0; j < nt; ++j, ++gm) {
-          long long loc[NS];
-          unsigned ok_mask[NS];
+          for (int h = 0; h < NH; ++h, ++e) {
+            if (C::groups == 2 && (e & 1u) != static_cast<uint32_t>(lgrp)) continue;
+            unsigned char* ent = smem + G::ring_off + (e % NE) * ENT;
+            const uint32_t fb = bar(kBFull + e % NE);
+            auto publish_mask = [&](int u) {  // which keys of the group count, with a tile's first entry
+              if (!PROMPT && kv == 0 && h == 0 && lane == 0) {
+                maskw[4 * (gm % kMaskRing) + lw * NS + u] = ok_mask[u];
+                mbar_arrive(bar(kBMask + gm % kMaskRing));
+              }
+            };
+            if constexpr (MODE == kSharedE4m3) {
+              // 16 e4m3 values a lane, two 16-byte bf16 chunks; the rows are
+              // under way before the slot is free
+              constexpr int LPR = CPK / 2, RP8 = 32 / LPR, NP8 = 32 / RP8;
+              const int c8 = lane % LPR, r8 = lane / LPR;
+              uint4 x[NP8];
+#pragma unroll
+              for (int i = 0; i < NP8; ++i) {
+                const int kl = i * RP8 + r8;
+                const long long lc = __shfl_sync(0xffffffffu, loc[0], kl);
+                x[i] = ((ok_mask[0] >> kl) & 1u)
+                           ? __ldg(reinterpret_cast<const uint4*>(base + lc * s0 + h * G::ED + c8 * 16))
+                           : make_uint4(0u, 0u, 0u, 0u);
+              }
+              slot_wait(e);
+              publish_mask(0);
+#pragma unroll
+              for (int i = 0; i < NP8; ++i) {
+                const int key = 32 * lw + i * RP8 + r8;
+                const uint32_t wv[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t y[8];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  y[2 * u] = e4m3x2_to_bf16x2(static_cast<unsigned short>(wv[u] & 0xFFFFu));
+                  y[2 * u + 1] = e4m3x2_to_bf16x2(static_cast<unsigned short>(wv[u] >> 16));
+                }
+                *reinterpret_cast<uint4*>(ent + dst_off(key, 2 * c8)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(ent + dst_off(key, 2 * c8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+              }
+              fence_proxy_async();
+              mbar_arrive(fb);
+            } else {
+              slot_wait(e);
+#pragma unroll 1
+              for (int u = 0; u < NS; ++u) {
+                const int key0 = 32 * (lw * NS + u);  // first key of the group in the tile
+                const long long my_loc = loc[u];
+                const unsigned my_ok = ok_mask[u];
+                publish_mask(u);
+                if (PROMPT && p.tma && (kv == 0 || j < j_edge)) {
+                  // keys past the sequence may come along: their scores are
+                  // masked, and V tiles that hold any take the next branch
+                  if (lane == 0) {
+                    const uint32_t d0 = smem_u32(ent) + key0 * 128;
+                    mbar_arrive_warp_tx(fb, 32 * G::ED * 2);
+#pragma unroll
+                    for (int cb = 0; cb < G::ED / 64; ++cb)
+                      tma_load_box(d0 + cb * (KT * 128), kv ? &vmap : &kmap, fb, h * G::ED + cb * 64, head,
+                                   static_cast<int>(row0) + j * KT + key0);
+                  }
+                  __syncwarp();
+                } else if (PROMPT && kv == 1 && j >= j_edge) {
+                  // V on the diagonal: values that are not finite become 0 here
+                  // and are added by the epilogue to the rows that see them
+                  bool bad = false;
+#pragma unroll 1
+                  for (int i0 = 0; i0 < NP; i0 += 8) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                      const int kl = (i0 + i) * RPP + rr;
+                      const long long lc = __shfl_sync(0xffffffffu, my_loc, kl);
+                      x[i] = ((my_ok >> kl) & 1u)
+                                 ? __ldg(reinterpret_cast<const uint4*>(base + lc * s0 + h * G::ED * 2 + cc * 16))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                      const int key = key0 + (i0 + i) * RPP + rr;
+                      x[i].x = finite_bf16x2(x[i].x, bad);
+                      x[i].y = finite_bf16x2(x[i].y, bad);
+                      x[i].z = finite_bf16x2(x[i].z, bad);
+                      x[i].w = finite_bf16x2(x[i].w, bad);
+                      *reinterpret_cast<uint4*>(ent + dst_off(key, cc)) = x[i];
+                    }
+                  }
+                  if (bad) *const_cast<volatile int*>(&work[it & 1].bad_v) = 1;
+                  fence_proxy_async();
+                  mbar_arrive(fb);
+                } else if (MODE == kSharedBf16 && p.tma && my_ok == 0xFFFFFFFFu) {
+                  // 8 groups of 4 rows x ED / 64 column blocks, one gather a lane
+                  constexpr int NB = G::ED / 64;
+                  int r[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    r[i] = __shfl_sync(0xffffffffu, static_cast<int>(my_loc), (4 * (lane / NB) + i) & 31);
+                  if (lane == 0) mbar_arrive_warp_tx(fb, 32 * G::ED * 2);
+                  __syncwarp();
+                  if (lane < 8 * NB) {
+                    const int grp = lane / NB, cb = lane % NB;
+                    tma_gather4(smem_u32(ent) + cb * (KT * 128) + (key0 + 4 * grp) * 128, kv ? &vmap : &kmap, fb,
+                                head * static_cast<int>((kv ? p.v_s1 : p.k_s1) / 2) + h * G::ED + cb * 64, r[0], r[1],
+                                r[2], r[3]);
+                  }
+                  __syncwarp();
+                } else {
+                  const uint32_t d0 = smem_u32(ent);
+#pragma unroll 4
+                  for (int i = 0; i < NP; ++i) {
+                    const int kl = i * RPP + rr;
+                    const long long lc = __shfl_sync(0xffffffffu, my_loc, kl);
+                    const bool ok = (my_ok >> kl) & 1u;
+                    const unsigned char* src = ok ? base + lc * s0 + h * G::ED * 2 + cc * 16 : base;
+                    cp_async_16z(d0 + dst_off(key0 + kl, cc), src, ok);
+                  }
+                  cp_async_arrive_noinc(fb);
+                }
+              }
+            }
+          }
+        };
+        // pool rows of tile j, those of tile j + 1 asked for ahead
+        long long loc_next[NS];
+        auto rows_of = [&](int j, long long (&loc)[NS], unsigned (&ok_mask)[NS]) {
 #pragma unroll
           for (int u = 0; u < NS; ++u) {
             const int kg = lw * NS + u;
@@ -933,131 +1055,49 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
               ok_mask[u] = __ballot_sync(0xffffffffu, ok);
             }
           }
+        };
+        if constexpr (!PROMPT) {
+#pragma unroll
+          for (int u = 0; u < NS; ++u) loc_next[u] = load_idx(0, lw * NS + u);
+        }
+        // in the order in which the MMAs take the tiles: K and V in turn, or, where
+        // the next scores are issued before a tile's product, K one tile ahead
+        // (with V before K there the K tile waited for its entries until the
+        // product was done: three documents, 16/2 heads of 256, 39.6 us against 33.4)
+        if constexpr (NQ == 2) {
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            const unsigned char* base = kv ? p.v + head * p.v_s1 : p.k + head * p.k_s1;
-            const long long s0 = kv ? p.v_s0 : p.k_s0;
+          for (int j = 0; j < nt; ++j, ++gm) {
+            long long loc[NS];
+            unsigned ok_mask[NS];
+            rows_of(j, loc, ok_mask);
 #pragma unroll 1
-            for (int h = 0; h < NH; ++h, ++e) {
-              if (C::groups == 2 && (e & 1u) != static_cast<uint32_t>(lgrp)) continue;
-              unsigned char* ent = smem + G::ring_off + (e % NE) * ENT;
-              const uint32_t fb = bar(kBFull + e % NE);
-              auto publish_mask = [&](int u) {  // which keys of the group count, with a tile's first entry
-                if (!PROMPT && kv == 0 && h == 0 && lane == 0) {
-                  maskw[4 * (gm % kMaskRing) + lw * NS + u] = ok_mask[u];
-                  mbar_arrive(bar(kBMask + gm % kMaskRing));
-                }
-              };
-              if constexpr (MODE == kSharedE4m3) {
-                // 16 e4m3 values a lane, two 16-byte bf16 chunks; the rows are
-                // under way before the slot is free
-                constexpr int LPR = CPK / 2, RP8 = 32 / LPR, NP8 = 32 / RP8;
-                const int c8 = lane % LPR, r8 = lane / LPR;
-                uint4 x[NP8];
-#pragma unroll
-                for (int i = 0; i < NP8; ++i) {
-                  const int kl = i * RP8 + r8;
-                  const long long lc = __shfl_sync(0xffffffffu, loc[0], kl);
-                  x[i] = ((ok_mask[0] >> kl) & 1u)
-                             ? __ldg(reinterpret_cast<const uint4*>(base + lc * s0 + h * G::ED + c8 * 16))
-                             : make_uint4(0u, 0u, 0u, 0u);
-                }
-                slot_wait(e);
-                publish_mask(0);
-#pragma unroll
-                for (int i = 0; i < NP8; ++i) {
-                  const int key = 32 * lw + i * RP8 + r8;
-                  const uint32_t wv[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                  uint32_t y[8];
-#pragma unroll
-                  for (int u = 0; u < 4; ++u) {
-                    y[2 * u] = e4m3x2_to_bf16x2(static_cast<unsigned short>(wv[u] & 0xFFFFu));
-                    y[2 * u + 1] = e4m3x2_to_bf16x2(static_cast<unsigned short>(wv[u] >> 16));
-                  }
-                  *reinterpret_cast<uint4*>(ent + dst_off(key, 2 * c8)) = make_uint4(y[0], y[1], y[2], y[3]);
-                  *reinterpret_cast<uint4*>(ent + dst_off(key, 2 * c8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-                }
-                fence_proxy_async();
-                mbar_arrive(fb);
-              } else {
-                slot_wait(e);
+            for (int kv = 0; kv < 2; ++kv) load(kv, j, loc, ok_mask);
+          }
+        } else {
+          long long loc_k[NS], loc_v[NS];  // of the newest K tile and of the V tile that comes next
+          unsigned ok_k[NS], ok_v[NS];
+          const int tail = 2 * nt - 1;
 #pragma unroll 1
-                for (int u = 0; u < NS; ++u) {
-                  const int key0 = 32 * (lw * NS + u);  // first key of the group in the tile
-                  const long long my_loc = loc[u];
-                  const unsigned my_ok = ok_mask[u];
-                  publish_mask(u);
-                  if (PROMPT && p.tma && (kv == 0 || j < j_edge)) {
-                    // keys past the sequence may come along: their scores are
-                    // masked, and V tiles that hold any take the next branch
-                    if (lane == 0) {
-                      const uint32_t d0 = smem_u32(ent) + key0 * 128;
-                      mbar_arrive_warp_tx(fb, 32 * G::ED * 2);
+          for (int st = 0; st <= tail; ++st) {  // K0 K1 V0 K2 V1 ... V(nt - 2) V(nt - 1)
+            const int kv = st == 0 ? 0 : st == tail ? 1 : ~st & 1;
+            const int j = st == 0 ? 0 : st == tail ? nt - 1 : (st + 1) / 2 - kv;
+            if (st == 0) rows_of(0, loc_k, ok_k);
+            long long loc[NS];
+            unsigned ok_mask[NS];
 #pragma unroll
-                      for (int cb = 0; cb < G::ED / 64; ++cb)
-                        tma_load_box(d0 + cb * (KT * 128), kv ? &vmap : &kmap, fb, h * G::ED + cb * 64, head,
-                                     static_cast<int>(row0) + j * KT + key0);
-                    }
-                    __syncwarp();
-                  } else if (PROMPT && kv == 1 && j >= j_edge) {
-                    // V on the diagonal: values that are not finite become 0 here
-                    // and are added by the epilogue to the rows that see them
-                    bool bad = false;
-#pragma unroll 1
-                    for (int i0 = 0; i0 < NP; i0 += 8) {
-                      uint4 x[8];
-#pragma unroll
-                      for (int i = 0; i < 8; ++i) {
-                        const int kl = (i0 + i) * RPP + rr;
-                        const long long lc = __shfl_sync(0xffffffffu, my_loc, kl);
-                        x[i] = ((my_ok >> kl) & 1u)
-                                   ? __ldg(reinterpret_cast<const uint4*>(base + lc * s0 + h * G::ED * 2 + cc * 16))
-                                   : make_uint4(0u, 0u, 0u, 0u);
-                      }
-#pragma unroll
-                      for (int i = 0; i < 8; ++i) {
-                        const int key = key0 + (i0 + i) * RPP + rr;
-                        x[i].x = finite_bf16x2(x[i].x, bad);
-                        x[i].y = finite_bf16x2(x[i].y, bad);
-                        x[i].z = finite_bf16x2(x[i].z, bad);
-                        x[i].w = finite_bf16x2(x[i].w, bad);
-                        *reinterpret_cast<uint4*>(ent + dst_off(key, cc)) = x[i];
-                      }
-                    }
-                    if (bad) *const_cast<volatile int*>(&work[it & 1].bad_v) = 1;
-                    fence_proxy_async();
-                    mbar_arrive(fb);
-                  } else if (MODE == kSharedBf16 && p.tma && my_ok == 0xFFFFFFFFu) {
-                    // 8 groups of 4 rows x ED / 64 column blocks, one gather a lane
-                    constexpr int NB = G::ED / 64;
-                    int r[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                      r[i] = __shfl_sync(0xffffffffu, static_cast<int>(my_loc), (4 * (lane / NB) + i) & 31);
-                    if (lane == 0) mbar_arrive_warp_tx(fb, 32 * G::ED * 2);
-                    __syncwarp();
-                    if (lane < 8 * NB) {
-                      const int grp = lane / NB, cb = lane % NB;
-                      tma_gather4(smem_u32(ent) + cb * (KT * 128) + (key0 + 4 * grp) * 128, kv ? &vmap : &kmap, fb,
-                                  head * static_cast<int>((kv ? p.v_s1 : p.k_s1) / 2) + h * G::ED + cb * 64, r[0], r[1],
-                                  r[2], r[3]);
-                    }
-                    __syncwarp();
-                  } else {
-                    const uint32_t d0 = smem_u32(ent);
-#pragma unroll 4
-                    for (int i = 0; i < NP; ++i) {
-                      const int kl = i * RPP + rr;
-                      const long long lc = __shfl_sync(0xffffffffu, my_loc, kl);
-                      const bool ok = (my_ok >> kl) & 1u;
-                      const unsigned char* src = ok ? base + lc * s0 + h * G::ED * 2 + cc * 16 : base;
-                      cp_async_16z(d0 + dst_off(key0 + kl, cc), src, ok);
-                    }
-                    cp_async_arrive_noinc(fb);
-                  }
-                }
+            for (int u = 0; u < NS; ++u)
+              if (kv == 0 || st == tail) {
+                loc_v[u] = loc_k[u];
+                ok_v[u] = ok_k[u];
               }
+            if (kv == 0 && st > 0) rows_of(j, loc_k, ok_k);
+#pragma unroll
+            for (int u = 0; u < NS; ++u) {
+              loc[u] = kv ? loc_v[u] : loc_k[u];
+              ok_mask[u] = kv ? ok_v[u] : ok_k[u];
             }
+            load(kv, j, loc, ok_mask);
+            if (kv == 0) ++gm;
           }
         }
         if constexpr (PROMPT) {

@@ -1108,7 +1108,13 @@ int plan_stream_only(const CallShape& cs, StreamOnly& so) {
   so.wl = ws_layout(so.n_cta, cs.B, so.pl, cs.DV);
   const long long per = rows_m ? kPiecesPerSegment : kPiecesPerSegmentColSplit;
   const long long wp = (cs.mean_len / per + kStageTokens - 1) / kStageTokens * kStageTokens;
-  so.w_min = g_min_tokens > 0 ? g_min_tokens : std::max(kDefaultMinTokens, wp);
+  // Behind a shared prefix the own prefixes may be a few keys each: a share of
+  // 64 tokens is then dozens of segments, which a CTA takes one after the other
+  // at some 3 us (head_dim 256: 7).  A quarter of the mean keeps a CTA near one
+  // (32 own prefixes of 0 or 1 key behind 16,384 rows, 16/2 heads of 256: 267 us
+  // with 64 tokens, 70 so; 64 of 3 to 30 keys, 32/8 of 128: 88, 71).
+  const long long ws = std::min(kDefaultMinTokens, std::max(1LL, cs.mean_len / 4));
+  so.w_min = g_min_tokens > 0 ? g_min_tokens : wp > kDefaultMinTokens ? wp : ws;
   return 1;
 }
 

@@ -288,6 +288,16 @@ def test_shared_against_64_bits(vsk, case):
 
 
 @pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 1), (128, 8, 2), (256, 16, 2)])
+@pytest.mark.parametrize("own", [(0, 1) * 20, (0,) * 30 + (1500,) + (2,) * 9, (3, 17, 0, 64, 30, 5) * 6],
+                         ids=["none or one", "one long", "short"])
+def test_shared_with_short_own_prefixes(vsk, own, d, hq, hk, pool):
+    c = shared_case(200, own, 4, hq, hk, d, pool, seed=27)
+    check_attention(run_shared(vsk, c), *shared_want(c, d ** -0.5))
+    assert vsk.read_error_flags() == 0
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
 @pytest.mark.parametrize("ks,vs", [(0.5, 0.25), (-0.7, 2.0), (0.0, 1.0)])
 def test_shared_scales(vsk, pool, ks, vs):
     c = shared_case(300, (20, 0, 150), 4, 8, 2, 128, pool, seed=22)

@@ -472,9 +472,9 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
   cfg.stream = st;
   cfg.attrs = at;
   // starting under fa_kernel's end saves 1.5 us (four short sequences 17.0 ->
-  // 15.6) to 5 (serving batch 195 -> 189); behind the tensor-memory stream, which
-  // outlasts fa_kernel, it costs 4 (40 -> 44)
-  cfg.numAttrs = has_shared && !(has_own && so.rows_m) ? 1 : 0;
+  // 15.6) to 8 (32 own prefixes of 100 to 200 keys behind 16,384 e4m3 rows, 16/2
+  // heads of 256: 110 -> 101)
+  cfg.numAttrs = has_shared ? 1 : 0;
   e = cudaLaunchKernelExC(&cfg, fn, args);
   if (e != cudaSuccess) return fail("combine kernel launch failed: %s", cudaGetErrorString(e));
   return 1;

@@ -531,6 +531,14 @@ def test_evict_of_one_very_long_sequence(vsk):
     check_evict(got, (torch.tensor([0, k], dtype=torch.int32), kvi[keep].cpu(), mass[:, keep].cpu(), kvi[gone].cpu()))
 
 
+@pytest.mark.parametrize("lens", [(60000,) + (500,) * 31, (3,) * 100 + (60000,) + (700,) * 100, (9000,) * 20])
+def test_evict_of_uneven_lengths(vsk, lens):
+    g = gen(45)
+    t = sum(lens)
+    mass, kvi = masses(g, 2, t, "ties"), torch.randperm(t, generator=g, device=DEV)
+    check_evict(run_evict(vsk, mass, lens, kvi, 600, 30), evict_want(mass, kvi, lens, 600, 30))
+
+
 def test_evict_flags_bad_indptr_and_short_outputs(vsk):
     g = gen(44)
     mass, kvi = masses(g, 2, 100, "heavy"), torch.arange(100, device=DEV)

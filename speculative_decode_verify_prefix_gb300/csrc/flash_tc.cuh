@@ -894,7 +894,9 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
         if (p.qtma && lgrp == 0 && lw < NQ) {
           // query tile lw (rows past the sequence may come along: they are never stored)
           wait_all(bar(kBQEmpty + lw), static_cast<uint32_t>((it & 1) ^ 1), abort_flag, p.err);
-          if (lane == 0) {
+          if (lane == 0 && wk->n_tiles[lw] == 0) {
+            mbar_arrive(bar(kBQFull + lw));  // no MMA reads it
+          } else if (lane == 0) {
             const uint32_t fb = bar(kBQFull + lw);
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(fb),
                          "r"(p.tpb * p.gq * D * 2)
@@ -967,13 +969,14 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
                 const unsigned my_ok = ok_mask[u];
                 publish_mask(u);
                 if (PROMPT && p.tma && (kv == 0 || j < j_edge)) {
-                  // keys past the sequence may come along: their scores are
-                  // masked, and V tiles that hold any take the next branch
+                  // keys past the sequence may come along, or what was there before
+                  // stays: their scores are masked, and V tiles that hold any take
+                  // the next branch
                   if (lane == 0) {
                     const uint32_t d0 = smem_u32(ent) + key0 * 128;
-                    mbar_arrive_warp_tx(fb, 32 * G::ED * 2);
-#pragma unroll
-                    for (int cb = 0; cb < G::ED / 64; ++cb)
+                    const bool any = j * KT + key0 < n;
+                    mbar_arrive_warp_tx(fb, any ? 32 * G::ED * 2 : 0);
+                    for (int cb = 0; any && cb < G::ED / 64; ++cb)
                       tma_load_box(d0 + cb * (KT * 128), kv ? &vmap : &kmap, fb, h * G::ED + cb * 64, head,
                                    static_cast<int>(row0) + j * KT + key0);
                   }

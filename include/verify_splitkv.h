@@ -18,7 +18,9 @@
  * causal attention over the drafts alone.
  *
  * Threading and streams: every entry point may be called from any host
- * thread.  verify_splitkv_fwd enqueues one kernel on the given stream (two
+ * thread, also at once with the same workspace on one stream: a call's
+ * launches are then enqueued without another's between them.
+ * verify_splitkv_fwd enqueues one kernel on the given stream (two
  * for the small and mid-size shapes served by a prefix stream and a combine
  * kernel; vsk_launches_per_call tells which) and returns without
  * synchronising and without reading device memory.

@@ -315,6 +315,7 @@ int prompt_attn_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* 
   if (N == 0) return 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   size_t ws_bytes = 0;
+  WorkspaceHold hold(workspace);
   unsigned char* ws = take_workspace(workspace, workspace_bytes, 256, st, &ws_bytes);
   if (!ws) return 0;
   fa::FaParams p;
@@ -399,6 +400,7 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
   const size_t need = base + shared_partial_bytes(c.pieces, c.nq, cs.D) + so.wl.cnt_bytes;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   size_t ws_bytes = 0;
+  WorkspaceHold hold(workspace);
   unsigned char* ws = take_workspace(workspace, workspace_bytes, need, st, &ws_bytes);
   if (!ws) return 0;
 
@@ -516,6 +518,7 @@ int verify_splitkv_mass(const vsk_tensor* q, const vsk_tensor* ke, const vsk_ten
   m.pitch = m.cap + 8;  // 8 mod 32 floats: the four row groups of a fragment store meet different banks
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   size_t ws_bytes = 0;
+  WorkspaceHold hold(workspace);
   unsigned char* ws = take_workspace(workspace, workspace_bytes, 256, st, &ws_bytes);
   if (!ws) return 0;
   p.B = static_cast<int>(cs.B);
@@ -583,6 +586,7 @@ int kv_evict(const vsk_tensor* mass, const vsk_tensor* kvp, const vsk_tensor* kv
     }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   size_t ws_bytes = 0;
+  WorkspaceHold hold(workspace);
   unsigned char* ws = take_workspace(workspace, workspace_bytes, 256, st, &ws_bytes);
   if (!ws) return 0;
   ev::EvictParams p;

@@ -36,6 +36,20 @@ size_t align256(size_t x);
 int device_sms(int dev);
 int prepare_kernel(KernelFn fn);
 void* internal_workspace(int dev, size_t need, cudaStream_t stream, size_t* bytes);
+// Holds a workspace (NULL: the library-owned one) while a call enqueues its
+// launches.  Several launches hand partials on in it, so calls of two host
+// threads on one stream must not enqueue theirs in between; and the
+// library-owned one must not be replaced between its choice and the launch.
+class WorkspaceHold {
+ public:
+  explicit WorkspaceHold(const void* ws);
+  ~WorkspaceHold();
+  WorkspaceHold(const WorkspaceHold&) = delete;
+  WorkspaceHold& operator=(const WorkspaceHold&) = delete;
+
+ private:
+  const void* ws_;
+};
 bool make_plan(long long h_q, long long h_kv, long long D, long long L, bool fp8, Plan& pl, long long total_tokens,
                int tiles, long long DV = 0, int hc_cap = 0);
 WsLayout ws_layout(long long n_cta, long long B, const Plan& pl, long long DV);

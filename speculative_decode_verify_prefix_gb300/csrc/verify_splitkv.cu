@@ -506,6 +506,30 @@ void* internal_workspace(int dev, size_t need, cudaStream_t stream, size_t* byte
   return p;
 }
 
+// A lock per workspace in use, kept while some thread has or waits for it.
+struct HeldWs {
+  std::mutex mu;
+  int users = 0;
+};
+std::mutex g_held_mu;
+std::map<const void*, HeldWs> g_held;
+
+WorkspaceHold::WorkspaceHold(const void* ws) : ws_(ws) {
+  HeldWs* h;
+  {
+    std::lock_guard<std::mutex> lk(g_held_mu);
+    h = &g_held[ws];
+    ++h->users;
+  }
+  h->mu.lock();
+}
+WorkspaceHold::~WorkspaceHold() {
+  std::lock_guard<std::mutex> lk(g_held_mu);
+  const auto it = g_held.find(ws_);
+  it->second.mu.unlock();
+  if (--it->second.users == 0) g_held.erase(it);
+}
+
 // device address of the allocation-free entry point's built-in scratch
 void* static_scratch(int dev);
 
@@ -587,6 +611,7 @@ int vsk_read_error_flags(void* workspace, void* stream, uint32_t* flags) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return fail("cudaStreamSynchronize: %s", cudaGetErrorString(e));
+  WorkspaceHold hold(workspace);
   void* ws = workspace;
   if (!ws || ws == VSK_NOALLOC_SCRATCH) {
     int dev = 0;
@@ -951,6 +976,7 @@ static int launch_with_plan(Params& p, long long B, long long h_q, long long h_k
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   size_t ws_bytes = workspace_bytes;
+  WorkspaceHold hold(workspace);
   if (!ws) {
     ws = static_cast<unsigned char*>(internal_workspace(cp.dev, cp.wl.total, st, &ws_bytes));
     if (!ws) return fail("cannot allocate a %zu-byte workspace", cp.wl.total);
@@ -1381,6 +1407,7 @@ extern "C" int verify_splitkv_fwd_noalloc(const vsk_tensor* q, const vsk_tensor*
   // this call's whole ticket span (at the end of the array) before its
   // kernels run.
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  WorkspaceHold hold(scratch);
   cudaError_t e = cudaMemsetAsync(scratch, 0, 256, st);
   if (e == cudaSuccess)
     e = cudaMemsetAsync(scratch + VSK_NOALLOC_SCRATCH_BYTES - cp.wl.cnt_bytes, 0, cp.wl.cnt_bytes, st);

@@ -185,7 +185,7 @@ static size_t shared_partial_bytes(long long pieces, int nq, long long D) {
 static size_t shared_workspace_for_sms(int sms, long long max_bs, long long h_q, long long h_kv, long long D,
                                        long long L) {
   const size_t own = vsk_workspace_size_for_sms(sms, max_bs, h_q, h_kv, D, D, L);
-  if (own == 0 || h_q / h_kv > 128) return 0;
+  if (own == 0 || h_q < 1 || h_q / h_kv > 128) return 0;
   const SharedCut c = shared_cut(max_bs * L, h_q / h_kv, h_kv, D, 1, sms);
   return own + shared_partial_bytes(c.units + sms, c.nq, D);
 }
@@ -376,6 +376,7 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
   if (!prepare_verify(q, ke, ve, o, kb, vb, qo, kvp, kvi, 1, max_len_extend, k_scale, v_scale, sm_scale, nullptr,
                       nullptr, nullptr, p, cs))
     return 0;
+  if (cs.h_q < 1) return fail("h_q must be >= 1");
   if (cs.D != cs.DV) return fail("head_dim %lld and v_head_dim %lld must be equal", cs.D, cs.DV);
   if (!check_1d(shi, "shared_indices")) return 0;
   if (shi->dtype != VSK_DTYPE_I32 && shi->dtype != VSK_DTYPE_I64) return fail("shared_indices must be int32 or int64");

@@ -61,3 +61,12 @@ def test_threads_on_one_stream_keep_their_partials(vsk, form):
     wrong = [sum(not torch.equal(o, alone[i]) for o in outs[i]) for i in range(len(cases))]
     assert wrong == [0] * len(cases), f"calls of {calls} with another call's partials: {wrong}"
     assert vsk.read_error_flags() == 0
+
+
+# ---------------------------------------------------------------- sizes
+
+def test_shared_workspace_size_of_shapes_that_no_call_takes(vsk):
+    assert vsk.shared_workspace_size(2, 8, 2, 128, 4) > 0
+    for shape in ((2, 0, 2, 128, 4), (2, -4, 2, 128, 4), (2, 8, 0, 128, 4), (0, 8, 2, 128, 4), (2, 8, 2, 96, 4),
+                  (2, 8, 2, 128, 0), (2, 7, 2, 128, 4)):
+        assert vsk.shared_workspace_size(*shape) == 0, shape

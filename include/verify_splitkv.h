@@ -297,8 +297,8 @@ size_t vsk_shared_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv,
  *                   mass_in NULL counts as zeros; it may be mass itself and must
  *                   not overlap it otherwise
  *   other arguments and limits as verify_splitkv_fwd (head_dim in {64, 128,
- *                   256}, (h_q/h_kv)*l_ext <= 128, or 64 at 256); workspace as
- *                   prompt_attn_fwd.
+ *                   256}, (h_q/h_kv)*l_ext <= 128, or 64 at 256), n at most
+ *                   2^31 - 65536; workspace as prompt_attn_fwd.
  * One launch on `stream`; the sums have a fixed order. */
 int verify_splitkv_mass(const vsk_tensor* q_extend, const vsk_tensor* k_extend,
                         const vsk_tensor* k_buffer, const vsk_tensor* qo_indptr,
@@ -314,7 +314,7 @@ int verify_splitkv_mass(const vsk_tensor* q_extend, const vsk_tensor* k_extend,
  * ascending order; equal totals: the earliest entries; NaN counts as the
  * largest).  Kept entries stay in their order.
  *   mass            [h_kv, n] float32 (as verify_splitkv_mass leaves it)
- *   kv_indptr [B+1] int32, kv_indices [n] int32 or int64
+ *   kv_indptr [B+1] int32, kv_indices [n] int32 or int64, n at most 2^31 - 65536
  *   budget >= 1, 0 <= recent <= budget
  *   out_kv_indptr   [B+1] int32
  *   out_kv_indices  [m] of kv_indices' type, out_mass [h_kv, m] float32: the

@@ -273,6 +273,10 @@ static int mass_cluster(long long mean_len, long long cap, long long n_seg, int 
   return kSizes[i];
 }
 
+// The cluster kernels hold positions in kv_indices in 32 bits and step past the
+// last one by a cluster's or a chunk's worth.
+constexpr long long kMaxEntries = INT_MAX - 65535LL;
+
 static bool check_rows(const vsk_tensor* t, const char* name, long long rows) {
   if (!check_2d(t, name)) return false;
   if (t->dtype != VSK_DTYPE_F32) return fail("%s must be float32", name);
@@ -497,6 +501,7 @@ int verify_splitkv_mass(const vsk_tensor* q, const vsk_tensor* ke, const vsk_ten
                       nullptr, p, cs))
     return 0;
   const long long T = kvi->shape[0];
+  if (T > kMaxEntries) return fail("%lld kv_indices entries are too many (%lld at most)", T, kMaxEntries);
   if (!check_rows(mass, "mass", cs.h_kv)) return 0;
   if (mass->shape[1] != T) return fail("mass must have one column per kv_indices entry (%lld)", T);
   if (mass_in) {
@@ -552,6 +557,7 @@ int kv_evict(const vsk_tensor* mass, const vsk_tensor* kvp, const vsk_tensor* kv
     return 0;
   const long long B = kvp->shape[0] - 1, T = kvi->shape[0], h_kv = mass->shape[0];
   if (B < 1) return fail("batch size must be >= 1");
+  if (T > kMaxEntries) return fail("%lld kv_indices entries are too many (%lld at most)", T, kMaxEntries);
   if (kvp->dtype != VSK_DTYPE_I32 || out_kvp->dtype != VSK_DTYPE_I32) return fail("indptr arrays must be int32");
   if (out_kvp->shape[0] != B + 1) return fail("out_kv_indptr must have B+1 entries");
   if (kvi->dtype != VSK_DTYPE_I32 && kvi->dtype != VSK_DTYPE_I64) return fail("kv_indices must be int32 or int64");

@@ -1,5 +1,7 @@
 """More refusals of the calls around the verify call (no GPU needed): the
 checks read shapes, types, strides and pointers only, so CPU tensors stand in."""
+import ctypes
+
 import pytest
 import torch
 
@@ -11,3 +13,22 @@ from test_cache_ops_host import bf, built, call, evict_args, mass_args, ptr, ref
 def test_shared_without_query_heads_is_refused():
     """The cut of the work divides by the query heads of a KV head."""
     refused("h_q must be", call("verify_splitkv_shared_fwd", shared_args(q=bf(8, 0, 64), o=bf(8, 0, 64)), 4, 1.0, 1.0, 0.0))
+
+
+@pytest.mark.parametrize("name", ["verify_splitkv_mass", "kv_evict"])
+def test_indices_past_32_bit_positions_are_refused(name):
+    """Positions are 32-bit in the kernels, with room for a step behind the last one."""
+    def sized(t, n):  # the view of a longer array (never read here)
+        v = vsk.as_vsk(t)
+        v.shape[t.dim() - 1] = n
+        if t.dim() == 2:
+            v.stride[0] = n
+        return ctypes.byref(v)
+
+    for n, msg in ((2 ** 31 - 65536 + 1, "too many"), (2 ** 31 - 1, "too many")):
+        if name == "kv_evict":
+            a = evict_args(m=sized(torch.zeros(2, 20), n), kvi=sized(torch.arange(20), n))
+            refused(msg, call(name, a))
+        else:
+            a = mass_args(m=sized(torch.zeros(2, 20), n), kvi=sized(torch.arange(20), n))
+            refused(msg, call(name, a, 4, 1.0, 0.0))

@@ -10,9 +10,11 @@
 // m is raised (and O, l scaled by 2^(m_old - m_new)) only when a tile's maximum
 // exceeds it by more than 8: until then P stays below 2^8, far from any
 // limit of the 32-bit sums, and O in tensor memory need not be touched.
-// Scores, m, l and O are 32-bit; P is rounded to bf16 because both operands of
-// an MMA have one type and V is bf16 (relative error 2^-8 at most, that of the
-// output's own rounding; l sums the unrounded P).
+// Scores, m, l and O are 32-bit.  P is rounded to V's type, since both operands
+// of an MMA have one: to bf16 for bf16 V (relative error 2^-8 at most, that of
+// the output's own rounding), to f16 for e4m3 V (2^-11), which f16 holds exactly.
+// f16 ends at 2^-24, so P is there 2^(x - m + 7): at most 2^15, and exact to
+// 2^-11 down to 2^-21 of the reference.  l sums the unrounded P.
 //
 // Rows.  The g = h_q / h_kv query heads of a KV head share its keys, so the
 // packed row r of a query tile is (token r / g, head r % g): a 128-row tile
@@ -51,8 +53,8 @@
 //                    dimensions each, K then V of a tile): contiguous rows by
 //                    TMA boxes, gathered bf16 rows by TMA gathers of four rows,
 //                    either with 16-byte cp.async where base, strides or row
-//                    numbers do not fit a tensor map; e4m3 rows are widened to
-//                    bf16 (exact) in registers
+//                    numbers do not fit a tensor map; e4m3 rows are widened in
+//                    registers (exact), K to the queries' bf16, V to P's f16
 // S of the next tile is issued behind PV of this one: the issuing order makes
 // the overwrite of P by S safe.
 //
@@ -100,6 +102,8 @@ constexpr int kMaxNE = 8;        // ring entries at most
 constexpr int kMaskRing = 8;     // > the tiles loaders can run ahead of the softmax
 
 enum Mode { kPrompt = 0, kSharedBf16 = 1, kSharedE4m3 = 2 };
+
+constexpr float kPShift = 7.f;   // log2 of what f16 P are scaled by: 2^(kThr + kPShift) is below f16's largest
 
 // Warps and registers.  The softmax warps hold a row of 128 scores and half a
 // row of P, so they get what the launch's registers allow; where two warps
@@ -332,7 +336,8 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
   using G = fa::Geo<D>;
   using C = fa::Cfg<D, MODE>;
   constexpr int NQ = G::NQ, NH = G::NH, NE = G::NE, ENT = G::ENT;
-  constexpr bool PROMPT = MODE == kPrompt;
+  constexpr bool PROMPT = MODE == kPrompt, P16 = MODE == kSharedE4m3;  // P and V are f16, else bf16
+  constexpr float p_up = P16 ? kPShift : 0.f;                          // log2 of the scale of P, l and O
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
@@ -495,7 +500,7 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
         uint32_t pk[32];
         float2 l2[2];
         auto probs = [&](int h, float mref) {  // pk and the sum of half h
-          const float2 mn2 = make_float2(-mref, -mref);
+          const float2 mn2 = make_float2(p_up - mref, p_up - mref);
           l2[0] = l2[1] = make_float2(0.f, 0.f);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
             x.x = fast_exp2(x.x);
             x.y = fast_exp2(x.y);
             l2[i & 1] = add2(l2[i & 1], x);
-            pk[i] = pack_bf16(x.x, x.y);
+            pk[i] = P16 ? pack_f16(x.x, x.y) : pack_bf16(x.x, x.y);
           }
         };
         auto hide = [&](int h) {  // -inf for masked keys
@@ -620,10 +625,11 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
           }
         }
       } else if (my_tiles > 0) {
-        // partial of this key range: o v_scale / l and m + log2 l, -inf and 0 where no key was valid
+        // partial of this key range: o v_scale / l and m + log2 l (of l without the scale of P), -inf and 0
+        // where no key was valid
         const long long prow = wk->item * (NQ * 128) + t * 128 + r;
         const float inv = l > 0.f ? p.v_scale / l : 0.f;
-        if (real) p.plse[prow] = l > 0.f ? mrun + log2f(l) : (l == 0.f ? NEG_INF : l);
+        if (real) p.plse[prow] = l > 0.f ? mrun + (log2f(l) - p_up) : (l == 0.f ? NEG_INF : l);
         float* orow = p.po + prow * D;
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {
@@ -742,7 +748,7 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
       // ============================ MMA issue ============================
       const uint32_t tmem_u = __reduce_max_sync(0xffffffffu, tmem);
       constexpr uint32_t idS = idesc(1, 1, 0, 0, 128, KT);
-      constexpr uint32_t idPV = idesc(1, 1, 0, 1, 128, G::ED);
+      constexpr uint32_t idPV = idesc(P16 ? 0 : 1, P16 ? 0 : 1, 0, 1, 128, G::ED);
       const uint64_t dq0 = sdesc(q_s, 16, 1024), dk0 = sdesc(ring_s, 16, 1024), dv0 = sdesc(ring_s, KT * 128, 1024);
       using RP = Pos<NE>;
       RP kp{0u, 0u}, vp{NH, 0u};   // ring entries of the next K / V tile (NH each; at NQ = 1 of the next tile)
@@ -930,8 +936,8 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
               }
             };
             if constexpr (MODE == kSharedE4m3) {
-              // 16 e4m3 values a lane, two 16-byte bf16 chunks; the rows are
-              // under way before the slot is free
+              // 16 e4m3 values a lane, two 16-byte chunks of bf16 (K) or f16 (V);
+              // the rows are under way before the slot is free
               constexpr int LPR = CPK / 2, RP8 = 32 / LPR, NP8 = 32 / RP8;
               const int c8 = lane % LPR, r8 = lane / LPR;
               uint4 x[NP8];
@@ -952,8 +958,9 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
                 uint32_t y[8];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                  y[2 * u] = e4m3x2_to_bf16x2(static_cast<unsigned short>(wv[u] & 0xFFFFu));
-                  y[2 * u + 1] = e4m3x2_to_bf16x2(static_cast<unsigned short>(wv[u] >> 16));
+                  const auto lo = static_cast<unsigned short>(wv[u] & 0xFFFFu), hi = static_cast<unsigned short>(wv[u] >> 16);
+                  y[2 * u] = kv ? e4m3x2_to_f16x2(lo) : e4m3x2_to_bf16x2(lo);
+                  y[2 * u + 1] = kv ? e4m3x2_to_f16x2(hi) : e4m3x2_to_bf16x2(hi);
                 }
                 *reinterpret_cast<uint4*>(ent + dst_off(key, 2 * c8)) = make_uint4(y[0], y[1], y[2], y[3]);
                 *reinterpret_cast<uint4*>(ent + dst_off(key, 2 * c8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);

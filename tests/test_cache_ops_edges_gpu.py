@@ -70,3 +70,60 @@ def test_shared_workspace_size_of_shapes_that_no_call_takes(vsk):
     for shape in ((2, 0, 2, 128, 4), (2, -4, 2, 128, 4), (2, 8, 0, 128, 4), (0, 8, 2, 128, 4), (2, 8, 2, 96, 4),
                   (2, 8, 2, 128, 0), (2, 7, 2, 128, 4)):
         assert vsk.shared_workspace_size(*shape) == 0, shape
+
+
+# ---------------------------------------------------------------- e4m3 pools behind a shared prefix
+#
+# Softmax weights of e4m3 pools are held in f16, as in the verify call: 2^-11 of
+# themselves, so 2^-11 A in the output for the header's 2^-8 A of bf16 ones, and
+# below f16's normal range an absolute 2^-25 of the row's largest weight (2^-32
+# for shared rows) a key.
+
+
+def check_f16_weights(got, want, a, c, vs=1.0):
+    top = float(c["vb"].float().nan_to_num(0.0).abs().max()) * abs(vs)
+    small = (max(c["own"]) * 2.0 ** -25 + len(c["sh"]) * 2.0 ** -32) * top
+    tol = (2.0 ** -11 + 2.0 ** -12) * a + small + 2.0 ** -8 * want.abs() * (1 + 2.0 ** -8)
+    off = ((got.to(F64) - want).abs() / tol).max()
+    assert bool(off <= 1), float(off)
+
+
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 2), (256, 16, 2)])
+def test_shared_e4m3_weights_have_the_bits_of_f16(vsk, d, hq, hk):
+    """Every other key has a weight half a step of bf16 above 0.5 (not quite: bf16 would take it to 0.5, f16 to 2^-12 of
+    itself), and values that cancel: the output is what the weights' rounding leaves."""
+    n = 1024
+    c = shared_case(n, (0, 0), 4, hq, hk, d, "e4m3", seed=81)
+    low = torch.zeros(n, dtype=torch.bool, device=DEV)
+    low[c["sh"][1::2]] = True
+    c["q"].zero_()
+    c["q"][:, :, 0] = 1
+    c["ke"].zero_()
+    c["ve"].zero_()
+    kb = torch.zeros(n, hk, d, device=DEV)
+    kb[low, :, 0] = -1
+    c["kb"] = kb.to(E4M3)
+    c["vb"] = torch.where(low, -2.0, 1.0)[:, None, None].expand(n, hk, d).contiguous().to(E4M3)
+    sm = -math.log(0.5 + 2.0 ** -9 - 2.0 ** -14)
+    check_f16_weights(run_shared(vsk, c, sm_scale=sm), *shared_want(c, sm), c)
+
+
+@pytest.mark.parametrize("case", [c for c in base.SHARED if c[6] == "e4m3"], ids=lambda c: f"s{c[0]}b{len(c[1])}d{c[5]}")
+def test_shared_e4m3_within_the_bound_of_f16_weights(vsk, case):
+    c = shared_case(*case, seed=86)
+    check_f16_weights(run_shared(vsk, c, k_scale=0.5, v_scale=0.25), *shared_want(c, case[5] ** -0.5, 0.5, 0.25), c, 0.25)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_shared_e4m3_scores_far_apart(vsk, d):
+    """Weights from 1 down to 2^-30 of the largest, which comes late in the row: the reference moves, f16 keeps its range."""
+    c = shared_case(2000, (40, 0), 4, 8, 2, d, "e4m3", seed=87)
+    c["q"].zero_()
+    c["q"][:, :, 0] = 1
+    kb = c["kb"].float()
+    kb[:, :, 0] = 0
+    order = torch.cat([c["sh"], c["kvi"]])
+    kb[order, :, 0] = torch.linspace(-15, 15, 2040, device=DEV)[:, None]
+    c["kb"] = kb.to(E4M3)
+    sm = math.log(2.0)
+    check_f16_weights(run_shared(vsk, c, sm_scale=sm), *shared_want(c, sm), c)

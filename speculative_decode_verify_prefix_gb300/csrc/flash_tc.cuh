@@ -914,9 +914,10 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
           }
           __syncwarp();
         }
-        auto load_idx = [&](int j, int kg) -> long long {
-          const long long at = static_cast<long long>(j_first + j) * KT + 32 * kg + lane;
-          if (j >= nt || at >= p.n_keys) return -2;
+        auto key_at = [&](int j, int kg) { return static_cast<long long>(j_first + j) * KT + 32 * kg + lane; };
+        auto load_idx = [&](int j, int kg) -> long long {  // -1 where there is no key
+          const long long at = key_at(j, kg);
+          if (j >= nt || at >= p.n_keys) return -1;
           return p.idx64 ? __ldg(static_cast<const long long*>(p.idx) + at)
                          : static_cast<long long>(__ldg(static_cast<const int*>(p.idx) + at));
         };
@@ -1061,7 +1062,7 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
               loc[u] = loc_next[u];
               loc_next[u] = load_idx(j + 1, kg);
               const bool ok = loc[u] >= 0 && loc[u] < p.pool;
-              if (!ok && loc[u] != -2) atomicOr(p.err, kErrBadIndex);
+              if (!ok && key_at(j, kg) < p.n_keys) atomicOr(p.err, kErrBadIndex);
               ok_mask[u] = __ballot_sync(0xffffffffu, ok);
             }
           }

@@ -127,3 +127,24 @@ def test_shared_e4m3_scores_far_apart(vsk, d):
     c["kb"] = kb.to(E4M3)
     sm = math.log(2.0)
     check_f16_weights(run_shared(vsk, c, sm_scale=sm), *shared_want(c, sm), c)
+
+
+# ---------------------------------------------------------------- bad shared indices
+
+@pytest.mark.parametrize("pool,d", [("bf16", 128), ("e4m3", 128), ("bf16", 256), ("e4m3", 256)])
+@pytest.mark.parametrize("bad", [-1, -2, -3, -(1 << 31), -(1 << 63), (1 << 63) - 1, (1 << 32)])
+def test_every_bad_shared_index_is_flagged(vsk, pool, d, bad):
+    c = shared_case(300, (30, 8), 4, 8, 2, d, pool, seed=82)
+    run_shared(vsk, c)
+    assert vsk.read_error_flags() == 0  # (300 indices end inside a tile)
+    good = dict(c)
+    keep = torch.ones(300, dtype=torch.bool, device=DEV)
+    keep[[5, 299]] = False
+    good["sh"] = c["sh"][keep]
+    c["sh"][5] = c["sh"][299] = bad
+    check_attention(run_shared(vsk, c), *shared_want(good, d ** -0.5))
+    assert vsk.read_error_flags() == 1
+    if abs(bad) < 1 << 31 or bad == -(1 << 31):
+        c["sh"], c["kvi"] = c["sh"].int(), c["kvi"].int()
+        check_attention(run_shared(vsk, c), *shared_want(good, d ** -0.5))
+        assert vsk.read_error_flags() == 1

@@ -264,7 +264,8 @@ int prompt_attn_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* 
  * sequence.
  *   shared_indices  [S] int32 or int64, S >= 0
  *   other arguments, limits and device-side checks as verify_splitkv_fwd
- *   (causal drafts), with head_dim == v_head_dim.
+ *   (causal drafts), with head_dim == v_head_dim; sm_scale and sm_scale *
+ *   k_scale, times log2 e, must not exceed a float.
  *   workspace       vsk_shared_workspace_size(max_bs, ...) bytes hold it for
  *                   any B <= max_bs and any S; NULL selects the library-owned
  *                   buffer.
@@ -298,7 +299,8 @@ size_t vsk_shared_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv,
  *                   not overlap it otherwise
  *   other arguments and limits as verify_splitkv_fwd (head_dim in {64, 128,
  *                   256}, (h_q/h_kv)*l_ext <= 128, or 64 at 256), n at most
- *                   2^31 - 65536; workspace as prompt_attn_fwd.
+ *                   2^31 - 65536; scales as verify_splitkv_shared_fwd;
+ *                   workspace as prompt_attn_fwd.
  * One launch on `stream`; the sums have a fixed order. */
 int verify_splitkv_mass(const vsk_tensor* q_extend, const vsk_tensor* k_extend,
                         const vsk_tensor* k_buffer, const vsk_tensor* qo_indptr,

@@ -155,6 +155,12 @@ static double softmax_scale(float sm_scale, long long D) {
                                                      : 1.0 / std::sqrt(static_cast<double>(D));
 }
 constexpr double kLog2e = 1.4426950408889634;
+// An infinite scale makes every score infinite or NaN.
+static bool check_scales(const Params& p) {
+  if (!std::isfinite(p.dscale2)) return fail("sm_scale is too large");
+  if (!std::isfinite(p.scale2)) return fail("sm_scale * k_scale is too large");
+  return true;
+}
 
 // ---- shared prefix: how the work is cut ----
 // The key tiles of the units (row blocks x KV heads) are laid end to end and
@@ -386,7 +392,7 @@ int verify_splitkv_shared_fwd(const vsk_tensor* q, const vsk_tensor* ke, const v
   if (shi->dtype != VSK_DTYPE_I32 && shi->dtype != VSK_DTYPE_I64) return fail("shared_indices must be int32 or int64");
   if (!aligned(shi->data, shi->dtype == VSK_DTYPE_I64 ? 8 : 4)) return fail("shared_indices must be aligned to its type");
   if (cs.B * cs.L > INT_MAX - 1024) return fail("%lld rows are too many (2^31 - 1025 at most)", cs.B * cs.L);
-  if (!std::isfinite(p.scale2)) return fail("sm_scale * k_scale is too large");
+  if (!check_scales(p)) return 0;
   const int D = static_cast<int>(cs.D);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -502,6 +508,7 @@ int verify_splitkv_mass(const vsk_tensor* q, const vsk_tensor* ke, const vsk_ten
     return 0;
   const long long T = kvi->shape[0];
   if (T > kMaxEntries) return fail("%lld kv_indices entries are too many (%lld at most)", T, kMaxEntries);
+  if (!check_scales(p)) return 0;
   if (!check_rows(mass, "mass", cs.h_kv)) return 0;
   if (mass->shape[1] != T) return fail("mass must have one column per kv_indices entry (%lld)", T);
   if (mass_in) {

@@ -32,3 +32,15 @@ def test_indices_past_32_bit_positions_are_refused(name):
         else:
             a = mass_args(m=sized(torch.zeros(2, 20), n), kvi=sized(torch.arange(20), n))
             refused(msg, call(name, a, 4, 1.0, 0.0))
+
+
+@pytest.mark.parametrize("k_scale,sm_scale", [(100.0, 3e38), (-100.0, 3e38), (0.1, 3e38), (1e-38, 3.2e38)])
+@pytest.mark.parametrize("name", ["verify_splitkv_mass", "verify_splitkv_shared_fwd"])
+def test_scales_of_keys_and_drafts_beyond_a_float_are_refused(name, k_scale, sm_scale):
+    """Cached keys carry sm_scale k_scale log2 e, drafts sm_scale log2 e: with either infinite every weight is NaN, which
+    kv_evict takes for the largest."""
+    if name == "verify_splitkv_mass":
+        got = call(name, mass_args(), 4, k_scale, sm_scale)
+    else:
+        got = call(name, shared_args(), 4, k_scale, 1.0, sm_scale)
+    refused("too large", got)

@@ -296,7 +296,8 @@ size_t vsk_shared_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv,
  * weight 0 and sets error bit 1.
  *   mass, mass_in   [h_kv, n] float32, n = kv_indices entries, rows contiguous;
  *                   mass_in NULL counts as zeros; it may be mass itself and must
- *                   not overlap it otherwise
+ *                   not overlap it otherwise, nor rows of mass each other
+ *                   (refused)
  *   other arguments and limits as verify_splitkv_fwd (head_dim in {64, 128,
  *                   256}, (h_q/h_kv)*l_ext <= 128, or 64 at 256), n at most
  *                   2^31 - 65536; scales as verify_splitkv_shared_fwd;

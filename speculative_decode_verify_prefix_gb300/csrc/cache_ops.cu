@@ -291,6 +291,39 @@ static bool check_rows(const vsk_tensor* t, const char* name, long long rows) {
   return true;
 }
 
+// The memory of a 1-d or 2-d view: n rows of `bytes` bytes, `pitch` bytes apart.
+struct RowSpan {
+  uintptr_t at;
+  long long n, bytes, pitch;
+};
+static RowSpan row_span(const vsk_tensor* t, long long e) {
+  RowSpan r{reinterpret_cast<uintptr_t>(t->data), 1, e * t->shape[t->ndim - 1], 0};
+  if (t->ndim == 2 && t->shape[0] != 1) {
+    r.n = t->shape[0];
+    r.pitch = e * t->stride[0];
+    if (r.pitch < 0) {  // the same rows from the lowest one on
+      r.at += static_cast<uintptr_t>((r.n - 1) * r.pitch);
+      r.pitch = -r.pitch;
+    }
+  }
+  if (r.bytes == 0) r.n = 0;
+  return r;
+}
+static bool rows_overlap(const RowSpan& x) { return x.n > 1 && x.pitch < x.bytes; }
+// whether a row of x and one of y share a byte
+static bool rows_meet(const RowSpan& x, const RowSpan& y) {
+  if (x.n == 0 || y.n == 0) return false;
+  const long long base = static_cast<long long>(x.at - y.at);
+  for (long long i = 0; i < x.n; ++i) {
+    const long long a = base + i * x.pitch;  // this row against the rows at 0, y.pitch, ...
+    if (a + x.bytes <= 0 || a >= (y.n - 1) * y.pitch + y.bytes) continue;
+    // of the rows that begin before this one ends the last one ends last
+    const long long j = y.pitch > 0 ? std::min(y.n - 1, (a + x.bytes - 1) / y.pitch) : 0;
+    if (a < j * y.pitch + y.bytes) return true;
+  }
+  return false;
+}
+
 }  // namespace vsk
 
 using namespace vsk;
@@ -514,7 +547,10 @@ int verify_splitkv_mass(const vsk_tensor* q, const vsk_tensor* ke, const vsk_ten
   if (mass_in) {
     if (!check_rows(mass_in, "mass_in", cs.h_kv)) return 0;
     if (mass_in->shape[1] != T) return fail("mass_in must have one column per kv_indices entry (%lld)", T);
+    const bool same = mass_in->data == mass->data && (cs.h_kv == 1 || mass_in->stride[0] == mass->stride[0]);
+    if (!same && rows_meet(row_span(mass, 4), row_span(mass_in, 4))) return fail("mass overlaps mass_in");
   }
+  if (rows_overlap(row_span(mass, 4))) return fail("rows of mass overlap");
   if (kb->shape[0] >= 0xFFFFFFFFLL) return fail("a pool of %lld rows is too large", static_cast<long long>(kb->shape[0]));
   if (T == 0) return 1;
   if (kb->shape[0] == 0) return fail("k_buffer has no rows");

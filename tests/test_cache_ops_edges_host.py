@@ -44,3 +44,21 @@ def test_scales_of_keys_and_drafts_beyond_a_float_are_refused(name, k_scale, sm_
     else:
         got = call(name, shared_args(), 4, k_scale, 1.0, sm_scale)
     refused("too large", got)
+
+
+_BIG = torch.zeros(2, 64)
+
+
+@pytest.mark.parametrize("change,msg", [
+    # one column off, one row off, a view that begins inside, rows of one among the other's
+    (dict(m=_BIG[:, 1:21], m_in=_BIG[:, :20]), "mass overlaps mass_in"),
+    (dict(m=_BIG.view(-1)[:84].as_strided((2, 20), (64, 1)), m_in=_BIG.view(-1).as_strided((2, 20), (32, 1), 64)),
+     "mass overlaps mass_in"),
+    (dict(m=_BIG[:, :20], m_in=_BIG[:1, :20].expand(2, 20)), "mass overlaps mass_in"),
+    (dict(m=_BIG[:, :20], m_in=_BIG.view(-1).as_strided((2, 20), (44, 1))), "mass overlaps mass_in"),
+    # rows of mass that share elements
+    (dict(m=_BIG[:1, :20].expand(2, 20)), "rows of mass overlap"),
+    (dict(m=_BIG.view(-1).as_strided((2, 20), (19, 1))), "rows of mass overlap"),
+])
+def test_mass_outputs_that_overlap_are_refused(change, msg):
+    refused(msg, call("verify_splitkv_mass", mass_args(**change), 4, 1.0, 0.0))

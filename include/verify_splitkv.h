@@ -327,9 +327,10 @@ int verify_splitkv_mass(const vsk_tensor* q_extend, const vsk_tensor* k_extend,
  *   freed           of kv_indices' type: the other entries, sequence after
  *                   sequence in their order (n entries always suffice): the
  *                   pool rows that may be reused
- * Outputs must not overlap inputs (refused) nor each other.  An output that is
- * too short is filled and sets error bit 32.  Inconsistent kv_indptr entries
- * give an empty sequence and set bit 2.  workspace as prompt_attn_fwd.  One launch on `stream`. */
+ * Outputs must not overlap inputs, each other or themselves (refused).  An
+ * output that is too short is filled and sets error bit 32.  Inconsistent
+ * kv_indptr entries give an empty sequence and set bit 2.  workspace as
+ * prompt_attn_fwd.  One launch on `stream`. */
 int kv_evict(const vsk_tensor* mass, const vsk_tensor* kv_indptr, const vsk_tensor* kv_indices,
              int64_t budget, int64_t recent, const vsk_tensor* out_kv_indptr,
              const vsk_tensor* out_kv_indices, const vsk_tensor* out_mass,

@@ -617,23 +617,18 @@ int kv_evict(const vsk_tensor* mass, const vsk_tensor* kvp, const vsk_tensor* kv
   if (budget < 1) return fail("budget must be >= 1");
   if (recent < 0 || recent > budget) return fail("recent must be in [0, budget]");
   // the kernel packs while it reads
-  struct Range { const vsk_tensor* t; const char* name; size_t bytes; };
-  auto span2 = [](const vsk_tensor* t) {
-    return t->shape[0] * t->shape[1] == 0 ? size_t{0}
-                                          : static_cast<size_t>(4 * ((t->shape[0] - 1) * t->stride[0] + t->shape[1]));
-  };
-  const Range ins[] = {{kvp, "kv_indptr", 4 * static_cast<size_t>(B + 1)}, {kvi, "kv_indices", ei * static_cast<size_t>(T)},
-                       {mass, "mass", span2(mass)}};
-  const Range outs[] = {{out_kvp, "out_kv_indptr", 4 * static_cast<size_t>(B + 1)},
-                        {out_kvi, "out_kv_indices", ei * static_cast<size_t>(out_kvi->shape[0])},
-                        {out_mass, "out_mass", span2(out_mass)},
-                        {freed, "freed", ei * static_cast<size_t>(freed->shape[0])}};
-  for (const Range& o : outs)
-    for (const Range& i : ins) {
-      const char *a = static_cast<const char*>(o.t->data), *c = static_cast<const char*>(i.t->data);
-      if (o.bytes > 0 && i.bytes > 0 && a < c + i.bytes && c < a + o.bytes)
-        return fail("%s overlaps %s", o.name, i.name);
-    }
+  if (rows_overlap(row_span(out_mass, 4))) return fail("rows of out_mass overlap");
+  struct Named { const char* name; RowSpan span; };
+  const Named ins[] = {{"kv_indptr", row_span(kvp, 4)}, {"kv_indices", row_span(kvi, static_cast<long long>(ei))},
+                       {"mass", row_span(mass, 4)}};
+  const Named outs[] = {{"out_kv_indptr", row_span(out_kvp, 4)}, {"out_kv_indices", row_span(out_kvi, static_cast<long long>(ei))},
+                        {"out_mass", row_span(out_mass, 4)}, {"freed", row_span(freed, static_cast<long long>(ei))}};
+  for (const Named& o : outs) {
+    for (const Named& i : ins)
+      if (rows_meet(o.span, i.span)) return fail("%s overlaps %s", o.name, i.name);
+    for (const Named* x = outs; x != &o; ++x)
+      if (rows_meet(o.span, x->span)) return fail("%s overlaps %s", o.name, x->name);
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   size_t ws_bytes = 0;
   WorkspaceHold hold(workspace);

@@ -148,3 +148,22 @@ def test_every_bad_shared_index_is_flagged(vsk, pool, d, bad):
         c["sh"], c["kvi"] = c["sh"].int(), c["kvi"].int()
         check_attention(run_shared(vsk, c), *shared_want(good, d ** -0.5))
         assert vsk.read_error_flags() == 1
+
+
+# ---------------------------------------------------------------- windows of one buffer
+
+def test_windows_of_one_buffer_that_do_not_meet_are_taken(vsk):
+    """mass beside mass_in, and out_mass beside mass, as column windows of the same rows."""
+    c = shared_case(0, (300, 80), 4, 8, 2, 128, seed=88)
+    t = 380
+    big = torch.rand(2, 2 * t + 100, generator=gen(2), device=DEV)
+    before = big.clone()
+    run_mass(vsk, c, big[:, t:2 * t], mass_in=big[:, :t])
+    base.check_mass(big[:, t:2 * t], base.mass_want(c, 128 ** -0.5), before[:, :t].to(F64))
+    assert torch.equal(big[:, :t], before[:, :t]) and torch.equal(big[:, 2 * t:], before[:, 2 * t:])
+    mass = big[:, :t].clone()
+    out = [torch.zeros(3, dtype=torch.int32, device=DEV), torch.zeros(100, dtype=torch.long, device=DEV),
+           big[:, 2 * t:], torch.zeros(t, dtype=torch.long, device=DEV)]
+    vsk.kv_evict(big[:, :t], c["kvp"], c["kvi"], 50, 5, *out)
+    want = base.evict_want(mass, c["kvi"], (300, 80), 50, 5)
+    assert torch.equal(out[1].cpu(), want[1]) and torch.equal(out[2].cpu(), want[2]) and torch.equal(out[3][:280].cpu(), want[3])

@@ -62,3 +62,17 @@ _BIG = torch.zeros(2, 64)
 ])
 def test_mass_outputs_that_overlap_are_refused(change, msg):
     refused(msg, call("verify_splitkv_mass", mass_args(**change), 4, 1.0, 0.0))
+
+
+_OUT = torch.arange(64)
+
+
+@pytest.mark.parametrize("change,msg", [
+    (dict(oi=_OUT[:16], f=_OUT[10:30]), "freed overlaps out_kv_indices"),
+    (dict(om=_BIG[:1, :16].expand(2, 16)), "rows of out_mass overlap"),
+    (dict(om=_BIG.view(-1).as_strided((2, 16), (15, 1))), "rows of out_mass overlap"),
+    (dict(m=_BIG[:, :20], om=_BIG[:, 19:35]), "out_mass overlaps mass"),
+    (dict(kvp=_OUT.int()[:3], op=_OUT.int()[3:6], kvi=_OUT[:20], f=_OUT[19:39]), "freed overlaps kv_indices"),
+])
+def test_evict_outputs_that_overlap_are_refused(change, msg):
+    refused(msg, call("kv_evict", evict_args(**change)))

@@ -78,6 +78,7 @@ def can_handle(q_extend, k_extend, v_extend, k_buffer, v_buffer, qo_indptr, kv_i
 
 _WS = {}
 _WS_SIZE = {}  # (device, max_bs, h_q, h_kv, head_dim, v_head_dim, l_ext) -> bytes
+_SHARED_SIZE = {}  # (device, max_bs, h_q, h_kv, head_dim, l_ext) -> bytes, behind a shared prefix
 _WS_LOCK = threading.Lock()
 
 
@@ -274,14 +275,22 @@ def read_error_flags(workspace=None, stream=None) -> int:
     return int(flags.value)
 
 
+def _forget_sizes() -> None:
+    """After tuning that moves the workspace bounds."""
+    _WS_SIZE.clear()
+    _SHARED_SIZE.clear()
+
+
 def set_tuning(num_ctas: int = 0, min_tokens_per_cta: int = 0) -> None:
     """Override the CTA count / minimum tokens per CTA (0 = defaults)."""
     _native.lib().vsk_set_tuning(int(num_ctas), int(min_tokens_per_cta))
+    _forget_sizes()
 
 
 def set_tuning_shape(max_ring_stages: int = 0, max_kv_heads_per_cta: int = 0) -> None:
     """Override ring depth / KV heads per CTA (0 = defaults)."""
     _native.lib().vsk_set_tuning_shape(int(max_ring_stages), int(max_kv_heads_per_cta))
+    _forget_sizes()
 
 
 def set_tuning_tiles(tiles_per_warp: int = 0) -> None:

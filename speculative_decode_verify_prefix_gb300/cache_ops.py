@@ -16,7 +16,7 @@ import struct
 import torch
 
 from . import _native
-from .api import _DT, _WS, _WS_LOCK, _coerce
+from .api import _DT, _SHARED_SIZE as _SIZES, _WS, _WS_LOCK, _coerce
 
 # A vsk_tensor: data, dtype, ndim, shape[3], stride[3].  The views of a call are
 # packed into one buffer: a fraction of the time of filling a ctypes structure
@@ -120,9 +120,6 @@ def prompt_attn_fwd(q, k, v, o, qo_indptr, sm_scale=None, workspace=None, stream
     as they were.  ``workspace``: 256 bytes or more (the error word)."""
     _run("prompt_attn_fwd", ("q", "k", "v", "o", "qo_indptr"), (q, k, v, o, qo_indptr),
          (0.0 if sm_scale is None else float(sm_scale),), stream, workspace)
-
-
-_SIZES = {}  # (device, max_bs, h_q, h_kv, head_dim, l_ext) -> bytes
 
 
 def shared_workspace_size(max_bs, h_q, h_kv, head_dim, l_ext) -> int:

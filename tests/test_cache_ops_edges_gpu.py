@@ -167,3 +167,31 @@ def test_windows_of_one_buffer_that_do_not_meet_are_taken(vsk):
     vsk.kv_evict(big[:, :t], c["kvp"], c["kvi"], 50, 5, *out)
     want = base.evict_want(mass, c["kvi"], (300, 80), 50, 5)
     assert torch.equal(out[1].cpu(), want[1]) and torch.equal(out[2].cpu(), want[2]) and torch.equal(out[3][:280].cpu(), want[3])
+
+
+# ---------------------------------------------------------------- tuning
+
+def test_workspaces_follow_the_tuned_grid(vsk):
+    """More CTAs than the workspace of an earlier call was sized for: the size is asked again."""
+    c = shared_case(300, (300, 80), 4, 8, 2, 128, seed=83)
+    o = torch.empty_like(c["q"])
+
+    def verify():
+        vsk.verify_splitkv_fwd(c["q"], c["ke"], c["ve"], o, c["kb"], c["vb"], c["qo"], c["kvp"], c["kvi"], None, True, None,
+                               4, 1.0, 1.0)
+        return o
+
+    own = dict(c, sh=c["sh"][:0])
+    stream = torch.cuda.Stream()  # a workspace of its own, not grown by other tests
+    with torch.cuda.stream(stream):
+        stream.wait_stream(torch.cuda.default_stream())
+        run_shared(vsk, c)
+        verify()
+        vsk.set_tuning(num_ctas=40 * torch.cuda.get_device_properties(0).multi_processor_count)
+        try:
+            check_attention(verify(), *shared_want(own, 128 ** -0.5))
+            check_attention(run_shared(vsk, c), *shared_want(c, 128 ** -0.5))
+        finally:
+            vsk.set_tuning()
+        check_attention(run_shared(vsk, c), *shared_want(c, 128 ** -0.5))
+        assert vsk.read_error_flags() == 0

@@ -76,3 +76,23 @@ _OUT = torch.arange(64)
 ])
 def test_evict_outputs_that_overlap_are_refused(change, msg):
     refused(msg, call("kv_evict", evict_args(**change)))
+
+
+@pytest.mark.parametrize("change", [lambda: vsk.set_tuning(num_ctas=7), lambda: vsk.set_tuning(),
+                                    lambda: vsk.set_tuning_shape(max_kv_heads_per_cta=1)])
+def test_workspace_sizes_are_asked_again_after_tuning(change):
+    """What sizes a workspace is process-wide tuning too, so a size kept from before it says nothing."""
+    from speculative_decode_verify_prefix_gb300 import api, cache_ops
+
+    kept = dict(api._WS_SIZE), dict(cache_ops._SIZES)
+    try:
+        api._WS_SIZE["verify"] = cache_ops._SIZES["shared"] = 1
+        change()
+        assert "verify" not in api._WS_SIZE and "shared" not in cache_ops._SIZES
+    finally:
+        vsk.set_tuning()
+        vsk.set_tuning_shape()
+        api._WS_SIZE.clear()
+        cache_ops._SIZES.clear()
+        api._WS_SIZE.update(kept[0])
+        cache_ops._SIZES.update(kept[1])

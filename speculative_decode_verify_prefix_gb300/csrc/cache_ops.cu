@@ -535,9 +535,8 @@ int verify_splitkv_mass(const vsk_tensor* q, const vsk_tensor* ke, const vsk_ten
   clear_error();
   Params p;
   CallShape cs;
-  // the values play no part: the keys stand in for them in the checks, the queries for the output
   if (!prepare_verify(q, ke, ke, q, kb, kb, qo, kvp, kvi, 1, max_len_extend, k_scale, 1.f, sm_scale, nullptr, nullptr,
-                      nullptr, p, cs))
+                      nullptr, p, cs, true))
     return 0;
   const long long T = kvi->shape[0];
   if (T > kMaxEntries) return fail("%lld kv_indices entries are too many (%lld at most)", T, kMaxEntries);

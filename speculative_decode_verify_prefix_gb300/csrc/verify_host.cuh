@@ -53,12 +53,13 @@ class WorkspaceHold {
 bool make_plan(long long h_q, long long h_kv, long long D, long long L, bool fp8, Plan& pl, long long total_tokens,
                int tiles, long long DV = 0, int hc_cap = 0);
 WsLayout ws_layout(long long n_cta, long long B, const Plan& pl, long long DV);
-// checks and parameter block of a flat call (no launch, no workspace)
+// checks and parameter block of a flat call (no launch, no workspace);
+// keys_only: the call has no values, ke, kb and q stand in for ve, vb and o
 int prepare_verify(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tensor* ve, const vsk_tensor* o,
                    const vsk_tensor* kb, const vsk_tensor* vb, const vsk_tensor* qo, const vsk_tensor* kvp,
                    const vsk_tensor* kvi, int is_causal, int64_t max_len_extend, float k_scale, float v_scale,
                    float sm_scale, const vsk_tensor* cm, const vsk_tensor* mi, const vsk_tensor* ocl, Params& p,
-                   CallShape& cs);
+                   CallShape& cs, bool keys_only = false);
 // A prefix stream alone (no draft block, partials left in the workspace): its
 // plan, and the launch.
 struct StreamOnly {

@@ -364,10 +364,12 @@ bool check_1d(const vsk_tensor* t, const char* name) {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // can_handle of the "verify_splitkv.py" page plus this build's limits.
+// keys_only: a call without values (the keys stand in for them): its refusals
+// name none.
 bool gate(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tensor* ve, const vsk_tensor* kb,
           const vsk_tensor* vb, const vsk_tensor* qo, const vsk_tensor* kvp, const vsk_tensor* kvi,
           int is_causal, long long mle, long long sliding_window, int has_sinks, float logit_cap,
-          long long xai_len) {
+          long long xai_len, bool keys_only = false) {
   // features the kernel does not implement
   if (has_sinks) return fail("attention sinks are not supported");
   if (sliding_window > 0) return fail("sliding_window_size > 0 is not supported");
@@ -381,7 +383,7 @@ bool gate(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tensor* ve, const
   const long long h_q = q->shape[1], h_kv = ke->shape[1];
   if (h_kv == 0 || h_q % h_kv != 0) return fail("h_q (%lld) is not a multiple of h_kv (%lld)", h_q, h_kv);
   if (kb->shape[1] != h_kv || vb->shape[1] != h_kv || ve->shape[1] != h_kv)
-    return fail("KV head count mismatch between k_extend, v_extend and the buffers");
+    return fail("KV head count mismatch between %s", keys_only ? "k_extend and k_buffer" : "k_extend, v_extend and the buffers");
   const long long D = q->shape[2], Dv = ve->shape[2];
   if (ke->shape[2] != D || kb->shape[2] != D) return fail("head_dim mismatch between q, k_extend and k_buffer");
   if (vb->shape[2] != Dv) return fail("v_head_dim mismatch between v_extend and v_buffer");
@@ -390,15 +392,15 @@ bool gate(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tensor* ve, const
   if (kvp->shape[0] != bs + 1) return fail("kv_indptr must have B+1 entries");
   if (mle < 1) return fail("max_len_extend must be >= 1");
   if (q->shape[0] != bs * mle) return fail("ragged extend: q has %lld rows, expected B*max_len_extend = %lld", q->shape[0], bs * mle);
-  if (ke->shape[0] != q->shape[0] || ve->shape[0] != q->shape[0]) return fail("k_extend/v_extend rows differ from q_extend");
+  if (ke->shape[0] != q->shape[0] || ve->shape[0] != q->shape[0]) return fail("%s rows differ from q_extend", keys_only ? "k_extend" : "k_extend/v_extend");
   if (kb->shape[0] != vb->shape[0]) return fail("k_buffer and v_buffer pools differ in size");
   // this build's limits
   if (D != 64 && D != 128 && D != 256) return fail("head_dim %lld not in {64, 128, 256}", D);
   if (Dv != 64 && Dv != 128 && Dv != 256) return fail("v_head_dim %lld not in {64, 128, 256}", Dv);
   if (q->dtype != VSK_DTYPE_BF16 || ke->dtype != VSK_DTYPE_BF16 || ve->dtype != VSK_DTYPE_BF16)
-    return fail("q_extend, k_extend and v_extend must be bf16");
+    return fail("%s must be bf16", keys_only ? "q_extend and k_extend" : "q_extend, k_extend and v_extend");
   if (kb->dtype != vb->dtype || (kb->dtype != VSK_DTYPE_BF16 && kb->dtype != VSK_DTYPE_FP8E4M3))
-    return fail("k_buffer and v_buffer must both be bf16 or both fp8 e4m3");
+    return fail("%s", keys_only ? "k_buffer must be bf16 or fp8 e4m3" : "k_buffer and v_buffer must both be bf16 or both fp8 e4m3");
   if (qo->dtype != VSK_DTYPE_I32 || kvp->dtype != VSK_DTYPE_I32) return fail("indptr arrays must be int32");
   if (kvi->dtype != VSK_DTYPE_I32 && kvi->dtype != VSK_DTYPE_I64) return fail("kv_indices must be int32 or int64");
   const long long R = (h_q / h_kv) * mle;
@@ -407,11 +409,11 @@ bool gate(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tensor* ve, const
   const size_t ek = kb->dtype == VSK_DTYPE_BF16 ? 2 : 1;
   for (const vsk_tensor* t : {kb, vb}) {
     if (!aligned(t->data, 16) || (t->stride[0] * ek) % 16 != 0 || (t->stride[1] * ek) % 16 != 0)
-      return fail("K/V pool rows must be 16-byte aligned");
+      return fail("%s pool rows must be 16-byte aligned", keys_only ? "K" : "K/V");
   }
   for (const vsk_tensor* t : {q, ke, ve}) {
     if (!aligned(t->data, 4) || (t->stride[0] % 2) != 0 || (t->stride[1] % 2) != 0)
-      return fail("q_extend/k_extend/v_extend must be 4-byte aligned with even strides");
+      return fail("%s must be 4-byte aligned with even strides", keys_only ? "q_extend/k_extend" : "q_extend/k_extend/v_extend");
   }
   return true;
 }
@@ -996,15 +998,15 @@ int prepare_verify(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tensor* 
                    const vsk_tensor* kb, const vsk_tensor* vb, const vsk_tensor* qo, const vsk_tensor* kvp,
                    const vsk_tensor* kvi, int is_causal, int64_t max_len_extend, float k_scale, float v_scale,
                    float sm_scale, const vsk_tensor* cm, const vsk_tensor* mi, const vsk_tensor* ocl, Params& p,
-                   CallShape& cs) {
-  if (!gate(q, ke, ve, kb, vb, qo, kvp, kvi, is_causal, max_len_extend, -1, 0, 0.f, -1)) return 0;
+                   CallShape& cs, bool keys_only) {
+  if (!gate(q, ke, ve, kb, vb, qo, kvp, kvi, is_causal, max_len_extend, -1, 0, 0.f, -1, keys_only)) return 0;
   if (!check_3d(o, "o_extend")) return 0;
   if (o->dtype != VSK_DTYPE_BF16 || o->shape[0] != q->shape[0] || o->shape[1] != q->shape[1] ||
       o->shape[2] != ve->shape[2])
     return fail("o_extend must be bf16 [B*l_ext, h_q, v_head_dim]");
   if (!aligned(o->data, 4) || (o->stride[0] % 2) != 0 || (o->stride[1] % 2) != 0)
     return fail("o_extend must be 4-byte aligned with even strides");
-  if (!std::isfinite(k_scale) || !std::isfinite(v_scale)) return fail("k_scale and v_scale must be finite");
+  if (!std::isfinite(k_scale) || !std::isfinite(v_scale)) return fail("%s must be finite", keys_only ? "k_scale" : "k_scale and v_scale");
 
   memset(&p, 0, sizeof p);
   p.q = static_cast<const __nv_bfloat16*>(q->data);

@@ -96,3 +96,25 @@ def test_workspace_sizes_are_asked_again_after_tuning(change):
         cache_ops._SIZES.clear()
         api._WS_SIZE.update(kept[0])
         cache_ops._SIZES.update(kept[1])
+
+
+def _odd(t):
+    """The same values one element off the alignment that calls want."""
+    flat = torch.zeros(t.numel() + 1, dtype=t.dtype)
+    return flat[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("change,k_scale,msg", [
+    (dict(kb=bf(50, 2, 64).half()), 1.0, "k_buffer must be bf16 or fp8 e4m3"), (dict(ke=bf(8, 2, 64).half()), 1.0, "q_extend and k_extend must be bf16"),
+    (dict(kb=bf(50, 3, 64)), 1.0, "between k_extend and k_buffer"), (dict(ke=bf(7, 2, 64)), 1.0, "k_extend rows differ"),
+    (dict(kb=_odd(bf(50, 2, 64))), 1.0, "K pool rows"), (dict(ke=_odd(bf(8, 2, 64))), 1.0, "q_extend/k_extend must be 4-byte"),
+    (dict(ke=bf(8, 2, 128)), 1.0, "head_dim mismatch"), (dict(q=_odd(bf(8, 8, 64))), 1.0, "4-byte"), (dict(), float("inf"), "k_scale must be finite"),
+    (dict(kb=bf(50, 2, 64, 1)), 1.0, "k_buffer must be 3-d"),
+])
+def test_mass_refusals_name_its_own_arguments(change, k_scale, msg):
+    """The weights call has no values and no output rows."""
+    assert call("verify_splitkv_mass", mass_args(**change), 4, k_scale, 0.0) == 0
+    said = vsk.last_error()
+    assert msg in said, said
+    for other in ("v_extend", "v_buffer", "v_head_dim", "v_scale", "o_extend"):
+        assert other not in said, said

@@ -244,9 +244,13 @@ int verify_splitkv_paged_write_fwd(const vsk_tensor* q, const vsk_tensor* k_new,
  *   qo_indptr  [B+1] int32.  Rows of o outside every sequence are left as they
  *              were.  An entry pair that decreases or leaves [0, N] makes that
  *              sequence empty and sets error bit 4.
- *   workspace  256 bytes or more, 256-byte aligned (the error word is at its
- *              start; the rules of verify_splitkv_fwd apply), or NULL for the
- *              library-owned one.
+ *   workspace  256 bytes or more, 256-byte aligned, or NULL for the
+ *              library-owned one.  The error word is at its start, and 64 bytes
+ *              in are the counters by which the CTAs draw their work, which
+ *              every call leaves at zero: the rules of verify_splitkv_fwd apply
+ *              (zero-filled before its first use, one for each of the calls
+ *              that may overlap on the GPU).  With counters that are not zero,
+ *              rows of o are left out.
  * K and V values that a row must not see (later tokens, other sequences) never
  * reach it, infinities and NaN included.  Returns 1 once the kernel is
  * enqueued on `stream` (or there is no row), 0 with nothing enqueued

@@ -6,6 +6,12 @@ As in api.py: argument marshalling only, every step of the computation runs in
 the library's kernels, on the given stream (default: the current one of the
 tensors' device) and without synchronising.  A call that the library rejects
 raises ValueError with its message and launches nothing.
+
+``workspace``: a contiguous tensor on the tensors' device, 256-byte aligned,
+zero-filled once before its first use and then left to the calls, which keep
+counters in it between them; calls that may overlap on the GPU (two streams, two
+graphs) must each have their own.  None: the cached one of (device, stream);
+a call that is captured into a graph needs its own.
 """
 from __future__ import annotations
 
@@ -117,7 +123,9 @@ def prompt_attn_fwd(q, k, v, o, qo_indptr, sm_scale=None, workspace=None, stream
     {64, 128, 256}; ``qo_indptr``: [B+1] int32, sequence b owns rows
     qo_indptr[b] .. qo_indptr[b+1] - 1, of any lengths.  Row i of a sequence
     attends to its rows t <= i.  Rows of ``o`` outside every sequence are left
-    as they were.  ``workspace``: 256 bytes or more (the error word)."""
+    as they were.  ``workspace``: 256 bytes or more (the error word and the
+    counters by which CTAs draw their work: in a buffer that was not zeroed, or
+    that another call uses meanwhile, rows would be left out)."""
     _run("prompt_attn_fwd", ("q", "k", "v", "o", "qo_indptr"), (q, k, v, o, qo_indptr),
          (0.0 if sm_scale is None else float(sm_scale),), stream, workspace)
 
@@ -134,7 +142,8 @@ def verify_splitkv_shared_fwd(q_extend, k_extend, v_extend, o_extend, k_buffer, 
     """``verify_splitkv_fwd`` (causal drafts) for a batch whose sequences share
     a prefix: every sequence's prefix is the pool rows ``shared_indices``
     ([S] int32 or int64) followed by its own ``kv_indices`` rows.  The shared
-    rows are read for the whole batch at once, not per sequence."""
+    rows are read for the whole batch at once, not per sequence.
+    ``workspace``: ``shared_workspace_size`` bytes or more."""
     mle = int(max_len_extend)
 
     def need():
@@ -161,9 +170,10 @@ def verify_splitkv_mass(q_extend, k_extend, k_buffer, qo_indptr, kv_indptr, kv_i
                         k_scale=1.0, sm_scale=None, mass_in=None, workspace=None, stream=None) -> None:
     """Attention weight of the cached keys: writes to ``mass`` ([h_kv,
     len(kv_indices)] float32) ``mass_in`` (None: zeros; may be ``mass`` itself)
-    plus, for every entry of ``kv_indices``, the sum over the draft rows and the
-    query heads of the KV head of the softmax weight its key has in
-    ``verify_splitkv_fwd`` (causal drafts)."""
+    plus, for every entry of ``kv_indices`` that belongs to a sequence, the sum
+    over the draft rows and the query heads of the KV head of the softmax weight
+    its key has in ``verify_splitkv_fwd`` (causal drafts); other columns are left
+    as they were.  ``workspace``: 256 bytes or more (the error word)."""
     _run("verify_splitkv_mass",
          ("q_extend", "k_extend", "k_buffer", "qo_indptr", "kv_indptr", "kv_indices", "mass_in", "mass"),
          (q_extend, k_extend, k_buffer, qo_indptr, kv_indptr, kv_indices, mass_in, mass),
@@ -179,7 +189,8 @@ def kv_evict(mass, kv_indptr, kv_indices, budget, recent, out_kv_indptr, out_kv_
     Writes ``out_kv_indptr`` ([B+1] int32), the kept entries to
     ``out_kv_indices`` and their weights to ``out_mass`` (both packed; min(n, B *
     budget) columns always suffice) and the others, whose pool rows may be
-    reused, to ``freed`` (out_kv_indptr and kv_indptr tell how many)."""
+    reused, to ``freed`` (out_kv_indptr and kv_indptr tell how many).
+    ``workspace``: 256 bytes or more (the error word)."""
     _run("kv_evict",
          ("mass", "kv_indptr", "kv_indices", "out_kv_indptr", "out_kv_indices", "out_mass", "freed"),
          (mass, kv_indptr, kv_indices, out_kv_indptr, out_kv_indices, out_mass, freed), (int(budget), int(recent)),

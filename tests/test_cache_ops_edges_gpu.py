@@ -195,3 +195,122 @@ def test_workspaces_follow_the_tuned_grid(vsk):
             vsk.set_tuning()
         check_attention(run_shared(vsk, c), *shared_want(c, 128 ** -0.5))
         assert vsk.read_error_flags() == 0
+
+
+# ---------------------------------------------------------------- prompts at once
+
+def test_prompts_that_draw_their_work_on_two_streams_and_from_two_graphs(vsk):
+    """Several items a CTA, so that the counters in the workspace are drawn from, in calls that overlap: on two streams
+    and replayed from two graphs, each with its workspace."""
+    d, hq, hk, lens = 64, 16, 8, [((700,) * 12, 300, 64), ((33, 900, 5) * 9, 500, 1)]
+    cases = []
+    for i, (a, b, c) in enumerate(lens):
+        n = [*a, b, c]
+        assert sum(-(-x // 128) for x in n) * hk > 2 * torch.cuda.get_device_properties(0).multi_processor_count
+        q, k, v, p = base.prompt_case(n, hq, hk, d, seed=71 + i)
+        want = torch.full_like(q, float("nan"))
+        vsk.prompt_attn_fwd(q, k, v, want, p)
+        check_attention(want, *base.prompt_want(q, k, v, n, d ** -0.5))
+        cases.append((q, k, v, p, want))
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (q, k, v, p, _w) in zip(streams, cases):
+            with torch.cuda.stream(s):
+                outs.append(torch.full_like(q, float("nan")))
+                vsk.prompt_attn_fwd(q, k, v, outs[-1], p)
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert torch.equal(o, cases[i % 2][4]), i
+    graphs, graph_outs, spaces = [], [], [torch.zeros(256, dtype=torch.uint8, device=DEV) for _ in cases]
+    for (q, k, v, p, _w), ws in zip(cases, spaces):
+        o = torch.full_like(q, float("nan"))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            vsk.prompt_attn_fwd(q, k, v, o, p, workspace=ws)
+        graphs.append(g)
+        graph_outs.append(o)
+    for _ in range(10):
+        for o in graph_outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, c[4]) for o, c in zip(graph_outs, cases))
+    assert all(int(ws.sum()) == 0 for ws in spaces)  # no error, the counters back at zero
+
+
+# ---------------------------------------------------------------- every key counts
+#
+# With queries of zero all n visible keys weigh the same.  Key t has the value 1
+# in one place of (KV head, column), t mod (h_kv D), and 0 elsewhere, so every
+# output is count / n with its own count of keys: exact sums (P is a power of
+# two), then 1 / n and the product in 32 bits, joined pieces a few more (2^-18
+# of itself is ample), and the rounding to bf16.  Where at most 64 keys share a
+# place a key left out or taken twice moves the output by 1.5 % or more, further
+# than bf16 steps are apart (2^-7).
+
+
+def markers(t, hk, d, dtype):
+    v = torch.zeros(len(t), hk * d, device=DEV)
+    v[torch.arange(len(t), device=DEV), t % (hk * d)] = 1
+    return v.view(len(t), hk, d).to(dtype)
+
+
+def check_counts(got, count, n):
+    """got [rows, h, d] bf16 against count / n, [rows, h, d] and [rows]."""
+    x = count.to(F64) / n.to(F64)[:, None, None]
+    lo, hi = (x * (1 - 2.0 ** -18)).to(BF16), (x * (1 + 2.0 ** -18)).to(BF16)
+    bad = ~((got >= lo) & (got <= hi))
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:3].tolist())
+
+
+def counts_upto(rows, hk, d, start=0):
+    """[rows, hk * d]: how many of keys start .. start + i are in each place, for i < rows."""
+    c = torch.zeros(rows, hk * d, dtype=torch.int32, device=DEV)
+    c[torch.arange(rows, device=DEV), (start + torch.arange(rows, device=DEV)) % (hk * d)] = 1
+    return c.cumsum(0)
+
+
+@pytest.mark.parametrize("lens,hq,hk,d", [((4097,), 4, 1, 128), ((127, 128, 129, 255, 256, 257, 1, 2), 2, 2, 64), ((2500, 1), 6, 2, 256),
+                                          ((3000, 700), 4, 4, 64), ((1025,), 16, 1, 256), ((1300,), 5, 5, 128)])
+def test_prompt_counts_every_key(vsk, lens, hq, hk, d):
+    n = sum(lens)
+    q, k = torch.zeros(n, hq, d, dtype=BF16, device=DEV), normal(gen(3), n, hk, d)
+    t = torch.cat([torch.arange(x, device=DEV) for x in lens])
+    assert max(lens) <= 64 * hk * d
+    o = torch.full_like(q, float("nan"))
+    vsk.prompt_attn_fwd(q, k, markers(t, hk, d, BF16), o, indptr(lens))
+    count = torch.cat([counts_upto(x, hk, d) for x in lens]).view(n, hk, 1, d).expand(n, hk, hq // hk, d).reshape(n, hq, d)
+    check_counts(o, count, t + 1)
+    assert vsk.read_error_flags() == 0
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("s,own,l,hq,hk,d", [
+    (40000, (0, 7, 0), 4, 16, 4, 256), (40000, (900, 0, 33), 4, 32, 8, 128), (20000, (5,) * 9, 3, 8, 8, 64), (0, (5000, 1, 128), 4, 16, 2, 256),
+    (129, (300, 64, 65, 0), 2, 8, 2, 128), (8191, (0,) * 70, 4, 8, 2, 128), (6000, (0, 1) * 20, 4, 16, 1, 256), (255, (0,), 1, 1, 1, 64),
+])
+def test_shared_counts_every_key(vsk, s, own, l, hq, hk, d, pool):
+    c = shared_case(s, own, l, hq, hk, d, pool, seed=89)
+    assert s + max(own) + l <= 64 * hk * d
+    c["q"].zero_()
+    # a key's place goes by its position behind the shared prefix: keys, then drafts
+    place = torch.empty(len(c["kb"]), dtype=torch.long, device=DEV)
+    place[c["sh"]] = torch.arange(s, device=DEV)
+    at = 0
+    for n in own:
+        place[c["kvi"][at:at + n]] = s + torch.arange(n, device=DEV)
+        at += n
+    c["vb"] = markers(place, hk, d, c["vb"].dtype)
+    t = torch.cat([s + n + torch.arange(l, device=DEV) for n in own])
+    c["ve"] = markers(t, hk, d, BF16)
+    count = []
+    for n in own:
+        total = torch.bincount(torch.arange(s + n, device=DEV) % (hk * d), minlength=hk * d)
+        count.append(total + counts_upto(l, hk, d, s + n))
+    count = torch.cat(count).view(-1, hk, 1, d).expand(-1, hk, hq // hk, d).reshape(-1, hq, d)
+    check_counts(run_shared(vsk, c), count, t + 1)
+    assert vsk.read_error_flags() == 0

@@ -118,3 +118,13 @@ def test_mass_refusals_name_its_own_arguments(change, k_scale, msg):
     assert msg in said, said
     for other in ("v_extend", "v_buffer", "v_head_dim", "v_scale", "o_extend"):
         assert other not in said, said
+
+
+def test_outputs_of_neighbouring_key_counts_are_told_apart():
+    """The GPU tests that count keys take bf16 outputs within 2^-18 of count / n: with up to 64 keys of a place, one key
+    more or less is outside."""
+    count = torch.arange(0, 66, dtype=torch.float64)
+    for n in [*range(1, 300), 4097, 20000, 40008, 65537, *torch.randint(300, 70000, (2000,), generator=torch.manual_seed(1)).tolist()]:
+        x = count / n
+        lo, hi = (x * (1 - 2.0 ** -18)).bfloat16(), (x * (1 + 2.0 ** -18)).bfloat16()
+        assert bool((hi[:-1] < lo[1:]).all()), n

@@ -244,6 +244,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// The larger magnitude of a bf16 pair (bit patterns order like magnitudes) for a
+// scale that rows share: infinities and NaN count as 0, or one row that holds
+// any would scale its neighbours' numbers away.
+__device__ __forceinline__ unsigned finite_mag_bf16x2(uint32_t w) {
+  const unsigned lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
+  return max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u);
+}
 __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
   __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&w);
   return __bfloat1622float2(v);
@@ -411,7 +418,7 @@ __device__ __forceinline__ int load_q(const Params& p, const Seg& s, int hc, int
 // permuted within each 16-wide block (logical k 2j, 2j+1 -> d 4j, 4j+1 and
 // k 2j+8, 2j+9 -> d 4j+2, 4j+3), the order in which K fragments come straight
 // out of e4m3 rows.  The tile is scaled by 2^-sh (exact), sh chosen so that
-// its largest |q| stays below 2^15, inside the f16 range; returns 2^sh.
+// its largest finite |q| stays below 2^15, inside the f16 range; returns 2^sh.
 template <int KS>
 __device__ __forceinline__ float load_q_f16(const Params& p, const Seg& s, int hc, int r0, int r1, int j,
                                              bool flag_err, uint32_t (&qf)[KS][4], int d0 = 0) {
@@ -433,7 +440,7 @@ __device__ __forceinline__ float load_q_f16(const Params& p, const Seg& s, int h
     qf[kk][1] = v1 ? ld_u32(q1 + kk * 16 + 4 * j) : 0u;
     qf[kk][3] = v1 ? ld_u32(q1 + kk * 16 + 4 * j + 2) : 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx = max(mx, max(qf[kk][i] & 0x7FFFu, (qf[kk][i] >> 16) & 0x7FFFu));
+    for (int i = 0; i < 4; ++i) mx = max(mx, finite_mag_bf16x2(qf[kk][i]));
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
   const int ex = static_cast<int>(mx >> 7) - 127;  // exponent of the largest |q|

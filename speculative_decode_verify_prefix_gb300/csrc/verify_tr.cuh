@@ -260,12 +260,12 @@ __device__ __forceinline__ float tr_load_q(const Params& p, const Seg& s, unsign
     }
     return p.scale2;
   } else {
-    // largest |q| of the piece's rows (bf16 bit patterns order like magnitudes)
+    // largest finite |q| of the piece's rows
     unsigned mx = 0;
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
 #pragma unroll
-      for (int w = 0; w < 4; ++w) mx = max(mx, max(v[i][w] & 0x7FFFu, (v[i][w] >> 16) & 0x7FFFu));
+      for (int w = 0; w < 4; ++w) mx = max(mx, finite_mag_bf16x2(v[i][w]));
     mx = __reduce_max_sync(0xffffffffu, mx);
     if ((tw & 31) == 0) red_u[tw >> 5] = mx;
     named_bar_sync(1, tr::kSmThreads);
@@ -283,7 +283,9 @@ __device__ __forceinline__ float tr_load_q(const Params& p, const Seg& s, unsign
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const float2 f = unpack_bf16(v[i][w]);
-        const float x0 = f.x * up, x1 = f.y * up;
+        // (e4m3 has no infinity and would end at 448: an infinite query makes its row's scores infinite
+        // of both signs, so its softmax is NaN, which x - x makes of it here)
+        const float x0 = f.x * up + (f.x - f.x), x1 = f.y * up + (f.y - f.y);
         const unsigned short h = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
         const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3);
         const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hr));

@@ -314,3 +314,171 @@ def test_shared_counts_every_key(vsk, s, own, l, hq, hk, d, pool):
     count = torch.cat(count).view(-1, hk, 1, d).expand(-1, hk, hq // hk, d).reshape(-1, hq, d)
     check_counts(run_shared(vsk, c), count, t + 1)
     assert vsk.read_error_flags() == 0
+
+
+# ---------------------------------------------------------------- calls the documentation allows
+
+@pytest.mark.parametrize("hq,hk,d", [(6, 2, 64), (8, 2, 128), (16, 2, 256), (5, 5, 128)])
+def test_prompt_written_over_its_queries(vsk, hq, hk, d):
+    lens = (300, 1, 129, 500, 64)
+    q, k, v, p = base.prompt_case(lens, hq, hk, d, seed=101, extra=4)
+    want, a = base.prompt_want(q[:994], k[:994], v[:994], lens, d ** -0.5)
+    tail = q[994:].clone()
+    vsk.prompt_attn_fwd(q, k, v, q, p)
+    check_attention(q[:994], want, a)
+    assert torch.equal(q[994:], tail)
+
+
+def test_prompt_sequences_with_rows_between_them(vsk):
+    q, k, v, _ = base.prompt_case((400,), 4, 2, 128, seed=102)
+    k[:7], v[:7] = float("nan"), float("nan")  # rows before the first sequence
+    o = torch.full_like(q, 7.0)
+    vsk.prompt_attn_fwd(q, k, v, o, torch.tensor([7, 7, 150, 399], dtype=torch.int32, device=DEV))
+    want, a = base.prompt_want(q[7:399], k[7:399], v[7:399], (143, 249), 128 ** -0.5)
+    check_attention(o[7:399], want, a)
+    assert bool((o[:7] == 7.0).all()) and bool((o[399:] == 7.0).all())
+    assert vsk.read_error_flags() == 0
+
+
+@pytest.mark.parametrize("pool,d,hq,hk", [("bf16", 64, 6, 3), ("bf16", 128, 8, 2), ("e4m3", 128, 8, 2), ("bf16", 256, 16, 2), ("e4m3", 256, 16, 2)])
+@pytest.mark.parametrize("shift", [0, 2])
+def test_strided_drafts_and_pools(vsk, pool, d, hq, hk, shift):
+    """Drafts as windows of one projection (4-byte aligned where shift is 2), pools as windows of wider rows."""
+    c = shared_case(300, (40, 0, 99), 4, hq, hk, d, pool, seed=103)
+    n = len(c["q"])
+    wide = normal(gen(5), n * (hq + 2 * hk) * d + shift)[shift:].view(n, hq + 2 * hk, d)
+    c["q"], c["ke"], c["ve"] = wide[:, :hq], wide[:, hq:hq + hk], wide[:, hq + hk:]
+    both = torch.cat([c["kb"].float(), c["vb"].float()], 1).to(c["kb"].dtype)
+    c["kb"], c["vb"] = both[:, :hk], both[:, hk:]
+    space = torch.full((n * (hq + 1) * d + shift,), 7.0, dtype=BF16, device=DEV)
+    o = space[shift:].view(n, hq + 1, d)[:, 1:]
+    vsk.verify_splitkv_shared_fwd(c["q"], c["ke"], c["ve"], o, c["kb"], c["vb"], c["qo"], c["kvp"], c["kvi"], c["sh"], 4)
+    check_attention(o, *shared_want(c, d ** -0.5))
+    assert bool((space[shift:].view(n, hq + 1, d)[:, 0] == 7.0).all())
+    base.check_mass(run_mass(vsk, c, torch.empty(hk, 139, device=DEV)), base.mass_want(c, d ** -0.5))
+    assert vsk.read_error_flags() == 0
+
+
+def test_padded_indices_are_not_looked_at(vsk):
+    """kv_indices longer than the sequences, as a captured program keeps it: what lies behind is no index."""
+    c = shared_case(200, (70, 0, 33), 4, 8, 2, 128, seed=104)
+    padded = dict(c, kvi=torch.cat([c["kvi"], c["kvi"].new_full((400,), -9)]))
+    check_attention(run_shared(vsk, padded), *shared_want(c, 128 ** -0.5))
+    m = torch.full((2, 503), 7.0, device=DEV)
+    run_mass(vsk, padded, m)
+    base.check_mass(m[:, :103], base.mass_want(c, 128 ** -0.5))
+    assert bool((m[:, 103:] == 7.0).all())
+    out = [torch.full((4,), -7, dtype=torch.int32, device=DEV), torch.full((60,), -7, device=DEV), torch.full((2, 60), -7.0, device=DEV),
+           torch.full((503,), -7, device=DEV)]
+    vsk.kv_evict(m, c["kvp"], padded["kvi"], 20, 5, *out)
+    want = base.evict_want(m[:, :103], c["kvi"], (70, 0, 33), 20, 5)
+    base.check_evict([x.cpu() for x in out], want)
+    assert vsk.read_error_flags() == 0
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 2), (256, 16, 2)])
+def test_queries_that_are_no_numbers_stay_with_their_sequence(vsk, pool, d, hq, hk):
+    c = shared_case(500, (60, 20, 0, 9), 4, hq, hk, d, pool, seed=105)
+    want, a = shared_want(c, d ** -0.5)
+    w = base.mass_want(c, d ** -0.5)
+    c["q"] = c["q"].clone()
+    c["q"][4:6], c["q"][9, :, 3] = float("nan"), float("inf")
+    rows = torch.ones(16, dtype=torch.bool, device=DEV)
+    rows[[4, 5, 9]] = False
+    o = run_shared(vsk, c)
+    check_attention(o[rows], want[rows], a[rows])
+    assert bool(o[4:6].isnan().all())
+    m = run_mass(vsk, c, torch.empty(hk, 89, device=DEV))
+    base.check_mass(m[:, :60], w[:, :60])
+    base.check_mass(m[:, 80:], w[:, 80:])
+    assert bool(m[:, 60:80].isnan().all())
+
+
+def test_prompt_queries_that_are_no_numbers_stay_with_their_row(vsk):
+    for d, hq, hk in ((64, 4, 2), (128, 8, 2), (256, 16, 2)):
+        lens = (200, 90)
+        q, k, v, p = base.prompt_case(lens, hq, hk, d, seed=106)
+        want, a = base.prompt_want(q, k, v, lens, d ** -0.5)
+        q[37], q[250] = float("nan"), float("inf")
+        o = torch.empty_like(q)
+        vsk.prompt_attn_fwd(q, k, v, o, p)
+        rows = torch.ones(290, dtype=torch.bool, device=DEV)
+        rows[[37, 250]] = False
+        check_attention(o[rows], want[rows], a[rows])
+        assert bool(o[37].isnan().all())
+
+
+def test_evict_of_nothing_and_of_what_stays(vsk):
+    none = torch.zeros(0, dtype=torch.long, device=DEV)
+    ptr = torch.full((4,), -7, dtype=torch.int32, device=DEV)
+    vsk.kv_evict(torch.zeros(2, 0, device=DEV), indptr((0, 0, 0)), none, 5, 1, ptr, none.clone(), torch.zeros(2, 0, device=DEV), none.clone())
+    assert ptr.tolist() == [0, 0, 0, 0] and vsk.read_error_flags() == 0
+    m, kvi = torch.rand(2, 30, device=DEV), torch.arange(30, device=DEV)
+    out = [ptr, torch.zeros(30, dtype=torch.long, device=DEV), torch.zeros(2, 30, device=DEV), none.clone()]  # nothing is freed
+    vsk.kv_evict(m, indptr((10, 0, 20)), kvi, 1 << 40, 1 << 33, *out)
+    assert ptr.tolist() == [0, 10, 10, 30] and torch.equal(out[1], kvi) and torch.equal(out[2], m)
+    assert vsk.read_error_flags() == 0
+
+
+def test_lengths_that_change_under_a_captured_graph(vsk):
+    """One graph of the shared call, the weights and the eviction; replayed with other indptrs over the same arrays."""
+    t, b, d = 400, 3, 128
+    c = shared_case(250, (t, 0, 0), 4, 8, 2, d, seed=107)
+    o, m = torch.zeros_like(c["q"]), torch.zeros(2, t, device=DEV)
+    out = [torch.zeros(b + 1, dtype=torch.int32, device=DEV), torch.zeros(t, dtype=torch.long, device=DEV), torch.zeros(2, t, device=DEV),
+           torch.zeros(t, dtype=torch.long, device=DEV)]
+    ws = torch.zeros(vsk.shared_workspace_size(b, 8, 2, d, 4), dtype=torch.uint8, device=DEV)
+    run_shared(vsk, c)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        vsk.verify_splitkv_shared_fwd(c["q"], c["ke"], c["ve"], o, c["kb"], c["vb"], c["qo"], c["kvp"], c["kvi"], c["sh"], 4, workspace=ws)
+        run_mass(vsk, c, m, workspace=ws)
+        vsk.kv_evict(m, c["kvp"], c["kvi"], 64, 16, *out, workspace=ws)
+    for lens in ((0, 0, 0), (1, 399, 0), (133, 134, 133), (0, 17, 300), (400, 0, 0)):
+        c["kvp"].copy_(indptr(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        n = sum(lens)
+        now = dict(c, own=lens, kvi=c["kvi"][:n])
+        check_attention(o, *shared_want(now, d ** -0.5))
+        base.check_mass(m[:, :n], base.mass_want(now, d ** -0.5))
+        want = base.evict_want(m[:, :n], c["kvi"][:n], lens, 64, 16)
+        assert torch.equal(out[0].cpu(), want[0]) and torch.equal(out[1][:len(want[1])].cpu(), want[1])
+        assert torch.equal(out[3][:len(want[3])].cpu(), want[3])
+    assert vsk.read_error_flags(ws) == 0
+
+
+FORMS = [
+    # (name, tuning of the verify call, head_dims)
+    ("default", {}, (64, 128, 256)), ("one launch", {"tc": 0, "colsplit": 0, "split_launch": 0}, (64, 128, 256)),
+    ("stream and combine", {"tc": 0, "colsplit": 0, "split_launch": 2}, (64, 128, 256)), ("column split", {"tc": 0, "colsplit": 2}, (256,)),
+    ("cluster", {"tc": 0, "cluster": 2}, (64, 128, 256)), ("keys on M", {"tc": 1}, (256,)), ("rows on M", {"tc": 2}, (256,)),
+]
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("form,d", [(f, d) for f in FORMS for d in f[2]], ids=lambda x: x[0] if isinstance(x, tuple) else str(x))
+def test_verify_queries_that_are_no_numbers_stay_with_their_row(vsk, form, d, pool):
+    """Rows of one tile share a scale over e4m3 pools: it goes by their finite values."""
+    name, tuning, _ = form
+    hq, hk = (16, 2) if d == 256 else (8, 2)
+    c = shared_case(0, (60, 200, 9, 0), 4, hq, hk, d, pool, seed=108)
+    want, a = shared_want(c, d ** -0.5)
+    c["q"] = c["q"].clone()
+    c["q"][1], c["q"][4:6], c["q"][9, :, 3] = float("inf"), float("nan"), float("-inf")
+    rows = torch.ones(16, dtype=torch.bool, device=DEV)
+    rows[[1, 4, 5, 9]] = False
+    o = torch.full_like(c["q"], 7.0)
+    try:
+        for k, v in tuning.items():
+            getattr(vsk, "set_tuning_" + k)(v)
+        assert vsk.verify_splitkv_fwd(c["q"], c["ke"], c["ve"], o, c["kb"], c["vb"], c["qo"], c["kvp"], c["kvi"], None, True, None, 4, 1.0, 1.0)
+    finally:
+        vsk.set_tuning_tc()
+        vsk.set_tuning_colsplit()
+        vsk.set_tuning_split_launch()
+        vsk.set_tuning_cluster()
+    check_attention(o[rows], want[rows], a[rows])
+    assert bool(o[~rows].isnan().all())
+    assert vsk.read_error_flags() == 0

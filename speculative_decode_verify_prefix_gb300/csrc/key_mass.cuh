@@ -22,7 +22,8 @@
 // ldmatrix or staging buffer is needed.  The next stage's loads are in flight
 // while one is multiplied (deeper queues cost registers: the serving batch
 // 1354 us with three stages, 1213 with two; a ring filled by cp.async 1211
-// against 1072).  e4m3 keys are widened to f16 (exact) and meet queries scaled by a power of two so that the largest lies in [2^14, 2^15)
+// against 1072).  e4m3 keys are widened to f16 (exact) and meet queries scaled
+// by a power of two so that the largest finite one lies in [2^14, 2^15)
 // (elements more than 2^29 smaller than it lose bits).
 //
 // Measured: 64 sequences of 8,192 to 32,768 keys, 32/8 heads of 128, 4 drafts,
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(km::kThreads, 2) mass_kernel(const __grid_cons
       if constexpr (FP8) {
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx = max(mx, max(w[u] & 0x7FFFu, (w[u] >> 16) & 0x7FFFu));
+        for (int u = 0; u < 4; ++u) mx = max(mx, finite_mag_bf16x2(w[u]));
       }
       *reinterpret_cast<uint4*>(qs + r * (D * 2) + ((c ^ (r & 7)) << 4)) = x;
     }

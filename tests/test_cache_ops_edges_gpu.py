@@ -482,3 +482,31 @@ def test_verify_queries_that_are_no_numbers_stay_with_their_row(vsk, form, d, po
     check_attention(o[rows], want[rows], a[rows])
     assert bool(o[~rows].isnan().all())
     assert vsk.read_error_flags() == 0
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 2), (256, 16, 2)])
+def test_mass_of_a_row_that_sees_only_minus_infinity(vsk, pool, d, hq, hk):
+    """Such a row gives no weight, like one that sees nothing, and leaves the other rows' weights alone."""
+    c = shared_case(0, (500, 30), 4, hq, hk, d, pool, seed=109)
+    kb = c["kb"].float()
+    kb[:, :, 5] = kb[:, :, 5].abs() + 0.5
+    c["kb"], c["ke"] = kb.to(c["kb"].dtype), c["ke"].clone()
+    c["ke"][:, :, 5] = c["ke"][:, :, 5].abs() + 0.5
+    q = c["q"].clone()
+    q[2, 0, 5] = q[5, :, 5] = -math.inf
+    blind = torch.zeros(8, hq, dtype=torch.bool, device=DEV)
+    blind[2, 0] = blind[5] = True
+    g, w, at = hq // hk, torch.zeros(hk, 530, dtype=F64, device=DEV), 0
+    for b, n in enumerate(c["own"]):
+        r = slice(4 * b, 4 * b + 4)
+        k = torch.cat([base.rows64(c["kb"], c["kvi"][at:at + n]), c["ke"][r].to(F64)])
+        vis = torch.ones(4, n + 4, dtype=torch.bool, device=DEV).tril(n)
+        for h in range(hq):
+            x = (c["q"][r, h].to(F64) @ k[:, h // g].T) * d ** -0.5
+            p = torch.softmax(x.masked_fill(~vis, -math.inf), 1)
+            w[h // g, at:at + n] += p[~blind[r, h], :n].sum(0)
+        at += n
+    c["q"] = q
+    base.check_mass(run_mass(vsk, c, torch.empty(hk, 530, device=DEV)), w)
+    assert vsk.read_error_flags() == 0

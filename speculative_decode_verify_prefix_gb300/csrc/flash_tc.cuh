@@ -318,6 +318,12 @@ __device__ __forceinline__ void mbar_arrive_warp_tx(uint32_t bar, uint32_t bytes
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 31;" ::"r"(bar) : "memory");
 }
 
+// An f16 pair that came of e4m3 values as bf16 (exact).
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_bf16(f.x, f.y);
+}
+
 // bf16 pair with infinities and NaN replaced by 0; bad: whether there were any
 __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w, bool& bad) {
   const bool lo = (w & 0x7F80u) == 0x7F80u, hi = (w & 0x7F800000u) == 0x7F800000u;
@@ -959,9 +965,12 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
                 uint32_t y[8];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                  const auto lo = static_cast<unsigned short>(wv[u] & 0xFFFFu), hi = static_cast<unsigned short>(wv[u] >> 16);
-                  y[2 * u] = kv ? e4m3x2_to_f16x2(lo) : e4m3x2_to_bf16x2(lo);
-                  y[2 * u + 1] = kv ? e4m3x2_to_f16x2(hi) : e4m3x2_to_bf16x2(hi);
+                  y[2 * u] = e4m3x2_to_f16x2(static_cast<unsigned short>(wv[u] & 0xFFFFu));
+                  y[2 * u + 1] = e4m3x2_to_f16x2(static_cast<unsigned short>(wv[u] >> 16));
+                }
+                if (kv == 0) {
+#pragma unroll
+                  for (int u = 0; u < 8; ++u) y[u] = f16x2_to_bf16x2(y[u]);
                 }
                 *reinterpret_cast<uint4*>(ent + dst_off(key, 2 * c8)) = make_uint4(y[0], y[1], y[2], y[3]);
                 *reinterpret_cast<uint4*>(ent + dst_off(key, 2 * c8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);

@@ -244,12 +244,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// The larger magnitude of a bf16 pair (bit patterns order like magnitudes) for a
-// scale that rows share: infinities and NaN count as 0, or one row that holds
-// any would scale its neighbours' numbers away.
+// The larger magnitude of a bf16 pair (bit patterns order like magnitudes), and
+// with infinities and NaN as 0: a scale that rows share goes by finite values,
+// or one row that holds others would scale its neighbours' numbers away.
+constexpr unsigned kBf16Inf = 0x7F80u;
+__device__ __forceinline__ unsigned mag_bf16x2(uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); }
 __device__ __forceinline__ unsigned finite_mag_bf16x2(uint32_t w) {
   const unsigned lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
-  return max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u);
+  return max(lo < kBf16Inf ? lo : 0u, hi < kBf16Inf ? hi : 0u);
+}
+// The pair with NaN for infinities.
+__device__ __forceinline__ uint32_t inf_to_nan_bf16x2(uint32_t w) {
+  const uint32_t lo = (w & 0x7FFFu) == kBf16Inf ? 0x40u : 0u, hi = (w & 0x7FFF0000u) == kBf16Inf << 16 ? 0x400000u : 0u;
+  return w | lo | hi;
 }
 __device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
   __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&w);
@@ -440,9 +447,17 @@ __device__ __forceinline__ float load_q_f16(const Params& p, const Seg& s, int h
     qf[kk][1] = v1 ? ld_u32(q1 + kk * 16 + 4 * j) : 0u;
     qf[kk][3] = v1 ? ld_u32(q1 + kk * 16 + 4 * j + 2) : 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx = max(mx, finite_mag_bf16x2(qf[kk][i]));
+    for (int i = 0; i < 4; ++i) mx = max(mx, mag_bf16x2(qf[kk][i]));
   }
   mx = __reduce_max_sync(0xffffffffu, mx);
+  if (mx >= kBf16Inf) {  // (rare, so not looked at in the loop above)
+    mx = 0;
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = max(mx, finite_mag_bf16x2(qf[kk][i]));
+    mx = __reduce_max_sync(0xffffffffu, mx);
+  }
   const int ex = static_cast<int>(mx >> 7) - 127;  // exponent of the largest |q|
   const int sh = ex > 14 ? ex - 14 : 0;
   const float down = __int_as_float((127 - sh) << 23);

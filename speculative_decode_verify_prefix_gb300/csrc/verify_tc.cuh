@@ -402,12 +402,28 @@ __device__ __forceinline__ float tc_load_q(const Params& p, const Seg& s, unsign
 #pragma unroll
     for (int i = 0; i < NCH; ++i)
 #pragma unroll
-      for (int w = 0; w < 4; ++w) mx = max(mx, finite_mag_bf16x2(v[i][w]));
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if ((tw & 31) == 0) red_u[tw >> 5] = mx;
-    named_bar_sync(1 + wg, 128);
-    mx = max(max(red_u[0], red_u[1]), max(red_u[2], red_u[3]));
-    named_bar_sync(1 + wg, 128);  // red_u is free again
+      for (int w = 0; w < 4; ++w) mx = max(mx, mag_bf16x2(v[i][w]));
+    auto largest = [&] {  // of the four warps
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      if ((tw & 31) == 0) red_u[tw >> 5] = mx;
+      named_bar_sync(1 + wg, 128);
+      mx = max(max(red_u[0], red_u[1]), max(red_u[2], red_u[3]));
+      named_bar_sync(1 + wg, 128);  // red_u is free again
+    };
+    largest();
+    if (mx >= kBf16Inf) {  // rare, and the same for all four warps
+      // e4m3 has no infinity and would end at 448.  An infinite query makes its
+      // row's scores infinite and so its softmax NaN, which NaN does as well.
+      mx = 0;
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          mx = max(mx, finite_mag_bf16x2(v[i][w]));
+          v[i][w] = inf_to_nan_bf16x2(v[i][w]);
+        }
+      largest();
+    }
     const int ex = static_cast<int>(mx >> 7) - 127;
     int sh = mx == 0 ? 0 : 7 - ex;  // the largest |q| * 2^sh lies in [128, 256)
     sh = max(-120, min(120, sh));
@@ -422,9 +438,7 @@ __device__ __forceinline__ float tc_load_q(const Params& p, const Seg& s, unsign
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const float2 f = unpack_bf16(v[i][w]);
-        // (e4m3 has no infinity and would end at 448: an infinite query makes its row's scores infinite
-        // of both signs, so its softmax is NaN, which x - x makes of it here)
-        const float x0 = f.x * up + (f.x - f.x), x1 = f.y * up + (f.y - f.y);
+        const float x0 = f.x * up, x1 = f.y * up;
         const unsigned short h = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
         const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3);
         const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hr));

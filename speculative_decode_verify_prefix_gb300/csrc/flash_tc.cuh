@@ -69,7 +69,8 @@
 // epilogue adds them to the rows that do see them.
 //
 // Every mbarrier wait is bounded (one second): a wait that gives up sets error
-// bit 8 and the CTA drains, frees its tensor memory and exits.
+// bit 8 and the CTA's abort flag; no further tile is loaded then, and the CTA
+// waits for its copies and products under way, frees its tensor memory and exits.
 #pragma once
 #include <cuda.h>
 
@@ -271,17 +272,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // once: a suspended warp (try_wait) wakes some hundred cycles late, which the
 // chain of scores, softmax and product pays several times a tile (long prompts
 // 1129 us suspended, 676 us so); the clock is read only after many looks.
-__device__ __forceinline__ void wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+// False: the phase is not complete and the CTA gives up.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
   unsigned long long t0 = 0;
   for (int looks = 0; !__all_sync(0xffffffffu, tr::test(bar, parity)); ++looks) {
-    if (__any_sync(0xffffffffu, *abort_flag != 0)) return;
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
     if (looks == 65536) t0 = tc::global_ns();
     if (looks > 65536 && (looks & 1023) == 0 && __all_sync(0xffffffffu, tc::global_ns() - t0 > 1000000000ull)) {
       *abort_flag = 1;
       if ((threadIdx.x & 31) == 0) atomicOr(err, kErrTimeout);
-      return;
+      return false;
     }
   }
+  return true;
+}
+// The wait before a CTA that gave up exits: a phase that completes by itself,
+// one second at most, whatever the abort flag says.
+__device__ __forceinline__ void wait_last(uint32_t bar, uint32_t parity) {
+  const unsigned long long t0 = tc::global_ns();
+  while (!__all_sync(0xffffffffu, tr::test(bar, parity)))
+    if (__all_sync(0xffffffffu, tc::global_ns() - t0 > 1000000000ull)) return;
 }
 // Position in the ring: slot and the parity of its lap.
 template <int NE>
@@ -742,7 +752,8 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
             x.j_edge = PROMPT ? x.tok0 / KT : 0;  // first tile with keys that some row of the block must not see
           }
         }
-        wait_all(bar(kBWEmpty + (it & 1)), static_cast<uint32_t>(((it >> 1) & 1) ^ 1), abort_flag, p.err);
+        // (a slot that is still in use is left as it is)
+        if (!wait_all(bar(kBWEmpty + (it & 1)), static_cast<uint32_t>(((it >> 1) & 1) ^ 1), abort_flag, p.err)) break;
         if (lane == 0) {
           work[it & 1] = x;
           mbar_arrive(bar(kBWFull + (it & 1)));
@@ -877,7 +888,7 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
         }
       }
       if (elect_one()) mma_commit(bar(kBDone));
-      wait_all(bar(kBDone), 0u, abort_flag, p.err);  // no arrival is pending when the CTA exits
+      wait_last(bar(kBDone), 0u);  // no product or arrival is pending when the CTA exits
     } else if (warp >= C::warp_load || (C::groups == 2 && warp < kWarpMma)) {
       // ================================ loaders ================================
       // A warp has NS of the four 32-key groups of every entry (with two groups
@@ -888,8 +899,11 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
       constexpr int RPP = 32 / CPK;         // rows of a warp's pass
       constexpr int NP = 32 / RPP;          // passes over 32 rows
       const int cc = lane % CPK, rr = lane / CPK;
+      int nt;  // key tiles of the item
+      // (a wait that gives up ends the item with this tile; looking at the abort
+      // flag every tile cost the gathers of a long shared prefix 1.5 %)
       auto slot_wait = [&](uint32_t e) {
-        wait_all(bar(kBEmpty + e % NE), ((e / NE) & 1) ^ 1, abort_flag, p.err);
+        if (!wait_all(bar(kBEmpty + e % NE), ((e / NE) & 1) ^ 1, abort_flag, p.err)) nt = 0;
       };
       auto dst_off = [&](int key, int c) -> uint32_t {
         return static_cast<uint32_t>((c >> 3) * (KT * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4));
@@ -900,15 +914,15 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
       for (int it = 0;; ++it) {
         const Work* wk;
         if (!take(it, wk)) break;
-        const int nt = max(wk->n_tiles[0], wk->n_tiles[1]);
+        nt = max(wk->n_tiles[0], wk->n_tiles[1]);
         const int head = wk->head, n = wk->n, j_first = wk->j_first, j_edge = wk->j_edge;
         const long long row0 = wk->row0;
         if (p.qtma && lgrp == 0 && lw < NQ) {
           // query tile lw (rows past the sequence may come along: they are never stored)
-          wait_all(bar(kBQEmpty + lw), static_cast<uint32_t>((it & 1) ^ 1), abort_flag, p.err);
+          const bool go = wait_all(bar(kBQEmpty + lw), static_cast<uint32_t>((it & 1) ^ 1), abort_flag, p.err);
           if (lane == 0 && wk->n_tiles[lw] == 0) {
             mbar_arrive(bar(kBQFull + lw));  // no MMA reads it
-          } else if (lane == 0) {
+          } else if (go && lane == 0) {
             const uint32_t fb = bar(kBQFull + lw);
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(fb),
                          "r"(p.tpb * p.gq * D * 2)
@@ -1096,9 +1110,9 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
         } else {
           long long loc_k[NS], loc_v[NS];  // of the newest K tile and of the V tile that comes next
           unsigned ok_k[NS], ok_v[NS];
-          const int tail = 2 * nt - 1;
 #pragma unroll 1
-          for (int st = 0; st <= tail; ++st) {  // K0 K1 V0 K2 V1 ... V(nt - 2) V(nt - 1)
+          for (int st = 0; st < 2 * nt; ++st) {  // K0 K1 V0 K2 V1 ... V(nt - 2) V(nt - 1)
+            const int tail = 2 * nt - 1;
             const int kv = st == 0 ? 0 : st == tail ? 1 : ~st & 1;
             const int j = st == 0 ? 0 : st == tail ? nt - 1 : (st + 1) / 2 - kv;
             if (st == 0) rows_of(0, loc_k, ok_k);
@@ -1127,6 +1141,11 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
         give_back(it);
       }
       cp_async_wait<0>();
+      // TMA copies that no product waits for any more: two milliseconds, far beyond the latency of any
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) {
+        const unsigned long long t0 = tc::global_ns();
+        while (tc::global_ns() - t0 < 2000000ull) __nanosleep(1000);
+      }
     }
     __syncwarp();
   }

@@ -510,3 +510,20 @@ def test_mass_of_a_row_that_sees_only_minus_infinity(vsk, pool, d, hq, hk):
     c["q"] = q
     base.check_mass(run_mass(vsk, c, torch.empty(hk, 530, device=DEV)), w)
     assert vsk.read_error_flags() == 0
+
+
+# ---------------------------------------------------------------- repeats
+
+@pytest.mark.parametrize("d,hq,hk", [(64, 8, 2), (128, 32, 8), (256, 16, 2)])
+def test_calls_repeat_bit_for_bit(vsk, d, hq, hk):
+    """Which CTA takes which item, and when, plays no part in the result."""
+    lens = (1500, 70, 700, 1, 333) * 3
+    q, k, v, p = base.prompt_case(lens, hq, hk, d, seed=110)
+    shared = [shared_case(5000, (300, 0, 45, 800) * 3, 4, hq, hk, d, pool, seed=111) for pool in ("bf16", "e4m3")]
+    first = None
+    for _ in range(10):
+        o = torch.full_like(q, float("nan"))
+        vsk.prompt_attn_fwd(q, k, v, o, p)
+        got = [o] + [run_shared(vsk, c) for c in shared] + [run_mass(vsk, c, torch.empty(hk, len(c["kvi"]), device=DEV)) for c in shared]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))

@@ -644,8 +644,8 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
         // partial of this key range: o v_scale / l and m + log2 l (of l without the scale of P), -inf and 0
         // where no key was valid
         const long long prow = wk->item * (NQ * 128) + t * 128 + r;
-        const float inv = l > 0.f ? p.v_scale / l : 0.f;
-        if (real) p.plse[prow] = l > 0.f ? mrun + (log2f(l) - p_up) : (l == 0.f ? NEG_INF : l);
+        const float inv = l == 0.f ? 0.f : p.v_scale / l;
+        if (real) p.plse[prow] = l == 0.f ? NEG_INF : mrun + (log2f(l) - p_up);
         float* orow = p.po + prow * D;
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {

@@ -421,7 +421,7 @@ __device__ __forceinline__ void combine_unit(const Params& p, unsigned char* sme
   }
   // a row with nothing visible (empty prefix, no visible draft) is 0
   if (prow < p.R) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     __nv_bfloat16* op = p.o + (static_cast<long long>(s_b) + prow / p.gq) * p.o_s0 +
                         static_cast<long long>(kvh * p.gq + prow % p.gq) * p.o_s1 + col0 + c4;
     *reinterpret_cast<uint32_t*>(op) = pack_bf16(acc[0] * inv, acc[1] * inv);

@@ -1352,11 +1352,12 @@ __global__ void __launch_bounds__(CS == 2 ? (MTW == 2 ? 64 : 128) : MaxWarps<Max
       for (int t = 0; t < MTW; ++t) {
         const int r0 = r0s[t], r1 = r1s[t];
         const float s0 = quad_sum(l0[t]), s1 = quad_sum(l1[t]);
-        const float inv0 = s0 > 0.f ? p.v_scale / s0 : 0.f;
-        const float inv1 = s1 > 0.f ? p.v_scale / s1 : 0.f;
+        // (a sum that is NaN is no empty piece: it goes on to the row's result)
+        const float inv0 = s0 == 0.f ? 0.f : p.v_scale / s0;
+        const float inv1 = s1 == 0.f ? 0.f : p.v_scale / s1;
         if (j == 0 && csi == 0) {
-          st_keep(lse_p + r0, s0 > 0.f ? m0[t] + log2f(s0) : NEG_INF, keep);
-          st_keep(lse_p + r1, s1 > 0.f ? m1[t] + log2f(s1) : NEG_INF, keep);
+          st_keep(lse_p + r0, s0 == 0.f ? NEG_INF : m0[t] + log2f(s0), keep);
+          st_keep(lse_p + r1, s1 == 0.f ? NEG_INF : m1[t] + log2f(s1), keep);
         }
         float* o0p = o_p + r0 * DV + csi * DVH;  // this warp's columns
         float* o1p = o_p + r1 * DV + csi * DVH;
@@ -1522,10 +1523,10 @@ __global__ void __launch_bounds__(CS == 2 ? (MTW == 2 ? 64 : 128) : MaxWarps<Max
         for (int t = 0; t < MTW; ++t) {
           const int r0 = r0s[t], r1 = r1s[t];
           fold(gfirst + s_idx, 1, gcount, r0, r1);
-          const float inv0 = l0 > 0.f ? 1.f / l0 : 0.f, inv1 = l1 > 0.f ? 1.f / l1 : 0.f;
+          const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
           if (j == 0) {
-            lse_p[r0] = l0 > 0.f ? m0 + log2f(l0) : NEG_INF;
-            lse_p[r1] = l1 > 0.f ? m1 + log2f(l1) : NEG_INF;
+            lse_p[r0] = l0 == 0.f ? NEG_INF : m0 + log2f(l0);
+            lse_p[r1] = l1 == 0.f ? NEG_INF : m1 + log2f(l1);
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -1834,7 +1835,7 @@ __global__ void __launch_bounds__(CS == 2 ? (MTW == 2 ? 64 : 128) : MaxWarps<Max
       }
       // ------------------------------ output ------------------------------
       // a row with nothing visible (empty prefix, no visible draft) is 0
-      const float inv0 = l0 > 0.f ? 1.f / l0 : 0.f, inv1 = l1 > 0.f ? 1.f / l1 : 0.f;
+      const float inv0 = l0 == 0.f ? 0.f : 1.f / l0, inv1 = l1 == 0.f ? 0.f : 1.f / l1;
       if (r0 < p.R) {
         __nv_bfloat16* op = p.o + (static_cast<long long>(s_b) + r0 / p.gq) * p.o_s0 +
                             static_cast<long long>(kvh * p.gq + r0 % p.gq) * p.o_s1 + 2 * j;

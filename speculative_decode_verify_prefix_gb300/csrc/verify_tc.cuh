@@ -859,8 +859,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1) vtc_kernel(const __grid_const
 #pragma unroll
           for (int r = 0; r < RH; ++r) {
             const float l = (red[r] + red[32 + r]) + (red[64 + r] + red[96 + r]);
-            inv[r] = l > 0.f ? p.v_scale / l : 0.f;
-            if (r == tw) lse_mine = l > 0.f ? mrun[r] + log2f(l) : NEG_INF;
+            inv[r] = l == 0.f ? 0.f : p.v_scale / l;  // (a sum that is NaN is no empty piece)
+            if (r == tw) lse_mine = l == 0.f ? NEG_INF : mrun[r] + log2f(l);
           }
           named_bar_sync(bid, 128);
           if (tw < RH) st_keep(lse_p + wg * RH + tw, lse_mine, keep);

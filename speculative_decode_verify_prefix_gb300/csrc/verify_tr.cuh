@@ -724,8 +724,9 @@ __global__ void __launch_bounds__(tr::kThreads, 1) vtr_kernel(const __grid_const
           float l = lp + __shfl_xor_sync(0xffffffffu, lp, 1);
           l += __shfl_xor_sync(0xffffffffu, l, 2);
           const bool wr = prow < RM;
-          const float inv = l > 0.f ? p.v_scale / l : 0.f;
-          if (wr && c4 == 0) st_keep(lse_p + prow, l > 0.f ? mrun + log2f(l) : NEG_INF, keep);
+          // (a sum that is NaN is no empty piece)
+          const float inv = l == 0.f ? 0.f : p.v_scale / l;
+          if (wr && c4 == 0) st_keep(lse_p + prow, l == 0.f ? NEG_INF : mrun + log2f(l), keep);
 #pragma unroll 1
           for (int cb = 0; cb < D / 64; ++cb) {
             float o[32];

@@ -527,3 +527,72 @@ def test_calls_repeat_bit_for_bit(vsk, d, hq, hk):
         got = [o] + [run_shared(vsk, c) for c in shared] + [run_mass(vsk, c, torch.empty(hk, len(c["kvi"]), device=DEV)) for c in shared]
         first = first or got
         assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+# ---------------------------------------------------------------- keys and values that are no numbers
+#
+# One element of one KV head's key (or value) is NaN or infinite: every row that
+# sees it has no finite output where the 64-bit form has none, and no other row,
+# head or column changes.
+
+
+def poison(c, which, bad, row):
+    t = c[which].float().clone()
+    t[row, 1, 3] = bad
+    c[which] = t.to(c[which].dtype)
+
+
+def check_poisoned(c, o, want, a, which, rows, d):
+    exact, _ = shared_want(c, d ** -0.5)
+    hit = torch.zeros(o.shape, dtype=torch.bool, device=DEV)
+    g = o.shape[1] // c["ke"].shape[1]
+    if which[0] == "k":
+        hit[rows, g:] = True
+    else:
+        hit[rows, g:, 3] = True
+    check_attention(o[~hit], want[~hit], a[~hit])
+    assert not bool((o[hit].isfinite() & ~exact[hit].isfinite()).any())
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_shared_keys_that_are_no_numbers(vsk, d, pool):
+    """In the shared prefix, a sequence's own (over many pieces) and the drafts."""
+    hq, hk = (16, 2) if d == 256 else (8, 2)
+    c0 = shared_case(600, (60, 900, 9, 0), 4, hq, hk, d, pool, seed=112)
+    want, a = shared_want(c0, d ** -0.5)
+    places = [("b", int(c0["sh"][333]), slice(0, 16)), ("b", int(c0["kvi"][60 + 777]), slice(4, 8)), ("e", 5, slice(5, 8))]
+    for kind, row, rows in places:
+        for which in ("k" + kind, "v" + kind):
+            for bad in (math.nan, math.inf):
+                if bad == math.inf and pool == "e4m3" and kind == "b":
+                    continue  # e4m3 has none
+                c = dict(c0)
+                poison(c, which, bad, row)
+                check_poisoned(c, run_shared(vsk, c), want, a, which, rows, d)
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("form,d", [(f, d) for f in FORMS for d in f[2]], ids=lambda x: x[0] if isinstance(x, tuple) else str(x))
+def test_verify_keys_that_are_no_numbers(vsk, form, d, pool):
+    _, tuning, _ = form
+    hq, hk = (16, 2) if d == 256 else (8, 2)
+    c0 = shared_case(0, (60, 900, 9, 0), 4, hq, hk, d, pool, seed=113)
+    want, a = shared_want(c0, d ** -0.5)
+    try:
+        for k, v in tuning.items():
+            getattr(vsk, "set_tuning_" + k)(v)
+        for which, bad in [("kb", math.nan), ("vb", math.nan), ("ke", math.nan), ("ke", math.inf)] + (
+                [("kb", math.inf), ("vb", math.inf)] if pool == "bf16" else []):
+            c = dict(c0)
+            row, rows = (int(c0["kvi"][60 + 777]), slice(4, 8)) if which[1] == "b" else (5, slice(5, 8))
+            poison(c, which, bad, row)
+            o = torch.full_like(c["q"], 7.0)
+            assert vsk.verify_splitkv_fwd(c["q"], c["ke"], c["ve"], o, c["kb"], c["vb"], c["qo"], c["kvp"], c["kvi"], None, True, None,
+                                          4, 1.0, 1.0)
+            check_poisoned(c, o, want, a, which, rows, d)
+    finally:
+        vsk.set_tuning_tc()
+        vsk.set_tuning_colsplit()
+        vsk.set_tuning_split_launch()
+        vsk.set_tuning_cluster()

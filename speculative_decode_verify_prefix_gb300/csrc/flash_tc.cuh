@@ -117,7 +117,9 @@ struct Cfg {
   static constexpr int n_load = kWide ? 4 : 2;       // loader warps (of a group), 4 / n_load 32-key groups of a tile each
   static constexpr int groups = D == 256 ? 2 : 1;    // groups of loader warps (head_dim 256: warps 4-7 too)
   static constexpr int regs_softmax = D == 256 ? 232 : kWide ? 184 : 216;
-  static constexpr int regs_other = 72;
+  // (head_dim 256, 72: loaders of e4m3 rows spill, 64 sequences behind 32,768 of
+  // them 233 us for 219, three documents 41.4 for 40.3)
+  static constexpr int regs_other = D == 256 ? 88 : 72;
   static constexpr int regs_launch = 65536 / threads / 8 * 8;
   static_assert((D == 256 ? regs_softmax + 3 * regs_other : 2 * regs_softmax + (threads / 128 - 2) * regs_other) <=
                     threads / 128 * regs_launch, "register shares exceed the launch's");
@@ -326,12 +328,6 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void mbar_arrive_warp_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 31;" ::"r"(bar) : "memory");
-}
-
-// An f16 pair that came of e4m3 values as bf16 (exact).
-__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return pack_bf16(f.x, f.y);
 }
 
 // bf16 pair with infinities and NaN replaced by 0; bad: whether there were any
@@ -901,9 +897,11 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
       const int cc = lane % CPK, rr = lane / CPK;
       int nt;  // key tiles of the item
       // (a wait that gives up ends the item with this tile; looking at the abort
-      // flag every tile cost the gathers of a long shared prefix 1.5 %)
+      // flag every tile cost the gathers of a long shared prefix 1.5 %.  e4m3 rows
+      // come by plain loads, which may run on: nothing of them is under way later)
       auto slot_wait = [&](uint32_t e) {
-        if (!wait_all(bar(kBEmpty + e % NE), ((e / NE) & 1) ^ 1, abort_flag, p.err)) nt = 0;
+        const bool go = wait_all(bar(kBEmpty + e % NE), ((e / NE) & 1) ^ 1, abort_flag, p.err);
+        if (MODE != kSharedE4m3 && !go) nt = 0;
       };
       auto dst_off = [&](int key, int c) -> uint32_t {
         return static_cast<uint32_t>((c >> 3) * (KT * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4));
@@ -979,12 +977,9 @@ __global__ void __launch_bounds__(fa::Cfg<D, MODE>::threads, 1) fa_kernel(const 
                 uint32_t y[8];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                  y[2 * u] = e4m3x2_to_f16x2(static_cast<unsigned short>(wv[u] & 0xFFFFu));
-                  y[2 * u + 1] = e4m3x2_to_f16x2(static_cast<unsigned short>(wv[u] >> 16));
-                }
-                if (kv == 0) {
-#pragma unroll
-                  for (int u = 0; u < 8; ++u) y[u] = f16x2_to_bf16x2(y[u]);
+                  const auto lo = static_cast<unsigned short>(wv[u] & 0xFFFFu), hi = static_cast<unsigned short>(wv[u] >> 16);
+                  y[2 * u] = kv ? e4m3x2_to_f16x2(lo) : e4m3x2_to_bf16x2(lo);
+                  y[2 * u + 1] = kv ? e4m3x2_to_f16x2(hi) : e4m3x2_to_bf16x2(hi);
                 }
                 *reinterpret_cast<uint4*>(ent + dst_off(key, 2 * c8)) = make_uint4(y[0], y[1], y[2], y[3]);
                 *reinterpret_cast<uint4*>(ent + dst_off(key, 2 * c8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);

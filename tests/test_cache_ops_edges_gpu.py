@@ -596,3 +596,15 @@ def test_verify_keys_that_are_no_numbers(vsk, form, d, pool):
         vsk.set_tuning_colsplit()
         vsk.set_tuning_split_launch()
         vsk.set_tuning_cluster()
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 8, 2), (256, 16, 2)])
+def test_the_same_pool_row_more_than_once(vsk, pool, d, hq, hk):
+    """Twice in the shared prefix, there and in a sequence's own, in two sequences: every entry is a key."""
+    c = shared_case(260, (70, 5, 90), 4, hq, hk, d, pool, seed=115)
+    c["sh"][7] = c["sh"][8] = c["sh"][200]
+    c["kvi"][3], c["kvi"][71], c["kvi"][80:85] = c["sh"][7], c["kvi"][3], c["kvi"][0]
+    check_attention(run_shared(vsk, c), *shared_want(c, d ** -0.5))
+    base.check_mass(run_mass(vsk, c, torch.empty(hk, 165, device=DEV)), base.mass_want(c, d ** -0.5))
+    assert vsk.read_error_flags() == 0

@@ -28,9 +28,12 @@
 // What bounds it: per 128-key tile and query tile 2 MMAs of 128 x 128 x D
 // against 16,384 exponentials; both pipes are busy at once, and each waits for
 // the other at a tile's hand-overs.  Measured: four prompts, 21,716 tokens,
-// 32/8 heads of 128, 674 us = 0.79 of the library matrix product's rate; three
-// documents, 2,296 tokens, 16/2 heads of 256, 33 us (too few items to fill the
-// SMs evenly; two prompts of 4,096 223 us); a prefix of 32,768 rows shared by 64 sequences of 4 drafts, 32/8
+// 32/8 heads of 128, 678 us = 0.78 of the library matrix product's rate over 20
+// calls on a cool GPU, 725 us in a long run, where the power cap lowers the
+// clocks of both (0.79 of the product's rate there); at 64, where the
+// exponentials of a tile outlast its MMAs, 592; three documents, 2,296 tokens,
+// 16/2 heads of 256, 38 us (too few items to fill the SMs evenly; two prompts of
+// 4,096 225 us); a prefix of 32,768 rows shared by 64 sequences of 4 drafts, 32/8
 // of 128, 126 us at 45 % of the tensor pipe (each of the four row blocks of a KV
 // head gathers the rows again, 4.2 TB/s in all).
 //

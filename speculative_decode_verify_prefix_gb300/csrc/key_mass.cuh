@@ -11,8 +11,9 @@
 // computes their scores once and keeps them in shared memory (32-bit, R x 4
 // bytes a key), then the CTAs exchange their rows' maxima and sums through
 // distributed shared memory and turn the kept scores into weights.  K is read
-// once as long as a slice's scores fit (about 1,600 keys a CTA at 16 rows);
-// of a longer slice all but the last chunk is computed again.
+// once as long as a slice's scores fit (1,536 keys a CTA at 16 rows
+// of head_dim 128, 320 at 64 rows, 96 at 128); of a longer slice all but the last
+// chunk is loaded and computed again.
 //
 // Bound by the K stream.  Each warp loads 8-key groups straight into the
 // registers of the mma.sync B operand: lane (g, j) of the fragment needs key
@@ -27,8 +28,11 @@
 // (elements more than 2^29 smaller than it lose bits).
 //
 // Measured: 64 sequences of 8,192 to 32,768 keys, 32/8 heads of 128, 4 drafts,
-// bf16: 1,064 us, 2.7 TB/s over the call and about 4 while keys load; exchange,
-// weights and the wait for a whole cluster's place on the GPU take the rest.
+// bf16: 1,064 us, 2.7 TB/s of keys over the call (a fifth of them, in the 43
+// sequences longer than their 12 CTAs' scores, is loaded twice) and about 4 while
+// keys load; nothing loads while a CTA sweeps its scores, exchanges and weighs.
+// With 64 packed rows 16 sequences of 8,192 keys take 530 us, with 128 1,520:
+// short chunks, most keys loaded twice.
 //
 // The sum over a head's rows runs in row order and every key has one writer:
 // the result does not depend on scheduling.

@@ -63,6 +63,43 @@ def test_threads_on_one_stream_keep_their_partials(vsk, form):
     assert vsk.read_error_flags() == 0
 
 
+def test_threads_and_the_library_owned_workspace(vsk):
+    """Calls without a workspace from four threads on one stream, of sizes that make the library's buffer grow: it is not
+    replaced between its choice and a launch."""
+    import ctypes
+
+    from speculative_decode_verify_prefix_gb300 import _native
+
+    d, l = 128, 4
+    cases = [shared_case(500, (90,) * b, l, 8, 2, d, seed=95 + b) for b in (1, 3, 9, 40)]
+    alone = [run_shared(vsk, c) for c in cases]
+    outs = [[torch.full_like(c["q"], float("nan")) for _ in range(25)] for c in cases]
+    ref, failed, start = vsk.api._ref, [], threading.Barrier(len(cases))
+    stream = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            c = cases[i]
+            start.wait(30)
+            for o in outs[i]:
+                t = (c["q"], c["ke"], c["ve"], o, c["kb"], c["vb"], c["qo"], c["kvp"], c["kvi"], c["sh"])
+                if not _native.lib().verify_splitkv_shared_fwd(*[ref(x) for x in t], l, 1.0, 1.0, 0.0, None, 0, ctypes.c_void_p(stream)):
+                    failed.append(vsk.last_error())
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for i, c in enumerate(cases):
+        assert all(torch.equal(o, alone[i]) for o in outs[i])
+
+
 # ---------------------------------------------------------------- sizes
 
 def test_shared_workspace_size_of_shapes_that_no_call_takes(vsk):

@@ -45,7 +45,7 @@ enum {
   VSK_DTYPE_I32 = 2,      /* int32                                      */
   VSK_DTYPE_I64 = 3,      /* int64                                      */
   VSK_DTYPE_U8 = 4,       /* uint8 (also used for bool masks)           */
-  VSK_DTYPE_F32 = 5       /* float32 (attention weights)                */
+  VSK_DTYPE_F32 = 5       /* float32 (attention weights, block scales)  */
 };
 
 /* A strided view of device memory.  Strides and shape are in ELEMENTS.  For
@@ -340,6 +340,129 @@ int kv_evict(const vsk_tensor* mass, const vsk_tensor* kv_indptr, const vsk_tens
              const vsk_tensor* out_kv_indices, const vsk_tensor* out_mass,
              const vsk_tensor* freed, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Frequencies of the rotary positions: out[i] (i < rot_dim / 2, HOST memory) is
+ * what pair i turns by per position, in radians, and the return value what the
+ * rotated elements are multiplied by (attention_factor below).  Plain:
+ * f_i = base^(-2 i / rot_dim).  For contexts `factor` times longer than the
+ * original_len positions a model was trained on:
+ *   VSK_ROPE_LINEAR  f_i / factor
+ *   VSK_ROPE_BASE    base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   VSK_ROPE_RAMP    f_i where a pair turns `high` times or more over
+ *                    original_len, f_i / factor where `low` times or fewer, a
+ *                    straight line in i between the two pairs (rounded outwards);
+ *                    returns 1 + 0.1 ln factor
+ *   VSK_ROPE_BANDS   the same with a straight line in the number of turns;
+ *                    returns 1
+ * `factor` is ignored by the plain ones, original_len, low and high by all but
+ * the last two.  Returns 0 and sets vsk_last_error() when refused.  Host only. */
+enum { VSK_ROPE_PLAIN = 0, VSK_ROPE_LINEAR = 1, VSK_ROPE_BASE = 2, VSK_ROPE_RAMP = 3, VSK_ROPE_BANDS = 4 };
+float vsk_rope_frequencies(float* out, int64_t rot_dim, double base, int scaling, double factor,
+                           double original_len, double low, double high);
+
+/* Rotary positions of query and key rows.  The first R = 2 * len(inv_freq)
+ * elements of a head are pairs (i, i + R/2), or (2 i, 2 i + 1) if interleaved is
+ * nonzero; pair i of row t, (a, b), becomes
+ *   attention_factor * (a cos x - b sin x, b cos x + a sin x),
+ *   x = positions[t] * inv_freq[i],
+ * in 32 bits (the angle exactly, so far positions lose nothing), rounded to bf16
+ * once; elements from R on are copied.
+ *   q, q_out   [N, h_q, D]  bf16, D in {64, 128, 256}; both NULL: keys only
+ *   k, k_out   [N, h_kv, D] bf16
+ *   positions  [N] int32 or int64, any sign; inv_freq [R/2] float32, R a
+ *              multiple of 16 up to D (a value that is no number gives NaN)
+ * Rows 16-byte aligned (data pointer and the byte strides of both leading
+ * dimensions).  An output may be its own input (the same view) and must share no
+ * byte with anything else (refused, also where views of different strides only
+ * lie in one another's range).  One launch on `stream`; no workspace. */
+int rope_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* q_out, const vsk_tensor* k_out,
+             const vsk_tensor* positions, const vsk_tensor* inv_freq, int interleaved, float attention_factor,
+             void* stream);
+
+/* rope_fwd that also stores the keys (rotated) and values: row t goes to pool
+ * row out_cache_loc[t] of k_buffer / v_buffer, as the pool type's
+ * round-to-nearest-even of x / k_scale (x / v_scale for V) in binary32, e4m3
+ * saturating to +-448 (NaN stays NaN); the rotated key is not rounded to bf16 on
+ * the way.  A paged cache is such a pool: row = page * page_size + offset.
+ *   v                   [N, h_kv, D] bf16
+ *   k_buffer, v_buffer  [pool, h_kv, D] both bf16 or both e4m3, rows 16-byte aligned
+ *   out_cache_loc       [N] int32 or int64, distinct places (of rows with one
+ *                       place any may be found there, in part).  -1: the row has
+ *                       no place and is not stored (a padded batch); any other
+ *                       value outside [0, pool) is not stored either and sets
+ *                       error bit 1.
+ *   k_out               NULL: the rotated keys go to the pool only
+ *   k_scale, v_scale    > 0 and finite (1 for a bf16 pool)
+ * Other arguments as rope_fwd, workspace as prompt_attn_fwd (the error word
+ * alone).  One launch on `stream`. */
+int rope_append_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* v, const vsk_tensor* q_out,
+                    const vsk_tensor* k_out, const vsk_tensor* k_buffer, const vsk_tensor* v_buffer,
+                    const vsk_tensor* out_cache_loc, const vsk_tensor* positions, const vsk_tensor* inv_freq,
+                    int interleaved, float attention_factor, float k_scale, float v_scale, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* The same into an e4m3 cache of blocks, each with a scale for every KV head, one
+ * for K and one for V: a stored code stands for code * scale.  No calibration is
+ * needed: a block's scale follows its rows.  Rows qo_indptr[b] .. qo_indptr[b+1] -
+ * 1 go to cache positions cache_lens[b], cache_lens[b] + 1, ... of sequence b;
+ * position t lies in row t % block_size of block block_table[b][t / block_size].
+ * For every (block, KV head) that gets rows, for K and V apart:
+ *   need = the smallest power of two 2^e, -40 <= e <= 40, with
+ *          (largest finite magnitude of the new rows) <= 448 * 2^e
+ *   s    = max(old scale, need) if the block holds earlier rows (positions
+ *          before cache_lens[b]), need otherwise
+ * The new rows are stored as round-to-nearest-even of x / s, saturating; where s
+ * is not the old scale the earlier rows' codes c become those of c * (old / s).
+ * Rows behind the last new one are left as they were.
+ *   k_cache, v_cache    [blocks * block_size, h_kv, D] e4m3, rows 16-byte
+ *                       aligned; block_size a multiple of 16 up to 128
+ *   k_scales, v_scales  [blocks, h_kv] float32, rows contiguous (read where a
+ *                       block holds earlier rows, written)
+ *   qo_indptr [B+1] int32, block_table [B, columns] int32 (rows contiguous),
+ *   cache_lens [B] int32 rows before the new ones
+ * A block that gets rows belongs to one sequence of the call.  Rows of q_out and
+ * k_out outside every sequence are left as they were.  Device-side checks: a
+ * block id outside the cache sets error bit 1, cache_lens[b] < 0 or new rows
+ * beyond the table's columns bit 2: those rows are rotated and not stored; an
+ * inconsistent qo_indptr pair sets bit 4 and makes the sequence empty.  Other
+ * arguments as rope_append_fwd.  One launch on `stream`. */
+int rope_append_block_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* v, const vsk_tensor* q_out,
+                          const vsk_tensor* k_out, const vsk_tensor* k_cache, const vsk_tensor* v_cache,
+                          const vsk_tensor* k_scales, const vsk_tensor* v_scales, const vsk_tensor* qo_indptr,
+                          const vsk_tensor* block_table, const vsk_tensor* cache_lens, const vsk_tensor* positions,
+                          const vsk_tensor* inv_freq, int64_t block_size, int interleaved, float attention_factor,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* verify_splitkv_fwd over such a cache: sequence b's prefix is cache positions
+ * [0, seq_lens[b]), whose keys and values are code * scale of their block and KV
+ * head; its drafts are the bf16 rows k_extend / v_extend, causal, or under
+ * custom_mask / mask_indptr as in verify_splitkv_tree_fwd.  With one draft, the
+ * new token itself, it is a decode step.
+ *   q_extend, o_extend  [B*l_ext, h_q, D], k_extend and v_extend [B*l_ext, h_kv,
+ *                       D] bf16, 4-byte aligned with even strides, D in {64,
+ *                       128, 256}, (h_q/h_kv)*l_ext <= 128; o_extend must not
+ *                       overlap the other tensors
+ *   k_cache .. block_size   as rope_append_block_fwd; scales may be any numbers
+ *                       in [2^-40, 2^40].  Another one sets error bit 64, and
+ *                       the rows that see its block become NaN.
+ *   seq_lens            [B] int32
+ *   custom_mask, mask_indptr   both NULL: causal drafts
+ *   workspace           vsk_block_workspace_size(max_bs, ...) bytes for any B <=
+ *                       max_bs and any lengths; NULL: the library-owned one
+ * A row with nothing to see is 0.  Device-side checks: a block id outside the
+ * cache sets error bit 1 and its keys are left out; seq_lens[b] < 0 or beyond the
+ * table's columns sets bit 2 (an empty prefix); qo_indptr bit 4, mask_indptr
+ * bit 16 as the calls above.  Two launches on `stream`. */
+int verify_splitkv_block_fwd(const vsk_tensor* q_extend, const vsk_tensor* k_extend, const vsk_tensor* v_extend,
+                             const vsk_tensor* o_extend, const vsk_tensor* k_cache, const vsk_tensor* v_cache,
+                             const vsk_tensor* k_scales, const vsk_tensor* v_scales, const vsk_tensor* qo_indptr,
+                             const vsk_tensor* block_table, const vsk_tensor* seq_lens, const vsk_tensor* custom_mask,
+                             const vsk_tensor* mask_indptr, int64_t block_size, int64_t max_len_extend, float sm_scale,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bound of verify_splitkv_block_fwd on the CURRENT device (0 when the
+ * shapes are unsupported or there is none). */
+size_t vsk_block_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv, int64_t head_dim, int64_t max_len_extend);
+
 /* Upper bound, in bytes, of the workspace verify_splitkv_fwd needs for any
  * batch of up to max_bs sequences with these head counts and sizes on the
  * CURRENT CUDA device (its SM count sets the number of persistent CTAs).
@@ -365,11 +488,11 @@ int vsk_workspace_init(void* workspace, size_t bytes, void* stream);
  * not non-decreasing or beyond kv_indices; 4 = qo_indptr inconsistent with
  * l_ext; 8 = a pipeline wait that gave up after one second (only the
  * tensor-memory forms of the stream, see vsk_set_tuning_tc, and of
- * prompt_attn_fwd and verify_splitkv_shared_fwd have such waits: the CTA then
+ * prompt_attn_fwd, verify_splitkv_shared_fwd and verify_splitkv_block_fwd have such waits: the CTA then
  * stops streaming, frees its tensor memory and exits, and that call's output
  * is not valid; the other kernels have no waits that can time out); 16 = a mask_indptr entry of
  * verify_splitkv_tree_fwd outside custom_mask; 32 = an output of kv_evict too
- * short for what is kept or freed.  Returns 1 on success, 0 on a
+ * short for what is kept or freed; 64 = a block scale outside [2^-40, 2^40].  Returns 1 on success, 0 on a
  * CUDA error.
  * Intended for tests and debugging: it blocks the host. */
 int vsk_read_error_flags(void* workspace, void* stream, uint32_t* flags);

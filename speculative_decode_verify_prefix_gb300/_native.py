@@ -121,6 +121,22 @@ def _bind(lib):
     lib.kv_evict.restype = ctypes.c_int
     lib.kv_evict.argtypes = [_V] * 3 + [ctypes.c_int64, ctypes.c_int64] + [_V] * 4 + [
         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.rope_fwd.restype = ctypes.c_int
+    lib.rope_fwd.argtypes = [_V] * 6 + [ctypes.c_int, ctypes.c_float, ctypes.c_void_p]
+    lib.rope_append_fwd.restype = ctypes.c_int
+    lib.rope_append_fwd.argtypes = [_V] * 10 + [ctypes.c_int, ctypes.c_float, ctypes.c_float, ctypes.c_float,
+                                                ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.rope_append_block_fwd.restype = ctypes.c_int
+    lib.rope_append_block_fwd.argtypes = [_V] * 14 + [ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_void_p,
+                                                      ctypes.c_size_t, ctypes.c_void_p]
+    lib.verify_splitkv_block_fwd.restype = ctypes.c_int
+    lib.verify_splitkv_block_fwd.argtypes = [_V] * 13 + [ctypes.c_int64, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p,
+                                                         ctypes.c_size_t, ctypes.c_void_p]
+    lib.vsk_rope_frequencies.restype = ctypes.c_float
+    lib.vsk_rope_frequencies.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_double, ctypes.c_int] + [
+        ctypes.c_double] * 4
+    lib.vsk_block_workspace_size.restype = ctypes.c_size_t
+    lib.vsk_block_workspace_size.argtypes = [ctypes.c_int64] * 5
     lib.vsk_shared_workspace_size.restype = ctypes.c_size_t
     lib.vsk_shared_workspace_size.argtypes = [ctypes.c_int64] * 5
     lib.vsk_workspace_size.restype = ctypes.c_size_t

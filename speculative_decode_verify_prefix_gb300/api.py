@@ -79,6 +79,7 @@ def can_handle(q_extend, k_extend, v_extend, k_buffer, v_buffer, qo_indptr, kv_i
 _WS = {}
 _WS_SIZE = {}  # (device, max_bs, h_q, h_kv, head_dim, v_head_dim, l_ext) -> bytes
 _SHARED_SIZE = {}  # (device, max_bs, h_q, h_kv, head_dim, l_ext) -> bytes, behind a shared prefix
+_BLOCK_SIZE = {}  # (device, max_bs, h_q, h_kv, head_dim, l_ext) -> bytes, over a block-scaled cache
 _WS_LOCK = threading.Lock()
 
 
@@ -279,6 +280,7 @@ def _forget_sizes() -> None:
     """After tuning that moves the workspace bounds."""
     _WS_SIZE.clear()
     _SHARED_SIZE.clear()
+    _BLOCK_SIZE.clear()
 
 
 def set_tuning(num_ctas: int = 0, min_tokens_per_cta: int = 0) -> None:

@@ -101,12 +101,16 @@ def _run(name, names, tensors, scalars, stream, workspace, need=None, scalars_at
     """Calls a library entry point: the tensors' views, the scalars (after
     ``scalars_at`` tensors; None: after all), then workspace, its bytes and the
     stream, with the tensors' device current.  ``need``: workspace bytes (None:
-    the error word)."""
+    the error word; 0: the entry point takes none)."""
     device, buf, args = _views(names, tensors)
     if device != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _run(name, names, tensors, scalars, stream, workspace, need, scalars_at)
     raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if need == 0:
+        if not getattr(_native.lib(), name)(*args, *scalars, raw):
+            raise ValueError(f"{name}: {_native.last_error()}")
+        return
     if workspace is None:
         workspace = _workspace_of(device, stream, raw, 256 if need is None else need())
     elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != device or not workspace.is_contiguous():

@@ -1,0 +1,9 @@
+// Instances of the block-scaled cache's stream and of its joining launch, head_dim 128.
+#include "block_combine.cuh"
+
+namespace vsk {
+
+bk::BkFn kernel_block_stream_128() { return block_stream_kernel<128>; }
+bk::BkJoinFn kernel_block_combine_128() { return block_combine_kernel<128>; }
+
+}  // namespace vsk

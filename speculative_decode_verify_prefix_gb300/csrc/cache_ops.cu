@@ -11,8 +11,6 @@
 #include <set>
 #include <tuple>
 
-#include <cudaTypedefs.h>
-
 #include "flash_tc.cuh"
 #include "key_mass.cuh"
 #include "kv_evict.cuh"
@@ -29,7 +27,7 @@ static int fa_smem(int D) { return D == 64 ? fa::Geo<64>::smem : D == 128 ? fa::
 constexpr size_t kSchedOff = 64;  // fa_kernel's counters, between the error word and the partials
 static int fa_nq(int D) { return D == 256 ? 1 : 2; }
 
-static PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   std::call_once(once, [] {
@@ -46,7 +44,6 @@ static PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
 // Tensor map of bf16 rows [rows][heads][D] for boxes of [n_rows][n_heads][64
 // columns] in the 128-byte swizzle.  False where base or strides are none that
 // a map takes (the rows are then copied without one).
-static bool rows16(const vsk_tensor* t, int e);
 static bool rows_map(const vsk_tensor* t, int n_rows, int n_heads, CUtensorMap* map) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
   // a dimension of one element has any stride
@@ -122,7 +119,7 @@ static int launch_fa(const fa::FaParams& p, const CUtensorMap* maps, int D, int 
 }
 
 // The caller's workspace, or the library's own for the current device.
-static unsigned char* take_workspace(void* workspace, size_t bytes, size_t need, cudaStream_t st, size_t* got) {
+unsigned char* take_workspace(void* workspace, size_t bytes, size_t need, cudaStream_t st, size_t* got) {
   if (workspace) {
     if (bytes < need) {
       fail("workspace of %zu bytes is smaller than the %zu bytes needed", bytes, need);
@@ -145,16 +142,15 @@ static unsigned char* take_workspace(void* workspace, size_t bytes, size_t need,
   return static_cast<unsigned char*>(w);
 }
 
-static bool rows16(const vsk_tensor* t, int e) {
+bool rows16(const vsk_tensor* t, int e) {
   return aligned(t->data, 16) && (t->stride[0] * e) % 16 == 0 && (t->stride[1] * e) % 16 == 0;
 }
-static bool rows4(const vsk_tensor* t) { return aligned(t->data, 4) && t->stride[0] % 2 == 0 && t->stride[1] % 2 == 0; }
+bool rows4(const vsk_tensor* t) { return aligned(t->data, 4) && t->stride[0] % 2 == 0 && t->stride[1] % 2 == 0; }
 
-static double softmax_scale(float sm_scale, long long D) {
+double softmax_scale(float sm_scale, long long D) {
   return (sm_scale > 0.f && std::isfinite(sm_scale)) ? static_cast<double>(sm_scale)
                                                      : 1.0 / std::sqrt(static_cast<double>(D));
 }
-constexpr double kLog2e = 1.4426950408889634;
 // An infinite scale makes every score infinite or NaN.
 static bool check_scales(const Params& p) {
   if (!std::isfinite(p.dscale2)) return fail("sm_scale is too large");

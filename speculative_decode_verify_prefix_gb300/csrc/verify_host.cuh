@@ -1,8 +1,9 @@
 // What the host files of the library share: the error text, the argument
 // checks, the CTA plan and the workspace layout of the prefix stream
-// (verify_splitkv.cu) for the calls built around it (cache_ops.cu).
+// (verify_splitkv.cu) for the calls built around it (cache_ops.cu, block_ops.cu).
 #pragma once
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include "../../include/verify_splitkv.h"
 #include "verify_kernel.cuh"
@@ -74,5 +75,12 @@ struct StreamOnly {
 int plan_stream_only(const CallShape& cs, StreamOnly& so);
 int launch_stream_only(Params& p, const CallShape& cs, const StreamOnly& so, unsigned char* ws, size_t ws_bytes,
                        cudaStream_t st);
+// The caller's workspace, or (NULL) the library's own for the current device.
+unsigned char* take_workspace(void* workspace, size_t bytes, size_t need, cudaStream_t st, size_t* got);
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder();
+bool rows16(const vsk_tensor* t, int e);  // 16-byte aligned rows of elements of e bytes
+bool rows4(const vsk_tensor* t);          // 4-byte aligned bf16 rows
+double softmax_scale(float sm_scale, long long D);
+constexpr double kLog2e = 1.4426950408889634;
 
 }  // namespace vsk

@@ -3,7 +3,9 @@
 
 namespace vsk {
 
-bk::BkFn kernel_block_stream_64() { return block_stream_kernel<64>; }
+bk::BkFn kernel_block_stream_64(int nr) {
+  return nr == 8 ? block_stream_kernel<64, 8> : nr == 16 ? block_stream_kernel<64, 16> : block_stream_kernel<64, 32>;
+}
 bk::BkJoinFn kernel_block_combine_64() { return block_combine_kernel<64>; }
 
 }  // namespace vsk

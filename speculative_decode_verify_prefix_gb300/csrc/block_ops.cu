@@ -265,23 +265,26 @@ struct BlockForm {
   int smem, per_sm;
 };
 template <int D>
-static BlockForm form_of(bk::BkFn s, bk::BkJoinFn j) {
-  return BlockForm{s, j, bk::Geo<D>::smem, bk::Geo<D>::per_sm};
+static BlockForm form_of(int nr, bk::BkFn s, bk::BkJoinFn j) {
+  const int smem = nr == 8 ? bk::Geo<D, 8>::smem : nr == 16 ? bk::Geo<D, 16>::smem : bk::Geo<D, 32>::smem;
+  return BlockForm{s, j, smem, bk::Geo<D, 32>::per_sm};
 }
-static BlockForm block_form(long long D) {
-  return D == 64    ? form_of<64>(kernel_block_stream_64(), kernel_block_combine_64())
-         : D == 128 ? form_of<128>(kernel_block_stream_128(), kernel_block_combine_128())
-                    : form_of<256>(kernel_block_stream_256(), kernel_block_combine_256());
+static BlockForm block_form(long long D, long long R) {
+  const int nr = bk::row_tile(static_cast<int>(R));
+  return D == 64    ? form_of<64>(nr, kernel_block_stream_64(nr), kernel_block_combine_64())
+         : D == 128 ? form_of<128>(nr, kernel_block_stream_128(nr), kernel_block_combine_128())
+                    : form_of<256>(nr, kernel_block_stream_256(nr), kernel_block_combine_256());
 }
 
-// Partials: a slot per piece (CTA c, segment s: slot c + s), 32 rows a row tile.
+// Partials: a slot per piece (CTA c, segment s: slot c + s), whole row tiles.
 struct BlockWs {
   long long rows;
   size_t o_off, need;
 };
 static BlockWs block_ws(long long n_cta, long long B, long long h_kv, long long R, long long D) {
   BlockWs w;
-  w.rows = (R + bk::RT - 1) / bk::RT * bk::RT;
+  const long long nr = bk::row_tile(static_cast<int>(R));
+  w.rows = (R + nr - 1) / nr * nr;
   const size_t rows = static_cast<size_t>(n_cta + B * h_kv) * static_cast<size_t>(w.rows);
   w.o_off = 256 + align256(4 * rows);
   // the buffer's last 64 KiB hold the counters of other calls
@@ -448,7 +451,7 @@ size_t vsk_block_workspace_size(int64_t max_bs, int64_t h_q, int64_t h_kv, int64
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
   const long long R = h_q / h_kv * max_len_extend;
   if (R > kMaxRows || !current_sms(&sms)) return 0;
-  return block_ws(static_cast<long long>(sms) * block_form(head_dim).per_sm, max_bs, h_kv, R, head_dim).need;
+  return block_ws(static_cast<long long>(sms) * block_form(head_dim, R).per_sm, max_bs, h_kv, R, head_dim).need;
 }
 
 int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vsk_tensor* ve, const vsk_tensor* o,
@@ -499,7 +502,7 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
                           runs_of("k_cache", kc, 1), runs_of("v_cache", vc, 1)})
       if (meet(ro, r)) return fail("o_extend overlaps %s", r.name);
   }
-  const BlockForm f = block_form(D);
+  const BlockForm f = block_form(D, R);
   int sms = 0;
   if (!current_sms(&sms)) return 0;
   const long long n_cta = static_cast<long long>(sms) * f.per_sm;
@@ -562,7 +565,7 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   if (!allow_smem(reinterpret_cast<const void*>(f.stream), f.smem)) return 0;
   void* args[] = {&p, &maps[0], &maps[1]};
   cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void*>(f.stream),
-                                   dim3(static_cast<unsigned>(n_cta), static_cast<unsigned>(w.rows / bk::RT)),
+                                   dim3(static_cast<unsigned>(n_cta), static_cast<unsigned>(w.rows / bk::row_tile(p.R))),
                                    dim3(bk::kThreads), args, f.smem, st);
   if (e != cudaSuccess) return fail("kernel launch failed: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};

@@ -28,9 +28,15 @@
 // The groups of 16 keys of all (sequence, KV head) segments are laid end to end
 // and every CTA takes an equal share; a segment's part of a share is a piece,
 // whose partial (o, log2 of its sum) block_combine_kernel folds.
-// Every wait is bounded (one second); a CTA that gives up sets error bit 8,
-// waits for its copies and MMAs in flight, frees its tensor memory and exits.
+// Every wait is bounded (one second); in a CTA that gives up every role ends its
+// loop without copying, multiplying or arriving anywhere (the copies' barriers then
+// still tell when those under way are done), sets error bit 8, waits for copies and
+// MMAs in flight, frees the tensor memory and exits.  No barrier can run two phases
+// ahead of a wait for it: each phase needs an arrival that follows the wait for the
+// one before.
 #pragma once
+#include <type_traits>
+
 #include "flash_tc.cuh"
 
 namespace vsk {
@@ -42,7 +48,6 @@ namespace bk {
 constexpr int KT = 128;      // keys of a tile
 constexpr int GK = 16;       // keys of a group (one TMA box, one block's scale)
 constexpr int GT = KT / GK;  // groups of a tile
-constexpr int RT = 32;       // packed rows of a CTA
 constexpr int kThreads = 192;
 constexpr int kSm = 128;     // softmax threads
 constexpr int kMeta = 8;     // tiles whose scales are kept (more than the ring holds)
@@ -81,38 +86,47 @@ struct BkParams {
 using BkFn = void (*)(const BkParams, const CUtensorMap, const CUtensorMap);
 using BkJoinFn = void (*)(const BkParams);
 
-template <int D>
+// Packed rows of a CTA: the smallest of 8, 16, 32 that holds them (32: in row
+// tiles, the grid's y).  A warp finds NR rows 32 / NR times in its lanes and its
+// lanes share the keys: with 32 rows for all a serving batch of 16 took 537 us, so
+// XXX, and single tokens of 4 rows 122, so XXX.
+__host__ __device__ constexpr int row_tile(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
+
+template <int D, int NR>
 struct Geo {
   static constexpr int CB = D < 128 ? 64 : 128;     // bytes of a shared-memory row
   static constexpr int NB = D / CB;                 // column blocks of a K / V tile
   static constexpr int ENT = KT * D;                // K (or V) rows of a tile
   static constexpr int QB = 128 * 2 * D;            // Q: [hi | lo] in 128-byte column blocks
-  static constexpr int PB = 96 * 128;               // P; the MMA reads 32 rows more, whose result nobody takes
+  static constexpr int PB = 3 * NR * 128;           // P; the MMA reads 128 rows, of the others nobody takes the result
+  static constexpr int NP = D == 128 && NR == 32 ? 1 : 2;  // its buffers
   static constexpr int per_sm = D == 256 ? 1 : 2;
   static constexpr int ctl = 3072;                  // barriers, scales, exchanges
-  static constexpr int room = (per_sm == 1 ? kSmemPerCTAMax : kSmemPerSM / 2 - kReservedPerCTA) - ctl - QB - PB;
+  static constexpr int room = (per_sm == 1 ? kSmemPerCTAMax : kSmemPerSM / 2 - kReservedPerCTA) - ctl - QB - NP * PB;
   static constexpr int NS = room / (2 * ENT) < 5 ? room / (2 * ENT) : 5;  // stages
   static constexpr int q_off = ctl;
   static constexpr int p_off = q_off + QB;
-  static constexpr int ring_off = p_off + PB;
+  static constexpr int ring_off = p_off + NP * PB;
   static constexpr int smem = ring_off + 2 * NS * ENT;
   static constexpr int cols = D == 256 ? 512 : 256;  // S 128, O D
   static_assert(NS >= 1 && NS + 2 < kMeta, "ring");
-  static_assert(2 * ENT >= 32 * 128, "P's last rows are read from the ring");
+  static_assert(2 * NS * ENT >= 128 * 128, "the rows behind P are read from the ring");
+  static_assert(q_off % 1024 == 0 && p_off % 1024 == 0 && PB % 1024 == 0 && ring_off % 1024 == 0, "swizzled layouts");
 };
 
 // control block
 constexpr int kScanOff = 0;    // 6 warps' sums, then the CTA's first segment
 constexpr int kBarOff = 128;
 constexpr int kBKFull = 0, kBKEmpty = 5, kBVFull = 10, kBVEmpty = 15, kBSFull = 20, kBSEmpty = 21, kBPFull = 22,
-              kBPEmpty = 23, kBQFull = 24, kBDone = 25, kNumBars = 26;
+              kBPEmpty = 24, kBQFull = 26, kBDone = 27, kNumBars = 28;
 constexpr int kTmemOff = kBarOff + 8 * kNumBars;
 constexpr int kAbortOff = kTmemOff + 4;
-constexpr int kQscOff = 352;   // [32] float: a row's score scale
+constexpr int kQscOff = 384;   // [32] float: a row's score scale
 constexpr int kMetaOff = 512;  // [kMeta][GT] float4: ks, log2 vs, 1 / vs, keys that are there (+ 256: the tile lacks some)
-constexpr int kRedOff = 1536;  // [2][4][32] float: maxima of a tile
-constexpr int kSumOff = 2560;  // [4][32] float: sums of a piece
-static_assert(kAbortOff + 4 <= kQscOff && kMetaOff + kMeta * GT * 16 <= kRedOff && kRedOff + 1024 <= kSumOff, "control block");
+constexpr int kRedOff = 1536;  // [4][NR] float: maxima of a tile
+constexpr int kRowOff = 2048;  // [kMeta][GT] int: the groups' first rows in the cache; [kMeta] int: the KV head
+constexpr int kSumOff = 2560;  // [4][NR] float: sums of a piece
+static_assert(kAbortOff + 4 <= kQscOff && kMetaOff + kMeta * GT * 16 <= kRedOff && kRedOff + 512 <= kRowOff && kRowOff + kMeta * (GT + 1) * 4 <= kSumOff, "control block");
 
 // Segments and their cut, the same in both kernels.
 struct Cut {
@@ -241,6 +255,9 @@ __device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo, uint32_t 
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16) |
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (static_cast<uint64_t>(CB == 128 ? 2 : 4) << 61);
 }
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
@@ -248,19 +265,20 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 }
 
 // The row tile's packed rows (row r = draft r / gq, query head h gq + r % gq;
-// rows from R on are zero) into Q, as hi and lo terms, four times, and their
-// score scales; by the softmax warps, eight rows each.
-template <int D>
+// rows from R on are zero) into Q, as hi and lo terms, 128 / NR times, and their
+// score scales; by the softmax warps, NR / 4 rows each.
+template <int D, int NR>
 __device__ __forceinline__ void load_rows(const BkParams& p, const BSeg& s, unsigned char* smem, int warp, int lane) {
   constexpr int W = D / 64;  // 32-bit words of a row per lane
+  constexpr int J = NR / 4;
   const int a = __ldg(p.qo + s.b), e = __ldg(p.qo + s.b + 1);
   const bool ok = a >= 0 && e - a == p.L && static_cast<long long>(a) + p.L <= p.n_rows;
   const long long first = ok ? a : static_cast<long long>(s.b) * p.L;
   float* qsc = reinterpret_cast<float*>(smem + kQscOff);
-  uint32_t v[8][W];
+  uint32_t v[J][W];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = static_cast<int>(blockIdx.y) * RT + 8 * warp + j;
+  for (int j = 0; j < J; ++j) {
+    const int r = static_cast<int>(blockIdx.y) * NR + J * warp + j;
     const bool live = r < p.R;
     const int rr = live ? r : 0;
     const __nv_bfloat16* src = p.q + (first + rr / p.gq) * p.q_s0 + static_cast<long long>(s.h * p.gq + rr % p.gq) * p.q_s1;
@@ -268,8 +286,8 @@ __device__ __forceinline__ void load_rows(const BkParams& p, const BSeg& s, unsi
     for (int w = 0; w < W; ++w) v[j][w] = live ? ld_u32(src + 2 * (W * lane + w)) : 0u;
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int row = 8 * warp + j;
+  for (int j = 0; j < J; ++j) {
+    const int row = J * warp + j;
     unsigned mx = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) mx = max(mx, mag_bf16x2(v[j][w]));
@@ -304,10 +322,10 @@ __device__ __forceinline__ void load_rows(const BkParams& p, const BSeg& s, unsi
     for (int t = 0; t < 2; ++t) {
       const uint32_t* x = t ? lo : hi;
       const int at = t * D + 2 * W * lane;  // byte of the row [hi | lo]
-      unsigned char* d = smem + Geo<D>::q_off + (at >> 7) * (128 * 128) + row * 128 + ((((at & 127) >> 4) ^ (row & 7)) << 4) + (at & 15);
+      unsigned char* d = smem + Geo<D, NR>::q_off + (at >> 7) * (128 * 128) + row * 128 + ((((at & 127) >> 4) ^ (row & 7)) << 4) + (at & 15);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        unsigned char* dk = d + k * (32 * 128);
+      for (int k = 0; k < 128 / NR; ++k) {
+        unsigned char* dk = d + k * (NR * 128);
         if constexpr (W == 1)
           *reinterpret_cast<unsigned short*>(dk) = static_cast<unsigned short>(x[0]);
         else if constexpr (W == 2)
@@ -321,15 +339,15 @@ __device__ __forceinline__ void load_rows(const BkParams& p, const BSeg& s, unsi
 
 }  // namespace bk
 
-template <int D>
-__global__ void __launch_bounds__(bk::kThreads, bk::Geo<D>::per_sm)
+template <int D, int NR>
+__global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
     block_stream_kernel(const __grid_constant__ bk::BkParams p, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
   using namespace bk;
   using tc::idesc, tc::mbar_arrive, tc::mbar_init, tc::mma_commit, tc::mma_f8_ss, tc::fence_proxy_async;
   using tc::tc_fence_after, tc::tc_fence_before, tc::tmem_ld, tc::tmem_st, tc::tmem_wait_st;
-  using G = bk::Geo<D>;
-  constexpr int NS = G::NS, CB = G::CB, ENT = G::ENT;
+  using G = bk::Geo<D, NR>;
+  constexpr int NS = G::NS, CB = G::CB, ENT = G::ENT, NP = G::NP;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // block_combine_kernel's CTAs may start (they wait for this grid themselves)
@@ -356,8 +374,10 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D>::per_sm)
     }
     mbar_init(bar(kBSFull), 1);
     mbar_init(bar(kBSEmpty), 4);
-    mbar_init(bar(kBPFull), 4);
-    mbar_init(bar(kBPEmpty), 1);
+    for (int i = 0; i < NP; ++i) {
+      mbar_init(bar(kBPFull + i), 4);
+      mbar_init(bar(kBPEmpty + i), 1);
+    }
     mbar_init(bar(kBQFull), 4);
     mbar_init(bar(kBDone), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -396,61 +416,93 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D>::per_sm)
       ks = __ldg(p.ks + page * p.ks_s0 + it.s.h);
       vs = __ldg(p.vs + page * p.vs_s0 + it.s.h);
     };
-    cur.first(p, seg0, start, end);
-    ahead = cur;
     int row, keys, row2, keys2;
     float ks, vs, ks2, vs2;
+    cur.first(p, seg0, start, end);
     fetch(cur, row, keys, ks, vs);
+    // K and V go on by themselves: a K slot is free once its scores are done, a V
+    // slot only when its weights have met it.  (One after the other, K waited for
+    // the V of a tile before: XXX.)
+    volatile int* rows = reinterpret_cast<volatile int*>(smem + kRowOff);
+    volatile int* heads = rows + kMeta * GT;
     uint32_t nk = 0, nv = 0;  // K and V tiles whose copies were issued
-    uint32_t u = 0;
+    int j = 0, looks = 0;     // tile of the batch
+    unsigned long long since = 0;
+    ahead = cur;
+    if (cur.valid) ahead.next(p, start, end);
+    fetch(ahead, row2, keys2, ks2, vs2);
 #pragma unroll 1
-    while (cur.valid) {
-      ahead.next(p, start, end);
-      fetch(ahead, row2, keys2, ks2, vs2);
-      const int tiles = (min(32, cur.ge - cur.g) + GT - 1) / GT;
-#pragma unroll 1
-      for (int j = 0; j < tiles; ++j, ++u) {
-        const uint32_t st = u % NS, par = (u / NS) & 1u;
+    while (cur.valid || nv < nk) {
+      bool moved = false;
+      // a tile's rows are kept until its V is on its way
+      if (cur.valid && nk - nv < kMeta && __all_sync(0xffffffffu, tr::test(bar(kBKEmpty + nk % NS), ((nk / NS) & 1u) ^ 1u))) {
+        const uint32_t st = nk % NS;
         const bool mine = (lane >> 3) == j;
         const unsigned there = __ballot_sync(0xffffffffu, mine && keys > 0);
         const bool lacks = __any_sync(0xffffffffu, mine && keys < GK);
-        const uint32_t bytes = __popc(there) * (GK * D);
-        const uint32_t kd = ring_s + st * (2 * ENT) + (lane & 7) * (GK * CB), vd = kd + ENT;
-        if (fa::wait_all(bar(kBKEmpty + st), par ^ 1u, abort_flag, p.err)) {
-          if (lane == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar(kBKFull + st)), "r"(bytes) : "memory");
-          __syncwarp();
-          if (mine && keys > 0)
+        if (lane == 0) expect(bar(kBKFull + st), __popc(there) * (GK * D));
+        __syncwarp();
+        if (mine) {
+          const uint32_t kd = ring_s + st * (2 * ENT) + (lane & 7) * (GK * CB);
+          if (keys > 0) {
 #pragma unroll
             for (int c = 0; c < G::NB; ++c)
               fa::tma_load_box(kd + c * (KT * CB), &kmap, bar(kBKFull + st), c * CB, cur.s.h, row);
-          nk = u + 1;
-        }
-        // the tile before the last kMeta's scales have been read: V of tile u - NS was multiplied after that
-        if (fa::wait_all(bar(kBVEmpty + st), par ^ 1u, abort_flag, p.err)) {
-          if (lane == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar(kBVFull + st)), "r"(bytes) : "memory");
-          __syncwarp();
-          if (mine && keys > 0)
-#pragma unroll
-            for (int c = 0; c < G::NB; ++c)
-              fa::tma_load_box(vd + c * (KT * CB), &vmap, bar(kBVFull + st), c * CB, cur.s.h, row);
-          nv = u + 1;
-        }
-        if (mine) {
+          }
           // a scale that is no positive finite number in the range gives NaN
           const bool good = ks >= kMinScale && ks <= kMaxScale && vs >= kMinScale && vs <= kMaxScale;
           if (!good) atomicOr(p.err, kErrBadScale);
           const float nan = __int_as_float(0x7FC00000);
-          meta[(u % kMeta) * GT + (lane & 7)] =
+          meta[(nk % kMeta) * GT + (lane & 7)] =
               make_float4(good ? ks : nan, good ? log2f(vs) : nan, good ? 1.f / vs : nan, __int_as_float(keys + (lacks ? 256 : 0)));
+          rows[(nk % kMeta) * GT + (lane & 7)] = keys > 0 ? row : -1;
+          if ((lane & 7) == 0) heads[nk % kMeta] = cur.s.h;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBKFull + st));
+        ++nk;
+        moved = true;
+        if (cur.g + GT * ++j >= min(cur.ge, cur.g + 32)) {
+          cur = ahead;
+          row = row2;
+          keys = keys2;
+          ks = ks2;
+          vs = vs2;
+          j = 0;
+          if (cur.valid) {
+            ahead.next(p, start, end);
+            fetch(ahead, row2, keys2, ks2, vs2);
+          }
+        }
       }
-      cur = ahead;
-      row = row2;
-      keys = keys2;
-      ks = ks2;
-      vs = vs2;
+      if (nv < nk && __all_sync(0xffffffffu, tr::test(bar(kBVEmpty + nv % NS), ((nv / NS) & 1u) ^ 1u))) {
+        const uint32_t st = nv % NS;
+        const int vhead = heads[nv % kMeta];
+        const int vrow = lane < GT ? rows[(nv % kMeta) * GT + lane] : -1;
+        const unsigned there = __ballot_sync(0xffffffffu, vrow >= 0);
+        if (lane == 0) expect(bar(kBVFull + st), __popc(there) * (GK * D));
+        __syncwarp();
+        if (vrow >= 0) {
+          const uint32_t vd = ring_s + st * (2 * ENT) + ENT + lane * (GK * CB);
+#pragma unroll
+          for (int c = 0; c < G::NB; ++c)
+            fa::tma_load_box(vd + c * (KT * CB), &vmap, bar(kBVFull + st), c * CB, vhead, vrow);
+        }
+        ++nv;
+        moved = true;
+      }
+      if (moved) {
+        looks = 0;
+      } else {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+        if (++looks == 4096) since = tc::global_ns();
+        if (looks > 4096 && (looks & 255) == 0 && __all_sync(0xffffffffu, tc::global_ns() - since > 1000000000ull)) {
+          *abort_flag = 1;
+          if (lane == 0) atomicOr(p.err, kErrTimeout);
+          break;
+        }
+        __nanosleep(20);
+      }
     }
     // the copies end before the CTA does (in a CTA that gave up, nobody else waits for them)
     for (uint32_t k = 1; k <= NS; ++k) {
@@ -463,18 +515,20 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D>::per_sm)
     const uint64_t dq = desc<128>(smem_u32(smem + G::q_off), 16, 1024), dp = desc<128>(smem_u32(smem + G::p_off), 16, 1024);
     const uint64_t dk = desc<CB>(ring_s, 16, 8 * CB), dv = desc<CB>(ring_s + ENT, KT * CB, 8 * CB);
     uint32_t u = 0, piece = 0;
-    bool pending = false, pfirst = false;
+    bool pending = false, pfirst = false, alive = true;
+    auto wait = [&](int i, uint32_t parity) { alive = alive && fa::wait_all(bar(i), parity, abort_flag, p.err); };
     auto weigh = [&](uint32_t w, bool first) {  // O += P V of tile w
       const uint32_t st = w % NS;
-      fa::wait_all(bar(kBPFull), w & 1u, abort_flag, p.err);
-      fa::wait_all(bar(kBVFull + st), (w / NS) & 1u, abort_flag, p.err);
+      wait(kBPFull + w % NP, (w / NP) & 1u);
+      wait(kBVFull + st, (w / NS) & 1u);
       tc_fence_after();
-      if (fa::elect_one()) {
+      if (alive && fa::elect_one()) {
         const uint64_t vd = dv + static_cast<uint64_t>((st * (2 * ENT)) >> 4);
+        const uint64_t pd = dp + static_cast<uint64_t>(((w % NP) * G::PB) >> 4);
 #pragma unroll
         for (int k = 0; k < KT / 32; ++k)
-          mma_f8_ss(tO, dp + static_cast<uint64_t>(2 * k), vd + static_cast<uint64_t>((k * 32 * CB) >> 4), idO, !(first && k == 0));
-        mma_commit(bar(kBPEmpty));
+          mma_f8_ss(tO, pd + static_cast<uint64_t>(2 * k), vd + static_cast<uint64_t>((k * 32 * CB) >> 4), idO, !(first && k == 0));
+        mma_commit(bar(kBPEmpty + w % NP));
         mma_commit(bar(kBVEmpty + st));
       }
       __syncwarp();
@@ -489,15 +543,15 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D>::per_sm)
           weigh(u - 1, pfirst);
           pending = false;
         }
-        fa::wait_all(bar(kBQFull), piece & 1u, abort_flag, p.err);
+        wait(kBQFull, piece & 1u);
         ++piece;
 #pragma unroll 1
         for (int g = g0; g < ge; g += GT, ++u) {
           const uint32_t st = u % NS;
-          fa::wait_all(bar(kBKFull + st), (u / NS) & 1u, abort_flag, p.err);
-          fa::wait_all(bar(kBSEmpty), (u & 1u) ^ 1u, abort_flag, p.err);
+          wait(kBKFull + st, (u / NS) & 1u);
+          wait(kBSEmpty, (u & 1u) ^ 1u);
           tc_fence_after();
-          if (fa::elect_one()) {
+          if (alive && fa::elect_one()) {
             const uint64_t kd = dk + static_cast<uint64_t>((st * (2 * ENT)) >> 4);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -524,121 +578,158 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D>::per_sm)
     fa::wait_last(bar(kBDone), 0);
   } else {
     // ================================ softmax ================================
+    // Thread (warp w, lane): row lane % NR, its KN = NR keys 32 w + NR (lane / NR) ..
+    constexpr int KN = NR;              // keys of a thread
+    constexpr int NG = KN > GK ? 2 : 1;  // their groups
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const float NEG_INF = -INFINITY;
+    const int r = lane & (NR - 1), part = lane / NR;
+    const int key0 = 32 * warp + KN * part;  // this thread's first key of a tile
     const float4* meta = reinterpret_cast<const float4*>(smem + kMetaOff);
     float* red = reinterpret_cast<float*>(smem + kRedOff);
     float* sums = reinterpret_cast<float*>(smem + kSumOff);
     const float* qscs = reinterpret_cast<const float*>(smem + kQscOff);
     uint32_t u = 0;
+    bool alive = true;
+    auto wait = [&](int i, uint32_t parity) { alive = alive && fa::wait_all(bar(i), parity, abort_flag, p.err); };
+    auto arrive = [&](int i) {
+      if (lane == 0 && alive) mbar_arrive(bar(i));
+    };
+    auto wait_weighed = [&](uint32_t v) {  // P V of tile v done (and so of those before)
+      wait(kBPEmpty + v % NP, (v / NP) & 1u);
+      tc_fence_after();
+    };
     BSeg s = seg0;
 #pragma unroll 1
     for (; s.b < p.B && s.off < end; seg_next(p, s)) {
       int g0, ge;
       piece_of(s, start, end, g0, ge);
       const long long slot = blockIdx.x + static_cast<long long>(s.b) * p.h_kv + s.h;
-      const int row0 = static_cast<int>(blockIdx.y) * RT;
+      const int row0 = static_cast<int>(blockIdx.y) * NR;
       float* lse_p = p.plse + slot * p.rows + row0;
       float* o_p = p.po + (slot * p.rows + row0) * D;
-      const int live = min(RT, p.R - row0);
+      const int live = min(NR, p.R - row0);
       if (g0 >= ge) {  // no key: an empty partial
         if (tid < live) lse_p[tid] = NEG_INF;
         continue;
       }
-      load_rows<D>(p, s, smem, warp, lane);
+      load_rows<D, NR>(p, s, smem, warp, lane);
       fence_proxy_async();
       named_bar_sync(1, kSm);  // the rows' scales
-      if (lane == 0) mbar_arrive(bar(kBQFull));
-      const float qsc = qscs[lane];
+      arrive(kBQFull);
+      const float qsc = qscs[r];
       float m = NEG_INF, l = 0.f;
 #pragma unroll 1
       for (int g = g0; g < ge; g += GT, ++u) {
-        fa::wait_all(bar(kBSFull), u & 1u, abort_flag, p.err);
+        wait(kBSFull, u & 1u);
         tc_fence_after();
-        float x[32];
-        tmem_ld<32>(tS + lanes + 32 * warp, x);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBSEmpty));
-        const float4 me[2] = {meta[(u % kMeta) * GT + 2 * warp], meta[(u % kMeta) * GT + 2 * warp + 1]};
-        float tm = NEG_INF;
+        float x[KN];
+        {
+          float y[32];
+          tmem_ld<32>(tS + lanes + 32 * warp, y);
+          tc_fence_before();
+          __syncwarp();
+          arrive(kBSEmpty);
+          if constexpr (NR == 32) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float c = qsc * me[h].x;
+            for (int i = 0; i < KN; ++i) x[i] = y[i];
+          } else if constexpr (NR == 16) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[16 * h + i] = fmaf(x[16 * h + i], c, me[h].y);
+            for (int i = 0; i < KN; ++i) x[i] = part ? y[16 + i] : y[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < KN; ++i) {
+              const float lo = part & 1 ? y[8 + i] : y[i], hi = part & 1 ? y[24 + i] : y[16 + i];
+              x[i] = part & 2 ? hi : lo;
+            }
+          }
         }
+        const float4* mt = meta + (u % kMeta) * GT + key0 / GK;
+        float4 me[NG];
+#pragma unroll
+        for (int h = 0; h < NG; ++h) me[h] = mt[h];
+#pragma unroll
+        for (int i = 0; i < KN; ++i) x[i] = fmaf(x[i], qsc * me[i / GK].x, me[i / GK].y);
         const bool lacks = __float_as_int(me[0].w) >= 256;
         if (lacks) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int keys = __float_as_int(me[h].w) & 255;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (i >= keys) x[16 * h + i] = NEG_INF;
-          }
+          for (int i = 0; i < KN; ++i)
+            if ((key0 & (GK - 1)) + (i & (GK - 1)) >= (__float_as_int(me[i / GK].w) & 255)) x[i] = NEG_INF;
         }
+        float t4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) tm = fmaxf(tm, x[i]);
-        float* rd = red + (u & 1) * 128;
-        rd[tid] = tm;
-        named_bar_sync(1, kSm);
-        tm = fmaxf(fmaxf(rd[lane], rd[32 + lane]), fmaxf(rd[64 + lane], rd[96 + lane]));  // alike in the four warps
-        // P and O are free once the tile before is weighed
-        if (g > g0) {
-          fa::wait_all(bar(kBPEmpty), (u & 1u) ^ 1u, abort_flag, p.err);
-          tc_fence_after();
-        }
-        if (__any_sync(0xffffffffu, tm > m + kThr)) {
+        for (int i = 0; i < KN; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i]);
+        float tm = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        // The reference stays while no row of the tile passes it by 2^kThr.
+        if (tc::bar_red_or(1, kSm, tm > m + kThr)) {  // alike in the four warps
+#pragma unroll
+          for (int o = NR; o < 32; o *= 2) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
+          if (lane < NR) red[warp * NR + lane] = tm;
+          named_bar_sync(1, kSm);
+          tm = fmaxf(fmaxf(red[r], red[NR + r]), fmaxf(red[2 * NR + r], red[3 * NR + r]));
           const float mn = fmaxf(m, tm);
           const float al = mn == NEG_INF ? 1.f : fast_exp2(m - mn);
-          if (g > g0 && warp < 3) {
+          if (g > g0) {  // O holds the piece's earlier tiles
+            wait_weighed(u - 1);
+            if (32 * warp < 3 * NR) {
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              tmem_ld<32>(tO + lanes + c, o);
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld<32>(tO + lanes + c, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= al;
-              tmem_st<32>(tO + lanes + c, o);
+                for (int i = 0; i < 32; ++i) o[i] *= al;
+                tmem_st<32>(tO + lanes + c, o);
+              }
+              tmem_wait_st();
             }
-            tmem_wait_st();
           }
           l *= al;
           m = mn;
         }
         const float up = m == NEG_INF ? 0.f : static_cast<float>(kUp) - m;
+        uint32_t w[3][KN / 4];
+        float sum[NG];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float sum = 0.f;
-          uint32_t w[3][4];
+        for (int h = 0; h < NG; ++h) sum[h] = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float t[3][4];
+        for (int i = 0; i < KN / 4; ++i) {
+          float t[3][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float y = fast_exp2(x[16 * h + 4 * i + e] + up);
-              sum += y;
-              // the top 4 bits where e4m3 has them all (2^-6 and above), and what they leave
-              const float a = y < 0.015625f ? 0.f : __uint_as_float(__float_as_uint(y) & 0xFFF00000u);
-              const float z = (y - a) * 16.f;
-              const float b = z < 0.015625f ? 0.f : __uint_as_float(__float_as_uint(z) & 0xFFF00000u);
-              t[0][e] = a;
-              t[1][e] = b;
-              t[2][e] = (z - b) * 16.f;
-            }
-#pragma unroll
-            for (int k = 0; k < 3; ++k) w[k][i] = e4m3x4(t[k][0], t[k][1], t[k][2], t[k][3]);
+          for (int e = 0; e < 4; ++e) {
+            const float y = fast_exp2(x[4 * i + e] + up);
+            sum[i / 4] += y;
+            // the top 4 bits where e4m3 has them all (2^-6 and above), and what they leave
+            const float a = y < 0.015625f ? 0.f : __uint_as_float(__float_as_uint(y) & 0xFFF00000u);
+            const float z = (y - a) * 16.f;
+            const float b = z < 0.015625f ? 0.f : __uint_as_float(__float_as_uint(z) & 0xFFF00000u);
+            t[0][e] = a;
+            t[1][e] = b;
+            t[2][e] = (z - b) * 16.f;
           }
-          l = fmaf(sum, me[h].z, l);
 #pragma unroll
-          for (int k = 0; k < 3; ++k)
-            *reinterpret_cast<uint4*>(smem + G::p_off + (32 * k + lane) * 128 + (((2 * warp + h) ^ (lane & 7)) << 4)) =
-                make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+          for (int k = 0; k < 3; ++k) w[k][i] = e4m3x4(t[k][0], t[k][1], t[k][2], t[k][3]);
+        }
+#pragma unroll
+        for (int h = 0; h < NG; ++h) l = fmaf(sum[h], me[h].z, l);
+        if (u >= NP) wait_weighed(u - NP);  // the buffer is free once its tile before is weighed
+        unsigned char* pb = smem + G::p_off + (u % NP) * G::PB;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const int pr = NR * k + r;
+          unsigned char* at = pb + pr * 128;
+          if constexpr (KN >= 16) {
+#pragma unroll
+            for (int h = 0; h < KN / 16; ++h)
+              *reinterpret_cast<uint4*>(at + (((key0 / 16 + h) ^ (pr & 7)) << 4)) =
+                  make_uint4(w[k][4 * h], w[k][4 * h + 1], w[k][4 * h + 2], w[k][4 * h + 3]);
+          } else {
+            *reinterpret_cast<uint2*>(at + (((key0 / 16) ^ (pr & 7)) << 4) + (key0 & 15)) = make_uint2(w[k][0], w[k][1]);
+          }
         }
         if (lacks) {
           // V rows of keys that are not there: 0 times what lies there may be NaN
           const uint32_t st = u % NS;
-          fa::wait_all(bar(kBVFull + st), (u / NS) & 1u, abort_flag, p.err);
+          wait(kBVFull + st, (u / NS) & 1u);
           if ((tid & 15) >= (__float_as_int(meta[(u % kMeta) * GT + (tid >> 4)].w) & 255)) {
             unsigned char* v = smem + G::ring_off + st * (2 * ENT) + ENT + tid * CB;
 #pragma unroll
@@ -650,45 +741,55 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D>::per_sm)
         fence_proxy_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBPFull));
+        arrive(kBPFull + u % NP);
       }
       // ---- the piece's partial: o = sum of the terms / l, log2 of the sum ----
-      sums[tid] = l;
-      fa::wait_all(bar(kBPEmpty), (u & 1u) ^ 1u, abort_flag, p.err);
-      tc_fence_after();
-      unsigned char* stage = smem + G::p_off;  // [3 terms][32 rows][32 columns], P is free
-      const int row = tid >> 2, quarter = tid & 3;
+#pragma unroll
+      for (int o = NR; o < 32; o *= 2) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane < NR) sums[warp * NR + lane] = l;
+      wait_weighed(u - 1);
       named_bar_sync(1, kSm);
-      const float lr = (sums[row] + sums[32 + row]) + (sums[64 + row] + sums[96 + row]);
-      const float inv = lr == 0.f ? 0.f : 1.f / lr;
-      if (warp == 0 && lane < live) {
-        const float la = (sums[lane] + sums[32 + lane]) + (sums[64 + lane] + sums[96 + lane]);
-        lse_p[lane] = la == 0.f ? NEG_INF : m + (log2f(la) - static_cast<float>(kUp));
-      }
+      const float lt = (sums[r] + sums[NR + r]) + (sums[2 * NR + r] + sums[3 * NR + r]);
+      if (warp == 0 && lane < live) lse_p[lane] = lt == 0.f ? NEG_INF : m + (log2f(lt) - static_cast<float>(kUp));
+      // the terms meet in shared memory, [3][NR rows][32 columns] at a time: P is free
+      unsigned char* stage = smem + G::p_off;
+      constexpr int TPR = 128 / NR, CPT = 32 / TPR;  // threads of a row, columns of a thread
+      const int orow = tid / TPR, oc = (tid % TPR) * CPT;
+      const float lo = (sums[orow] + sums[NR + orow]) + (sums[2 * NR + orow] + sums[3 * NR + orow]);
+      const float inv = lo == 0.f ? 0.f : 1.f / lo;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
-        if (warp < 3) {
+        if (32 * warp < 3 * NR) {
           float o[32];
           tmem_ld<32>(tO + lanes + c, o);
+          const int pr = 32 * warp + lane;  // term pr / NR of row pr % NR
+          if (pr < 3 * NR) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(stage + (warp * 32 + lane) * 128 + ((i ^ (lane & 7)) << 4)) =
-                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(stage + pr * 128 + ((i ^ (pr & 7)) << 4)) =
+                  make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
         }
         named_bar_sync(1, kSm);
-        if (row < live) {
+        if (orow < live) {
+          // NR is a multiple of 8: the three terms' rows are swizzled alike
+          using V = std::conditional_t<CPT == 2, float2, float4>;
+          constexpr int VN = sizeof(V) / 4;
+          float res[CPT];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const unsigned char* at = stage + row * 128 + (((2 * quarter + i) ^ (row & 7)) << 4);
-            const float4 a = *reinterpret_cast<const float4*>(at), b = *reinterpret_cast<const float4*>(at + 4096),
-                         d = *reinterpret_cast<const float4*>(at + 8192);
-            float4 r;
-            r.x = fmaf(d.x, 0.00390625f, fmaf(b.x, 0.0625f, a.x)) * inv;
-            r.y = fmaf(d.y, 0.00390625f, fmaf(b.y, 0.0625f, a.y)) * inv;
-            r.z = fmaf(d.z, 0.00390625f, fmaf(b.z, 0.0625f, a.z)) * inv;
-            r.w = fmaf(d.w, 0.00390625f, fmaf(b.w, 0.0625f, a.w)) * inv;
-            *reinterpret_cast<float4*>(o_p + row * D + c + 8 * quarter + 4 * i) = r;
+          for (int i = 0; i < CPT; i += VN) {
+            const unsigned char* at = stage + orow * 128 + ((((oc + i) >> 2) ^ (orow & 7)) << 4) + (oc & (4 - VN)) * 4;
+            V term[3];
+#pragma unroll
+            for (int k = 0; k < 3; ++k) term[k] = *reinterpret_cast<const V*>(at + k * (NR * 128));
+            const float *a = reinterpret_cast<const float*>(&term[0]), *b = reinterpret_cast<const float*>(&term[1]),
+                        *d = reinterpret_cast<const float*>(&term[2]);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) res[i + e] = fmaf(d[e], 0.00390625f, fmaf(b[e], 0.0625f, a[e])) * inv;
           }
+          float* out = o_p + orow * D + c + oc;
+#pragma unroll
+          for (int i = 0; i < CPT; i += 2) *reinterpret_cast<float2*>(out + i) = make_float2(res[i], res[i + 1]);
         }
         named_bar_sync(1, kSm);
       }
@@ -703,9 +804,9 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D>::per_sm)
   }
 }
 
-bk::BkFn kernel_block_stream_64();
-bk::BkFn kernel_block_stream_128();
-bk::BkFn kernel_block_stream_256();
+bk::BkFn kernel_block_stream_64(int nr);  // nr: rows of a CTA
+bk::BkFn kernel_block_stream_128(int nr);  // nr: rows of a CTA
+bk::BkFn kernel_block_stream_256(int nr);  // nr: rows of a CTA
 bk::BkJoinFn kernel_block_combine_64();
 bk::BkJoinFn kernel_block_combine_128();
 bk::BkJoinFn kernel_block_combine_256();

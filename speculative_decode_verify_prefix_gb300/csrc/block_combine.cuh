@@ -118,17 +118,20 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
   }
 
   // ---- pieces: those of the stream's cut ----
-  const long long total = (scan[0] + scan[1] + scan[2] + scan[3]) * p.h_kv;
-  const long long off = (scan[4] + scan[5] + scan[6] + scan[7]) * p.h_kv + static_cast<long long>(h) * G;
+  const long long total = (scan[0] + scan[1] + scan[2] + scan[3]) * p.n_hg;
+  const long long off = (scan[4] + scan[5] + scan[6] + scan[7]) * p.n_hg + static_cast<long long>(h / p.team) * G;
   const long long W = share_of(p, total);
   const long long c0 = off / W;
   const int pieces = static_cast<int>((off + G - 1) / W - c0) + 1;
-  const float* lse = p.plse + (c0 + seg) * p.rows + row;
-  const float* po = p.po + ((c0 + seg) * p.rows + row) * D + E * lane;
+  // piece i: CTA (c0 + i) team + h % team of the stream
+  const long long slot = c0 * p.team + static_cast<long long>(b) * p.h_kv + h;
+  const long long step = static_cast<long long>(p.team) * p.rows;
+  const float* lse = p.plse + slot * p.rows + row;
+  const float* po = p.po + (slot * p.rows + row) * D + E * lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i0 = 0; i0 < pieces; i0 += 32) {
     const int n = min(32, pieces - i0);
-    const float x = lane < n ? lse[static_cast<long long>(i0 + lane) * p.rows] : NEG_INF;
+    const float x = lane < n ? lse[(i0 + lane) * step] : NEG_INF;
     float mx = x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -149,7 +152,7 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
       float2 v[U][E / 2];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float* src = po + static_cast<long long>(i0 + min(u0 + u, n - 1)) * p.rows * D;
+        const float* src = po + (i0 + min(u0 + u, n - 1)) * step * D;
 #pragma unroll
         for (int c = 0; c < E / 2; ++c) v[u][c] = *reinterpret_cast<const float2*>(src + 2 * c);
       }

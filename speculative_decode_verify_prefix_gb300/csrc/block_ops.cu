@@ -546,7 +546,9 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   p.h_kv = static_cast<int>(h_kv);
   p.rows = static_cast<int>(w.rows);
   p.w_min = 4;
-  p.n_cta = static_cast<int>(n_cta);
+  for (p.team = 8; p.h_kv % p.team != 0;) --p.team;
+  p.n_hg = p.h_kv / p.team;
+  p.n_team = static_cast<int>(n_cta) / p.team;
   if (cm) {
     p.cmask = static_cast<const unsigned char*>(cm->data);
     p.n_mask = cm->shape[0];
@@ -565,7 +567,7 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   if (!allow_smem(reinterpret_cast<const void*>(f.stream), f.smem)) return 0;
   void* args[] = {&p, &maps[0], &maps[1]};
   cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void*>(f.stream),
-                                   dim3(static_cast<unsigned>(n_cta), static_cast<unsigned>(w.rows / bk::row_tile(p.R))),
+                                   dim3(static_cast<unsigned>(p.n_team * p.team), static_cast<unsigned>(w.rows / bk::row_tile(p.R))),
                                    dim3(bk::kThreads), args, f.smem, st);
   if (e != cudaSuccess) return fail("kernel launch failed: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};

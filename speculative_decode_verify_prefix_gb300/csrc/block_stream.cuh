@@ -25,9 +25,12 @@
 //   warps 0-3  softmax: thread (w, r) holds keys 32 w .. 32 w + 31 of row r.
 //   warp 4     block table and scales, TMA of 16-key boxes into the ring.
 //   warp 5     tensor memory, MMAs.
-// The groups of 16 keys of all (sequence, KV head) segments are laid end to end
-// and every CTA takes an equal share; a segment's part of a share is a piece,
-// whose partial (o, log2 of its sum) block_combine_kernel folds.
+// Up to eight KV heads are taken by a team of as many CTAs, each its own over the
+// same keys: what lies side by side in memory is read at about the same time (8
+// heads of 128: XXX).  The groups of 16 keys of all (sequence, head group) segments
+// are laid end to end and every team takes an equal share; a segment's part of a
+// share is a piece, whose partial (o, log2 of its sum) block_combine_kernel folds:
+// of CTA c and segment s, slot c + team * s.
 // Every wait is bounded (one second); in a CTA that gives up every role ends its
 // loop without copying, multiplying or arriving anywhere (the copies' barriers then
 // still tell when those under way are done), sets error bit 8, waits for copies and
@@ -73,7 +76,7 @@ struct BkParams {
   int B, L, gq, R, h_kv, rows;  // rows: of a partial (RT row tiles of 32)
   float scale2;         // softmax scale in base 2
   int w_min;            // groups of a share at least
-  int n_cta;
+  int team, n_hg, n_team;  // CTAs of a team, h_kv / team, teams
   const unsigned char* cmask;
   const void* mindptr;
   int mindptr64;
@@ -140,13 +143,13 @@ __device__ __forceinline__ bool prefix_len(const BkParams& p, int b, int& P) {
 }
 __device__ __forceinline__ int seg_groups(int P) { return P > 0 ? static_cast<int>((static_cast<long long>(P) + GK - 1) / GK) : 1; }
 __device__ __forceinline__ long long share_of(const BkParams& p, long long total) {
-  long long W = (total + p.n_cta - 1) / p.n_cta;
+  long long W = (total + p.n_team - 1) / p.n_team;
   if (W < p.w_min) W = p.w_min;
   return W > GT ? (W + GT - 1) / GT * GT : W;
 }
 struct BSeg {
-  int b, h, P, G;
-  long long off;  // its first group among all
+  int b, h, P, G;  // h: this CTA's head of the head group
+  long long off;   // its first group among all
 };
 __device__ __forceinline__ void seg_load(const BkParams& p, BSeg& s) {
   prefix_len(p, s.b, s.P);
@@ -154,8 +157,9 @@ __device__ __forceinline__ void seg_load(const BkParams& p, BSeg& s) {
 }
 __device__ __forceinline__ void seg_next(const BkParams& p, BSeg& s) {
   s.off += s.G;
-  if (++s.h == p.h_kv) {
-    s.h = 0;
+  s.h += p.team;
+  if (s.h >= p.h_kv) {
+    s.h %= p.team;
     if (++s.b < p.B) seg_load(p, s);
   }
 }
@@ -198,17 +202,18 @@ __device__ __forceinline__ bool my_share(const BkParams& p, unsigned char* smem,
     if (w < warp) at += scan[w];
     all += scan[w];
   }
-  const long long total = all * p.h_kv, W = share_of(p, total);
-  start = blockIdx.x * W;
+  const long long total = all * p.n_hg, W = share_of(p, total);
+  const int member = static_cast<int>(blockIdx.x) % p.team;
+  start = static_cast<long long>(blockIdx.x) / p.team * W;
   if (start >= total) return false;  // uniform
   end = min(total, start + W);
   for (int b = lo; b < hi; ++b) {
     int P;
     prefix_len(p, b, P);
     const int G = seg_groups(P);
-    if (start >= at * p.h_kv && start < (at + G) * p.h_kv) {
+    if (start >= at * p.n_hg && start < (at + G) * p.n_hg) {
       *found = b;
-      *base = at * p.h_kv;
+      *base = at * p.n_hg;
     }
     at += G;
   }
@@ -216,8 +221,9 @@ __device__ __forceinline__ bool my_share(const BkParams& p, unsigned char* smem,
   s.b = *found;
   if (s.b < 0) return false;  // not reached: guards the walk
   seg_load(p, s);
-  s.h = static_cast<int>((start - *base) / s.G);
-  s.off = *base + static_cast<long long>(s.h) * s.G;
+  const long long hg = (start - *base) / s.G;
+  s.h = static_cast<int>(hg) * p.team + member;
+  s.off = *base + hg * s.G;
   return true;
 }
 
@@ -350,9 +356,6 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
   constexpr int NS = G::NS, CB = G::CB, ENT = G::ENT, NP = G::NP;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // block_combine_kernel's CTAs may start (they wait for this grid themselves)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
   long long start, end;
   BSeg seg0;
   if (!my_share(p, smem, start, end, seg0)) return;  // uniform
@@ -504,6 +507,8 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
         __nanosleep(20);
       }
     }
+    // block_combine_kernel's CTAs may start (they wait for this grid themselves)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the copies end before the CTA does (in a CTA that gave up, nobody else waits for them)
     for (uint32_t k = 1; k <= NS; ++k) {
       if (k <= nk) fa::wait_last(bar(kBKFull + (nk - k) % NS), ((nk - k) / NS) & 1u);
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
     for (; s.b < p.B && s.off < end; seg_next(p, s)) {
       int g0, ge;
       piece_of(s, start, end, g0, ge);
-      const long long slot = blockIdx.x + static_cast<long long>(s.b) * p.h_kv + s.h;
+      const long long slot = blockIdx.x + static_cast<long long>(s.b) * p.h_kv + s.h / p.team * p.team;
       const int row0 = static_cast<int>(blockIdx.y) * NR;
       float* lse_p = p.plse + slot * p.rows + row0;
       float* o_p = p.po + (slot * p.rows + row0) * D;

@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
   for (int i = tid; i < p.B; i += 128) {
     int P;
     prefix_len(p, i, P);
-    const int n = seg_groups(P);
+    const int n = seg_tiles(P);
     all += n;
     if (i < b) before += n;
   }
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
   const int i = row / p.gq, head = h * p.gq + row % p.gq;
   int P;
   prefix_len(p, b, P);
-  const int G = seg_groups(P);
+  const int T = seg_tiles(P);
   // draft visibility: causal, or the tree mask's row
   const unsigned char* seen = nullptr;
   if (p.cmask) {
@@ -119,10 +119,10 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
 
   // ---- pieces: those of the stream's cut ----
   const long long total = (scan[0] + scan[1] + scan[2] + scan[3]) * p.n_hg;
-  const long long off = (scan[4] + scan[5] + scan[6] + scan[7]) * p.n_hg + static_cast<long long>(h / p.team) * G;
+  const long long off = (scan[4] + scan[5] + scan[6] + scan[7]) * p.n_hg + static_cast<long long>(h / p.team) * T;
   const long long W = share_of(p, total);
   const long long c0 = off / W;
-  const int pieces = static_cast<int>((off + G - 1) / W - c0) + 1;
+  const int pieces = static_cast<int>((off + T - 1) / W - c0) + 1;
   // piece i: CTA (c0 + i) team + h % team of the stream
   const long long slot = c0 * p.team + static_cast<long long>(b) * p.h_kv + h;
   const long long step = static_cast<long long>(p.team) * p.rows;

@@ -241,9 +241,9 @@ static bool check_block_cache(const vsk_tensor* kc, const vsk_tensor* vc, const 
   return true;
 }
 
-// Tensor map of e4m3 rows [rows][heads][D] for boxes of 16 rows of one head and
+// Tensor map of e4m3 rows [n][heads][D] for boxes of `rows` rows of one head and
 // `cols` columns, swizzled over their width.
-static bool block_map(const vsk_tensor* t, int cols, CUtensorMap* map) {
+static bool block_map(const vsk_tensor* t, int cols, int rows, CUtensorMap* map) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
   if (!encode) return fail("cuTensorMapEncodeTiled is not available");
   const long long n = t->shape[0], h = t->shape[1], d = t->shape[2];
@@ -251,7 +251,7 @@ static bool block_map(const vsk_tensor* t, int cols, CUtensorMap* map) {
   if (s1 < d || s0 < d || s0 >= (1LL << 38) || s1 >= (1LL << 38)) return fail("the cache's strides fit no tensor map");
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(h), static_cast<cuuint64_t>(n)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1), static_cast<cuuint64_t>(s0)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(cols), 1, bk::GK}, unit[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(cols), 1, static_cast<cuuint32_t>(rows)}, unit[3] = {1, 1, 1};
   if (encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(t->data), dims, strides, box, unit,
              CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -539,13 +539,14 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   p.n_rows = N;
   p.block = static_cast<int>(block_size);
   p.bgroups = p.block / bk::GK;
+  p.box = std::min(bk::GT, p.bgroups & -p.bgroups);
   p.B = static_cast<int>(B);
   p.L = static_cast<int>(L);
   p.gq = static_cast<int>(h_q / h_kv);
   p.R = static_cast<int>(R);
   p.h_kv = static_cast<int>(h_kv);
   p.rows = static_cast<int>(w.rows);
-  p.w_min = 4;
+  p.w_min = 1;
   for (p.team = 8; p.h_kv % p.team != 0;) --p.team;
   p.n_hg = p.h_kv / p.team;
   p.n_team = static_cast<int>(n_cta) / p.team;
@@ -562,7 +563,8 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   CUtensorMap maps[2];
   memset(maps, 0, sizeof maps);
   if (kc->shape[0] > 0) {
-    if (!block_map(kc, D < 128 ? 64 : 128, &maps[0]) || !block_map(vc, D < 128 ? 64 : 128, &maps[1])) return 0;
+    const int cols = D < 128 ? 64 : 128, rows = p.box * bk::GK;
+    if (!block_map(kc, cols, rows, &maps[0]) || !block_map(vc, cols, rows, &maps[1])) return 0;
   }
   if (!allow_smem(reinterpret_cast<const void*>(f.stream), f.smem)) return 0;
   void* args[] = {&p, &maps[0], &maps[1]};

@@ -73,9 +73,10 @@ struct BkParams {
   long long ks_s0, vs_s0;
   long long n_blocks, n_rows;
   int block, bgroups;   // keys, groups of a block
+  int box;              // groups of a TMA box: a power of two that divides bgroups, GT at most
   int B, L, gq, R, h_kv, rows;  // rows: of a partial (RT row tiles of 32)
   float scale2;         // softmax scale in base 2
-  int w_min;            // groups of a share at least
+  int w_min;            // tiles of a share at least
   int team, n_hg, n_team;  // CTAs of a team, h_kv / team, teams
   const unsigned char* cmask;
   const void* mindptr;
@@ -141,35 +142,34 @@ __device__ __forceinline__ bool prefix_len(const BkParams& p, int b, int& P) {
   P = ok ? n : 0;
   return ok;
 }
-__device__ __forceinline__ int seg_groups(int P) { return P > 0 ? static_cast<int>((static_cast<long long>(P) + GK - 1) / GK) : 1; }
+__device__ __forceinline__ int seg_tiles(int P) { return P > 0 ? (P - 1) / KT + 1 : 1; }
 __device__ __forceinline__ long long share_of(const BkParams& p, long long total) {
-  long long W = (total + p.n_team - 1) / p.n_team;
-  if (W < p.w_min) W = p.w_min;
-  return W > GT ? (W + GT - 1) / GT * GT : W;
+  return max((total + p.n_team - 1) / p.n_team, static_cast<long long>(p.w_min));
 }
 struct BSeg {
-  int b, h, P, G;  // h: this CTA's head of the head group
-  long long off;   // its first group among all
+  int b, h, P, T;  // h: this CTA's head of the head group; T: tiles
+  long long off;   // its first tile among all
 };
 __device__ __forceinline__ void seg_load(const BkParams& p, BSeg& s) {
   prefix_len(p, s.b, s.P);
-  s.G = seg_groups(s.P);
+  s.T = seg_tiles(s.P);
 }
 __device__ __forceinline__ void seg_next(const BkParams& p, BSeg& s) {
-  s.off += s.G;
+  s.off += s.T;
   s.h += p.team;
   if (s.h >= p.h_kv) {
     s.h %= p.team;
     if (++s.b < p.B) seg_load(p, s);
   }
 }
-// The real groups [g0, ge) of a segment in a share; empty where there are none.
+// The groups [g0, ge) of a segment's share, from a whole tile on; empty where the
+// prefix is.
 __device__ __forceinline__ void piece_of(const BSeg& s, long long start, long long end, int& g0, int& ge) {
-  g0 = static_cast<int>(max(start, s.off) - s.off);
-  ge = s.P > 0 ? static_cast<int>(min(static_cast<long long>(s.G), end - s.off)) : 0;
+  g0 = static_cast<int>(max(start, s.off) - s.off) * GT;
+  ge = static_cast<int>(min((static_cast<long long>(s.P) + GK - 1) / GK, (end - s.off) * GT));
 }
 
-// The CTA's share [start, end) of the groups and the segment it begins in; all
+// The CTA's share [start, end) of the tiles and the segment it begins in; all
 // threads call it.  False: nothing to do.
 __device__ __forceinline__ bool my_share(const BkParams& p, unsigned char* smem, long long& start, long long& end, BSeg& s) {
   long long* scan = reinterpret_cast<long long*>(smem + kScanOff);
@@ -185,7 +185,7 @@ __device__ __forceinline__ bool my_share(const BkParams& p, unsigned char* smem,
   for (int b = lo; b < hi; ++b) {
     int P;
     bad |= !prefix_len(p, b, P);
-    mine += seg_groups(P);
+    mine += seg_tiles(P);
   }
   if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrBadKvIndptr);
   long long incl = mine;
@@ -210,20 +210,20 @@ __device__ __forceinline__ bool my_share(const BkParams& p, unsigned char* smem,
   for (int b = lo; b < hi; ++b) {
     int P;
     prefix_len(p, b, P);
-    const int G = seg_groups(P);
-    if (start >= at * p.n_hg && start < (at + G) * p.n_hg) {
+    const int T = seg_tiles(P);
+    if (start >= at * p.n_hg && start < (at + T) * p.n_hg) {
       *found = b;
       *base = at * p.n_hg;
     }
-    at += G;
+    at += T;
   }
   __syncthreads();
   s.b = *found;
   if (s.b < 0) return false;  // not reached: guards the walk
   seg_load(p, s);
-  const long long hg = (start - *base) / s.G;
+  const long long hg = (start - *base) / s.T;
   s.h = static_cast<int>(hg) * p.team + member;
-  s.off = *base + hg * s.G;
+  s.off = *base + hg * s.T;
   return true;
 }
 
@@ -426,8 +426,20 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
     // K and V go on by themselves: a K slot is free once its scores are done, a V
     // slot only when its weights have met it.  (One after the other, K waited for
     // the V of a tile before: XXX.)
-    volatile int* rows = reinterpret_cast<volatile int*>(smem + kRowOff);
-    volatile int* heads = rows + kMeta * GT;
+    int* rows = reinterpret_cast<int*>(smem + kRowOff);
+    // A tile's boxes by one lane (lanes that each copy a box are taken one after the
+    // other, some 130 cycles each), after announcing their bytes.
+    auto load_boxes = [&](const int (&at)[GT], const CUtensorMap* map, uint32_t full, uint32_t dst, int head) {
+      uint32_t n = 0;
+#pragma unroll
+      for (int i = 0; i < GT; ++i) n += (i & (p.box - 1)) == 0 && at[i] >= 0;
+      expect(full, n * p.box * (GK * D));
+#pragma unroll
+      for (int i = 0; i < GT; ++i)
+        if ((i & (p.box - 1)) == 0 && at[i] >= 0)
+#pragma unroll
+          for (int c = 0; c < G::NB; ++c) fa::tma_load_box(dst + c * (KT * CB) + i * (GK * CB), map, full, c * CB, head, at[i]);
+    };
     uint32_t nk = 0, nv = 0;  // K and V tiles whose copies were issued
     int j = 0, looks = 0;     // tile of the batch
     unsigned long long since = 0;
@@ -441,25 +453,23 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
       if (cur.valid && nk - nv < kMeta && __all_sync(0xffffffffu, tr::test(bar(kBKEmpty + nk % NS), ((nk / NS) & 1u) ^ 1u))) {
         const uint32_t st = nk % NS;
         const bool mine = (lane >> 3) == j;
-        const unsigned there = __ballot_sync(0xffffffffu, mine && keys > 0);
         const bool lacks = __any_sync(0xffffffffu, mine && keys < GK);
-        if (lane == 0) expect(bar(kBKFull + st), __popc(there) * (GK * D));
-        __syncwarp();
-        if (mine) {
-          const uint32_t kd = ring_s + st * (2 * ENT) + (lane & 7) * (GK * CB);
-          if (keys > 0) {
+        int at[GT];  // first rows in the cache
 #pragma unroll
-            for (int c = 0; c < G::NB; ++c)
-              fa::tma_load_box(kd + c * (KT * CB), &kmap, bar(kBKFull + st), c * CB, cur.s.h, row);
-          }
+        for (int i = 0; i < GT; ++i) at[i] = __shfl_sync(0xffffffffu, keys > 0 ? row : -1, GT * j + i);
+        if (fa::elect_one()) {
+          load_boxes(at, &kmap, bar(kBKFull + st), ring_s + st * (2 * ENT), cur.s.h);
+          *reinterpret_cast<int4*>(rows + (nk % kMeta) * GT) = make_int4(at[0], at[1], at[2], at[3]);
+          *reinterpret_cast<int4*>(rows + (nk % kMeta) * GT + 4) = make_int4(at[4], at[5], at[6], at[7]);
+          rows[kMeta * GT + nk % kMeta] = cur.s.h;
+        }
+        if (mine) {
           // a scale that is no positive finite number in the range gives NaN
           const bool good = ks >= kMinScale && ks <= kMaxScale && vs >= kMinScale && vs <= kMaxScale;
           if (!good) atomicOr(p.err, kErrBadScale);
           const float nan = __int_as_float(0x7FC00000);
           meta[(nk % kMeta) * GT + (lane & 7)] =
               make_float4(good ? ks : nan, good ? log2f(vs) : nan, good ? 1.f / vs : nan, __int_as_float(keys + (lacks ? 256 : 0)));
-          rows[(nk % kMeta) * GT + (lane & 7)] = keys > 0 ? row : -1;
-          if ((lane & 7) == 0) heads[nk % kMeta] = cur.s.h;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBKFull + st));
@@ -480,17 +490,12 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
       }
       if (nv < nk && __all_sync(0xffffffffu, tr::test(bar(kBVEmpty + nv % NS), ((nv / NS) & 1u) ^ 1u))) {
         const uint32_t st = nv % NS;
-        const int vhead = heads[nv % kMeta];
-        const int vrow = lane < GT ? rows[(nv % kMeta) * GT + lane] : -1;
-        const unsigned there = __ballot_sync(0xffffffffu, vrow >= 0);
-        if (lane == 0) expect(bar(kBVFull + st), __popc(there) * (GK * D));
-        __syncwarp();
-        if (vrow >= 0) {
-          const uint32_t vd = ring_s + st * (2 * ENT) + ENT + lane * (GK * CB);
-#pragma unroll
-          for (int c = 0; c < G::NB; ++c)
-            fa::tma_load_box(vd + c * (KT * CB), &vmap, bar(kBVFull + st), c * CB, vhead, vrow);
+        if (fa::elect_one()) {
+          const int4 r0 = *reinterpret_cast<const int4*>(rows + (nv % kMeta) * GT), r1 = *reinterpret_cast<const int4*>(rows + (nv % kMeta) * GT + 4);
+          const int at[GT] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+          load_boxes(at, &vmap, bar(kBVFull + st), ring_s + st * (2 * ENT) + ENT, rows[kMeta * GT + nv % kMeta]);
         }
+        __syncwarp();
         ++nv;
         moved = true;
       }

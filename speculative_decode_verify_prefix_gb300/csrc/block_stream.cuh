@@ -12,18 +12,18 @@
 // nothing is widened.  What is not e4m3 is written as a sum of e4m3 terms:
 //   queries  q 2^sh = hi + lo exactly (bf16 has 8 significant bits, a term 4;
 //            elements 2^17 below the row's largest lose bits that no score
-//            shows), both terms along K of one accumulator;
+//            shows), along K of one accumulator, or 16 lanes apart;
 //   weights  y = 2^6 x: the top 4 bits, the next 4 and the rest rounded to 4, as
 //            three groups of rows of one M = 128 product under scales 1, 2^4,
 //            2^8: 12 bits, and 2^-24 of the reference at the lower end.
 // A tile is 128 keys of one KV head:
-//   S[128][128 keys] = Q[128][hi | lo] x K^T   (up to 32 packed rows, four times:
-//                      every warp then finds all rows in its own lanes)
+//   S[128][128 keys] = Q[128] x K^T   (all packed rows several times over: every
+//                      warp finds them in its own lanes)
 //   O[128][D]       += P[128][128 keys] x V    (rows 32 p + r: term p of row r)
 //
-// Roles (6 warps; two CTAs an SM at head_dim 64 and 128, one at 256):
+// Roles (7 warps; two CTAs an SM at head_dim 64 and 128, one at 256):
 //   warps 0-3  softmax: thread (w, r) holds keys 32 w .. 32 w + 31 of row r.
-//   warp 4     block table and scales, TMA of 16-key boxes into the ring.
+//   warps 4, 6 block table, TMA of boxes of up to 128 keys into the K and V rings, scales.
 //   warp 5     tensor memory, MMAs.
 // Up to eight KV heads are taken by a team of as many CTAs, each its own over the
 // same keys: what lies side by side in memory is read at about the same time (8
@@ -51,7 +51,7 @@ namespace bk {
 constexpr int KT = 128;      // keys of a tile
 constexpr int GK = 16;       // keys of a group (one TMA box, one block's scale)
 constexpr int GT = KT / GK;  // groups of a tile
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kSm = 128;     // softmax threads
 constexpr int kMeta = 8;     // tiles whose scales are kept (more than the ring holds)
 constexpr float kThr = 2.f;  // log2 headroom before a reference is raised
@@ -101,36 +101,43 @@ struct Geo {
   static constexpr int CB = D < 128 ? 64 : 128;     // bytes of a shared-memory row
   static constexpr int NB = D / CB;                 // column blocks of a K / V tile
   static constexpr int ENT = KT * D;                // K (or V) rows of a tile
-  static constexpr int QB = 128 * 2 * D;            // Q: [hi | lo] in 128-byte column blocks
+  // Q: 128 rows.  16 rows fit a warp's lanes with both their terms (hi in the lower
+  // half, lo in the upper); 32 have them one behind the other along K.
+  static constexpr bool both = NR == 32;
+  static constexpr int QW = both ? 2 * D : D;       // bytes of a row
+  static constexpr int QCB = QW < 128 ? 64 : 128;   // bytes of its column blocks
+  static constexpr int QB = 128 * QW;
   static constexpr int PB = 3 * NR * 128;           // P; the MMA reads 128 rows, of the others nobody takes the result
   static constexpr int NP = D == 128 && NR == 32 ? 1 : 2;  // its buffers
   static constexpr int per_sm = D == 256 ? 1 : 2;
   static constexpr int ctl = 3072;                  // barriers, scales, exchanges
   static constexpr int room = (per_sm == 1 ? kSmemPerCTAMax : kSmemPerSM / 2 - kReservedPerCTA) - ctl - QB - NP * PB;
-  static constexpr int NS = room / (2 * ENT) < 5 ? room / (2 * ENT) : 5;  // stages
+  static constexpr int entries = room / ENT < 10 ? room / ENT : 10;
+  static constexpr int NK = entries / 2, NV = entries - NK;  // ring entries of K and of V (which stay longer)
   static constexpr int q_off = ctl;
   static constexpr int p_off = q_off + QB;
   static constexpr int ring_off = p_off + NP * PB;
-  static constexpr int smem = ring_off + 2 * NS * ENT;
+  static constexpr int v_off = ring_off + NK * ENT;
+  static constexpr int smem = v_off + NV * ENT;
   static constexpr int cols = D == 256 ? 512 : 256;  // S 128, O D
-  static_assert(NS >= 1 && NS + 2 < kMeta, "ring");
-  static_assert(2 * NS * ENT >= 128 * 128, "the rows behind P are read from the ring");
+  static_assert(NK >= 2 && NV <= 5 && NK + 2 < kMeta, "ring");
+  static_assert((NK + NV) * ENT >= 128 * 128, "the rows behind P are read from the ring");
   static_assert(q_off % 1024 == 0 && p_off % 1024 == 0 && PB % 1024 == 0 && ring_off % 1024 == 0, "swizzled layouts");
 };
 
 // control block
-constexpr int kScanOff = 0;    // 6 warps' sums, then the CTA's first segment
+constexpr int kScanOff = 0;     // the warps' sums, then the CTA's first segment
 constexpr int kBarOff = 128;
 constexpr int kBKFull = 0, kBKEmpty = 5, kBVFull = 10, kBVEmpty = 15, kBSFull = 20, kBSEmpty = 21, kBPFull = 22,
-              kBPEmpty = 24, kBQFull = 26, kBDone = 27, kNumBars = 28;
+              kBPEmpty = 24, kBQFull = 26, kBDone = 27, kBMeta = 28, kNumBars = kBMeta + kMeta;
 constexpr int kTmemOff = kBarOff + 8 * kNumBars;
 constexpr int kAbortOff = kTmemOff + 4;
-constexpr int kQscOff = 384;   // [32] float: a row's score scale
-constexpr int kMetaOff = 512;  // [kMeta][GT] float4: ks, log2 vs, 1 / vs, keys that are there (+ 256: the tile lacks some)
-constexpr int kRedOff = 1536;  // [4][NR] float: maxima of a tile
-constexpr int kRowOff = 2048;  // [kMeta][GT] int: the groups' first rows in the cache; [kMeta] int: the KV head
-constexpr int kSumOff = 2560;  // [4][NR] float: sums of a piece
-static_assert(kAbortOff + 4 <= kQscOff && kMetaOff + kMeta * GT * 16 <= kRedOff && kRedOff + 512 <= kRowOff && kRowOff + kMeta * (GT + 1) * 4 <= kSumOff, "control block");
+constexpr int kQscOff = 448;    // [32] float: a row's score scale
+constexpr int kRedOff = 576;    // [4][NR] float: maxima of a tile
+constexpr int kSumOff = 1088;   // [4][NR] float: sums of a piece
+constexpr int kMetaOff = 1600;  // [kMeta][GT] float4: ks, log2 vs, 1 / vs, keys that are there (+ 256: the tile lacks some)
+static_assert(kAbortOff + 4 <= kQscOff && kRedOff + 512 <= kSumOff && kSumOff + 512 <= kMetaOff && kMetaOff + kMeta * GT * 16 <= 3072,
+              "control block");
 
 // Segments and their cut, the same in both kernels.
 struct Cut {
@@ -261,6 +268,12 @@ __device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo, uint32_t 
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16) |
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32) | (1ull << 46) | (static_cast<uint64_t>(CB == 128 ? 2 : 4) << 61);
 }
+// fa::wait_all for two phases at once (a look takes some 150 cycles).
+__device__ __forceinline__ bool wait_both(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, volatile int* abort_flag, unsigned* err) {
+  const bool x = tr::test(a, pa), y = tr::test(b, pb);
+  if (__all_sync(0xffffffffu, x && y)) return true;
+  return fa::wait_all(a, pa, abort_flag, err) && fa::wait_all(b, pb, abort_flag, err);
+}
 __device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -275,6 +288,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // score scales; by the softmax warps, NR / 4 rows each.
 template <int D, int NR>
 __device__ __forceinline__ void load_rows(const BkParams& p, const BSeg& s, unsigned char* smem, int warp, int lane) {
+  using G = Geo<D, NR>;
   constexpr int W = D / 64;  // 32-bit words of a row per lane
   constexpr int J = NR / 4;
   const int a = __ldg(p.qo + s.b), e = __ldg(p.qo + s.b + 1);
@@ -327,17 +341,21 @@ __device__ __forceinline__ void load_rows(const BkParams& p, const BSeg& s, unsi
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const uint32_t* x = t ? lo : hi;
-      const int at = t * D + 2 * W * lane;  // byte of the row [hi | lo]
-      unsigned char* d = smem + Geo<D, NR>::q_off + (at >> 7) * (128 * 128) + row * 128 + ((((at & 127) >> 4) ^ (row & 7)) << 4) + (at & 15);
+      // NR 32: byte t D + .. of row `row`, four times; else row `row` of each 16 (or
+      // twice 8) rows, hi and lo in turn
+      const int at = (G::both ? t * D : 0) + 2 * W * lane;
 #pragma unroll
-      for (int k = 0; k < 128 / NR; ++k) {
-        unsigned char* dk = d + k * (NR * 128);
+      for (int k = 0; k < (G::both ? 4 : 64 / NR); ++k) {
+        const int qr = G::both ? 32 * k + row : 32 * (k * NR / 16) + 16 * t + k * NR % 16 + row;
+        constexpr int CB = G::QCB;
+        const int swz = CB == 128 ? qr & 7 : (qr >> 1) & 3;
+        unsigned char* d = smem + G::q_off + at / CB * (128 * CB) + qr * CB + (((at % CB >> 4) ^ swz) << 4) + (at & 15);
         if constexpr (W == 1)
-          *reinterpret_cast<unsigned short*>(dk) = static_cast<unsigned short>(x[0]);
+          *reinterpret_cast<unsigned short*>(d) = static_cast<unsigned short>(x[0]);
         else if constexpr (W == 2)
-          *reinterpret_cast<uint32_t*>(dk) = x[0];
+          *reinterpret_cast<uint32_t*>(d) = x[0];
         else
-          *reinterpret_cast<uint2*>(dk) = make_uint2(x[0], x[1]);
+          *reinterpret_cast<uint2*>(d) = make_uint2(x[0], x[1]);
       }
     }
   }
@@ -353,7 +371,7 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
   using tc::idesc, tc::mbar_arrive, tc::mbar_init, tc::mma_commit, tc::mma_f8_ss, tc::fence_proxy_async;
   using tc::tc_fence_after, tc::tc_fence_before, tc::tmem_ld, tc::tmem_st, tc::tmem_wait_st;
   using G = bk::Geo<D, NR>;
-  constexpr int NS = G::NS, CB = G::CB, ENT = G::ENT, NP = G::NP;
+  constexpr int NK = G::NK, NV = G::NV, CB = G::CB, ENT = G::ENT, NP = G::NP;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   long long start, end;
@@ -366,12 +384,14 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
   auto bar = [&](int i) -> uint32_t { return smem_u32(bars + i); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kAbortOff);
-  const uint32_t ring_s = smem_u32(smem + G::ring_off);
+  const uint32_t k_s = smem_u32(smem + G::ring_off), v_s = smem_u32(smem + G::v_off);
   if (tid == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(bar(kBKFull + i), 2);  // the copies' bytes; the tile's scales
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(bar(kBKFull + i), 1);
       mbar_init(bar(kBKEmpty + i), 1);
+    }
+    for (int i = 0; i < NV; ++i) {
       mbar_init(bar(kBVFull + i), 1);
       mbar_init(bar(kBVEmpty + i), 1);
     }
@@ -381,6 +401,7 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
       mbar_init(bar(kBPFull + i), 4);
       mbar_init(bar(kBPEmpty + i), 1);
     }
+    for (int i = 0; i < kMeta; ++i) mbar_init(bar(kBMeta + i), 1);
     mbar_init(bar(kBQFull), 4);
     mbar_init(bar(kBDone), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -397,143 +418,118 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTmemOff);
   const uint32_t tS = tmem, tO = tmem + KT;
 
-  if (warp == 4) {
-    // ================================ loader ================================
+  if (warp == 4 || warp == 6) {
+    // ================================ loaders ================================
+    // Warp 4 brings K, warp 6 V and the scales.  Each goes on by itself: a K entry is
+    // free once its scores are done, a V entry only when its weights have met it; and a
+    // tile costs a warp some hundred cycles (one for both, 64 of 8k..16k keys at
+    // head_dim 64: 229 us, so XXX).
+    const bool isv = warp == 6;
+    const CUtensorMap* map = isv ? &vmap : &kmap;
+    const uint32_t n_ent = isv ? NV : NK, ring = isv ? v_s : k_s;
+    const int full0 = isv ? kBVFull : kBKFull, empty0 = isv ? kBVEmpty : kBKEmpty;
     float4* meta = reinterpret_cast<float4*>(smem + kMetaOff);
     BatchIt cur, ahead;
-    // group `lane` of a batch: its first row in the cache, its keys, its scales
-    auto fetch = [&](const BatchIt& it, int& row, int& keys, float& ks, float& vs) {
-      row = 0;
-      keys = 0;
-      ks = vs = 1.f;
+    // group `lane` of a batch: its block, and (a batch later) its scales
+    auto page_of_group = [&](const BatchIt& it) -> int {
       const int gi = it.g + lane;
-      if (!it.valid || gi >= it.ge) return;
-      const int col = gi / p.bgroups;
-      const long long page = __ldg(p.bt + static_cast<long long>(it.s.b) * p.bt_s0 + col);
-      if (page < 0 || page >= p.n_blocks) {
-        atomicOr(p.err, kErrBadIndex);
-        return;
+      return it.valid && gi < it.ge ? __ldg(p.bt + static_cast<long long>(it.s.b) * p.bt_s0 + gi / p.bgroups) : -1;
+    };
+    int page, page2;
+    float ks = 1.f, vs = 1.f, ks2 = 1.f, vs2 = 1.f;
+    auto scales = [&](int pg, int h, float& k, float& v) {
+      k = v = 1.f;
+      if (isv && pg >= 0 && pg < p.n_blocks) {
+        k = __ldg(p.ks + pg * p.ks_s0 + h);
+        v = __ldg(p.vs + pg * p.vs_s0 + h);
       }
-      row = static_cast<int>(page * p.block) + (gi - col * p.bgroups) * GK;
-      keys = min(GK, it.s.P - gi * GK);
-      ks = __ldg(p.ks + page * p.ks_s0 + it.s.h);
-      vs = __ldg(p.vs + page * p.vs_s0 + it.s.h);
     };
-    int row, keys, row2, keys2;
-    float ks, vs, ks2, vs2;
     cur.first(p, seg0, start, end);
-    fetch(cur, row, keys, ks, vs);
-    // K and V go on by themselves: a K slot is free once its scores are done, a V
-    // slot only when its weights have met it.  (One after the other, K waited for
-    // the V of a tile before: XXX.)
-    int* rows = reinterpret_cast<int*>(smem + kRowOff);
-    // A tile's boxes by one lane (lanes that each copy a box are taken one after the
-    // other, some 130 cycles each), after announcing their bytes.
-    auto load_boxes = [&](const int (&at)[GT], const CUtensorMap* map, uint32_t full, uint32_t dst, int head) {
-      uint32_t n = 0;
-#pragma unroll
-      for (int i = 0; i < GT; ++i) n += (i & (p.box - 1)) == 0 && at[i] >= 0;
-      expect(full, n * p.box * (GK * D));
-#pragma unroll
-      for (int i = 0; i < GT; ++i)
-        if ((i & (p.box - 1)) == 0 && at[i] >= 0)
-#pragma unroll
-          for (int c = 0; c < G::NB; ++c) fa::tma_load_box(dst + c * (KT * CB) + i * (GK * CB), map, full, c * CB, head, at[i]);
-    };
-    uint32_t nk = 0, nv = 0;  // K and V tiles whose copies were issued
-    int j = 0, looks = 0;     // tile of the batch
-    unsigned long long since = 0;
-    ahead = cur;
-    if (cur.valid) ahead.next(p, start, end);
-    fetch(ahead, row2, keys2, ks2, vs2);
+    page = page_of_group(cur);
+    scales(page, cur.s.h, ks, vs);
+    uint32_t u = 0, issued = 0;
+    uint32_t st = 0, par = 1;
+    bool alive = true;
 #pragma unroll 1
-    while (cur.valid || nv < nk) {
-      bool moved = false;
-      // a tile's rows are kept until its V is on its way
-      if (cur.valid && nk - nv < kMeta && __all_sync(0xffffffffu, tr::test(bar(kBKEmpty + nk % NS), ((nk / NS) & 1u) ^ 1u))) {
-        const uint32_t st = nk % NS;
-        const bool mine = (lane >> 3) == j;
-        const bool lacks = __any_sync(0xffffffffu, mine && keys < GK);
+    while (cur.valid && alive) {
+      // (the next batch's blocks now, their scales once this batch is on its way)
+      ahead = cur;
+      ahead.next(p, start, end);
+      page2 = page_of_group(ahead);
+      const int gi = cur.g + lane;
+      const bool in = gi < cur.ge, ok = in && page >= 0 && page < p.n_blocks;
+      if (in && !ok && isv) atomicOr(p.err, kErrBadIndex);
+      const int keys = ok ? min(GK, cur.s.P - gi * GK) : 0;
+      const int row = ok ? page * p.block + gi % p.bgroups * GK : -1;
+      // a scale that is no positive finite number in the range gives NaN
+      const bool good = ks >= kMinScale && ks <= kMaxScale && vs >= kMinScale && vs <= kMaxScale;
+      if (!good) atomicOr(p.err, kErrBadScale);
+      const float nan = __int_as_float(0x7FC00000);
+      const float4 mine = make_float4(good ? ks : nan, good ? log2f(vs) : nan, good ? 1.f / vs : nan, __int_as_float(keys));
+      const int tiles = (min(32, cur.ge - cur.g) + GT - 1) / GT;
+#pragma unroll 1
+      for (int j = 0; j < tiles; ++j, ++u) {
+        if (isv) {
+          const bool lacks = __any_sync(0xffffffffu, (lane >> 3) == j && keys < GK);
+          if ((lane >> 3) == j) {
+            float4 x = mine;
+            if (lacks) x.w = __int_as_float(keys + 256);
+            meta[(u % kMeta) * GT + (lane & 7)] = x;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBMeta + u % kMeta));
+        }
+        alive = fa::wait_all(bar(empty0 + st), par, abort_flag, p.err);
+        if (!alive) break;
         int at[GT];  // first rows in the cache
 #pragma unroll
-        for (int i = 0; i < GT; ++i) at[i] = __shfl_sync(0xffffffffu, keys > 0 ? row : -1, GT * j + i);
+        for (int i = 0; i < GT; ++i) at[i] = __shfl_sync(0xffffffffu, row, GT * j + i);
+        // one lane copies all boxes (lanes that each copy one are taken one after the
+        // other, some 130 cycles each)
         if (fa::elect_one()) {
-          load_boxes(at, &kmap, bar(kBKFull + st), ring_s + st * (2 * ENT), cur.s.h);
-          *reinterpret_cast<int4*>(rows + (nk % kMeta) * GT) = make_int4(at[0], at[1], at[2], at[3]);
-          *reinterpret_cast<int4*>(rows + (nk % kMeta) * GT + 4) = make_int4(at[4], at[5], at[6], at[7]);
-          rows[kMeta * GT + nk % kMeta] = cur.s.h;
-        }
-        if (mine) {
-          // a scale that is no positive finite number in the range gives NaN
-          const bool good = ks >= kMinScale && ks <= kMaxScale && vs >= kMinScale && vs <= kMaxScale;
-          if (!good) atomicOr(p.err, kErrBadScale);
-          const float nan = __int_as_float(0x7FC00000);
-          meta[(nk % kMeta) * GT + (lane & 7)] =
-              make_float4(good ? ks : nan, good ? log2f(vs) : nan, good ? 1.f / vs : nan, __int_as_float(keys + (lacks ? 256 : 0)));
+          uint32_t n = 0;
+#pragma unroll
+          for (int i = 0; i < GT; ++i) n += (i & (p.box - 1)) == 0 && at[i] >= 0;
+          expect(bar(full0 + st), n * p.box * (GK * D));
+#pragma unroll
+          for (int i = 0; i < GT; ++i)
+            if ((i & (p.box - 1)) == 0 && at[i] >= 0)
+#pragma unroll
+              for (int c = 0; c < G::NB; ++c)
+                fa::tma_load_box(ring + st * ENT + c * (KT * CB) + i * (GK * CB), map, bar(full0 + st), c * CB, cur.s.h, at[i]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBKFull + st));
-        ++nk;
-        moved = true;
-        if (cur.g + GT * ++j >= min(cur.ge, cur.g + 32)) {
-          cur = ahead;
-          row = row2;
-          keys = keys2;
-          ks = ks2;
-          vs = vs2;
-          j = 0;
-          if (cur.valid) {
-            ahead.next(p, start, end);
-            fetch(ahead, row2, keys2, ks2, vs2);
-          }
+        issued = u + 1;
+        if (++st == n_ent) {
+          st = 0;
+          par ^= 1u;
         }
       }
-      if (nv < nk && __all_sync(0xffffffffu, tr::test(bar(kBVEmpty + nv % NS), ((nv / NS) & 1u) ^ 1u))) {
-        const uint32_t st = nv % NS;
-        if (fa::elect_one()) {
-          const int4 r0 = *reinterpret_cast<const int4*>(rows + (nv % kMeta) * GT), r1 = *reinterpret_cast<const int4*>(rows + (nv % kMeta) * GT + 4);
-          const int at[GT] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-          load_boxes(at, &vmap, bar(kBVFull + st), ring_s + st * (2 * ENT) + ENT, rows[kMeta * GT + nv % kMeta]);
-        }
-        __syncwarp();
-        ++nv;
-        moved = true;
-      }
-      if (moved) {
-        looks = 0;
-      } else {
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-        if (++looks == 4096) since = tc::global_ns();
-        if (looks > 4096 && (looks & 255) == 0 && __all_sync(0xffffffffu, tc::global_ns() - since > 1000000000ull)) {
-          *abort_flag = 1;
-          if (lane == 0) atomicOr(p.err, kErrTimeout);
-          break;
-        }
-        __nanosleep(20);
-      }
+      scales(page2, ahead.valid ? ahead.s.h : 0, ks2, vs2);
+      cur = ahead;
+      page = page2;
+      ks = ks2;
+      vs = vs2;
     }
     // block_combine_kernel's CTAs may start (they wait for this grid themselves)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the copies end before the CTA does (in a CTA that gave up, nobody else waits for them)
-    for (uint32_t k = 1; k <= NS; ++k) {
-      if (k <= nk) fa::wait_last(bar(kBKFull + (nk - k) % NS), ((nk - k) / NS) & 1u);
-      if (k <= nv) fa::wait_last(bar(kBVFull + (nv - k) % NS), ((nv - k) / NS) & 1u);
-    }
+    for (uint32_t k = 1; k <= n_ent && k <= issued; ++k)
+      fa::wait_last(bar(full0 + (issued - k) % n_ent), ((issued - k) / n_ent) & 1u);
   } else if (warp == 5) {
     // ================================ MMAs ================================
     constexpr uint32_t idS = idesc(0, 0, 0, 0, 128, KT), idO = idesc(0, 0, 0, 1, 128, D);
-    const uint64_t dq = desc<128>(smem_u32(smem + G::q_off), 16, 1024), dp = desc<128>(smem_u32(smem + G::p_off), 16, 1024);
-    const uint64_t dk = desc<CB>(ring_s, 16, 8 * CB), dv = desc<CB>(ring_s + ENT, KT * CB, 8 * CB);
+    const uint64_t dq = desc<G::QCB>(smem_u32(smem + G::q_off), 16, 8 * G::QCB), dp = desc<128>(smem_u32(smem + G::p_off), 16, 1024);
+    const uint64_t dk = desc<CB>(k_s, 16, 8 * CB), dv = desc<CB>(v_s, KT * CB, 8 * CB);
     uint32_t u = 0, piece = 0;
     bool pending = false, pfirst = false, alive = true;
-    auto wait = [&](int i, uint32_t parity) { alive = alive && fa::wait_all(bar(i), parity, abort_flag, p.err); };
+    auto wait = [&](int i, uint32_t pi, int k, uint32_t pk) { alive = alive && wait_both(bar(i), pi, bar(k), pk, abort_flag, p.err); };
     auto weigh = [&](uint32_t w, bool first) {  // O += P V of tile w
-      const uint32_t st = w % NS;
-      wait(kBPFull + w % NP, (w / NP) & 1u);
-      wait(kBVFull + st, (w / NS) & 1u);
+      const uint32_t st = w % NV;
+      wait(kBPFull + w % NP, (w / NP) & 1u, kBVFull + st, (w / NV) & 1u);
       tc_fence_after();
       if (alive && fa::elect_one()) {
-        const uint64_t vd = dv + static_cast<uint64_t>((st * (2 * ENT)) >> 4);
+        const uint64_t vd = dv + static_cast<uint64_t>((st * ENT) >> 4);
         const uint64_t pd = dp + static_cast<uint64_t>(((w % NP) * G::PB) >> 4);
 #pragma unroll
         for (int k = 0; k < KT / 32; ++k)
@@ -553,22 +549,21 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
           weigh(u - 1, pfirst);
           pending = false;
         }
-        wait(kBQFull, piece & 1u);
+        wait(kBQFull, piece & 1u, kBQFull, piece & 1u);
         ++piece;
 #pragma unroll 1
         for (int g = g0; g < ge; g += GT, ++u) {
-          const uint32_t st = u % NS;
-          wait(kBKFull + st, (u / NS) & 1u);
-          wait(kBSEmpty, (u & 1u) ^ 1u);
+          const uint32_t st = u % NK;
+          wait(kBKFull + st, (u / NK) & 1u, kBSEmpty, (u & 1u) ^ 1u);
           tc_fence_after();
           if (alive && fa::elect_one()) {
-            const uint64_t kd = dk + static_cast<uint64_t>((st * (2 * ENT)) >> 4);
+            const uint64_t kd = dk + static_cast<uint64_t>((st * ENT) >> 4);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < (G::both ? 2 : 1); ++t)
 #pragma unroll
               for (int k = 0; k < D / 32; ++k) {
                 const int qb = t * D + 32 * k, kb = 32 * k;
-                mma_f8_ss(tS, dq + static_cast<uint64_t>(((qb >> 7) * (128 * 128) + (qb & 127)) >> 4),
+                mma_f8_ss(tS, dq + static_cast<uint64_t>((qb / G::QCB * (128 * G::QCB) + qb % G::QCB) >> 4),
                           kd + static_cast<uint64_t>(((kb / CB) * (KT * CB) + kb % CB) >> 4), idS, t + k > 0);
               }
             mma_commit(bar(kBSFull));
@@ -631,7 +626,7 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
       float m = NEG_INF, l = 0.f;
 #pragma unroll 1
       for (int g = g0; g < ge; g += GT, ++u) {
-        wait(kBSFull, u & 1u);
+        alive = alive && wait_both(bar(kBSFull), u & 1u, bar(kBMeta + u % kMeta), (u / kMeta) & 1u, abort_flag, p.err);
         tc_fence_after();
         float x[KN];
         {
@@ -640,17 +635,24 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
           tc_fence_before();
           __syncwarp();
           arrive(kBSEmpty);
+          // with 16 rows or fewer the lower half of the lanes holds the hi terms' scores
+          // of all 32 keys and the upper half the lo terms': each gets those of its keys
+          // from lane ^ 16
           if constexpr (NR == 32) {
 #pragma unroll
             for (int i = 0; i < KN; ++i) x[i] = y[i];
           } else if constexpr (NR == 16) {
 #pragma unroll
-            for (int i = 0; i < KN; ++i) x[i] = part ? y[16 + i] : y[i];
+            for (int i = 0; i < KN; ++i) {
+              const float mine = part ? y[16 + i] : y[i], its = part ? y[i] : y[16 + i];
+              x[i] = mine + __shfl_xor_sync(0xffffffffu, its, 16);
+            }
           } else {
 #pragma unroll
             for (int i = 0; i < KN; ++i) {
               const float lo = part & 1 ? y[8 + i] : y[i], hi = part & 1 ? y[24 + i] : y[16 + i];
-              x[i] = part & 2 ? hi : lo;
+              const float mine = part & 2 ? hi : lo, its = part & 2 ? lo : hi;
+              x[i] = mine + __shfl_xor_sync(0xffffffffu, its, 16);
             }
           }
         }
@@ -696,6 +698,8 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
           l *= al;
           m = mn;
         }
+        // (looked at here: the answer comes while the weights are computed)
+        const bool is_free = u < NP || tr::test(bar(kBPEmpty + u % NP), ((u / NP) & 1u) ^ 1u);
         const float up = m == NEG_INF ? 0.f : static_cast<float>(kUp) - m;
         uint32_t w[3][KN / 4];
         float sum[NG];
@@ -721,7 +725,7 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
         }
 #pragma unroll
         for (int h = 0; h < NG; ++h) l = fmaf(sum[h], me[h].z, l);
-        if (u >= NP) wait_weighed(u - NP);  // the buffer is free once its tile before is weighed
+        if (!__all_sync(0xffffffffu, is_free)) wait_weighed(u - NP);  // the buffer's tile before
         unsigned char* pb = smem + G::p_off + (u % NP) * G::PB;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
@@ -738,10 +742,10 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
         }
         if (lacks) {
           // V rows of keys that are not there: 0 times what lies there may be NaN
-          const uint32_t st = u % NS;
-          wait(kBVFull + st, (u / NS) & 1u);
+          const uint32_t st = u % NV;
+          wait(kBVFull + st, (u / NV) & 1u);
           if ((tid & 15) >= (__float_as_int(meta[(u % kMeta) * GT + (tid >> 4)].w) & 255)) {
-            unsigned char* v = smem + G::ring_off + st * (2 * ENT) + ENT + tid * CB;
+            unsigned char* v = smem + G::v_off + st * ENT + tid * CB;
 #pragma unroll
             for (int c = 0; c < G::NB; ++c)
 #pragma unroll

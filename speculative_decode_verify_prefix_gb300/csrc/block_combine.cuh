@@ -5,22 +5,25 @@
 // With (lse, o) of each piece in base 2 the row is sum 2^(lse - m) o / sum
 // 2^(lse - m); a draft key counts as a piece of one key.  A warp takes one packed
 // row, lane l the columns D / 32 l on, so a piece's row is one coalesced load and
-// nothing is computed twice.  The drafts need nothing of the stream and come first:
-// the kernel is a programmatic dependent of it.  All sums are 32-bit.
+// nothing is computed twice.  SPLIT: the four warps of a CTA share a row's pieces (a
+// segment in many pieces is a long chain of loads: two sequences of 6k keys, 2 KV
+// heads of 256, XXX).  The drafts need nothing of the stream and come first: the
+// kernel is a programmatic dependent of it.  All sums are 32-bit.
 #pragma once
 #include "block_stream.cuh"
 
 namespace vsk {
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constant__ bk::BkParams p) {
   using namespace bk;
   constexpr int E = D / 32;  // columns of a lane
+  constexpr int ROWS = SPLIT ? 1 : 4;  // rows of a CTA
   __shared__ long long scan[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per_seg = (p.R + 3) / 4;
+  const int per_seg = (p.R + ROWS - 1) / ROWS;
   const long long seg = blockIdx.x / per_seg;
-  const int row = static_cast<int>(blockIdx.x - seg * per_seg) * 4 + warp;
+  const int row = static_cast<int>(blockIdx.x - seg * per_seg) * ROWS + (SPLIT ? 0 : warp);
   const int b = static_cast<int>(seg / p.h_kv), h = static_cast<int>(seg - static_cast<long long>(b) * p.h_kv);
   const float NEG_INF = -INFINITY;
 
@@ -78,7 +81,7 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
   for (int c = 0; c < E; ++c) acc[c] = 0.f;
 
   // ---- drafts ----
-  const int nd = seen ? p.L : i + 1;
+  const int nd = SPLIT && warp > 0 ? 0 : seen ? p.L : i + 1;  // (by the first warp)
   for (int t0 = 0; t0 < nd; t0 += 4) {
     float sc[4], v[4][E];
     bool vis[4];
@@ -122,12 +125,15 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
   const long long off = (scan[4] + scan[5] + scan[6] + scan[7]) * p.n_hg + static_cast<long long>(h / p.team) * T;
   const long long W = share_of(p, total);
   const long long c0 = off / W;
-  const int pieces = static_cast<int>((off + T - 1) / W - c0) + 1;
+  const int all_pieces = static_cast<int>((off + T - 1) / W - c0) + 1;
+  constexpr int PARTS = SPLIT ? 4 : 1;
+  const int pieces = SPLIT ? (all_pieces - warp + PARTS - 1) / PARTS : all_pieces;  // warp, warp + 4, ...
   // piece i: CTA (c0 + i) team + h % team of the stream
   const long long slot = c0 * p.team + static_cast<long long>(b) * p.h_kv + h;
-  const long long step = static_cast<long long>(p.team) * p.rows;
-  const float* lse = p.plse + slot * p.rows + row;
-  const float* po = p.po + (slot * p.rows + row) * D + E * lane;
+  const long long step = static_cast<long long>(p.team) * p.rows * PARTS;
+  const long long at0 = (slot + (SPLIT ? warp * p.team : 0)) * p.rows + row;
+  const float* lse = p.plse + at0;
+  const float* po = p.po + at0 * D + E * lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i0 = 0; i0 < pieces; i0 += 32) {
     const int n = min(32, pieces - i0);
@@ -167,6 +173,35 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
           }
         }
       }
+    }
+  }
+  if constexpr (SPLIT) {
+    __shared__ float part[3][D + 2];
+    if (warp > 0) {
+#pragma unroll
+      for (int c = 0; c < E; ++c) part[warp - 1][32 * c + lane] = acc[c];
+      if (lane == 0) {
+        part[warp - 1][D] = m;
+        part[warp - 1][D + 1] = l;
+      }
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    float mx = m;
+#pragma unroll
+    for (int w = 0; w < 3; ++w) mx = fmaxf(mx, part[w][D]);
+    const float ms = mx == NEG_INF ? 0.f : mx;
+    float a = exp2f(m - ms);
+    l *= a;
+#pragma unroll
+    for (int c = 0; c < E; ++c) acc[c] *= a;
+#pragma unroll
+    for (int w = 0; w < 3; ++w) {
+      if (part[w][D + 1] == 0.f) continue;  // (a sum that is NaN is none)
+      a = exp2f(part[w][D] - ms);
+      l = fmaf(a, part[w][D + 1], l);
+#pragma unroll
+      for (int c = 0; c < E; ++c) acc[c] = fmaf(a, part[w][32 * c + lane], acc[c]);
     }
   }
   // a row with nothing to see is 0

@@ -261,19 +261,19 @@ static bool block_map(const vsk_tensor* t, int cols, int rows, CUtensorMap* map)
 
 struct BlockForm {
   bk::BkFn stream;
-  bk::BkJoinFn join;
+  bk::BkJoinFn join[2];  // a row a warp, a row a CTA
   int smem, per_sm;
 };
 template <int D>
-static BlockForm form_of(int nr, bk::BkFn s, bk::BkJoinFn j) {
+static BlockForm form_of(int nr, bk::BkFn s, bk::BkJoinFn j, bk::BkJoinFn j4) {
   const int smem = nr == 8 ? bk::Geo<D, 8>::smem : nr == 16 ? bk::Geo<D, 16>::smem : bk::Geo<D, 32>::smem;
-  return BlockForm{s, j, smem, bk::Geo<D, 32>::per_sm};
+  return BlockForm{s, {j, j4}, smem, bk::Geo<D, 32>::per_sm};
 }
 static BlockForm block_form(long long D, long long R) {
   const int nr = bk::row_tile(static_cast<int>(R));
-  return D == 64    ? form_of<64>(nr, kernel_block_stream_64(nr), kernel_block_combine_64())
-         : D == 128 ? form_of<128>(nr, kernel_block_stream_128(nr), kernel_block_combine_128())
-                    : form_of<256>(nr, kernel_block_stream_256(nr), kernel_block_combine_256());
+  return D == 64    ? form_of<64>(nr, kernel_block_stream_64(nr), kernel_block_combine_64(false), kernel_block_combine_64(true))
+         : D == 128 ? form_of<128>(nr, kernel_block_stream_128(nr), kernel_block_combine_128(false), kernel_block_combine_128(true))
+                    : form_of<256>(nr, kernel_block_stream_256(nr), kernel_block_combine_256(false), kernel_block_combine_256(true));
 }
 
 // Partials: a slot per piece (CTA c, segment s: slot c + s), whole row tiles.
@@ -292,6 +292,7 @@ static BlockWs block_ws(long long n_cta, long long B, long long h_kv, long long 
   return w;
 }
 constexpr long long kMaxRows = 128;  // packed rows of a KV head
+constexpr long long kSplitJoin = 4;  // pieces of a segment from which the joining CTA's warps share a row
 
 }  // namespace vsk
 
@@ -507,7 +508,11 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   if (!current_sms(&sms)) return 0;
   const long long n_cta = static_cast<long long>(sms) * f.per_sm;
   const BlockWs w = block_ws(n_cta, B, h_kv, R, D);
-  const long long joins = B * h_kv * ((R + 3) / 4);
+  // teams over segments: a segment's pieces, about
+  int team = 8;
+  while (h_kv % team != 0) --team;
+  const bool split = n_cta / team > kSplitJoin * B * (h_kv / team);
+  const long long joins = B * h_kv * (split ? R : (R + 3) / 4);
   if (joins > INT_MAX) return fail("grid of %lld CTAs too large", joins);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   size_t ws_bytes = 0;
@@ -547,7 +552,7 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   p.h_kv = static_cast<int>(h_kv);
   p.rows = static_cast<int>(w.rows);
   p.w_min = 1;
-  for (p.team = 8; p.h_kv % p.team != 0;) --p.team;
+  p.team = team;
   p.n_hg = p.h_kv / p.team;
   p.n_team = static_cast<int>(n_cta) / p.team;
   if (cm) {
@@ -581,7 +586,7 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(f.join), args);
+  e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(f.join[split]), args);
   if (e != cudaSuccess) return fail("combine kernel launch failed: %s", cudaGetErrorString(e));
   return 1;
 }

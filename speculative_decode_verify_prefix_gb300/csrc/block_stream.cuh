@@ -121,6 +121,7 @@ struct Geo {
   static constexpr int smem = v_off + NV * ENT;
   static constexpr int cols = D == 256 ? 512 : 256;  // S 128, O D
   static_assert(NK >= 2 && NV <= 5 && NK + 2 < kMeta, "ring");
+  static_assert(QB >= PB, "a piece's terms meet where P and Q were");
   static_assert((NK + NV) * ENT >= 128 * 128, "the rows behind P are read from the ring");
   static_assert(q_off % 1024 == 0 && p_off % 1024 == 0 && PB % 1024 == 0 && ring_off % 1024 == 0, "swizzled layouts");
 };
@@ -189,8 +190,8 @@ __device__ __forceinline__ bool my_share(const BkParams& p, unsigned char* smem,
   const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
   long long mine = 0;
   bool bad = false;
+  int P = 0;  // the only one where a thread has one sequence: not loaded twice
   for (int b = lo; b < hi; ++b) {
-    int P;
     bad |= !prefix_len(p, b, P);
     mine += seg_tiles(P);
   }
@@ -214,20 +215,24 @@ __device__ __forceinline__ bool my_share(const BkParams& p, unsigned char* smem,
   start = static_cast<long long>(blockIdx.x) / p.team * W;
   if (start >= total) return false;  // uniform
   end = min(total, start + W);
-  for (int b = lo; b < hi; ++b) {
-    int P;
-    prefix_len(p, b, P);
-    const int T = seg_tiles(P);
-    if (start >= at * p.n_hg && start < (at + T) * p.n_hg) {
-      *found = b;
-      *base = at * p.n_hg;
+  if (start >= at * p.n_hg && start < (at + mine) * p.n_hg) {
+    for (int b = lo; b < hi; ++b) {
+      if (per > 1) prefix_len(p, b, P);
+      const int T = seg_tiles(P);
+      if (start < (at + T) * p.n_hg) {
+        found[0] = b;
+        found[1] = P;
+        *base = at * p.n_hg;
+        break;
+      }
+      at += T;
     }
-    at += T;
   }
   __syncthreads();
-  s.b = *found;
+  s.b = found[0];
   if (s.b < 0) return false;  // not reached: guards the walk
-  seg_load(p, s);
+  s.P = found[1];
+  s.T = seg_tiles(s.P);
   const long long hg = (start - *base) / s.T;
   s.h = static_cast<int>(hg) * p.team + member;
   s.off = *base + hg * s.T;
@@ -284,44 +289,60 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 }
 
 // The row tile's packed rows (row r = draft r / gq, query head h gq + r % gq;
-// rows from R on are zero) into Q, as hi and lo terms, 128 / NR times, and their
-// score scales; by the softmax warps, NR / 4 rows each.
+// rows from R on are zero) into Q, as hi and lo terms, 128 / NR times (64 / NR), and
+// their score scales; by the softmax warps, NR / 4 rows each.  First the loads alone.
 template <int D, int NR>
-__device__ __forceinline__ void load_rows(const BkParams& p, const BSeg& s, unsigned char* smem, int warp, int lane) {
-  using G = Geo<D, NR>;
-  constexpr int W = D / 64;  // 32-bit words of a row per lane
-  constexpr int J = NR / 4;
-  const int a = __ldg(p.qo + s.b), e = __ldg(p.qo + s.b + 1);
-  const bool ok = a >= 0 && e - a == p.L && static_cast<long long>(a) + p.L <= p.n_rows;
-  const long long first = ok ? a : static_cast<long long>(s.b) * p.L;
-  float* qsc = reinterpret_cast<float*>(smem + kQscOff);
+struct Rows {
+  static constexpr int W = D / 64;  // 32-bit words of a row per lane
+  static constexpr int J = NR / 4;
   uint32_t v[J][W];
+  __device__ __forceinline__ void fetch(const BkParams& p, const BSeg& s, int warp, int lane) {
+    const int a = __ldg(p.qo + s.b), e = __ldg(p.qo + s.b + 1);
+    const bool ok = a >= 0 && e - a == p.L && static_cast<long long>(a) + p.L <= p.n_rows;
+    const long long first = ok ? a : static_cast<long long>(s.b) * p.L;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int r = static_cast<int>(blockIdx.y) * NR + J * warp + j;
+      const bool live = r < p.R;
+      const int rr = live ? r : 0;
+      const __nv_bfloat16* src = p.q + (first + rr / p.gq) * p.q_s0 + static_cast<long long>(s.h * p.gq + rr % p.gq) * p.q_s1;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v[j][w] = live ? ld_u32(src + 2 * (W * lane + w)) : 0u;
+    }
+  }
+};
+template <int D, int NR>
+__device__ __forceinline__ void put_rows(const BkParams& p, Rows<D, NR>& rows, unsigned char* smem, int warp, int lane) {
+  using G = Geo<D, NR>;
+  constexpr int W = Rows<D, NR>::W, J = Rows<D, NR>::J;
+  uint32_t (&v)[J][W] = rows.v;
+  float* qsc = reinterpret_cast<float*>(smem + kQscOff);
+  unsigned most[J], all = 0;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int r = static_cast<int>(blockIdx.y) * NR + J * warp + j;
-    const bool live = r < p.R;
-    const int rr = live ? r : 0;
-    const __nv_bfloat16* src = p.q + (first + rr / p.gq) * p.q_s0 + static_cast<long long>(s.h * p.gq + rr % p.gq) * p.q_s1;
+    most[j] = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) v[j][w] = live ? ld_u32(src + 2 * (W * lane + w)) : 0u;
+    for (int w = 0; w < W; ++w) most[j] = max(most[j], mag_bf16x2(v[j][w]));
+    most[j] = __reduce_max_sync(0xffffffffu, most[j]);
+    all = max(all, most[j]);
+  }
+  if (all >= kBf16Inf) {
+    // e4m3 has no infinity; an infinite query makes its row's softmax NaN, as NaN does
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      most[j] = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        most[j] = max(most[j], finite_mag_bf16x2(v[j][w]));
+        v[j][w] = inf_to_nan_bf16x2(v[j][w]);
+      }
+      most[j] = __reduce_max_sync(0xffffffffu, most[j]);
+    }
   }
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int row = J * warp + j;
-    unsigned mx = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) mx = max(mx, mag_bf16x2(v[j][w]));
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if (mx >= kBf16Inf) {
-      // e4m3 has no infinity; an infinite query makes its row's softmax NaN, as NaN does
-      mx = 0;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        mx = max(mx, finite_mag_bf16x2(v[j][w]));
-        v[j][w] = inf_to_nan_bf16x2(v[j][w]);
-      }
-      mx = __reduce_max_sync(0xffffffffu, mx);
-    }
+    const unsigned mx = most[j];
     // the row's largest |q| 2^sh lies in [128, 256)
     const int sh = mx == 0 ? 0 : max(-120, min(120, 7 - (static_cast<int>(mx >> 7) - 127)));
     const float up = __int_as_float((127 + sh) << 23);
@@ -385,6 +406,20 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
   auto bar = [&](int i) -> uint32_t { return smem_u32(bars + i); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kAbortOff);
   const uint32_t k_s = smem_u32(smem + G::ring_off), v_s = smem_u32(smem + G::v_off);
+  // what the first tile needs from memory is asked for before the set-up
+  Rows<D, NR> rows;
+  BatchIt cur;
+  int page = -1;
+  auto page_of_group = [&](const BatchIt& it) -> int {  // block of group `lane` of a batch
+    const int gi = it.g + lane;
+    return it.valid && gi < it.ge ? __ldg(p.bt + static_cast<long long>(it.s.b) * p.bt_s0 + gi / p.bgroups) : -1;
+  };
+  if (warp < 4) {
+    rows.fetch(p, seg0, warp, lane);
+  } else if (warp != 5) {
+    cur.first(p, seg0, start, end);
+    page = page_of_group(cur);
+  }
   if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < NK; ++i) {
@@ -429,13 +464,8 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
     const uint32_t n_ent = isv ? NV : NK, ring = isv ? v_s : k_s;
     const int full0 = isv ? kBVFull : kBKFull, empty0 = isv ? kBVEmpty : kBKEmpty;
     float4* meta = reinterpret_cast<float4*>(smem + kMetaOff);
-    BatchIt cur, ahead;
-    // group `lane` of a batch: its block, and (a batch later) its scales
-    auto page_of_group = [&](const BatchIt& it) -> int {
-      const int gi = it.g + lane;
-      return it.valid && gi < it.ge ? __ldg(p.bt + static_cast<long long>(it.s.b) * p.bt_s0 + gi / p.bgroups) : -1;
-    };
-    int page, page2;
+    BatchIt ahead;
+    int page2 = -1;
     float ks = 1.f, vs = 1.f, ks2 = 1.f, vs2 = 1.f;
     auto scales = [&](int pg, int h, float& k, float& v) {
       k = v = 1.f;
@@ -444,32 +474,32 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
         v = __ldg(p.vs + pg * p.vs_s0 + h);
       }
     };
-    cur.first(p, seg0, start, end);
-    page = page_of_group(cur);
     scales(page, cur.s.h, ks, vs);
     uint32_t u = 0, issued = 0;
     uint32_t st = 0, par = 1;
     bool alive = true;
 #pragma unroll 1
     while (cur.valid && alive) {
-      // (the next batch's blocks now, their scales once this batch is on its way)
-      ahead = cur;
-      ahead.next(p, start, end);
-      page2 = page_of_group(ahead);
       const int gi = cur.g + lane;
       const bool in = gi < cur.ge, ok = in && page >= 0 && page < p.n_blocks;
       if (in && !ok && isv) atomicOr(p.err, kErrBadIndex);
       const int keys = ok ? min(GK, cur.s.P - gi * GK) : 0;
       const int row = ok ? page * p.block + gi % p.bgroups * GK : -1;
-      // a scale that is no positive finite number in the range gives NaN
-      const bool good = ks >= kMinScale && ks <= kMaxScale && vs >= kMinScale && vs <= kMaxScale;
-      if (!good) atomicOr(p.err, kErrBadScale);
-      const float nan = __int_as_float(0x7FC00000);
-      const float4 mine = make_float4(good ? ks : nan, good ? log2f(vs) : nan, good ? 1.f / vs : nan, __int_as_float(keys));
       const int tiles = (min(32, cur.ge - cur.g) + GT - 1) / GT;
+      float4 mine;
 #pragma unroll 1
       for (int j = 0; j < tiles; ++j, ++u) {
-        if (isv) {
+        // V's entry waits for the weights of a tile before; the scales are asked for with
+        // the first tile's scores
+        const bool late = isv && u < n_ent;
+        auto tell = [&] {
+          if (j == 0) {
+            // a scale that is no positive finite number in the range gives NaN
+            const bool good = ks >= kMinScale && ks <= kMaxScale && vs >= kMinScale && vs <= kMaxScale;
+            if (!good) atomicOr(p.err, kErrBadScale);
+            const float nan = __int_as_float(0x7FC00000);
+            mine = make_float4(good ? ks : nan, good ? log2f(vs) : nan, good ? 1.f / vs : nan, __int_as_float(keys));
+          }
           const bool lacks = __any_sync(0xffffffffu, (lane >> 3) == j && keys < GK);
           if ((lane >> 3) == j) {
             float4 x = mine;
@@ -478,7 +508,8 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBMeta + u % kMeta));
-        }
+        };
+        if (isv && !late) tell();
         alive = fa::wait_all(bar(empty0 + st), par, abort_flag, p.err);
         if (!alive) break;
         int at[GT];  // first rows in the cache
@@ -499,12 +530,19 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
                 fa::tma_load_box(ring + st * ENT + c * (KT * CB) + i * (GK * CB), map, bar(full0 + st), c * CB, cur.s.h, at[i]);
         }
         __syncwarp();
+        if (late) tell();  // the first entries are free: copies first
         issued = u + 1;
+        if (j == 0) {  // the next batch's blocks, while this one's tiles are on their way
+          ahead = cur;
+          ahead.next(p, start, end);
+          page2 = page_of_group(ahead);
+        }
         if (++st == n_ent) {
           st = 0;
           par ^= 1u;
         }
       }
+      if (!alive) break;
       scales(page2, ahead.valid ? ahead.s.h : 0, ks2, vs2);
       cur = ahead;
       page = page2;
@@ -618,7 +656,8 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
         if (tid < live) lse_p[tid] = NEG_INF;
         continue;
       }
-      load_rows<D, NR>(p, s, smem, warp, lane);
+      if (s.off > start) rows.fetch(p, s, warp, lane);  // (the first piece's are on their way)
+      put_rows<D, NR>(p, rows, smem, warp, lane);
       fence_proxy_async();
       named_bar_sync(1, kSm);  // the rows' scales
       arrive(kBQFull);
@@ -673,7 +712,7 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
         for (int i = 0; i < KN; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i]);
         float tm = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         // The reference stays while no row of the tile passes it by 2^kThr.
-        if (tc::bar_red_or(1, kSm, tm > m + kThr)) {  // alike in the four warps
+        if (g == g0 || tc::bar_red_or(1, kSm, tm > m + kThr)) {  // alike in the four warps
 #pragma unroll
           for (int o = NR; o < 32; o *= 2) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
           if (lane < NR) red[warp * NR + lane] = tm;
@@ -765,18 +804,19 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
       named_bar_sync(1, kSm);
       const float lt = (sums[r] + sums[NR + r]) + (sums[2 * NR + r] + sums[3 * NR + r]);
       if (warp == 0 && lane < live) lse_p[lane] = lt == 0.f ? NEG_INF : m + (log2f(lt) - static_cast<float>(kUp));
-      // the terms meet in shared memory, [3][NR rows][32 columns] at a time: P is free
-      unsigned char* stage = smem + G::p_off;
+      // the terms meet in shared memory, [3][NR rows][32 columns] at a time, by turns where
+      // P and Q were: a warp that writes the next but one has seen all read this one
       constexpr int TPR = 128 / NR, CPT = 32 / TPR;  // threads of a row, columns of a thread
       const int orow = tid / TPR, oc = (tid % TPR) * CPT;
       const float lo = (sums[orow] + sums[NR + orow]) + (sums[2 * NR + orow] + sums[3 * NR + orow]);
       const float inv = lo == 0.f ? 0.f : 1.f / lo;
-#pragma unroll 1
+      const int pr = 32 * warp + lane;  // term pr / NR of row pr % NR
+#pragma unroll 2
       for (int c = 0; c < D; c += 32) {
+        unsigned char* stage = smem + (c & 32 ? G::q_off : G::p_off);
         if (32 * warp < 3 * NR) {
           float o[32];
           tmem_ld<32>(tO + lanes + c, o);
-          const int pr = 32 * warp + lane;  // term pr / NR of row pr % NR
           if (pr < 3 * NR) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -805,8 +845,8 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
 #pragma unroll
           for (int i = 0; i < CPT; i += 2) *reinterpret_cast<float2*>(out + i) = make_float2(res[i], res[i + 1]);
         }
-        named_bar_sync(1, kSm);
       }
+      named_bar_sync(1, kSm);  // P and Q are free
       tc_fence_before();
     }
   }
@@ -821,8 +861,8 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
 bk::BkFn kernel_block_stream_64(int nr);  // nr: rows of a CTA
 bk::BkFn kernel_block_stream_128(int nr);  // nr: rows of a CTA
 bk::BkFn kernel_block_stream_256(int nr);  // nr: rows of a CTA
-bk::BkJoinFn kernel_block_combine_64();
-bk::BkJoinFn kernel_block_combine_128();
-bk::BkJoinFn kernel_block_combine_256();
+bk::BkJoinFn kernel_block_combine_64(bool split);
+bk::BkJoinFn kernel_block_combine_128(bool split);
+bk::BkJoinFn kernel_block_combine_256(bool split);
 
 }  // namespace vsk

@@ -186,17 +186,24 @@ static int allow_smem(const void* fn, size_t smem) {
   return 1;
 }
 
+// Tokens and heads of a CTA that takes rows; the CTAs.  Few tokens: a row's heads
+// over several CTAs, a pass of the threads each at least.
+static long long cut_rows(rp::RopeParams& p, long long heads, long long D, int sms, int threads) {
+  if (heads == 0) return 0;
+  const long long slots = threads / (D / 16);
+  p.tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(rp::kMaxTokens, p.n / (4LL * sms))));
+  const long long tiles = (p.n + p.tokens - 1) / p.tokens;
+  const long long parts = std::max<long long>(1, std::min((heads + slots - 1) / slots, 4LL * sms / tiles));
+  p.heads = static_cast<int>((heads + parts - 1) / parts);
+  return tiles * ((heads + p.heads - 1) / p.heads);
+}
 static int launch_rope(rp::RopeParams& p, long long D, int pool, cudaStream_t st) {
   if (p.n == 0) return 1;
   int sms = 0;
   if (!current_sms(&sms)) return 0;
-  const long long heads = p.h_q + (pool ? 2LL : 1LL) * p.h_kv, slots = rp::kThreads / (D / 16);
-  p.tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(rp::kMaxTokens, p.n / (4LL * sms))));
-  const long long tiles = (p.n + p.tokens - 1) / p.tokens;
-  // few tokens: a row's heads over several CTAs, a pass of the threads each at least
-  const long long parts = std::max<long long>(1, std::min((heads + slots - 1) / slots, 4LL * sms / tiles));
-  p.heads = static_cast<int>((heads + parts - 1) / parts);
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((heads + p.heads - 1) / p.heads));
+  const long long heads = p.h_q + (pool ? 2LL : 1LL) * p.h_kv, ctas = cut_rows(p, heads, D, sms, rp::kThreads);
+  const long long per_tile = (heads + p.heads - 1) / p.heads;
+  const dim3 grid(static_cast<unsigned>(ctas / per_tile), static_cast<unsigned>(per_tile));
   if (grid.y > 65535) return fail("%lld heads are too many", heads);
   void* args[] = {&p};
   const cudaError_t e =
@@ -291,6 +298,7 @@ static BlockWs block_ws(long long n_cta, long long B, long long h_kv, long long 
   w.need = w.o_off + align256(4 * rows * static_cast<size_t>(D)) + kTicketBytes;
   return w;
 }
+constexpr long long kBlockParts = 2;  // CTAs of a block at most (appends)
 constexpr long long kMaxRows = 128;  // packed rows of a KV head
 constexpr long long kSplitJoin = 4;  // pieces of a segment from which the joining CTA's warps share a row
 
@@ -436,12 +444,21 @@ int rope_append_block_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_te
   p.err = reinterpret_cast<unsigned*>(ws);
   // a sequence adds to at most one block more than its rows fill, twice over, and to none without a row
   const long long units = std::min(p.n, p.n / block_size + 2 * B);
-  const long long parts = std::max<long long>(1, std::min<long long>(4, 2LL * sms / units));
+  // warps that hold the K or V rows of a block and head, 16 elements a thread
+  // (of the rows a block gets on the average)
+  const long long held = 32 * 16 / D, mean = std::min<long long>(block_size, (p.n + B - 1) / B);
+  for (p.warps = 1; p.warps * held < mean && p.warps < rp::kBlockThreads / 32;) p.warps *= 2;
+  const long long groups = rp::kBlockThreads / 32 / p.warps;
+  p.units = static_cast<int>(units);
+  p.parts = static_cast<int>(std::min((2LL * p.h_kv + groups - 1) / groups, kBlockParts));
+  const long long kv = units * p.parts, rows = cut_rows(p, p.h_q, D, sms, rp::kBlockThreads), grid = kv + rows;
+  p.turn = static_cast<int>(1 + rows / kv);
+  if (grid > INT_MAX) return fail("grid of %lld CTAs too large", grid);
   const void* fn = reinterpret_cast<const void*>(kernel_rope_block(static_cast<int>(D)));
   const size_t smem = sizeof(float2) * static_cast<size_t>(block_size) * static_cast<size_t>(p.rot / 2);
   if (!allow_smem(fn, sizeof(float2) * rp::kMaxBlock * 128)) return 0;
   void* args[] = {&p};
-  const cudaError_t e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(units), static_cast<unsigned>(parts)), dim3(rp::kThreads), args, smem, st);
+  const cudaError_t e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(grid)), dim3(rp::kBlockThreads), args, smem, st);
   if (e != cudaSuccess) return fail("kernel launch failed: %s", cudaGetErrorString(e));
   return 1;
 }

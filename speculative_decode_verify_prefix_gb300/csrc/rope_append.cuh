@@ -21,8 +21,9 @@ namespace vsk {
 namespace rp {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 16;   // rope_kernel: tokens of a CTA
+constexpr int kMaxTokens = 8;    // rope_kernel: tokens of a CTA
 constexpr int kMaxBlock = 128;   // rows of a block at most
+constexpr int kBlockThreads = 256;  // rope_block_kernel
 constexpr float kTop = 448.f;    // the largest e4m3 value
 constexpr int kMinExp = -40, kMaxExp = 40;  // powers of two a block's scale takes
 
@@ -56,6 +57,9 @@ struct RopeParams {
   const int* bt;
   long long bt_s0;
   int bt_cols, block, B;
+  int warps;  // of a (block, head, K or V): a power of two
+  int units, parts;  // blocks at most, CTAs of one
+  int turn;          // CTAs from one of keys and values to the next
   long long n_blocks;
 };
 
@@ -67,10 +71,11 @@ __device__ __forceinline__ unsigned long long turns_of(float f) {
   t -= floor(t);
   return __double2ull_rn(t * 18446744073709551616.0);
 }
-// (A cos, A sin) of a position; a frequency that is no number gives none.
+// (A cos, A sin) of a position; a frequency that is no number gives none.  32 bits
+// of the phase: 2^-32 of a turn.
 __device__ __forceinline__ float2 turn(unsigned long long f, long long pos, float size) {
-  const long long phase = static_cast<long long>(f * static_cast<unsigned long long>(pos));
-  const float half = __ll2float_rn(phase) * 1.0842021724855044e-19f;  // 2^-63: half turns in [-1, 1]
+  const int phase = static_cast<int>(f * static_cast<unsigned long long>(pos) >> 32);
+  const float half = static_cast<float>(phase) * 4.656612873077393e-10f;  // 2^-31: half turns in [-1, 1]
   float s, c;
   sincospif(half, &s, &c);
   return make_float2(size * c, size * s);
@@ -79,16 +84,21 @@ __device__ __forceinline__ long long index_at(const void* p, int wide, long long
   return wide ? __ldg(static_cast<const long long*>(p) + i) : static_cast<long long>(__ldg(static_cast<const int*>(p) + i));
 }
 
-// Table of tokens [t0, t0 + n): entry (i, pair).
+// Table of tokens [t0, t0 + n).  A thread reads the eight entries of pairs 8 c ..
+// 8 c + 7 in four pieces of two: piece k of all c lies together, so that the lanes
+// of a head read side by side (with a thread's entries together, 4 lanes met in a
+// bank: XXX).
+template <int NT>
 __device__ __forceinline__ void fill_table(const RopeParams& p, float2* cs, long long t0, int n) {
   const int pairs = p.rot >> 1;
-  const int step = kThreads / pairs;  // tokens a pass (rot <= 256: at least two)
+  const int step = NT / pairs;  // tokens a pass (rot <= 256: at least two)
   const int pair = threadIdx.x % pairs, first = threadIdx.x / pairs;
   if (first < step && first < n) {
     const float f = __ldg(p.freq + pair);
+    const int at = ((pair & 7) >> 1) * (pairs >> 2) + (pair >> 3) * 2 + (pair & 1);
     const unsigned long long turns = turns_of(f);
     const float size = isfinite(f) ? p.size : __int_as_float(0x7FC00000);
-    for (int i = first; i < n; i += step) cs[i * pairs + pair] = turn(turns, index_at(p.pos, p.pos64, t0 + i), size);
+    for (int i = first; i < n; i += step) cs[i * pairs + at] = turn(turns, index_at(p.pos, p.pos64, t0 + i), size);
   }
 }
 
@@ -104,7 +114,7 @@ __device__ __forceinline__ Item item_at(const RopeParams& p, const float2* row, 
   const bool split = turned && !p.inter;
   it.o1 = split ? 8 * c : 16 * c;
   it.o2 = split ? (p.rot >> 1) + 8 * c : 16 * c + 8;
-  it.cs = turned ? row + 8 * c : nullptr;
+  it.cs = turned ? row + 2 * c : nullptr;
   return it;
 }
 struct F16 {
@@ -119,11 +129,10 @@ __device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
 }
 __device__ __forceinline__ void rotate(const RopeParams& p, const float2* cs, F16& x) {
   if (cs == nullptr) return;
-  const float4* t4 = reinterpret_cast<const float4*>(cs);
   float2 t[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 w = t4[i];
+    const float4 w = *reinterpret_cast<const float4*>(cs + i * (p.rot >> 3));
     t[2 * i] = make_float2(w.x, w.y);
     t[2 * i + 1] = make_float2(w.z, w.w);
   }
@@ -146,13 +155,39 @@ __device__ __forceinline__ void rotate(const RopeParams& p, const float2* cs, F1
   }
 }
 
-// Eight values under scale s as e4m3 codes: round to nearest even of x / s in 32
-// bits, saturating.  A power of two divides exactly as its reciprocal multiplies.
-__device__ __forceinline__ bool is_pow2(float s) { return (__float_as_uint(s) & 0x007FFFFFu) == 0u; }
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, float inv, bool pow2) {
-  float y[8];
+// Values under scale s: the 32-bit quotients x / s.  A power of two divides exactly
+// as its reciprocal multiplies (one branch for all of them: 16 divisions are more
+// than the rest of the work).
+struct Under {
+  float s, inv;
+  bool exact;
+  __device__ __forceinline__ explicit Under(float scale) : s(scale), inv(1.f / scale) {
+    exact = (__float_as_uint(s) & 0x007FFFFFu) == 0u && s > 1e-30f && s < 1e30f;
+  }
+  __device__ __forceinline__ void operator()(F16& x) const {
+    if (exact) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = pow2 ? x[i] * inv : __fdiv_rn(x[i], s);
+      for (int i = 0; i < 8; ++i) {
+        x.a[i] *= inv;
+        x.b[i] *= inv;
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {  // (rotating through the first place: one copy of the division)
+        const float a = __fdiv_rn(x.a[0], s), b = __fdiv_rn(x.b[0], s);
+#pragma unroll
+        for (int k = 0; k < 7; ++k) {
+          x.a[k] = x.a[k + 1];
+          x.b[k] = x.b[k + 1];
+        }
+        x.a[7] = a;
+        x.b[7] = b;
+      }
+    }
+  }
+};
+// Eight values as e4m3 codes: to nearest even, saturating.
+__device__ __forceinline__ uint2 codes8(const float (&y)[8]) {
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -163,30 +198,41 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, float inv,
   return make_uint2(w[0], w[1]);
 }
 
+// Four codes under a scale `by` times larger.
+__device__ __forceinline__ uint32_t rescaled(uint32_t w, float by) {
+  uint32_t y = 0;
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    const uint32_t h2 = e4m3x2_to_f16x2(static_cast<unsigned short>(w >> (16 * z)));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    y |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f.x * by, f.y * by), __NV_SATFINITE, __NV_E4M3)) << (16 * z);
+  }
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ uint4 ld16(const unsigned char* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ void st16(unsigned char* p, const uint4& w) { *reinterpret_cast<uint4*>(p) = w; }
 __device__ __forceinline__ void st8(unsigned char* p, const uint2& w) { *reinterpret_cast<uint2*>(p) = w; }
 
 }  // namespace rp
 
-// Rows of q and k rotated; POOL 1 / 2: rotated k and v also stored to the rows
-// `loc` of a bf16 / e4m3 pool.  A CTA takes p.tokens tokens of p.heads heads (of
-// the h_q + h_kv, or h_q + 2 h_kv, of a row).
-template <int D, int POOL>
-__global__ void __launch_bounds__(rp::kThreads) rope_kernel(const __grid_constant__ rp::RopeParams p) {
+// Heads [h0, h0 + nh) of rows [t0, t0 + nt): q and k rotated; POOL 1 / 2: rotated k
+// and v also stored to the rows `loc` of a bf16 / e4m3 pool.  Rows whose bit of
+// `mask` is not set are left alone.
+template <int D, int POOL, int NT>
+__device__ __forceinline__ void rotate_rows(const rp::RopeParams& p, const float2* cs, long long t0, int nt, int h0, int nh,
+                                            unsigned mask) {
   using namespace rp;
-  constexpr int CH = D / 16;              // items of a head
-  constexpr int SLOTS = kThreads / CH;    // heads in flight
-  __shared__ __align__(16) float2 cs[kMaxTokens * 128];
-  const long long t0 = static_cast<long long>(blockIdx.x) * p.tokens;
-  const int nt = static_cast<int>(min(static_cast<long long>(p.tokens), p.n - t0));
-  const int total = p.h_q + (POOL ? 2 : 1) * p.h_kv;
-  const int h0 = blockIdx.y * p.heads, nh = min(p.heads, total - h0);
-  fill_table(p, cs, t0, nt);
-  __syncthreads();
+  constexpr int CH = D / 16;            // items of a head
+  constexpr int SLOTS = NT / CH;  // heads in flight
   const int c = threadIdx.x % CH;
   for (int r = threadIdx.x / CH; r < nt * nh; r += SLOTS) {
     const int i = r / nh, h = h0 + r % nh;
+    if ((mask >> i & 1u) == 0u) continue;
     const long long t = t0 + i;
     const Item it = item_at(p, cs + i * (p.rot >> 1), c);
     const int kind = h < p.h_q ? 0 : h < p.h_q + p.h_kv ? 1 : 2;  // q, k, v
@@ -210,19 +256,12 @@ __global__ void __launch_bounds__(rp::kThreads) rope_kernel(const __grid_constan
         const long long row = index_at(p.loc, p.loc64, t);
         if (row >= 0 && row < p.pool) {
           const View& cache = kind == 1 ? p.kc : p.vc;
-          const float s = kind == 1 ? p.k_scale : p.v_scale;
           unsigned char* dst = cache.p + row * cache.s0 + hh * cache.s1;
-          const bool pow2 = is_pow2(s) && s > 1e-30f && s < 1e30f;
-          const float inv = __frcp_rn(s);
+          Under(kind == 1 ? p.k_scale : p.v_scale)(x);
           if constexpr (POOL == 2) {
-            st8(dst + it.o1, codes8(x.a, s, inv, pow2));
-            st8(dst + it.o2, codes8(x.b, s, inv, pow2));
+            st8(dst + it.o1, codes8(x.a));
+            st8(dst + it.o2, codes8(x.b));
           } else {
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              x.a[u] = pow2 ? x.a[u] * inv : __fdiv_rn(x.a[u], s);
-              x.b[u] = pow2 ? x.b[u] * inv : __fdiv_rn(x.b[u], s);
-            }
             st16(dst + 2 * it.o1, narrow(x.a));
             st16(dst + 2 * it.o2, narrow(x.b));
           }
@@ -234,22 +273,65 @@ __global__ void __launch_bounds__(rp::kThreads) rope_kernel(const __grid_constan
   }
 }
 
-// The same into a cache of e4m3 blocks.  Unit u of the grid is a block that the
-// call adds rows to (sequence after sequence); its CTAs (grid y) share its heads.
-// A warp takes K or V of one head: the largest magnitude of the new rows gives
-// the scale, a power of two, so that e4m3 loses nothing to it but at the lower
-// end of its range; if the block holds earlier rows its scale never falls, and
-// where it grows they are rounded again under the new one.
+// A CTA takes p.tokens tokens of p.heads heads (of the h_q + h_kv, or h_q + 2 h_kv,
+// of a row).
+template <int D, int POOL>
+__global__ void __launch_bounds__(rp::kThreads) rope_kernel(const __grid_constant__ rp::RopeParams p) {
+  using namespace rp;
+  __shared__ __align__(16) float2 cs[kMaxTokens * 128];
+  const long long t0 = static_cast<long long>(blockIdx.x) * p.tokens;
+  const int nt = static_cast<int>(min(static_cast<long long>(p.tokens), p.n - t0));
+  const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.h_q + (POOL ? 2 : 1) * p.h_kv - h0);
+  fill_table<kThreads>(p, cs, t0, nt);
+  __syncthreads();
+  rotate_rows<D, POOL, kThreads>(p, cs, t0, nt, h0, nh, ~0u);
+}
+
+// The same into a cache of e4m3 blocks.  p.units * p.parts of the CTAs take keys
+// and values: unit u is a block that the call adds rows to (sequence after sequence),
+// whose heads p.parts CTAs share.  p.warps warps take K or V of one head, a thread
+// 16 elements of a row, which it rotates and holds: the largest magnitude of the new
+// rows gives the scale, a power of two, so that e4m3 loses nothing to it but at the
+// lower end of its range; if the block holds earlier rows its scale never falls, and
+// where it grows they are rounded again under the new one.  Instructions bound these
+// (XXX).
+// The other CTAs take the queries as rope_kernel does: they are most of the bytes,
+// and need none of this.
 template <int D>
-__global__ void __launch_bounds__(rp::kThreads) rope_block_kernel(const __grid_constant__ rp::RopeParams p) {
+__global__ void __launch_bounds__(rp::kBlockThreads, 4) rope_block_kernel(const __grid_constant__ rp::RopeParams p) {
   using namespace rp;
   constexpr int CH = D / 16, RPI = 32 / CH;  // items of a head; rows of a warp's pass
-  constexpr int NW = kThreads / 32;
+  constexpr int NT = kBlockThreads, NW = NT / 32;
+  __shared__ unsigned tops[2][NW];
   extern __shared__ __align__(16) float2 cs_dyn[];
-  __shared__ long long scan[NW];
-  __shared__ long long found_base;
-  __shared__ int found_b;
+  __shared__ int scan[NW];
+  __shared__ int found[6];  // sequence (-1: none), its block, rows: seq's answers
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // every p.turn-th CTA is one of keys and values, as long as there are any: the two
+  // kinds run side by side, latency beside bandwidth
+  const int group_of = static_cast<int>(blockIdx.x) / p.turn, kv_ctas = p.units * p.parts;
+  const int kv = group_of * p.turn == static_cast<int>(blockIdx.x) && group_of < kv_ctas ? group_of : -1;
+  if (kv < 0) {
+    // ---- queries ----
+    const int x = static_cast<int>(blockIdx.x) - min(group_of + 1, kv_ctas), per_tile = (p.h_q + p.heads - 1) / p.heads;
+    const long long t0 = static_cast<long long>(x / per_tile) * p.tokens;
+    const int nt = static_cast<int>(min(static_cast<long long>(p.tokens), p.n - t0));
+    const int h0 = x % per_tile * p.heads;
+    if (tid == 0) tops[0][0] = 0u;
+    __syncthreads();
+    // rows that belong to a sequence
+    for (int b = tid; b < p.B; b += NT) {
+      const int a = __ldg(p.qo_ptr + b), e = __ldg(p.qo_ptr + b + 1);
+      if (a < 0 || e < a || e > p.n) continue;
+      const int from = static_cast<int>(max(a - t0, 0LL)), to = static_cast<int>(min(e - t0, static_cast<long long>(nt)));
+      if (from < to) atomicOr(&tops[0][0], ((1u << (to - from)) - 1u) << from);
+    }
+    fill_table<NT>(p, cs_dyn, t0, nt);
+    __syncthreads();
+    rotate_rows<D, 0, NT>(p, cs_dyn, t0, nt, h0, min(p.heads, p.h_q - h0), tops[0][0]);
+    return;
+  }
+  const int unit = kv / p.parts, member = kv % p.parts;
   // rows, and rows of the first block that are there already, of a sequence
   auto seq = [&](int b, int& row0, int& n, int& len, bool& held) -> int {  // its blocks
     const int a = __ldg(p.qo_ptr + b), e = __ldg(p.qo_ptr + b + 1);
@@ -258,161 +340,174 @@ __global__ void __launch_bounds__(rp::kThreads) rope_block_kernel(const __grid_c
     n = ok ? e - a : 0;
     len = __ldg(p.lens + b);
     held = len >= 0 && static_cast<long long>(len) + n <= static_cast<long long>(p.bt_cols) * p.block;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && (!ok || !held)) atomicOr(p.err, !ok ? kErrBadQoIndptr : kErrBadKvIndptr);
+    if (kv == 0 && (!ok || !held)) atomicOr(p.err, !ok ? kErrBadQoIndptr : kErrBadKvIndptr);
     if (!held) len = 0;
-    return n == 0 ? 0 : static_cast<int>((static_cast<long long>(len % p.block) + n - 1) / p.block) + 1;
+    return n == 0 ? 0 : (len % p.block + n - 1) / p.block + 1;
   };
-  if (tid == 0) found_b = -1;
+  if (tid == 0) found[0] = -1;
   int row0, n, len;
   bool held;
-  const int per = (p.B + kThreads - 1) / kThreads;
+  const int per = (p.B + NT - 1) / NT;
   const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
-  long long mine = 0;
+  int mine = 0;
   for (int b = lo; b < hi; ++b) mine += seq(b, row0, n, len, held);
-  long long incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  long long at = incl - mine;
-  for (int w = 0; w < warp; ++w) at += scan[w];
-  const long long unit = blockIdx.x;
-  if (unit >= at && unit < at + mine) {
+  int at0 = incl - mine;
+  for (int w = 0; w < warp; ++w) at0 += scan[w];
+  if (unit >= at0 && unit < at0 + mine) {
     for (int b = lo; b < hi; ++b) {
-      const int k = seq(b, row0, n, len, held);
-      if (unit < at + k) {
-        found_b = b;
-        found_base = unit - at;
+      const int k = per > 1 ? seq(b, row0, n, len, held) : mine;
+      if (unit < at0 + k) {
+        found[0] = b;
+        found[1] = unit - at0;
+        found[2] = row0;
+        found[3] = n;
+        found[4] = len;
+        found[5] = held;
         break;
       }
-      at += k;
+      at0 += k;
     }
   }
   __syncthreads();
-  if (found_b < 0) return;  // uniform: fewer blocks than the host allowed for
-  const int b = found_b;
-  seq(b, row0, n, len, held);
+  const int b = found[0], found_base = found[1];
+  if (b < 0) return;  // uniform: fewer blocks than the host allowed for
+  row0 = found[2];
+  n = found[3];
+  len = found[4];
+  held = found[5] != 0;
   // block `found_base` of the sequence's new ones: rows [off, off + nt) of it
-  const long long head = found_base * p.block - len % p.block;  // new rows before the block (negative: none)
+  const long long head = static_cast<long long>(found_base) * p.block - len % p.block;  // new rows before it (negative: none)
   const int off = head < 0 ? static_cast<int>(-head) : 0;
-  const long long done = head < 0 ? 0 : head;
-  const int nt = static_cast<int>(min(static_cast<long long>(p.block - off), n - done));
+  const int done = head < 0 ? 0 : static_cast<int>(head);
+  const int nt = min(p.block - off, n - done);
   const long long t0 = row0 + done;
-  long long page = -1;
-  if (held) {
-    const long long col = len / p.block + found_base;
-    page = __ldg(p.bt + b * p.bt_s0 + col);
-    if (page < 0 || page >= p.n_blocks) {
-      page = -1;
-      if (tid == 0 && blockIdx.y == 0) atomicOr(p.err, kErrBadIndex);
-    }
-  }
-  fill_table(p, cs_dyn, t0, nt);
-  __syncthreads();
+  const int found_page = held ? __ldg(p.bt + b * p.bt_s0 + len / p.block + found_base) : -1;  // asked for, not waited for
   const int pairs = p.rot >> 1;
-  const int c = lane % CH, sub = lane / CH;
-  // ---- keys and values: a warp per (head, K or V) ----
-  for (int task = blockIdx.y * NW + warp; task < 2 * p.h_kv; task += NW * gridDim.y) {
+  const int c = lane % CH;
+  const Item it = item_at(p, cs_dyn, c);
+  const int wt = p.warps, groups = NW / wt, group = warp / wt, part = warp % wt, step = groups * p.parts;
+  // this thread's row of the new ones, and again `chunk` rows on (more rows than the
+  // warps hold are read twice)
+  const int first = part * RPI + lane / CH, chunk = wt * RPI;
+  const int last = (nt - 1) / chunk * chunk;
+  int task = member * groups + group;
+  uint4 n1, n2;  // the next task's row
+  float next_old = 0.f;
+  auto fetch = [&](int which, int at, uint4& a, uint4& b2) {
+    const View& in = which & 1 ? p.v : p.k;
+    a = b2 = make_uint4(0u, 0u, 0u, 0u);
+    if (at + first < nt) {
+      const unsigned char* src = in.p + (t0 + at + first) * in.s0 + (which >> 1) * in.s1;
+      a = ld16(src + 2 * it.o1);
+      b2 = ld16(src + 2 * it.o2);
+    }
+  };
+  auto scale_of = [&](long long page, int which) -> float* {
+    return (which & 1 ? p.vs + page * p.vs_s0 : p.ks + page * p.ks_s0) + (which >> 1);
+  };
+  if (task < 2 * p.h_kv) fetch(task, 0, n1, n2);
+  fill_table<NT>(p, cs_dyn, t0, nt);  // while the first loads are on their way
+  const long long page = found_page >= 0 && found_page < p.n_blocks ? found_page : -1;
+  if (held && page < 0 && tid == 0 && member == 0) atomicOr(p.err, kErrBadIndex);
+  const bool grows = page >= 0 && off > 0;
+  if (grows && task < 2 * p.h_kv) next_old = *scale_of(page, task);
+  __syncthreads();
+  int turn_of = 0;
+  for (; task < 2 * p.h_kv; task += step, turn_of ^= 1) {
     const int h = task >> 1;
     const bool isv = task & 1;
-    const View& in = isv ? p.v : p.k;
-    const View& cache = isv ? p.vc : p.kc;
-    const unsigned char* src = in.p + t0 * in.s0 + h * in.s1;
-    auto load = [&](int i, Item& it, F16& x) {
-      it = item_at(p, cs_dyn + i * pairs, c);
-      const unsigned char* r = src + i * in.s0;
-      widen(ld16(r + 2 * it.o1), x.a);
-      widen(ld16(r + 2 * it.o2), x.b);
-      if (!isv) rotate(p, it.cs, x);
+    const float old = next_old;
+    F16 x;
+    auto take = [&](int at, const uint4& a, const uint4& b2) {
+      widen(a, x.a);
+      widen(b2, x.b);
+      if (!isv && it.cs && at + first < nt) rotate(p, it.cs + (at + first) * pairs, x);
     };
-    float s = 1.f, old = 1.f;
+    take(0, n1, n2);
+    if (task + step < 2 * p.h_kv) {  // while this one is worked on
+      fetch(task + step, 0, n1, n2);
+      if (grows) next_old = *scale_of(page, task + step);
+    }
+    float s = 1.f;
     if (page >= 0) {
-      float top = 0.f;  // of the finite values
-      for (int i = sub; i < nt; i += RPI) {
-        Item it;
-        F16 x;
-        load(i, it, x);
+      unsigned most = 0;  // bits of the largest finite magnitude
+      for (int at = 0;;) {
+        float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float a = fabsf(x.a[u]), d = fabsf(x.b[u]);
-          top = fmaxf(top, a < INFINITY ? a : 0.f);
-          top = fmaxf(top, d < INFINITY ? d : 0.f);
-        }
-      }
+        for (int e = 0; e < 8; ++e) m[e & 3] = max3(m[e & 3], fabsf(x.a[e]), fabsf(x.b[e]));
+        unsigned top = __float_as_uint(max3(max3(m[0], m[1], m[2]), m[3], 0.f));
+        if (top >= 0x7F800000u) {  // rare: infinities and NaN do not count
+          top = 0;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // the smallest 2^e with top <= 448 2^e = 1.75 2^(8 + e)
-      const unsigned bits = __float_as_uint(top);
-      int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x007FFFFFu) > 0x00600000u ? 1 : 0);
-      e = max(kMinExp, min(kMaxExp, e));
-      const float need = __int_as_float((127 + e) << 23);
-      float* sp = (isv ? p.vs + page * p.vs_s0 : p.ks + page * p.ks_s0) + h;
-      if (off > 0) {
-        old = *sp;
-        s = fmaxf(old, need);
-      } else {
-        s = need;
-      }
-      if (off > 0 && s != old) {
-        const float by = __fdiv_rn(old, s);
-        for (int i = sub; i < off; i += RPI) {
-          unsigned char* r = cache.p + (page * p.block + i) * cache.s0 + h * cache.s1 + 16 * c;
-          const uint4 w = ld16(r);
-          const uint32_t in4[4] = {w.x, w.y, w.z, w.w};
-          uint32_t out4[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t y = 0;
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t h2 = e4m3x2_to_f16x2(static_cast<unsigned short>(in4[u] >> (16 * z)));
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-              y |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f.x * by, f.y * by), __NV_SATFINITE, __NV_E4M3))
-                   << (16 * z);
-            }
-            out4[u] = y;
+          for (int e = 0; e < 8; ++e) {
+            const unsigned a = __float_as_uint(x.a[e]) & 0x7FFFFFFFu, d = __float_as_uint(x.b[e]) & 0x7FFFFFFFu;
+            top = max(top, max(a < 0x7F800000u ? a : 0u, d < 0x7F800000u ? d : 0u));
           }
-          st16(r, make_uint4(out4[0], out4[1], out4[2], out4[3]));
+        }
+        most = max(most, top);
+        if (at == last) break;
+        at += chunk;
+        uint4 a, b2;
+        fetch(task, at, a, b2);
+        take(at, a, b2);
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (wt > 1) {
+        if (lane == 0) tops[turn_of][warp] = most;
+        named_bar_sync(1 + group, 32 * wt);  // (everyone has read the old scale, too)
+        most = __reduce_max_sync(0xffffffffu, tops[turn_of][group * wt + (lane & (wt - 1))]);
+      }
+      // the smallest 2^e with the maximum <= 448 2^e = 1.75 2^(8 + e)
+      int e = static_cast<int>(most >> 23) - 127 - 8 + ((most & 0x007FFFFFu) > 0x00600000u ? 1 : 0);
+      e = max(kMinExp, min(kMaxExp, e));
+      s = __int_as_float((127 + e) << 23);
+      if (off > 0) {
+        s = fmaxf(old, s);
+        if (s != old) {
+          const View& cache = isv ? p.vc : p.kc;
+          const float by = __fdiv_rn(old, s);
+          for (int i = first; i < off; i += chunk) {
+            unsigned char* r = cache.p + (page * p.block + i) * cache.s0 + h * cache.s1 + 16 * c;
+            const uint4 w = ld16(r);
+            st16(r, make_uint4(rescaled(w.x, by), rescaled(w.y, by), rescaled(w.z, by), rescaled(w.w, by)));
+          }
         }
       }
       __syncwarp();  // every lane has read the old scale
-      if (lane == 0) *sp = s;
+      if (part == 0 && lane == 0) *scale_of(page, task) = s;
     }
-    if (page < 0 && (isv || p.ko.p == nullptr)) continue;
-    const bool pow2 = is_pow2(s);
-    const float inv = __frcp_rn(s);
-    for (int i = sub; i < nt; i += RPI) {
-      Item it;
-      F16 x;
-      load(i, it, x);
-      if (!isv && p.ko.p) {
-        unsigned char* dst = p.ko.p + (t0 + i) * p.ko.s0 + h * p.ko.s1;
-        st16(dst + 2 * it.o1, narrow(x.a));
-        st16(dst + 2 * it.o2, narrow(x.b));
+    const Under under(s);
+    // (with a block the last rows are in hand, without one the first)
+    for (int at = page >= 0 ? last : 0;;) {
+      const int i = at + first;
+      if (i < nt) {
+        if (!isv && p.ko.p) {
+          unsigned char* dst = p.ko.p + (t0 + i) * p.ko.s0 + h * p.ko.s1;
+          st16(dst + 2 * it.o1, narrow(x.a));
+          st16(dst + 2 * it.o2, narrow(x.b));
+        }
+        if (page >= 0) {
+          const View& cache = isv ? p.vc : p.kc;
+          unsigned char* dst = cache.p + (page * p.block + off + i) * cache.s0 + h * cache.s1;
+          under(x);
+          st8(dst + it.o1, codes8(x.a));
+          st8(dst + it.o2, codes8(x.b));
+        }
       }
-      if (page >= 0) {
-        unsigned char* dst = cache.p + (page * p.block + off + i) * cache.s0 + h * cache.s1;
-        st8(dst + it.o1, codes8(x.a, s, inv, pow2));
-        st8(dst + it.o2, codes8(x.b, s, inv, pow2));
-      }
+      at = page >= 0 ? at - chunk : at + chunk;
+      if (at < 0 || at >= nt) break;
+      uint4 a, b2;
+      fetch(task, at, a, b2);
+      take(at, a, b2);
     }
-  }
-  // ---- queries ----
-  const int slots = kThreads / CH * gridDim.y;
-  for (int r = (blockIdx.y * kThreads + tid) / CH; r < nt * p.h_q; r += slots) {
-    const int i = r / p.h_q, h = r % p.h_q;
-    const Item it = item_at(p, cs_dyn + i * pairs, tid % CH);
-    const unsigned char* src = p.q.p + (t0 + i) * p.q.s0 + h * p.q.s1;
-    F16 x;
-    widen(ld16(src + 2 * it.o1), x.a);
-    widen(ld16(src + 2 * it.o2), x.b);
-    rotate(p, it.cs, x);
-    unsigned char* dst = p.qo.p + (t0 + i) * p.qo.s0 + h * p.qo.s1;
-    st16(dst + 2 * it.o1, narrow(x.a));
-    st16(dst + 2 * it.o2, narrow(x.b));
   }
 }
 

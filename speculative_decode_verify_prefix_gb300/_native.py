@@ -2,9 +2,10 @@
 
 The library is compiled from ``csrc/*.cu`` with nvcc into ``_build/`` next to
 this file: every translation unit (the host side, and the kernels of each
-head_dim) in parallel, then linked into one shared library.  Loading never
-falls back to anything: if the library is missing or fails to load, callers
-get an exception.
+head_dim) in parallel, then linked into one shared library.  ``csrc/views.cpp``
+becomes the extension module that packs the views of a call's tensors.  Loading
+never falls back to anything: if the library or the module is missing or fails to
+load, callers get an exception.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import ctypes
 import os
 import platform
 import subprocess
+import sysconfig
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,8 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "verify_splitkv.h")
 BUILD_DIR = os.path.join(_HERE, "_build")
 OBJ_DIR = os.path.join(BUILD_DIR, f"obj_{platform.machine()}")
 LIB_PATH = os.path.join(BUILD_DIR, f"libverify_splitkv_{platform.machine()}.so")
+VIEWS_SRC = os.path.join(CSRC, "views.cpp")
+VIEWS_PATH = os.path.join(BUILD_DIR, f"vsk_views_{platform.machine()}.so")
 NVCC_ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [*NVCC_ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC"]
 
@@ -39,6 +43,42 @@ def build(force: bool = False, verbose: bool = False) -> str:
     from concurrent.futures import ThreadPoolExecutor
 
     os.makedirs(OBJ_DIR, exist_ok=True)
+    with ThreadPoolExecutor(1) as ex:
+        views = ex.submit(_build_views, force)
+        path = _build_lib(force, verbose)
+        views.result()
+    return path
+
+
+def _build_views(force: bool) -> None:
+    """The views module, with the host compiler, against the torch that runs it."""
+    import torch
+
+    stamp = VIEWS_PATH + ".torch"  # the version it was built against
+    if not force and os.path.exists(VIEWS_PATH) and os.path.exists(stamp):
+        with open(stamp) as f:
+            same = f.read() == torch.__version__
+        if same and os.path.getmtime(VIEWS_PATH) >= max(os.path.getmtime(VIEWS_SRC), os.path.getmtime(HEADER)):
+            return
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+    lib = os.path.join(root, "lib")
+    tmp = VIEWS_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{p}" for p in inc], VIEWS_SRC, "-o", tmp,
+           f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on views.cpp:\n{r.stderr}")
+    os.replace(tmp, VIEWS_PATH)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
+    from concurrent.futures import ThreadPoolExecutor
+
     headers = [HEADER] + [os.path.join(CSRC, n) for n in os.listdir(CSRC) if n.endswith(".cuh")]
     newest_header = max(os.path.getmtime(h) for h in headers)
     if not force and os.path.exists(LIB_PATH):
@@ -190,6 +230,28 @@ def lib():
                         "(there is no CPU fallback)")
                 _lib = _bind(ctypes.CDLL(LIB_PATH))
     return _lib
+
+
+_views = None
+
+
+def views():
+    """The function of the views module; raises if it was not built."""
+    global _views
+    if _views is None:
+        with _lock:
+            if _views is None:
+                if not os.path.exists(VIEWS_PATH):
+                    raise RuntimeError(f"module {VIEWS_PATH} is missing: run __graft_entry__.build()")
+                import torch  # noqa: F401  (its libraries, before the module that needs them)
+                from importlib.machinery import ExtensionFileLoader
+                from importlib.util import module_from_spec, spec_from_loader
+
+                spec = spec_from_loader("vsk_views", ExtensionFileLoader("vsk_views", VIEWS_PATH))
+                module = module_from_spec(spec)
+                spec.loader.exec_module(module)
+                _views = module.views
+    return _views
 
 
 def last_error() -> str:

@@ -15,60 +15,12 @@ a call that is captured into a graph needs its own.
 """
 from __future__ import annotations
 
-import ctypes
 import functools
-import struct
 
 import torch
 
 from . import _native
-from .api import _DT, _SHARED_SIZE as _SIZES, _WS, _WS_LOCK, _coerce
-
-# A vsk_tensor: data, dtype, ndim, shape[3], stride[3].  The views of a call are
-# packed into one buffer: a fraction of the time of filling a ctypes structure
-# per tensor.
-_VIEW = struct.Struct("Pii6q")
-assert _VIEW.size == ctypes.sizeof(_native.VskTensor)
-
-
-_ARENA = {n: ctypes.c_char * (_VIEW.size * n) for n in range(1, 16)}
-_pack, _SIZE, _code = _VIEW.pack_into, _VIEW.size, _DT.get
-
-
-def _views(names, tensors):
-    """The packed views of a call's tensors (None stays None) and their
-    addresses; all tensors must be on one CUDA device, which is returned."""
-    buf = _ARENA[len(tensors)]()
-    at = ctypes.addressof(buf)
-    device, args, off = -1, [], 0
-    for t in tensors:
-        if t is None:
-            args.append(None)
-            continue
-        try:
-            dev, shape, stride = t.get_device(), t.shape, t.stride()
-        except AttributeError:
-            dev = -1
-        if dev != device or dev < 0:
-            name = names[len(args)]
-            if dev < 0:
-                raise ValueError(f"{name} must be a CUDA tensor")
-            if device >= 0:
-                raise ValueError(f"{name} is on cuda:{dev}, the call's other tensors on cuda:{device}")
-            device = dev
-        n = len(shape)
-        if n == 3:
-            _pack(buf, off, t.data_ptr(), _code(t.dtype, -1), 3, *shape, *stride)
-        elif n == 1:
-            _pack(buf, off, t.data_ptr(), _code(t.dtype, -1), 1, shape[0], 0, 0, stride[0], 0, 0)
-        else:
-            _pack(buf, off, t.data_ptr(), _code(t.dtype, -1), n, *(*shape, 0, 0, 0)[:3], *(*stride, 0, 0, 0)[:3])
-        args.append(at + off)
-        off += _SIZE
-    if device < 0:
-        raise ValueError(f"{names[0]} must be a CUDA tensor")
-    return device, buf, args
-
+from .api import _SHARED_SIZE as _SIZES, _WS, _WS_LOCK, _coerce
 
 @functools.lru_cache(maxsize=None)
 def _device(index):
@@ -102,8 +54,8 @@ def _run(name, names, tensors, scalars, stream, workspace, need=None, scalars_at
     ``scalars_at`` tensors; None: after all), then workspace, its bytes and the
     stream, with the tensors' device current.  ``need``: workspace bytes (None:
     the error word; 0: the entry point takes none)."""
-    device, buf, args = _views(names, tensors)
-    if device != torch.cuda.current_device():
+    device, buf, args = (_native._views or _native.views())(names, tensors)  # buf: the views' memory
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _run(name, names, tensors, scalars, stream, workspace, need, scalars_at)
     raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream

@@ -870,3 +870,24 @@ def test_append_and_verify_over_a_pool(vsk):
     s = s.masked_fill(~torch.ones(l_ext, n + l_ext, dtype=torch.bool, device=DEV).tril(n), -math.inf)
     want = torch.einsum("hij,jhd->ihd", torch.softmax(s, 2), vals.repeat_interleave(hq // hk, 1))
     assert float((o.to(F64) - want).abs().max()) < 0.02
+
+
+# ---------------------------------------------------------------- the binding
+
+def test_binding_names_what_is_no_dense_cuda_tensor(vsk):
+    q, k = (torch.zeros(2, 1, 64, dtype=BF16, device=DEV) for _ in "qk")
+    pos, f = ints([0, 1]), frequencies(64)
+    with pytest.raises(ValueError, match="k must be a CUDA tensor"):
+        vsk.rope_fwd(q, k.cpu(), q, k, pos, f)
+    with pytest.raises(ValueError, match="positions must be a CUDA tensor"):
+        vsk.rope_fwd(q, k, q, k, [0, 1], f)
+    with pytest.raises(ValueError, match="strided"):
+        vsk.rope_fwd(q, k, q, k, pos.to_sparse(), f)
+    with pytest.raises(ValueError, match="inv_freq must be float32"):
+        vsk.rope_fwd(q, k, q, k, pos, f.double())
+    with pytest.raises(ValueError, match="3-d"):
+        vsk.rope_fwd(q[None], k, q, k, pos, f)
+    # a scalar, an empty and a five-dimensional tensor are told apart from what is wanted
+    for bad in (torch.zeros((), device=DEV, dtype=BF16), torch.zeros(0, device=DEV, dtype=BF16), q[None, None]):
+        with pytest.raises(ValueError, match="3-d"):
+            vsk.rope_fwd(bad, k, q, k, pos, f)

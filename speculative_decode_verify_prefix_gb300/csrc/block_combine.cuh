@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
   using namespace bk;
   constexpr int E = D / 32;  // columns of a lane
   constexpr int ROWS = SPLIT ? 1 : 4;  // rows of a CTA
-  __shared__ long long scan[8];
+  __shared__ int scan[8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per_seg = (p.R + ROWS - 1) / ROWS;
   const long long seg = blockIdx.x / per_seg;
@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
   const int b = static_cast<int>(seg / p.h_kv), h = static_cast<int>(seg - static_cast<long long>(b) * p.h_kv);
   const float NEG_INF = -INFINITY;
 
-  long long all = 0, before = 0;
+  int all = 0, before = 0;
   for (int i = tid; i < p.B; i += 128) {
     int P;
     prefix_len(p, i, P);
@@ -121,15 +121,14 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
   }
 
   // ---- pieces: those of the stream's cut ----
-  const long long total = (scan[0] + scan[1] + scan[2] + scan[3]) * p.n_hg;
-  const long long off = (scan[4] + scan[5] + scan[6] + scan[7]) * p.n_hg + static_cast<long long>(h / p.team) * T;
-  const long long W = share_of(p, total);
-  const long long c0 = off / W;
-  const int all_pieces = static_cast<int>((off + T - 1) / W - c0) + 1;
+  const int total = (scan[0] + scan[1] + scan[2] + scan[3]) * p.n_hg;
+  const int off = (scan[4] + scan[5] + scan[6] + scan[7]) * p.n_hg + h / p.team * T;
+  const int W = share_of(p, total);
+  const int c0 = off / W, all_pieces = (off + T - 1) / W - c0 + 1;
   constexpr int PARTS = SPLIT ? 4 : 1;
   const int pieces = SPLIT ? (all_pieces - warp + PARTS - 1) / PARTS : all_pieces;  // warp, warp + 4, ...
   // piece i: CTA (c0 + i) team + h % team of the stream
-  const long long slot = c0 * p.team + static_cast<long long>(b) * p.h_kv + h;
+  const long long slot = static_cast<long long>(c0) * p.team + static_cast<long long>(b) * p.h_kv + h;
   const long long step = static_cast<long long>(p.team) * p.rows * PARTS;
   const long long at0 = (slot + (SPLIT ? warp * p.team : 0)) * p.rows + row;
   const float* lse = p.plse + at0;

@@ -528,7 +528,10 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   // teams over segments: a segment's pieces, about
   int team = 8;
   while (h_kv % team != 0) --team;
-  const bool split = n_cta / team > kSplitJoin * B * (h_kv / team);
+  const long long tiles = w.rows / bk::row_tile(static_cast<int>(R)), n_team = std::max(1LL, n_cta / (team * tiles));
+  const bool split = n_team > kSplitJoin * B * (h_kv / team);
+  if (B * (h_kv / team) * ((bt->shape[1] * block_size - 1) / bk::KT + 1) > INT_MAX / 2)
+    return fail("%lld sequences of up to %lld blocks are too many", B, static_cast<long long>(bt->shape[1]));
   const long long joins = B * h_kv * (split ? R : (R + 3) / 4);
   if (joins > INT_MAX) return fail("grid of %lld CTAs too large", joins);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -571,7 +574,8 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   p.w_min = 1;
   p.team = team;
   p.n_hg = p.h_kv / p.team;
-  p.n_team = static_cast<int>(n_cta) / p.team;
+  p.n_team = static_cast<int>(n_team);
+  p.tiles = static_cast<int>(tiles);
   if (cm) {
     p.cmask = static_cast<const unsigned char*>(cm->data);
     p.n_mask = cm->shape[0];
@@ -591,8 +595,7 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   if (!allow_smem(reinterpret_cast<const void*>(f.stream), f.smem)) return 0;
   void* args[] = {&p, &maps[0], &maps[1]};
   cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void*>(f.stream),
-                                   dim3(static_cast<unsigned>(p.n_team * p.team), static_cast<unsigned>(w.rows / bk::row_tile(p.R))),
-                                   dim3(bk::kThreads), args, f.smem, st);
+                                   dim3(static_cast<unsigned>(n_team * team * tiles)), dim3(bk::kThreads), args, f.smem, st);
   if (e != cudaSuccess) return fail("kernel launch failed: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[1];

@@ -27,7 +27,8 @@
 //   warp 5     tensor memory, MMAs.
 // Up to eight KV heads are taken by a team of as many CTAs, each its own over the
 // same keys: what lies side by side in memory is read at about the same time (8
-// heads of 128: XXX).  The groups of 16 keys of all (sequence, head group) segments
+// heads of 128: XXX).  More than 32 packed rows are row tiles, a CTA each beside the
+// others: the keys come from memory once (64 rows: XXX).  The groups of 16 keys of all (sequence, head group) segments
 // are laid end to end and every team takes an equal share; a segment's part of a
 // share is a piece, whose partial (o, log2 of its sum) block_combine_kernel folds:
 // of CTA c and segment s, slot c + team * s.
@@ -77,7 +78,8 @@ struct BkParams {
   int B, L, gq, R, h_kv, rows;  // rows: of a partial (RT row tiles of 32)
   float scale2;         // softmax scale in base 2
   int w_min;            // tiles of a share at least
-  int team, n_hg, n_team;  // CTAs of a team, h_kv / team, teams
+  int team, n_hg, n_team;  // KV heads of a team, h_kv / team, teams
+  int tiles;               // row tiles: CTAs of a head in a team
   const unsigned char* cmask;
   const void* mindptr;
   int mindptr64;
@@ -141,9 +143,6 @@ static_assert(kAbortOff + 4 <= kQscOff && kRedOff + 512 <= kSumOff && kSumOff + 
               "control block");
 
 // Segments and their cut, the same in both kernels.
-struct Cut {
-  long long total, W;
-};
 __device__ __forceinline__ bool prefix_len(const BkParams& p, int b, int& P) {
   const int n = __ldg(p.lens + b);
   const bool ok = n >= 0 && static_cast<long long>(n) <= static_cast<long long>(p.bt_cols) * p.block;
@@ -151,12 +150,12 @@ __device__ __forceinline__ bool prefix_len(const BkParams& p, int b, int& P) {
   return ok;
 }
 __device__ __forceinline__ int seg_tiles(int P) { return P > 0 ? (P - 1) / KT + 1 : 1; }
-__device__ __forceinline__ long long share_of(const BkParams& p, long long total) {
-  return max((total + p.n_team - 1) / p.n_team, static_cast<long long>(p.w_min));
+__device__ __forceinline__ int share_of(const BkParams& p, int total) {  // (the host bounds the total)
+  return max((total - 1) / p.n_team + 1, p.w_min);
 }
 struct BSeg {
   int b, h, P, T;  // h: this CTA's head of the head group; T: tiles
-  long long off;   // its first tile among all
+  int off;         // its first tile among all
 };
 __device__ __forceinline__ void seg_load(const BkParams& p, BSeg& s) {
   prefix_len(p, s.b, s.P);
@@ -172,49 +171,48 @@ __device__ __forceinline__ void seg_next(const BkParams& p, BSeg& s) {
 }
 // The groups [g0, ge) of a segment's share, from a whole tile on; empty where the
 // prefix is.
-__device__ __forceinline__ void piece_of(const BSeg& s, long long start, long long end, int& g0, int& ge) {
-  g0 = static_cast<int>(max(start, s.off) - s.off) * GT;
-  ge = static_cast<int>(min((static_cast<long long>(s.P) + GK - 1) / GK, (end - s.off) * GT));
+__device__ __forceinline__ void piece_of(const BSeg& s, int start, int end, int& g0, int& ge) {
+  g0 = (max(start, s.off) - s.off) * GT;
+  ge = static_cast<int>(min((static_cast<long long>(s.P) + GK - 1) / GK, static_cast<long long>(end - s.off) * GT));
 }
 
 // The CTA's share [start, end) of the tiles and the segment it begins in; all
 // threads call it.  False: nothing to do.
-__device__ __forceinline__ bool my_share(const BkParams& p, unsigned char* smem, long long& start, long long& end, BSeg& s) {
-  long long* scan = reinterpret_cast<long long*>(smem + kScanOff);
-  volatile long long* base = scan + 8;
-  volatile int* found = reinterpret_cast<volatile int*>(scan + 9);
+__device__ __forceinline__ bool my_share(const BkParams& p, unsigned char* smem, int& start, int& end, BSeg& s) {
+  int* scan = reinterpret_cast<int*>(smem + kScanOff);
+  volatile int* found = scan + 8;  // sequence, its length, its first tile
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int NW = kThreads / 32;
   if (tid == 0) *found = -1;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
-  long long mine = 0;
+  int mine = 0;
   bool bad = false;
   int P = 0;  // the only one where a thread has one sequence: not loaded twice
   for (int b = lo; b < hi; ++b) {
     bad |= !prefix_len(p, b, P);
     mine += seg_tiles(P);
   }
-  if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrBadKvIndptr);
-  long long incl = mine;
+  if (bad && blockIdx.x == 0) atomicOr(p.err, kErrBadKvIndptr);
+  int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  long long at = incl - mine, all = 0;
+  int at = incl - mine, all = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
     if (w < warp) at += scan[w];
     all += scan[w];
   }
-  const long long total = all * p.n_hg, W = share_of(p, total);
-  const int member = static_cast<int>(blockIdx.x) % p.team;
-  start = static_cast<long long>(blockIdx.x) / p.team * W;
-  if (start >= total) return false;  // uniform
-  end = min(total, start + W);
+  const int total = all * p.n_hg, W = share_of(p, total);
+  const int cta = static_cast<int>(blockIdx.x) / p.tiles, member = cta % p.team;
+  if (static_cast<long long>(cta / p.team) * W >= total) return false;  // uniform
+  start = cta / p.team * W;
+  end = static_cast<int>(min(static_cast<long long>(total), static_cast<long long>(start) + W));
   if (start >= at * p.n_hg && start < (at + mine) * p.n_hg) {
     for (int b = lo; b < hi; ++b) {
       if (per > 1) prefix_len(p, b, P);
@@ -222,7 +220,7 @@ __device__ __forceinline__ bool my_share(const BkParams& p, unsigned char* smem,
       if (start < (at + T) * p.n_hg) {
         found[0] = b;
         found[1] = P;
-        *base = at * p.n_hg;
+        found[2] = at * p.n_hg;
         break;
       }
       at += T;
@@ -233,9 +231,9 @@ __device__ __forceinline__ bool my_share(const BkParams& p, unsigned char* smem,
   if (s.b < 0) return false;  // not reached: guards the walk
   s.P = found[1];
   s.T = seg_tiles(s.P);
-  const long long hg = (start - *base) / s.T;
-  s.h = static_cast<int>(hg) * p.team + member;
-  s.off = *base + hg * s.T;
+  const int hg = (start - found[2]) / s.T;
+  s.h = hg * p.team + member;
+  s.off = found[2] + hg * s.T;
   return true;
 }
 
@@ -244,7 +242,7 @@ struct BatchIt {
   BSeg s;
   int g, ge;
   bool valid;
-  __device__ __forceinline__ void settle(const BkParams& p, long long start, long long end) {
+  __device__ __forceinline__ void settle(const BkParams& p, int start, int end) {
     while (g >= ge) {
       seg_next(p, s);
       if (s.b >= p.B || s.off >= end) {
@@ -254,13 +252,13 @@ struct BatchIt {
       piece_of(s, start, end, g, ge);
     }
   }
-  __device__ __forceinline__ void first(const BkParams& p, const BSeg& s0, long long start, long long end) {
+  __device__ __forceinline__ void first(const BkParams& p, const BSeg& s0, int start, int end) {
     s = s0;
     valid = true;
     piece_of(s, start, end, g, ge);
     settle(p, start, end);
   }
-  __device__ __forceinline__ void next(const BkParams& p, long long start, long long end) {
+  __device__ __forceinline__ void next(const BkParams& p, int start, int end) {
     g += 32;
     settle(p, start, end);
   }
@@ -282,6 +280,12 @@ __device__ __forceinline__ bool wait_both(uint32_t a, uint32_t pa, uint32_t b, u
 __device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// The top 4 significant bits of y where e4m3 has them all (2^-6 and above), else 0.
+__device__ __forceinline__ float top_bits(float y) {
+  uint32_t there;
+  asm("set.geu.u32.f32 %0, %1, 0f3C800000;" : "=r"(there) : "f"(y));  // (unordered: NaN stays NaN)
+  return __uint_as_float(__float_as_uint(y) & 0xFFF00000u & there);
+}
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
@@ -302,7 +306,7 @@ struct Rows {
     const long long first = ok ? a : static_cast<long long>(s.b) * p.L;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int r = static_cast<int>(blockIdx.y) * NR + J * warp + j;
+      const int r = static_cast<int>(blockIdx.x) % p.tiles * NR + J * warp + j;
       const bool live = r < p.R;
       const int rr = live ? r : 0;
       const __nv_bfloat16* src = p.q + (first + rr / p.gq) * p.q_s0 + static_cast<long long>(s.h * p.gq + rr % p.gq) * p.q_s1;
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
   constexpr int NK = G::NK, NV = G::NV, CB = G::CB, ENT = G::ENT, NP = G::NP;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  long long start, end;
+  int start, end;
   BSeg seg0;
   if (!my_share(p, smem, start, end, seg0)) return;  // uniform
   if ((smem_u32(smem) & 1023u) != 0u) {  // the swizzled layouts need it; dynamic shared memory starts so
@@ -647,8 +651,8 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
     for (; s.b < p.B && s.off < end; seg_next(p, s)) {
       int g0, ge;
       piece_of(s, start, end, g0, ge);
-      const long long slot = blockIdx.x + static_cast<long long>(s.b) * p.h_kv + s.h / p.team * p.team;
-      const int row0 = static_cast<int>(blockIdx.y) * NR;
+      const long long slot = static_cast<int>(blockIdx.x) / p.tiles + static_cast<long long>(s.b) * p.h_kv + s.h / p.team * p.team;
+      const int row0 = static_cast<int>(blockIdx.x) % p.tiles * NR;
       float* lse_p = p.plse + slot * p.rows + row0;
       float* o_p = p.po + (slot * p.rows + row0) * D;
       const int live = min(NR, p.R - row0);
@@ -700,17 +704,22 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
 #pragma unroll
         for (int h = 0; h < NG; ++h) me[h] = mt[h];
 #pragma unroll
-        for (int i = 0; i < KN; ++i) x[i] = fmaf(x[i], qsc * me[i / GK].x, me[i / GK].y);
+        for (int i = 0; i < KN; i += 2) {
+          const float c = qsc * me[i / GK].x;
+          const float2 y = fa::fma2(make_float2(x[i], x[i + 1]), make_float2(c, c), make_float2(me[i / GK].y, me[i / GK].y));
+          x[i] = y.x;
+          x[i + 1] = y.y;
+        }
         const bool lacks = __float_as_int(me[0].w) >= 256;
         if (lacks) {
 #pragma unroll
           for (int i = 0; i < KN; ++i)
             if ((key0 & (GK - 1)) + (i & (GK - 1)) >= (__float_as_int(me[i / GK].w) & 255)) x[i] = NEG_INF;
         }
-        float t4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+        float t2[2] = {NEG_INF, NEG_INF};
 #pragma unroll
-        for (int i = 0; i < KN; ++i) t4[i & 3] = fmaxf(t4[i & 3], x[i]);
-        float tm = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        for (int i = 0; i < KN; i += 2) t2[i >> 1 & 1] = fa::max3(t2[i >> 1 & 1], x[i], x[i + 1]);
+        float tm = fmaxf(t2[0], t2[1]);
         // The reference stays while no row of the tile passes it by 2^kThr.
         if (g == g0 || tc::bar_red_or(1, kSm, tm > m + kThr)) {  // alike in the four warps
 #pragma unroll
@@ -741,29 +750,30 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
         const bool is_free = u < NP || tr::test(bar(kBPEmpty + u % NP), ((u / NP) & 1u) ^ 1u);
         const float up = m == NEG_INF ? 0.f : static_cast<float>(kUp) - m;
         uint32_t w[3][KN / 4];
-        float sum[NG];
+        float2 sum[NG];
 #pragma unroll
-        for (int h = 0; h < NG; ++h) sum[h] = 0.f;
+        for (int h = 0; h < NG; ++h) sum[h] = make_float2(0.f, 0.f);
+        const float2 up2 = make_float2(up, up), k16 = make_float2(16.f, 16.f), zero = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < KN / 4; ++i) {
-          float t[3][4];
+          float2 t[3][2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y = fast_exp2(x[4 * i + e] + up);
-            sum[i / 4] += y;
-            // the top 4 bits where e4m3 has them all (2^-6 and above), and what they leave
-            const float a = y < 0.015625f ? 0.f : __uint_as_float(__float_as_uint(y) & 0xFFF00000u);
-            const float z = (y - a) * 16.f;
-            const float b = z < 0.015625f ? 0.f : __uint_as_float(__float_as_uint(z) & 0xFFF00000u);
+          for (int e = 0; e < 2; ++e) {
+            const float2 z = fa::add2(make_float2(x[4 * i + 2 * e], x[4 * i + 2 * e + 1]), up2);
+            const float2 y = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+            sum[i / 4] = fa::add2(sum[i / 4], y);
+            const float2 a = make_float2(top_bits(y.x), top_bits(y.y));
+            const float2 r = fa::fma2(fa::add2(y, make_float2(-a.x, -a.y)), k16, zero);
+            const float2 b = make_float2(top_bits(r.x), top_bits(r.y));
             t[0][e] = a;
             t[1][e] = b;
-            t[2][e] = (z - b) * 16.f;
+            t[2][e] = fa::fma2(fa::add2(r, make_float2(-b.x, -b.y)), k16, zero);
           }
 #pragma unroll
-          for (int k = 0; k < 3; ++k) w[k][i] = e4m3x4(t[k][0], t[k][1], t[k][2], t[k][3]);
+          for (int k = 0; k < 3; ++k) w[k][i] = e4m3x4(t[k][0].x, t[k][0].y, t[k][1].x, t[k][1].y);
         }
 #pragma unroll
-        for (int h = 0; h < NG; ++h) l = fmaf(sum[h], me[h].z, l);
+        for (int h = 0; h < NG; ++h) l = fmaf(sum[h].x + sum[h].y, me[h].z, l);
         if (!__all_sync(0xffffffffu, is_free)) wait_weighed(u - NP);  // the buffer's tile before
         unsigned char* pb = smem + G::p_off + (u % NP) * G::PB;
 #pragma unroll

@@ -222,26 +222,45 @@ __device__ __forceinline__ void st8(unsigned char* p, const uint2& w) { *reinter
 
 // Heads [h0, h0 + nh) of rows [t0, t0 + nt): q and k rotated; POOL 1 / 2: rotated k
 // and v also stored to the rows `loc` of a bf16 / e4m3 pool.  Rows whose bit of
-// `mask` is not set are left alone.
-template <int D, int POOL, int NT>
+// `mask` is not set are left alone.  A thread's next item is on its way while it works
+// on one, the first while `table` fills the table (which ends with a barrier and gives
+// the mask).
+template <int D, int POOL, int NT, typename Table>
 __device__ __forceinline__ void rotate_rows(const rp::RopeParams& p, const float2* cs, long long t0, int nt, int h0, int nh,
-                                            unsigned mask) {
+                                            Table table) {
   using namespace rp;
-  constexpr int CH = D / 16;            // items of a head
-  constexpr int SLOTS = NT / CH;  // heads in flight
-  const int c = threadIdx.x % CH;
-  for (int r = threadIdx.x / CH; r < nt * nh; r += SLOTS) {
-    const int i = r / nh, h = h0 + r % nh;
+  constexpr int CH = D / 16;        // items of a head
+  constexpr int SLOTS = NT / CH;    // heads in flight
+  const int c = threadIdx.x % CH, total = nt * nh;
+  const Item it0 = item_at(p, cs, c);
+  struct Row {
+    int i, kind, hh;  // row; q, k, v; its head
+    uint4 w1, w2;
+  } next;
+  auto fetch = [&](int r) {
+    next.i = r / nh;
+    const int h = h0 + r % nh;
+    next.kind = h < p.h_q ? 0 : h < p.h_q + p.h_kv ? 1 : 2;
+    next.hh = next.kind == 0 ? h : next.kind == 1 ? h - p.h_q : h - p.h_q - p.h_kv;
+    const View& in = next.kind == 0 ? p.q : next.kind == 1 ? p.k : p.v;
+    const unsigned char* src = in.p + (t0 + next.i) * in.s0 + next.hh * in.s1;
+    next.w1 = ld16(src + 2 * it0.o1);
+    next.w2 = ld16(src + 2 * it0.o2);
+  };
+  int r = threadIdx.x / CH;
+  if (r < total) fetch(r);
+  const unsigned mask = table();
+  for (; r < total; r += SLOTS) {
+    const Row now = next;
+    if (r + SLOTS < total) fetch(r + SLOTS);
+    const int i = now.i, kind = now.kind, hh = now.hh;
     if ((mask >> i & 1u) == 0u) continue;
     const long long t = t0 + i;
-    const Item it = item_at(p, cs + i * (p.rot >> 1), c);
-    const int kind = h < p.h_q ? 0 : h < p.h_q + p.h_kv ? 1 : 2;  // q, k, v
-    const int hh = kind == 0 ? h : kind == 1 ? h - p.h_q : h - p.h_q - p.h_kv;
-    const View& in = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-    const unsigned char* src = in.p + t * in.s0 + hh * in.s1;
+    Item it = it0;
+    if (it.cs) it.cs += i * (p.rot >> 1);
     F16 x;
-    widen(ld16(src + 2 * it.o1), x.a);
-    widen(ld16(src + 2 * it.o2), x.b);
+    widen(now.w1, x.a);
+    widen(now.w2, x.b);
     if (kind < 2) {
       rotate(p, it.cs, x);
       const View& out = kind == 0 ? p.qo : p.ko;
@@ -282,9 +301,11 @@ __global__ void __launch_bounds__(rp::kThreads) rope_kernel(const __grid_constan
   const long long t0 = static_cast<long long>(blockIdx.x) * p.tokens;
   const int nt = static_cast<int>(min(static_cast<long long>(p.tokens), p.n - t0));
   const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.h_q + (POOL ? 2 : 1) * p.h_kv - h0);
-  fill_table<kThreads>(p, cs, t0, nt);
-  __syncthreads();
-  rotate_rows<D, POOL, kThreads>(p, cs, t0, nt, h0, nh, ~0u);
+  rotate_rows<D, POOL, kThreads>(p, cs, t0, nt, h0, nh, [&] {
+    fill_table<kThreads>(p, cs, t0, nt);
+    __syncthreads();
+    return ~0u;
+  });
 }
 
 // The same into a cache of e4m3 blocks.  p.units * p.parts of the CTAs take keys
@@ -319,16 +340,18 @@ __global__ void __launch_bounds__(rp::kBlockThreads, 4) rope_block_kernel(const 
     const int h0 = x % per_tile * p.heads;
     if (tid == 0) tops[0][0] = 0u;
     __syncthreads();
-    // rows that belong to a sequence
-    for (int b = tid; b < p.B; b += NT) {
-      const int a = __ldg(p.qo_ptr + b), e = __ldg(p.qo_ptr + b + 1);
-      if (a < 0 || e < a || e > p.n) continue;
-      const int from = static_cast<int>(max(a - t0, 0LL)), to = static_cast<int>(min(e - t0, static_cast<long long>(nt)));
-      if (from < to) atomicOr(&tops[0][0], ((1u << (to - from)) - 1u) << from);
-    }
-    fill_table<NT>(p, cs_dyn, t0, nt);
-    __syncthreads();
-    rotate_rows<D, 0, NT>(p, cs_dyn, t0, nt, h0, min(p.heads, p.h_q - h0), tops[0][0]);
+    rotate_rows<D, 0, NT>(p, cs_dyn, t0, nt, h0, min(p.heads, p.h_q - h0), [&] {
+      // rows that belong to a sequence
+      for (int b = tid; b < p.B; b += NT) {
+        const int a = __ldg(p.qo_ptr + b), e = __ldg(p.qo_ptr + b + 1);
+        if (a < 0 || e < a || e > p.n) continue;
+        const int from = static_cast<int>(max(a - t0, 0LL)), to = static_cast<int>(min(e - t0, static_cast<long long>(nt)));
+        if (from < to) atomicOr(&tops[0][0], ((1u << (to - from)) - 1u) << from);
+      }
+      fill_table<NT>(p, cs_dyn, t0, nt);
+      __syncthreads();
+      return tops[0][0];
+    });
     return;
   }
   const int unit = kv / p.parts, member = kv % p.parts;

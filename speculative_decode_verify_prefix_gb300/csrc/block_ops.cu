@@ -298,7 +298,7 @@ static BlockWs block_ws(long long n_cta, long long B, long long h_kv, long long 
   w.need = w.o_off + align256(4 * rows * static_cast<size_t>(D)) + kTicketBytes;
   return w;
 }
-constexpr long long kBlockParts = 2;  // CTAs of a block at most (appends)
+constexpr long long kBlockParts = 4;  // CTAs of a block at most (appends)
 constexpr long long kMaxRows = 128;  // packed rows of a KV head
 constexpr long long kSplitJoin = 4;  // pieces of a segment from which the joining CTA's warps share a row
 

@@ -7,10 +7,10 @@
 // (i, i + R / 2), or (2 i, 2 i + 1) when interleaved.  Elements from R on stay.
 //
 // Angles.  A 32-bit product p f_i is off by more than a radian at far positions.
-// The frequency in turns, f / 2 pi, is taken once per thread in 64 bits and
-// written as a fraction of 2^64; p times it, in 64-bit integers, wraps at whole
-// turns by itself, so the phase is exact but for the frequency's own 2^-53.  One
-// table of (A cos, A sin) per CTA serves all heads of its tokens.
+// The frequency in turns, f / 2 pi, is a fraction of 2^64 here; p times it, in 64-bit
+// integers, wraps at whole turns by itself, so the phase is off by p 2^-64 of a turn
+// and what a 64-bit 2^64 / 2 pi leaves, p f 2^-62.  One table of (A cos, A sin) per CTA
+// serves all heads of its tokens.
 //
 // All of it is bound by memory: a thread takes 16 elements of one head of one
 // row, the two 16-byte loads whose pairs belong together.
@@ -65,20 +65,41 @@ struct RopeParams {
 
 using RopeFn = void (*)(const RopeParams);
 
-// The frequency as a fraction of 2^64 turns per position.
+// The frequency as a fraction of 2^64 turns per position: f = m 2^-s times 2^64 / 2 pi.
 __device__ __forceinline__ unsigned long long turns_of(float f) {
-  double t = static_cast<double>(f) * 0.15915494309189535;  // 1 / 2 pi
-  t -= floor(t);
-  return __double2ull_rn(t * 18446744073709551616.0);
+  constexpr unsigned long long C = 0x28BE60DB9391054Aull;  // 2^64 / 2 pi
+  const unsigned bits = __float_as_uint(f);
+  const int e = static_cast<int>(bits >> 23 & 255u), s = 150 - max(e, 1);
+  const unsigned long long m = (bits & 0x007FFFFFu) | (e ? 0x00800000u : 0u);
+  const unsigned long long lo = m * C, hi = __umul64hi(m, C);  // hi < 2^24
+  unsigned long long x;
+  if (s >= 64)
+    x = s < 128 ? hi >> (s - 64) : 0ull;
+  else if (s > 0)
+    x = hi << (64 - s) | lo >> s;
+  else
+    x = s > -64 ? lo << -s : 0ull;
+  return bits >> 31 ? 0ull - x : x;
 }
-// (A cos, A sin) of a position; a frequency that is no number gives none.  32 bits
-// of the phase: 2^-32 of a turn.
+// (A cos, A sin) of a position; a frequency that is no number gives none.  The upper
+// 32 bits of the phase, less the nearest quarter turn, leave an angle r of at most
+// pi / 4; Taylor's series to r^9 and r^8 end within 3e-8.
 __device__ __forceinline__ float2 turn(unsigned long long f, long long pos, float size) {
-  const int phase = static_cast<int>(f * static_cast<unsigned long long>(pos) >> 32);
-  const float half = static_cast<float>(phase) * 4.656612873077393e-10f;  // 2^-31: half turns in [-1, 1]
-  float s, c;
-  sincospif(half, &s, &c);
-  return make_float2(size * c, size * s);
+  const unsigned phase = static_cast<unsigned>(f * static_cast<unsigned long long>(pos) >> 32);
+  const unsigned q = (phase + 0x20000000u) >> 30;
+  const float r = static_cast<float>(static_cast<int>(phase - (q << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float z = r * r;
+  float s = fmaf(z, 1.f / 362880.f, -1.f / 5040.f), c = fmaf(z, 1.f / 40320.f, -1.f / 720.f);
+  s = fmaf(s, z, 1.f / 120.f);
+  c = fmaf(c, z, 1.f / 24.f);
+  s = fmaf(s, z, -1.f / 6.f);
+  c = fmaf(c, z, -0.5f);
+  s = fmaf(s * z, r, r);
+  c = fmaf(c, z, 1.f);
+  const float a = q & 1 ? s : c, b = q & 1 ? c : s;  // a quarter turn: (cos, sin) -> (-sin, cos)
+  const float as = __uint_as_float(__float_as_uint(size) ^ ((q + 1u) << 30 & 0x80000000u));
+  const float bs = __uint_as_float(__float_as_uint(size) ^ (q << 30 & 0x80000000u));
+  return make_float2(as * a, bs * b);
 }
 __device__ __forceinline__ long long index_at(const void* p, int wide, long long i) {
   return wide ? __ldg(static_cast<const long long*>(p) + i) : static_cast<long long>(__ldg(static_cast<const int*>(p) + i));
@@ -416,37 +437,39 @@ __global__ void __launch_bounds__(rp::kBlockThreads, 4) rope_block_kernel(const 
   const int pairs = p.rot >> 1;
   const int c = lane % CH;
   const Item it = item_at(p, cs_dyn, c);
-  const int wt = p.warps, groups = NW / wt, group = warp / wt, part = warp % wt, step = groups * p.parts;
+  const int wt = p.warps, groups = NW / wt, group = warp / wt, part = warp % wt;
   // this thread's row of the new ones, and again `chunk` rows on (more rows than the
   // warps hold are read twice)
   const int first = part * RPI + lane / CH, chunk = wt * RPI;
   const int last = (nt - 1) / chunk * chunk;
-  int task = member * groups + group;
+  // tasks: K of every head, then V of every head; this CTA's [.., tasks), its groups by turns
+  const int each = (2 * p.h_kv + p.parts - 1) / p.parts, tasks = min(2 * p.h_kv, (member + 1) * each);
+  int task = member * each + group;
   uint4 n1, n2;  // the next task's row
   float next_old = 0.f;
   auto fetch = [&](int which, int at, uint4& a, uint4& b2) {
-    const View& in = which & 1 ? p.v : p.k;
+    const View& in = which >= p.h_kv ? p.v : p.k;
     a = b2 = make_uint4(0u, 0u, 0u, 0u);
     if (at + first < nt) {
-      const unsigned char* src = in.p + (t0 + at + first) * in.s0 + (which >> 1) * in.s1;
+      const unsigned char* src = in.p + (t0 + at + first) * in.s0 + (which >= p.h_kv ? which - p.h_kv : which) * in.s1;
       a = ld16(src + 2 * it.o1);
       b2 = ld16(src + 2 * it.o2);
     }
   };
   auto scale_of = [&](long long page, int which) -> float* {
-    return (which & 1 ? p.vs + page * p.vs_s0 : p.ks + page * p.ks_s0) + (which >> 1);
+    return which >= p.h_kv ? p.vs + page * p.vs_s0 + (which - p.h_kv) : p.ks + page * p.ks_s0 + which;
   };
-  if (task < 2 * p.h_kv) fetch(task, 0, n1, n2);
-  fill_table<NT>(p, cs_dyn, t0, nt);  // while the first loads are on their way
+  if (task < tasks) fetch(task, 0, n1, n2);
+  if (member * each < p.h_kv) fill_table<NT>(p, cs_dyn, t0, nt);  // (V alone needs none) while the first loads are on their way
   const long long page = found_page >= 0 && found_page < p.n_blocks ? found_page : -1;
   if (held && page < 0 && tid == 0 && member == 0) atomicOr(p.err, kErrBadIndex);
   const bool grows = page >= 0 && off > 0;
-  if (grows && task < 2 * p.h_kv) next_old = *scale_of(page, task);
+  if (grows && task < tasks) next_old = *scale_of(page, task);
   __syncthreads();
   int turn_of = 0;
-  for (; task < 2 * p.h_kv; task += step, turn_of ^= 1) {
-    const int h = task >> 1;
-    const bool isv = task & 1;
+  for (; task < tasks; task += groups, turn_of ^= 1) {
+    const bool isv = task >= p.h_kv;
+    const int h = isv ? task - p.h_kv : task;
     const float old = next_old;
     F16 x;
     auto take = [&](int at, const uint4& a, const uint4& b2) {
@@ -455,9 +478,9 @@ __global__ void __launch_bounds__(rp::kBlockThreads, 4) rope_block_kernel(const 
       if (!isv && it.cs && at + first < nt) rotate(p, it.cs + (at + first) * pairs, x);
     };
     take(0, n1, n2);
-    if (task + step < 2 * p.h_kv) {  // while this one is worked on
-      fetch(task + step, 0, n1, n2);
-      if (grows) next_old = *scale_of(page, task + step);
+    if (task + groups < tasks) {  // while this one is worked on
+      fetch(task + groups, 0, n1, n2);
+      if (grows) next_old = *scale_of(page, task + groups);
     }
     float s = 1.f;
     if (page >= 0) {

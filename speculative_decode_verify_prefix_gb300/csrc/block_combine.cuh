@@ -7,8 +7,10 @@
 // row, lane l the columns D / 32 l on, so a piece's row is one coalesced load and
 // nothing is computed twice.  SPLIT: the four warps of a CTA share a row's pieces (a
 // segment in many pieces is a long chain of loads: two sequences of 6k keys, 2 KV
-// heads of 256, XXX).  The drafts need nothing of the stream and come first: the
-// kernel is a programmatic dependent of it.  All sums are 32-bit.
+// heads of 256, 25.6 us without, 23.6 so; 64 sequences in two pieces each 428 without,
+// 449 so).  The drafts need nothing of the stream and come first: the kernel is a
+// programmatic dependent of it (in plain stream order 3 to 4 us more a call).  All
+// sums are 32-bit.
 #pragma once
 #include "block_stream.cuh"
 

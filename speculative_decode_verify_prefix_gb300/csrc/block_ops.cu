@@ -571,7 +571,6 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   p.R = static_cast<int>(R);
   p.h_kv = static_cast<int>(h_kv);
   p.rows = static_cast<int>(w.rows);
-  p.w_min = 1;
   p.team = team;
   p.n_hg = p.h_kv / p.team;
   p.n_team = static_cast<int>(n_team);

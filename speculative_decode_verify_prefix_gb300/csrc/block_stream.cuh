@@ -10,9 +10,9 @@
 //
 // Both products run on tcgen05 straight from the cache's bytes (kind::f8f6f4);
 // nothing is widened.  What is not e4m3 is written as a sum of e4m3 terms:
-//   queries  q 2^sh = hi + lo exactly (bf16 has 8 significant bits, a term 4;
-//            elements 2^17 below the row's largest lose bits that no score
-//            shows), along K of one accumulator, or 16 lanes apart;
+//   queries  q 2^sh = hi + lo (bf16 has 8 significant bits, a term 4): exact, but that
+//            elements more than 2^10 below the row's largest are off by up to 2^-17 of
+//            that; along K of one accumulator, or 16 lanes apart;
 //   weights  y = 2^6 x: the top 4 bits, the next 4 and the rest rounded to 4, as
 //            three groups of rows of one M = 128 product under scales 1, 2^4,
 //            2^8: 12 bits, and 2^-24 of the reference at the lower end.
@@ -22,16 +22,21 @@
 //   O[128][D]       += P[128][128 keys] x V    (rows 32 p + r: term p of row r)
 //
 // Roles (7 warps; two CTAs an SM at head_dim 64 and 128, one at 256):
-//   warps 0-3  softmax: thread (w, r) holds keys 32 w .. 32 w + 31 of row r.
+//   warps 0-3  softmax: warp w the keys 32 w .. 32 w + 31 of all rows.
 //   warps 4, 6 block table, TMA of boxes of up to 128 keys into the K and V rings, scales.
 //   warp 5     tensor memory, MMAs.
 // Up to eight KV heads are taken by a team of as many CTAs, each its own over the
 // same keys: what lies side by side in memory is read at about the same time (8
-// heads of 128: XXX).  More than 32 packed rows are row tiles, a CTA each beside the
-// others: the keys come from memory once (64 rows: XXX).  The groups of 16 keys of all (sequence, head group) segments
-// are laid end to end and every team takes an equal share; a segment's part of a
-// share is a piece, whose partial (o, log2 of its sum) block_combine_kernel folds:
-// of CTA c and segment s, slot c + team * s.
+// heads of 128, 64 sequences: 488 us with heads apart, 428 so; 32 single tokens 100,
+// 91).  More than 32 packed rows are row tiles, a CTA each beside the others: the keys
+// come from memory once (64 rows: 139 us with the tiles one after the other, 115 so).
+// The tiles of all (sequence, head group) segments are laid end to end and every team
+// takes an equal share; a segment's part of a share is a piece, whose partial (o, log2
+// of its sum) block_combine_kernel folds: of CTA c and segment s, slot c + team * s.
+// What bounds it: 64 sequences of 8,259 to 32,600 keys (8 heads of 128, 16 rows) take
+// 420-428 us, 6.6-6.7 TB/s, memory; at head_dim 64 a tile's softmax outlasts its bytes
+// (189 us for 829 MB), with 32 rows the chain of scores, softmax and weights (313 us for
+// 1.66 GB).
 // Every wait is bounded (one second); in a CTA that gives up every role ends its
 // loop without copying, multiplying or arriving anywhere (the copies' barriers then
 // still tell when those under way are done), sets error bit 8, waits for copies and
@@ -77,7 +82,6 @@ struct BkParams {
   int box;              // groups of a TMA box: a power of two that divides bgroups, GT at most
   int B, L, gq, R, h_kv, rows;  // rows: of a partial (RT row tiles of 32)
   float scale2;         // softmax scale in base 2
-  int w_min;            // tiles of a share at least
   int team, n_hg, n_team;  // KV heads of a team, h_kv / team, teams
   int tiles;               // row tiles: CTAs of a head in a team
   const unsigned char* cmask;
@@ -93,9 +97,9 @@ using BkFn = void (*)(const BkParams, const CUtensorMap, const CUtensorMap);
 using BkJoinFn = void (*)(const BkParams);
 
 // Packed rows of a CTA: the smallest of 8, 16, 32 that holds them (32: in row
-// tiles, the grid's y).  A warp finds NR rows 32 / NR times in its lanes and its
-// lanes share the keys: with 32 rows for all a serving batch of 16 took 537 us, so
-// XXX, and single tokens of 4 rows 122, so XXX.
+// tiles).  A warp finds NR rows 32 / NR times in its lanes and its lanes share the keys:
+// with 32 rows for all 64 sequences of 16 rows take 467 us, so 428, 32 single tokens of 4
+// rows 109, so 91.
 __host__ __device__ constexpr int row_tile(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
 
 template <int D, int NR>
@@ -151,7 +155,7 @@ __device__ __forceinline__ bool prefix_len(const BkParams& p, int b, int& P) {
 }
 __device__ __forceinline__ int seg_tiles(int P) { return P > 0 ? (P - 1) / KT + 1 : 1; }
 __device__ __forceinline__ int share_of(const BkParams& p, int total) {  // (the host bounds the total)
-  return max((total - 1) / p.n_team + 1, p.w_min);
+  return (total - 1) / p.n_team + 1;
 }
 struct BSeg {
   int b, h, P, T;  // h: this CTA's head of the head group; T: tiles
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(bk::kThreads, bk::Geo<D, NR>::per_sm)
     // Warp 4 brings K, warp 6 V and the scales.  Each goes on by itself: a K entry is
     // free once its scores are done, a V entry only when its weights have met it; and a
     // tile costs a warp some hundred cycles (one for both, 64 of 8k..16k keys at
-    // head_dim 64: 229 us, so XXX).
+    // head_dim 64: 229 us, so 192).
     const bool isv = warp == 6;
     const CUtensorMap* map = isv ? &vmap : &kmap;
     const uint32_t n_ent = isv ? NV : NK, ring = isv ? v_s : k_s;

@@ -798,6 +798,71 @@ def test_block_graphs_streams_and_threads(vsk):
         assert not errors and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_block_head_major_caches(vsk):
+    """[h_kv, rows, D] storage seen as [rows, h_kv, D]; a row's heads far apart."""
+    lens, size, hq, hk, d, l_ext = [500, 77, 1], 32, 8, 4, 64, 3
+    c = block_case(lens, size, hq, hk, d, l_ext, seed=21)
+    want = run_block(vsk, c, size, l_ext)
+    for x in ("kc", "vc"):
+        c[x] = c[x].view(torch.uint8).transpose(0, 1).contiguous().transpose(0, 1).view(E4M3)
+        assert c[x].stride(1) > c[x].stride(0)
+    assert torch.equal(run_block(vsk, c, size, l_ext), want)
+
+
+def test_block_queries_with_an_outlier(vsk):
+    """One element of a query 64 times the others: those below 2^-10 of it are off by 2^-17 of it at most."""
+    lens, size, hq, hk, d, l_ext = [700], 16, 4, 1, 128, 2
+    c = block_case(lens, size, hq, hk, d, l_ext, seed=22)
+    c["q"][..., 5] = 64.0
+    c["kc"].view(torch.uint8)[:, :, 5] &= 0x80  # (its keys are zero there: the rest decides)
+    o = run_block(vsk, c, size, l_ext)
+    want, tol = block_want(c["q"], c["ke"], c["ve"], c["kc"], c["vc"], c["ks"], c["vs"], c["table"], lens, size, l_ext, d ** -0.5)
+    pages = c["table"][0, :-(-lens[0] // size)].long().repeat_interleave(size)[:lens[0]]
+    rows = c["table"][0].long()[torch.arange(lens[0], device=DEV) // size] * size + torch.arange(lens[0], device=DEV) % size
+    sums = (value(c["kc"][rows, 0]).abs().sum(1) * c["ks"][pages, 0].to(F64)).max()
+    # every score off by at most delta: a weight and the sum by e^delta - 1 each, of A = sum p |v|
+    delta = float(64.0 * 2.0 ** -17 * sums * d ** -0.5)
+    assert delta < 0.05
+    size_of, _ = block_want(c["q"], c["ke"], c["ve"].abs(), c["kc"], (c["vc"].view(torch.uint8) & 0x7F).view(E4M3), c["ks"], c["vs"], c["table"],
+                            lens, size, l_ext, d ** -0.5)
+    check_block(o, want, tol + 2.1 * delta * size_of)
+
+
+def test_offsets_beyond_32_bits(vsk):
+    """A cache of more than 2^32 bytes whose last blocks are used, and rows 2^31 elements apart."""
+    g = gen(23)
+    size, hk, d, hq, l_ext = 64, 8, 128, 8, 2
+    blocks = 68000  # 68000 * 64 * 1024 bytes
+    kc, vc = (torch.empty(blocks * size, hk, d, dtype=torch.uint8, device=DEV).view(E4M3) for _ in "kv")
+    ks, vs = torch.ones(blocks, hk, device=DEV), torch.ones(blocks, hk, device=DEV)
+    n = 200
+    table = ints([[blocks - 1, blocks - 3, 66000, blocks - 2]])
+    k, v = normal(g, n, hk, d), normal(g, n, hk, d)
+    pos, f = positions(g, n, "near"), frequencies(d)
+    vsk.rope_append_block_fwd(None, k, v, None, None, kc, vc, ks, vs, indptr([n]), table, ints([0]), size, pos, f)
+    assert vsk.read_error_flags() == 0
+    t = torch.arange(n, device=DEV)
+    rows = table[0].long()[t // size] * size + t % size
+    page = table[0].long()[t // size]
+    codes = (v.float() / vs[page][..., None]).clamp(-TOP, TOP).to(E4M3).view(torch.uint8)
+    assert torch.equal(vc.view(torch.uint8)[rows], codes)
+    q, ke, ve = normal(g, l_ext, hq, d), normal(g, l_ext, hk, d), normal(g, l_ext, hk, d)
+    c = dict(q=q, ke=ke, ve=ve, kc=kc, vc=vc, ks=ks, vs=vs, qo=indptr([l_ext]), table=table, lens=ints([n]))
+    o = run_block(vsk, c, size, l_ext)
+    assert vsk.read_error_flags() == 0
+    check_block(o, *block_want(q, ke, ve, kc, vc, ks, vs, table, [n], size, l_ext, d ** -0.5))
+    del kc, vc, c
+    torch.cuda.empty_cache()
+    base = torch.zeros((1 << 31) + 4096, dtype=BF16, device=DEV)
+    x = base.as_strided((2, 3, 64), (1 << 31, 64, 1))
+    x.copy_(normal(g, 2, 3, 64))
+    out, kk = torch.empty(2, 3, 64, dtype=BF16, device=DEV), normal(g, 2, 1, 64)
+    vsk.rope_fwd(x, kk, out, torch.empty_like(kk), ints([7, 9]), frequencies(64))
+    check_rotated(out, *turned64(x, ints([7, 9]), frequencies(64), False, 1.0), 1.0)
+    vsk.rope_fwd(out, kk, x, torch.empty_like(kk), ints([0, 0]), frequencies(64))
+    assert torch.equal(x, out)
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("d,inter", [(64, False), (128, True), (256, False)])

@@ -179,8 +179,8 @@ __device__ __forceinline__ void rotate(const RopeParams& p, const float2* cs, F1
 }
 
 // Values under scale s: the 32-bit quotients x / s.  A power of two divides exactly
-// as its reciprocal multiplies (one branch for all of them: 16 divisions are more
-// than the rest of the work).
+// as its reciprocal multiplies (one branch for all of them, not 16 divisions beside
+// 16 products).
 struct Under {
   float s, inv;
   bool exact;

@@ -14,8 +14,8 @@
 //
 // All of it but the blocks' keys and values is bound by memory: a thread takes 16
 // elements of one head of one row, the two 16-byte loads whose pairs belong together.
-// 24,335 rows of 32/8 heads of 128 take 75 us rotated (5.9 TB/s), 95 with K and V stored
-// to a pool (6.1); a plain copy of as many bytes 82.
+// 24,335 rows of 32/8 heads of 128 take 71 us rotated (6.3 TB/s), 94 with K and V stored
+// to a pool (6.2); a plain copy of as many bytes 82.
 #pragma once
 #include "verify_kernel.cuh"
 
@@ -248,54 +248,67 @@ __device__ __forceinline__ void st8(unsigned char* p, const uint2& w) { *reinter
 // `mask` is not set are left alone.  A thread's next item is on its way while it works
 // on one, the first while `table` fills the table (which ends with a barrier and gives
 // the mask).
-template <int D, int POOL, int NT, typename Table>
+template <int D, int POOL, int NT, bool Q_ONLY, typename Table>
 __device__ __forceinline__ void rotate_rows(const rp::RopeParams& p, const float2* cs, long long t0, int nt, int h0, int nh,
                                             Table table) {
   using namespace rp;
   constexpr int CH = D / 16;        // items of a head
   constexpr int SLOTS = NT / CH;    // heads in flight
-  const int c = threadIdx.x % CH, total = nt * nh;
-  const Item it0 = item_at(p, cs, c);
-  struct Row {
-    int i, kind, hh;  // row; q, k, v; its head
-    uint4 w1, w2;
-  } next;
-  auto fetch = [&](int r) {
-    next.i = r / nh;
-    const int h = h0 + r % nh;
-    next.kind = h < p.h_q ? 0 : h < p.h_q + p.h_kv ? 1 : 2;
-    next.hh = next.kind == 0 ? h : next.kind == 1 ? h - p.h_q : h - p.h_q - p.h_kv;
-    const View& in = next.kind == 0 ? p.q : next.kind == 1 ? p.k : p.v;
-    const unsigned char* src = in.p + (t0 + next.i) * in.s0 + next.hh * in.s1;
-    next.w1 = ld16(src + 2 * it0.o1);
-    next.w2 = ld16(src + 2 * it0.o2);
+  const int c = threadIdx.x % CH;
+  const Item it = item_at(p, cs, c);
+  const int gap = it.o2 - it.o1;
+  // (row, head) of an item; SLOTS items on, without dividing again
+  struct At {
+    int i, h;
   };
-  int r = threadIdx.x / CH;
-  if (r < total) fetch(r);
+  const int di = SLOTS / nh, dh = SLOTS % nh;
+  auto on = [&](At& a) {
+    a.i += di;
+    a.h += dh;
+    if (a.h >= nh) {
+      a.h -= nh;
+      ++a.i;
+    }
+  };
+  struct Row {
+    At a;
+    uint4 w1, w2;
+  } next = {};
+  auto kind_of = [&](int h) { return Q_ONLY || h < p.h_q ? 0 : h < p.h_q + p.h_kv ? 1 : 2; };  // q, k, v
+  auto head_of = [&](int h, int kind) { return kind == 0 ? h : kind == 1 ? h - p.h_q : h - p.h_q - p.h_kv; };
+  auto place = [&](const View& v, int i, int hh) { return v.p + (t0 + i) * v.s0 + hh * v.s1; };
+  auto fetch = [&] {
+    const int h = h0 + next.a.h, kind = kind_of(h);
+    const unsigned char* src = place(kind == 0 ? p.q : kind == 1 ? p.k : p.v, next.a.i, head_of(h, kind)) + 2 * it.o1;
+    next.w1 = ld16(src);
+    next.w2 = ld16(src + 2 * gap);
+  };
+  next.a.i = static_cast<int>(threadIdx.x) / CH / nh;
+  next.a.h = static_cast<int>(threadIdx.x) / CH % nh;
+  if (next.a.i < nt) fetch();
   const unsigned mask = table();
-  for (; r < total; r += SLOTS) {
+  while (next.a.i < nt) {
     const Row now = next;
-    if (r + SLOTS < total) fetch(r + SLOTS);
-    const int i = now.i, kind = now.kind, hh = now.hh;
+    on(next.a);
+    if (next.a.i < nt) fetch();
+    const int i = now.a.i;
     if ((mask >> i & 1u) == 0u) continue;
-    const long long t = t0 + i;
-    Item it = it0;
-    if (it.cs) it.cs += i * (p.rot >> 1);
+    const int h = h0 + now.a.h, kind = kind_of(h), hh = head_of(h, kind);
     F16 x;
     widen(now.w1, x.a);
     widen(now.w2, x.b);
     if (kind < 2) {
-      rotate(p, it.cs, x);
+      if (it.cs) rotate(p, it.cs + i * (p.rot >> 1), x);
       const View& out = kind == 0 ? p.qo : p.ko;
       if (out.p) {
-        unsigned char* dst = out.p + t * out.s0 + hh * out.s1;
-        st16(dst + 2 * it.o1, narrow(x.a));
-        st16(dst + 2 * it.o2, narrow(x.b));
+        unsigned char* dst = place(out, i, hh) + 2 * it.o1;
+        st16(dst, narrow(x.a));
+        st16(dst + 2 * gap, narrow(x.b));
       }
     }
     if constexpr (POOL != 0) {
       if (kind > 0) {
-        const long long row = index_at(p.loc, p.loc64, t);
+        const long long row = index_at(p.loc, p.loc64, t0 + i);
         if (row >= 0 && row < p.pool) {
           const View& cache = kind == 1 ? p.kc : p.vc;
           unsigned char* dst = cache.p + row * cache.s0 + hh * cache.s1;
@@ -316,15 +329,16 @@ __device__ __forceinline__ void rotate_rows(const rp::RopeParams& p, const float
 }
 
 // A CTA takes p.tokens tokens of p.heads heads (of the h_q + h_kv, or h_q + 2 h_kv,
-// of a row).
+// of a row).  Without a pool five CTAs fit an SM (24,335 rows, 32/8 heads of 128: four
+// 73.3 us, five 70.8, six 72.6); with one the fifth costs spills (94, so 96).
 template <int D, int POOL>
-__global__ void __launch_bounds__(rp::kThreads) rope_kernel(const __grid_constant__ rp::RopeParams p) {
+__global__ void __launch_bounds__(rp::kThreads, POOL == 0 ? 5 : 4) rope_kernel(const __grid_constant__ rp::RopeParams p) {
   using namespace rp;
   __shared__ __align__(16) float2 cs[kMaxTokens * 128];
   const long long t0 = static_cast<long long>(blockIdx.x) * p.tokens;
   const int nt = static_cast<int>(min(static_cast<long long>(p.tokens), p.n - t0));
   const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.h_q + (POOL ? 2 : 1) * p.h_kv - h0);
-  rotate_rows<D, POOL, kThreads>(p, cs, t0, nt, h0, nh, [&] {
+  rotate_rows<D, POOL, kThreads, false>(p, cs, t0, nt, h0, nh, [&] {
     fill_table<kThreads>(p, cs, t0, nt);
     __syncthreads();
     return ~0u;
@@ -341,7 +355,7 @@ __global__ void __launch_bounds__(rp::kThreads) rope_kernel(const __grid_constan
 // keys alone, some values alone: those need no table of angles.
 // The other CTAs take the queries as rope_kernel does: they are most of the bytes, and
 // need none of this.
-// 24,335 rows, 32/8 heads of 128, blocks of 64: 106 us, 5.0 TB/s, of which keys and
+// 24,335 rows, 32/8 heads of 128, blocks of 64: 104 us, 5.1 TB/s, of which keys and
 // values alone 61 at 3.3: instructions and latency (without loads and stores 41, of
 // which 10 to find the blocks and 14 for the tables).
 template <int D>
@@ -366,7 +380,7 @@ __global__ void __launch_bounds__(rp::kBlockThreads, 4) rope_block_kernel(const 
     const int h0 = x % per_tile * p.heads;
     if (tid == 0) tops[0][0] = 0u;
     __syncthreads();
-    rotate_rows<D, 0, NT>(p, cs_dyn, t0, nt, h0, min(p.heads, p.h_q - h0), [&] {
+    rotate_rows<D, 0, NT, true>(p, cs_dyn, t0, nt, h0, min(p.heads, p.h_q - h0), [&] {
       // rows that belong to a sequence
       for (int b = tid; b < p.B; b += NT) {
         const int a = __ldg(p.qo_ptr + b), e = __ldg(p.qo_ptr + b + 1);

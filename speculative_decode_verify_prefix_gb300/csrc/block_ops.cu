@@ -298,7 +298,7 @@ static BlockWs block_ws(long long n_cta, long long B, long long h_kv, long long 
   w.need = w.o_off + align256(4 * rows * static_cast<size_t>(D)) + kTicketBytes;
   return w;
 }
-constexpr long long kBlockParts = 4;  // CTAs of a block at most (appends)
+constexpr long long kBlockCtas = 10;  // appends: CTAs of keys and values per SM, about
 constexpr long long kMaxRows = 128;  // packed rows of a KV head
 constexpr long long kSplitJoin = 4;  // pieces of a segment from which the joining CTA's warps share a row
 
@@ -450,7 +450,17 @@ int rope_append_block_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_te
   for (p.warps = 1; p.warps * held < mean && p.warps < rp::kBlockThreads / 32;) p.warps *= 2;
   const long long groups = rp::kBlockThreads / 32 / p.warps;
   p.units = static_cast<int>(units);
-  p.parts = static_cast<int>(std::min((2LL * p.h_kv + groups - 1) / groups, kBlockParts));
+  // CTAs that share a block's heads: some ten an SM (24,335 rows, 32/8 heads of 128, us: blocks of 64
+  // with 7, 10, 14 an SM 105.7, 102.7, 106.5; in blocks of 32 as many as four a block 107, so 99, of 16
+  // 118, so 104), keys apart from values, which need no table of angles (8/1 heads together 37.9, apart
+  // 35.3); two heads a CTA at least (16/2 of 256: one 102, two 94) and 16 at most (32/32, blocks of 32:
+  // 32 heads 214, 16 207).  Where that leaves SMs without work, all that there are (4 x 300 rows: 21.5, so
+  // 15.4).
+  const long long most = (2LL * p.h_kv + groups - 1) / groups, want = (kBlockCtas * sms + units / 2) / units;
+  long long parts = std::min(std::max(2LL, most / 2), std::max(std::max(2LL, most / 16), want));
+  parts = std::min(most, std::max(parts, 4LL * sms / units));
+  const long long each = (most + parts - 1) / parts;
+  p.parts = static_cast<int>((most + each - 1) / each);
   const long long kv = units * p.parts, rows = cut_rows(p, p.h_q, D, sms, rp::kBlockThreads), grid = kv + rows;
   p.turn = static_cast<int>(1 + rows / kv);
   if (grid > INT_MAX) return fail("grid of %lld CTAs too large", grid);

@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(rp::kThreads, POOL == 0 ? 5 : 4) rope_kernel(c
 // keys alone, some values alone: those need no table of angles.
 // The other CTAs take the queries as rope_kernel does: they are most of the bytes, and
 // need none of this.
-// 24,335 rows, 32/8 heads of 128, blocks of 64: 104 us, 5.1 TB/s, of which keys and
+// 24,335 rows, 32/8 heads of 128, blocks of 64: 103 us, 5.2 TB/s, of which keys and
 // values alone 61 at 3.3: instructions and latency (without loads and stores 41, of
 // which 10 to find the blocks and 14 for the tables).
 template <int D>

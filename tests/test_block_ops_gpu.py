@@ -378,6 +378,37 @@ def test_block_append_against_64_bits(vsk, case, wide):
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(again, cache))
 
 
+@pytest.mark.parametrize("case", [
+    # (sequences, new rows of each at least, block, h_q, h_kv, d, rot, interleaved): enough blocks that a CTA
+    # takes several heads of one, of keys and values where they do not divide evenly
+    (60, 200, 32, 8, 8, 64, 64, False), (40, 640, 64, 2, 32, 128, 96, True), (30, 850, 128, 4, 4, 128, 128, False),
+    (80, 100, 16, 3, 1, 64, 16, False), (60, 350, 64, 0, 2, 256, 256, True),
+], ids=lambda c: f"b{c[0]}n{c[1]}s{c[2]}h{c[3]}x{c[4]}d{c[5]}r{c[6]}")
+def test_block_append_of_many_is_that_of_each(vsk, case):
+    b, least, size, hq, hk, d, rot, inter = case
+    g = gen(least)
+    lens, new = [(13 * i) % 97 for i in range(b)], [least + (29 * i) % 83 for i in range(b)]
+    n = sum(new)
+    q, k, v = (normal(g, n, h, d) * 40 if h else None for h in (hq, hk, hk))
+    held = [x + y for x, y in zip(lens, new)]
+    blocks = sum(-(-x // size) for x in held) + 2
+    table = table_of(g, held, size, blocks)
+    old = block_cache(g, blocks, size, hk, d)
+    pos, freq = positions(g, n, "near"), frequencies(rot)
+    many, each = [x.clone() for x in old], [x.clone() for x in old]
+    outs = [(torch.full_like(q, 7.0) if hq else None, torch.full_like(k, 7.0)) for _ in range(2)]
+    vsk.rope_append_block_fwd(q, k, v, *outs[0], *many, indptr(new), table, ints(lens), size, pos, freq, inter, 1.1)
+    at = 0
+    for i, m in enumerate(new):
+        r = slice(at, at + m)
+        vsk.rope_append_block_fwd(q[r] if hq else None, k[r], v[r], outs[1][0][r] if hq else None, outs[1][1][r], *each,
+                                  indptr([m]), table[i:i + 1], ints(lens[i:i + 1]), size, pos[r], freq, inter, 1.1)
+        at += m
+    assert vsk.read_error_flags() == 0
+    for x, y in zip([*many, *outs[0]], [*each, *outs[1]]):
+        assert x is None or torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+
+
 def test_block_append_extremes(vsk):
     """Rows of zeros, of the largest and smallest numbers, infinities and NaN."""
     g = gen(8)

@@ -116,7 +116,7 @@ struct Geo {
   static constexpr int PB = 3 * NR * 128;           // P; the MMA reads 128 rows, of the others nobody takes the result
   static constexpr int NP = D == 128 && NR == 32 ? 1 : 2;  // its buffers
   static constexpr int per_sm = D == 256 ? 1 : 2;
-  static constexpr int ctl = 3072;                  // barriers, scales, exchanges
+  static constexpr int ctl = 3 * 1024;              // barriers, scales, exchanges
   static constexpr int room = (per_sm == 1 ? kSmemPerCTAMax : kSmemPerSM / 2 - kReservedPerCTA) - ctl - QB - NP * PB;
   static constexpr int entries = room / ENT < 10 ? room / ENT : 10;
   static constexpr int NK = entries / 2, NV = entries - NK;  // ring entries of K and of V (which stay longer)
@@ -143,7 +143,7 @@ constexpr int kQscOff = 448;    // [32] float: a row's score scale
 constexpr int kRedOff = 576;    // [4][NR] float: maxima of a tile
 constexpr int kSumOff = 1088;   // [4][NR] float: sums of a piece
 constexpr int kMetaOff = 1600;  // [kMeta][GT] float4: ks, log2 vs, 1 / vs, keys that are there (+ 256: the tile lacks some)
-static_assert(kAbortOff + 4 <= kQscOff && kRedOff + 512 <= kSumOff && kSumOff + 512 <= kMetaOff && kMetaOff + kMeta * GT * 16 <= 3072,
+static_assert(kAbortOff + 4 <= kQscOff && kRedOff + 512 <= kSumOff && kSumOff + 512 <= kMetaOff && kMetaOff + kMeta * GT * 16 <= 3 * 1024,
               "control block");
 
 // Segments and their cut, the same in both kernels.

@@ -187,11 +187,16 @@ static int allow_smem(const void* fn, size_t smem) {
 }
 
 // Tokens and heads of a CTA that takes rows; the CTAs.  Few tokens: a row's heads
-// over several CTAs, a pass of the threads each at least.
-static long long cut_rows(rp::RopeParams& p, long long heads, long long D, int sms, int threads) {
+// over several CTAs, a pass of the threads each at least.  More: one wave of CTAs (four an
+// SM), rounded up so that it is no more than one (4,082 rows, 16/2 heads of 256, rotated
+// 9.2 us, with a few CTAs left over 10.2; appended 10.3, 11.3).  Where that takes more than
+// kMaxTokens, `many` a CTA (7,000 rows, 16/2 heads of 256: with 8 27.7 us, with 4 24.9; the
+// queries beside 24,335 rows into blocks: with 8 103 us in all, with 4 107).
+static long long cut_rows(rp::RopeParams& p, long long heads, long long D, int sms, int threads, int many) {
   if (heads == 0) return 0;
   const long long slots = threads / (D / 16);
-  p.tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(rp::kMaxTokens, p.n / (4LL * sms))));
+  const long long wave = (p.n + 4LL * sms - 1) / (4LL * sms);
+  p.tokens = wave <= rp::kMaxTokens ? static_cast<int>(wave) : many;
   const long long tiles = (p.n + p.tokens - 1) / p.tokens;
   const long long parts = std::max<long long>(1, std::min((heads + slots - 1) / slots, 4LL * sms / tiles));
   p.heads = static_cast<int>((heads + parts - 1) / parts);
@@ -201,7 +206,7 @@ static int launch_rope(rp::RopeParams& p, long long D, int pool, cudaStream_t st
   if (p.n == 0) return 1;
   int sms = 0;
   if (!current_sms(&sms)) return 0;
-  const long long heads = p.h_q + (pool ? 2LL : 1LL) * p.h_kv, ctas = cut_rows(p, heads, D, sms, rp::kThreads);
+  const long long heads = p.h_q + (pool ? 2LL : 1LL) * p.h_kv, ctas = cut_rows(p, heads, D, sms, rp::kThreads, 4);
   const long long per_tile = (heads + p.heads - 1) / p.heads;
   const dim3 grid(static_cast<unsigned>(ctas / per_tile), static_cast<unsigned>(per_tile));
   if (grid.y > 65535) return fail("%lld heads are too many", heads);
@@ -461,7 +466,7 @@ int rope_append_block_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_te
   parts = std::min(most, std::max(parts, 4LL * sms / units));
   const long long each = (most + parts - 1) / parts;
   p.parts = static_cast<int>((most + each - 1) / each);
-  const long long kv = units * p.parts, rows = cut_rows(p, p.h_q, D, sms, rp::kBlockThreads), grid = kv + rows;
+  const long long kv = units * p.parts, rows = cut_rows(p, p.h_q, D, sms, rp::kBlockThreads, rp::kMaxTokens), grid = kv + rows;
   p.turn = static_cast<int>(1 + rows / kv);
   if (grid > INT_MAX) return fail("grid of %lld CTAs too large", grid);
   const void* fn = reinterpret_cast<const void*>(kernel_rope_block(static_cast<int>(D)));

@@ -126,6 +126,17 @@ def _coerce(x) -> float:
         return 1.0
 
 
+def _flat_mask(mask, stream):
+    """A mask as one row of bytes.  One that is not contiguous is copied: on the
+    stream that will read the copy (None: the mask's device's current one), from
+    whose memory the copy then comes, too, so that it is written before and reused
+    after the call's kernels."""
+    if stream is None or mask.is_contiguous():
+        return mask.reshape(-1)
+    with torch.cuda.stream(stream):
+        return mask.reshape(-1)
+
+
 def verify_splitkv_fwd(q_extend, k_extend, v_extend, o_extend, k_buffer, v_buffer, qo_indptr, kv_indptr,
                        kv_indices, custom_mask, is_causal, mask_indptr, max_len_extend, k_scale, v_scale,
                        sm_scale=None, logit_cap=0.0, skip_prefix_custom_mask=True, sliding_window_size=-1,
@@ -164,9 +175,10 @@ def verify_splitkv_fwd(q_extend, k_extend, v_extend, o_extend, k_buffer, v_buffe
     sm = 0.0 if sm_scale is None else float(sm_scale)
     if custom_mask is not None:
         cm = custom_mask if custom_mask.dtype == torch.uint8 else custom_mask.view(torch.uint8)
+        cm = _flat_mask(cm, stream)
         r = [ctypes.byref(v) for v in views]
         ok = _native.lib().verify_splitkv_tree_fwd(
-            r[0], r[1], r[2], _ref(o_extend), r[3], r[4], r[5], r[6], r[7], _ref(cm.reshape(-1)), _ref(mask_indptr), mle,
+            r[0], r[1], r[2], _ref(o_extend), r[3], r[4], r[5], r[6], r[7], _ref(cm), _ref(mask_indptr), mle,
             _coerce(k_scale), _coerce(v_scale), sm, ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
             ctypes.c_void_p(stream.cuda_stream))
         if not ok:

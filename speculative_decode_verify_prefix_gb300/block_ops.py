@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import _native
-from .api import _BLOCK_SIZE as _SIZES
+from .api import _BLOCK_SIZE as _SIZES, _flat_mask
 from .cache_ops import _run
 
 _SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
@@ -109,7 +109,7 @@ def verify_splitkv_block_fwd(q_extend, k_extend, v_extend, o_extend, k_cache, v_
     ``workspace``: ``block_workspace_size`` bytes or more."""
     mle = int(max_len_extend)
     if custom_mask is not None:
-        custom_mask = custom_mask.reshape(-1)
+        custom_mask = _flat_mask(custom_mask, stream)
 
     def need():
         if q_extend.dim() != 3 or k_extend.dim() != 3 or qo_indptr.dim() != 1 or qo_indptr.shape[0] < 2:

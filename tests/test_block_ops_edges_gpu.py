@@ -1,0 +1,69 @@
+"""GPU tests of the rotary, append and block-scaled cache calls at corners that the
+tests of their formulas do not reach."""
+import pytest
+import torch
+
+from test_block_ops_gpu import DEV, block_case, block_want, check_block, ints, vsk  # noqa: F401
+from test_parity_gpu import gpu_problem, run_gpu
+
+import workloads
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- masks that are not contiguous
+
+def wide(mask):
+    """The same mask as a slice of a wider buffer."""
+    w = torch.zeros(mask.shape[0], mask.shape[1] + 5, dtype=mask.dtype, device=DEV)
+    w[:, :mask.shape[1]] = mask
+    return w[:, :mask.shape[1]]
+
+
+@pytest.mark.parametrize("call", ["blocks", "tree"])
+def test_mask_that_is_not_contiguous_on_another_stream(vsk, call):  # noqa: F811
+    """The copy is made on the call's stream, so it neither waits for the current one nor is overtaken by the kernels."""
+    n, l_ext = 40, 4
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    draft = torch.rand(2, l_ext, l_ext, generator=g, device=DEV) < 0.5
+    mask = wide(torch.cat([torch.ones(2 * l_ext, n, dtype=torch.bool, device=DEV), draft.view(-1, l_ext)], 1))
+    at = ints([0, l_ext * (n + l_ext), 2 * l_ext * (n + l_ext)])
+    assert not mask.is_contiguous()
+    if call == "blocks":
+        c = block_case([n, n], 16, 8, 2, 64, l_ext, seed=5)
+
+        def run(m, o=None, **kw):
+            o = torch.empty_like(c["q"]) if o is None else o
+            vsk.verify_splitkv_block_fwd(c["q"], c["ke"], c["ve"], o, c["kc"], c["vc"], c["ks"], c["vs"], c["qo"], c["table"],
+                                         c["lens"], 16, l_ext, custom_mask=m, mask_indptr=at, **kw)
+            return o
+
+        check_block(run(mask), *block_want(c["q"], c["ke"], c["ve"], c["kc"], c["vc"], c["ks"], c["vs"], c["table"], [n, n], 16,
+                                           l_ext, 64 ** -0.5, list(draft)))
+    else:
+        p = gpu_problem(workloads.Spec("wide_mask", (n, n), l_ext, 8, 2, 64, 64, perm=True, seed=209))
+
+        def run(m, o=None, **kw):
+            o = torch.empty_like(p["q"]) if o is None else o
+            assert vsk.verify_splitkv_fwd(p["q"], p["k_ext"], p["v_ext"], o, p["k_buffer"], p["v_buffer"], p["qo_indptr"],
+                                          p["kv_indptr"], p["kv_indices"], m, True, at, l_ext, p["k_scale"], p["v_scale"],
+                                          sm_scale=p["sm_scale"], **kw)
+            return o
+
+        assert not torch.equal(run(mask), run_gpu(vsk, p))  # (the mask is not the causal one)
+    want = run(mask.contiguous())
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run(mask.contiguous())  # the stream's workspace is there
+    o = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    late = torch.cuda.Event()
+    torch.cuda._sleep(200_000_000)  # the current stream is busy for some 0.1 s
+    late.record()
+    run(mask, o, stream=side)
+    over = torch.ones(mask.shape, dtype=torch.bool, device=DEV)  # the copy's memory, if it were the current stream's
+    side.synchronize()
+    assert not late.query()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and bool(over.all())

@@ -43,34 +43,39 @@ static bool folds(const Runs& r) {
   if (!rows || !heads) return false;
   return r.s0 >= r.s1 ? r.s0 < (r.h - 1) * r.s1 + r.d : r.s1 < (r.n - 1) * r.s0 + r.d;
 }
+// Whether a row of an runs and a row of bn runs, each s bytes after the one before, share a
+// byte; the runs are ad and bd bytes long, the first of a lies `delta` behind that of b.
+static bool lines_meet(long long delta, long long an, long long bn, long long s, long long ad, long long bd) {
+  if (s <= 0) return true;
+  auto below = [&](long long x) { return x / s - (x % s < 0 ? 1 : 0); };  // floor(x / s)
+  // run j of b against run i of a, y = j - i: -ad < delta - y s < bd
+  const long long lo = std::max(below(delta - bd) + 1, 1 - an), hi = std::min(-below(-delta - ad) - 1, bn - 1);
+  return lo <= hi;
+}
 // Whether two views share a byte.  Views of one buffer (equal strides) are told
-// apart exactly; of other strides, by the ranges they lie in.
+// apart exactly; of other strides, by the ranges they lie in.  A dimension of one element
+// has no stride of its own, whatever its view says.
 static bool meet(Runs a, Runs b) {
   if (a.n == 0 || b.n == 0) return false;
-  if (a.n == 1) a.s0 = b.s0;
+  if (a.n == 1) a.s0 = b.n == 1 ? 0 : b.s0;
   if (b.n == 1) b.s0 = a.s0;
-  if (a.h == 1) a.s1 = b.s1;
+  if (a.h == 1) a.s1 = b.h == 1 ? 0 : b.s1;
   if (b.h == 1) b.s1 = a.s1;
   auto last = [](const Runs& r) { return r.at + static_cast<uintptr_t>((r.n - 1) * r.s0 + (r.h - 1) * r.s1 + r.d); };
   if (last(a) <= b.at || last(b) <= a.at) return false;
   if (a.s0 != b.s0 || a.s1 != b.s1) return true;
+  const bool rows = a.n > 1 || b.n > 1, heads = a.h > 1 || b.h > 1;
+  if (!rows && !heads) return true;
+  const long long delta = static_cast<long long>(a.at - b.at);
+  if (!rows) return lines_meet(delta, a.h, b.h, a.s1, a.d, b.d);
+  if (!heads) return lines_meet(delta, a.n, b.n, a.s0, a.d, b.d);
   const bool rows_wide = a.s0 >= a.s1;
   const long long S = rows_wide ? a.s0 : a.s1, s = rows_wide ? a.s1 : a.s0;
   const long long aw = rows_wide ? a.n : a.h, bw = rows_wide ? b.n : b.h, an = rows_wide ? a.h : a.n, bn = rows_wide ? b.h : b.n;
-  const long long most = std::max(an, bn), d = std::max(a.d, b.d);
-  if (S <= 0 || (most > 1 && s <= 0) || (most - 1) * s + d > S) return std::max(aw, bw) > 1 || S <= 0 || most > 1;
-  const long long delta = static_cast<long long>(a.at - b.at);
+  if (s <= 0 || (std::max(an, bn) - 1) * s + std::max(a.d, b.d) > S) return true;
   const long long x0 = delta / S;
-  for (long long x = x0 - 2; x <= x0 + 2; ++x) {  // a's run against the one of b that lies x wide strides on
-    if (x <= -aw || x >= bw) continue;
-    const long long rest = delta - x * S;
-    const long long y0 = most > 1 ? rest / s : 0;
-    for (long long y = y0 - 2; y <= y0 + 2; ++y) {
-      if (y <= -an || y >= bn) continue;
-      const long long t = rest - y * s;
-      if (t < b.d && t + a.d > 0) return true;
-    }
-  }
+  for (long long x = x0 - 1; x <= x0 + 1; ++x)  // a's runs against those of b that lie x wide strides on
+    if (x > -aw && x < bw && lines_meet(delta - x * S, an, bn, s, a.d, b.d)) return true;
   return false;
 }
 static bool same_view(const Runs& a, const Runs& b) {

@@ -2,6 +2,8 @@
 the binding does with a call's tensors before the library sees them, and which views
 the library refuses (CPU tensors stand in, see test_block_ops_host.py)."""
 import contextlib
+import ctypes
+import random
 import types
 
 import pytest
@@ -9,7 +11,7 @@ import torch
 from torch.utils._python_dispatch import TorchDispatchMode
 
 import speculative_decode_verify_prefix_gb300 as vsk
-from speculative_decode_verify_prefix_gb300 import api, block_ops
+from speculative_decode_verify_prefix_gb300 import _native, api, block_ops
 
 BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
 
@@ -86,3 +88,71 @@ def test_tree_call_copies_a_mask_on_its_own_stream(monkeypatch, streams, cut):
                                       1.0, workspace=torch.zeros(256, dtype=torch.uint8), stream=other)
     assert copies.seen == ([other] if cut.stop else [])
     assert any(t.dtype == torch.uint8 and torch.equal(t.bool(), mask.flatten()) for t in kept if t.dim() == 1)
+
+
+# ------------------------------------------------------------------ views that share memory
+
+def call(name, args, *scalars, ws=None):
+    keep = [None if a is None else api.as_vsk(a) for a in args]
+    ptrs = [None if v is None else ctypes.addressof(v) for v in keep]
+    return getattr(_native.lib(), name)(*ptrs, *scalars, *([] if ws is None else [ctypes.c_void_p(ws[0]), ws[1]]), None)
+
+
+def shared_bytes_refused(name, args, *scalars, ws=None):
+    """The refusal for shared bytes, or none; without a GPU a call that passes ends at the device."""
+    if torch.cuda.is_available():
+        pytest.skip("a call that passes would run")
+    assert call(name, args, *scalars, ws=ws) == 0
+    return vsk.last_error() if "overlap" in vsk.last_error() else ""
+
+
+ROOM = torch.zeros(1 << 14, dtype=BF16)
+
+
+def rows_of(t):
+    """Where a view's elements lie."""
+    n, h, d = t.shape
+    first = torch.arange(n)[:, None] * t.stride(0) + torch.arange(h) * t.stride(1) + t.storage_offset()
+    return (first.flatten()[:, None] + torch.arange(d)).flatten()
+
+
+def test_one_run_shifted_by_less_than_itself():
+    k = ROOM.as_strided((1, 1, 64), (8, 8, 1), 0)
+    f, pos = torch.ones(32), torch.zeros(1, dtype=torch.int64)
+    for by, msg in ((8, "k_out overlaps k"), (56, "k_out overlaps k"), (64, ""), (0, "")):
+        ko = ROOM.as_strided((1, 1, 64), (8, 8, 1), by)
+        assert shared_bytes_refused("rope_fwd", [None, k, None, ko, pos, f], 0, 1.0) == msg
+
+
+@pytest.mark.parametrize("form", ["rows", "pool"])
+def test_views_of_all_strides_against_their_bytes(form):
+    """Views that share a byte are refused; views of equal strides whose runs lie in order are refused only then."""
+    r = random.Random(11)
+    counts = [0, 0, 0]
+    for _ in range(6000):
+        n, h, m = r.randint(1, 3), r.randint(1, 3), r.randint(1, 4)  # (the queries' heads, or the pool's rows)
+        steps = [8 * r.choice([0, 1, 3, 8, 9, 16, 17, 24, 32, 48, 64, 80]) for _ in range(4)]
+        same = r.random() < 0.6
+        a = ((n, m) if form == "rows" else (n, h), steps[:2])
+        b = ((n, h) if form == "rows" else (m, h), steps[:2] if same else steps[2:])
+        x = ROOM.as_strided((*a[0], 64), (*a[1], 1), 4096)
+        y = ROOM.as_strided((*b[0], 64), (*b[1], 1), 4096 + 8 * r.randint(-60, 60))
+        f, pos = torch.ones(32), torch.zeros(n, dtype=torch.int64)
+        if form == "rows":  # queries against the rotated keys
+            error = shared_bytes_refused("rope_fwd", [x, bf(n, h, 64), bf(n, m, 64), y, pos, f], 0, 1.0)
+        else:  # values against the pool
+            error = shared_bytes_refused("rope_append_fwd", [None, bf(n, h, 64), x, None, None, y, bf(m, h, 64), torch.arange(n), pos, f],
+                                         0, 1.0, 1.0, 1.0, ws=(256, 256))
+        bx, by = rows_of(x), rows_of(y)
+        folds = by.unique().numel() < by.numel()
+        shares = torch.isin(bx, by).any()
+        counts[0] += bool(shares)
+        if shares or folds:
+            assert error, (x.shape, x.stride(), y.shape, y.stride(), x.storage_offset() - y.storage_offset())
+        (s0, s1), hi = b[1], max(x.shape[1], y.shape[1])
+        ordered = s1 >= 64 and s0 >= (hi - 1) * s1 + 64
+        if same and ordered and not shares:
+            counts[1] += 1
+            assert not error, (x.shape, x.stride(), y.shape, y.stride(), x.storage_offset() - y.storage_offset())
+        counts[2] += not error
+    assert min(counts) > 50, counts

@@ -26,11 +26,12 @@ static Runs runs_of(const char* name, const vsk_tensor* t, long long e) {
   Runs r{name, 0, 0, 0, 0, 0, 0};
   if (!t) return r;
   r.at = reinterpret_cast<uintptr_t>(t->data);
-  if (t->ndim == 3) {
+  if (t->ndim == 3)
     r = Runs{name, r.at, t->shape[0], t->shape[1], e * t->shape[2], e * t->stride[0], e * t->stride[1]};
-  } else {
+  else if (t->ndim == 2)
     r = Runs{name, r.at, t->shape[0], 1, e * t->shape[1], e * t->stride[0], 0};
-  }
+  else
+    r = Runs{name, r.at, 1, 1, e * t->shape[0], 0, 0};
   if (r.d == 0 || r.h == 0) r.n = 0;
   return r;
 }
@@ -148,10 +149,14 @@ static bool prepare_rope(const vsk_tensor* q, const vsk_tensor* k, const vsk_ten
   p.inter = interleaved != 0;
   return true;
 }
+static Runs index_runs(const char* name, const vsk_tensor* t) {
+  return runs_of(name, t, t->dtype == VSK_DTYPE_I64 ? 8 : t->dtype == VSK_DTYPE_U8 ? 1 : 4);
+}
 // Rows are rewritten while others are read: an output may be its own input, and
-// shares no byte with anything else.
+// shares no byte with anything else (more: the caches; read: what the call reads beside
+// q, k and v).
 static bool check_apart(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* v, const vsk_tensor* qo,
-                        const vsk_tensor* ko, std::initializer_list<Runs> more) {
+                        const vsk_tensor* ko, std::initializer_list<Runs> more, std::initializer_list<Runs> read) {
   const Runs ins[] = {runs_of("q", q, 2), runs_of("k", k, 2), runs_of("v", v, 2)};
   Runs outs[8];
   int n = 0;
@@ -163,6 +168,8 @@ static bool check_apart(const vsk_tensor* q, const vsk_tensor* k, const vsk_tens
     for (int j = 0; j < 3; ++j)
       if (!(i == j && i < 2 && same_view(outs[i], ins[j])) && meet(outs[i], ins[j]))
         return fail("%s overlaps %s", outs[i].name, ins[j].name);
+    for (const Runs& r : read)
+      if (meet(outs[i], r)) return fail("%s overlaps %s", outs[i].name, r.name);
     for (int j = 0; j < i; ++j)
       if (meet(outs[i], outs[j])) return fail("%s overlaps %s", outs[i].name, outs[j].name);
   }
@@ -359,7 +366,8 @@ int rope_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* q_out, 
   long long D = 0;
   if (!k_out) return fail("k_out is NULL");
   if (!prepare_rope(q, k, nullptr, q_out, k_out, positions, inv_freq, interleaved, attention_factor, p, D)) return 0;
-  if (!check_apart(q, k, nullptr, q_out, k_out, {})) return 0;
+  if (!check_apart(q, k, nullptr, q_out, k_out, {}, {index_runs("positions", positions), index_runs("inv_freq", inv_freq)}))
+    return 0;
   return launch_rope(p, D, 0, static_cast<cudaStream_t>(stream));
 }
 
@@ -385,7 +393,9 @@ int rope_append_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_tensor* 
   if (!check_index(out_cache_loc, "out_cache_loc", k->shape[0])) return 0;
   if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
     return fail("storing into the cache needs finite k_scale > 0 and v_scale > 0");
-  if (!check_apart(q, k, v, q_out, k_out, {runs_of("k_buffer", k_buffer, e), runs_of("v_buffer", v_buffer, e)})) return 0;
+  if (!check_apart(q, k, v, q_out, k_out, {runs_of("k_buffer", k_buffer, e), runs_of("v_buffer", v_buffer, e)},
+                   {index_runs("positions", positions), index_runs("inv_freq", inv_freq), index_runs("out_cache_loc", out_cache_loc)}))
+    return 0;
   if (workspace && workspace_bytes < 256) return fail("workspace of %zu bytes is smaller than 256", workspace_bytes);
   if (p.n == 0) return 1;
   p.kc = view_of(k_buffer, e);
@@ -426,7 +436,9 @@ int rope_append_block_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_te
     return 0;
   if (!check_apart(q, k, v, q_out, k_out,
                    {runs_of("k_cache", k_cache, 1), runs_of("v_cache", v_cache, 1), runs_of("k_scales", k_scales, 4),
-                    runs_of("v_scales", v_scales, 4)}))
+                    runs_of("v_scales", v_scales, 4)},
+                   {index_runs("positions", positions), index_runs("inv_freq", inv_freq), index_runs("qo_indptr", qo_indptr),
+                    index_runs("block_table", block_table), index_runs("cache_lens", cache_lens)}))
     return 0;
   if (workspace && workspace_bytes < 256) return fail("workspace of %zu bytes is smaller than 256", workspace_bytes);
   if (p.n == 0) return 1;
@@ -536,8 +548,12 @@ int verify_splitkv_block_fwd(const vsk_tensor* q, const vsk_tensor* ke, const vs
   {
     const Runs ro = runs_of("o_extend", o, 2);
     if (folds(ro)) return fail("rows of o_extend overlap");
+    const Runs none = runs_of("", nullptr, 1);
     for (const Runs& r : {runs_of("q_extend", q, 2), runs_of("k_extend", ke, 2), runs_of("v_extend", ve, 2),
-                          runs_of("k_cache", kc, 1), runs_of("v_cache", vc, 1)})
+                          runs_of("k_cache", kc, 1), runs_of("v_cache", vc, 1), runs_of("k_scales", ks, 4),
+                          runs_of("v_scales", vs, 4), index_runs("qo_indptr", qo), index_runs("block_table", bt),
+                          index_runs("seq_lens", lens), cm ? index_runs("custom_mask", cm) : none,
+                          mi ? index_runs("mask_indptr", mi) : none})
       if (meet(ro, r)) return fail("o_extend overlaps %s", r.name);
   }
   const BlockForm f = block_form(D, R);

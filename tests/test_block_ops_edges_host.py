@@ -156,3 +156,66 @@ def test_views_of_all_strides_against_their_bytes(form):
             assert not error, (x.shape, x.stride(), y.shape, y.stride(), x.storage_offset() - y.storage_offset())
         counts[2] += not error
     assert min(counts) > 50, counts
+
+
+# ------------------------------------------------------------------ outputs over what a call reads beside q, k and v
+
+def rope_call(**change):
+    a = dict(q=bf(6, 4, 64), k=bf(6, 2, 64), q_out=bf(6, 4, 64), k_out=bf(6, 2, 64), positions=torch.arange(6), inv_freq=torch.ones(32))
+    a.update(change)
+    return "rope_fwd", a, (0, 1.0), None
+
+
+def append_call(**change):
+    a = dict(q=bf(6, 4, 64), k=bf(6, 2, 64), v=bf(6, 2, 64), q_out=bf(6, 4, 64), k_out=bf(6, 2, 64), k_buffer=bf(20, 2, 64),
+             v_buffer=bf(20, 2, 64), out_cache_loc=torch.arange(6), positions=torch.arange(6), inv_freq=torch.ones(32))
+    a.update(change)
+    return "rope_append_fwd", a, (0, 1.0, 1.0, 1.0), (256, 256)
+
+
+def cache():
+    return dict(k_cache=torch.zeros(64, 2, 64, dtype=torch.uint8).view(E4M3), v_cache=torch.zeros(64, 2, 64, dtype=torch.uint8).view(E4M3),
+                k_scales=torch.ones(4, 2), v_scales=torch.ones(4, 2), qo_indptr=ints(0, 3, 6),
+                block_table=torch.zeros(2, 2, dtype=torch.int32))
+
+
+def block_append_call(**change):
+    a = dict(q=bf(6, 4, 64), k=bf(6, 2, 64), v=bf(6, 2, 64), q_out=bf(6, 4, 64), k_out=bf(6, 2, 64), **cache(), cache_lens=ints(0, 3),
+             positions=torch.arange(6), inv_freq=torch.ones(32))
+    a.update(change)
+    return "rope_append_block_fwd", a, (16, 0, 1.0), (256, 256)
+
+
+def block_call(**change):
+    a = dict(q_extend=bf(6, 4, 64), k_extend=bf(6, 2, 64), v_extend=bf(6, 2, 64), o_extend=bf(6, 4, 64), **cache(), seq_lens=ints(0, 3),
+             custom_mask=torch.zeros(64, dtype=torch.uint8), mask_indptr=torch.tensor([0, 9, 27]))
+    a.update(change)
+    return "verify_splitkv_block_fwd", a, (16, 3, 0.0), (256, 256)
+
+
+READ = {rope_call: ("positions", "inv_freq"), append_call: ("positions", "inv_freq", "out_cache_loc"),
+        block_append_call: ("positions", "inv_freq", "qo_indptr", "block_table", "cache_lens"),
+        block_call: ("k_scales", "v_scales", "qo_indptr", "block_table", "seq_lens", "custom_mask", "mask_indptr")}
+WRITTEN = {rope_call: ("q_out", "k_out"), append_call: ("q_out", "k_out", "k_buffer", "v_buffer"),
+           block_append_call: ("q_out", "k_out", "k_cache", "v_cache", "k_scales", "v_scales"), block_call: ("o_extend",)}
+
+
+@pytest.mark.parametrize("make", READ, ids=lambda m: m.__name__)
+def test_outputs_over_indices_and_tables(make):
+    def error(**change):
+        name, a, scalars, ws = make(**change)
+        return shared_bytes_refused(name, list(a.values()), *scalars, ws=ws)
+
+    a = make()[1]
+    assert error() == ""
+    for out in WRITTEN[make]:
+        for read in READ[make]:
+            x, y = a[out], a[read]
+            room = torch.zeros(x.nbytes + y.nbytes, dtype=torch.uint8)
+
+            def at(t, by):
+                return room[by:by + t.nbytes].view(t.dtype).view(t.shape)
+
+            for by in (0, x.nbytes - 8):  # the first bytes of what is written, the last ones
+                assert error(**{out: at(x, 0), read: at(y, by)}) == f"{out} overlaps {read}", (out, read)
+            assert error(**{out: at(x, 0), read: at(y, x.nbytes)}) == "", (out, read)  # behind it

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
     const long long m0 = p.mindptr64 ? static_cast<const long long*>(p.mindptr)[b]
                                      : static_cast<long long>(static_cast<const int*>(p.mindptr)[b]);
     const long long width = static_cast<long long>(P) + p.L;
-    if (m0 >= 0 && m0 + p.L * width <= p.n_mask)
+    if (m0 >= 0 && m0 <= p.n_mask - p.L * width)
       seen = p.cmask + m0 + i * width + P;
     else if (lane == 0 && row == 0 && h == 0)
       atomicOr(p.err, kErrBadMaskIndptr);

@@ -1578,7 +1578,7 @@ __global__ void __launch_bounds__(CS == 2 ? (MTW == 2 ? 64 : 128) : MaxWarps<Max
         const long long m0 = p.mindptr64 ? static_cast<const long long*>(p.mindptr)[sg.b]
                                          : static_cast<long long>(static_cast<const int*>(p.mindptr)[sg.b]);
         const long long span = static_cast<long long>(p.L) * (sg.P + p.L);
-        if (m0 >= 0 && m0 + span <= p.n_mask) {
+        if (m0 >= 0 && m0 <= p.n_mask - span) {
           mbase = m0;
         } else if (flagger) {
           atomicOr(p.err, kErrBadMaskIndptr);

@@ -67,3 +67,36 @@ def test_mask_that_is_not_contiguous_on_another_stream(vsk, call):  # noqa: F811
     assert not late.query()
     torch.cuda.synchronize()
     assert torch.equal(o, want) and bool(over.all())
+
+
+# ---------------------------------------------------------------- mask offsets
+
+@pytest.mark.parametrize("call", ["blocks", "tree, one launch", "tree, two launches"])
+def test_mask_offsets_near_the_largest(vsk, call):  # noqa: F811
+    """An offset to which the mask's size cannot be added is outside the mask like any other: causal drafts, bit 16."""
+    n, l_ext = 40, 4
+    flat = torch.zeros(2 * l_ext * (n + l_ext), dtype=torch.uint8, device=DEV)
+    if call == "blocks":
+        c = block_case([n, n], 16, 8, 2, 64, l_ext, seed=5)
+
+        def run(m, at):
+            o = torch.empty_like(c["q"])
+            vsk.verify_splitkv_block_fwd(c["q"], c["ke"], c["ve"], o, c["kc"], c["vc"], c["ks"], c["vs"], c["qo"], c["table"],
+                                         c["lens"], 16, l_ext, custom_mask=m, mask_indptr=at)
+            return o
+    else:
+        p = gpu_problem(workloads.Spec("far_mask", (n, n), l_ext, 8, 2, 64, 64, perm=True, seed=210))
+
+        def run(m, at):
+            return run_gpu(vsk, p, custom_mask=m, mask_indptr=at)
+
+        vsk.set_tuning_split_launch(2 if "two" in call else 0)
+    try:
+        causal = run(None, None)
+        vsk.read_error_flags()
+        for far in (2 ** 63 - 1, 2 ** 63 - flat.numel() // 2, -2 ** 63):
+            at = torch.tensor([far, far, far], device=DEV)
+            assert torch.equal(run(flat, at), causal)
+            assert vsk.read_error_flags() == 16
+    finally:
+        vsk.set_tuning_split_launch(1)

@@ -24,7 +24,7 @@ BUILD_DIR = os.path.join(_HERE, "_build")
 OBJ_DIR = os.path.join(BUILD_DIR, f"obj_{platform.machine()}")
 LIB_PATH = os.path.join(BUILD_DIR, f"libverify_splitkv_{platform.machine()}.so")
 VIEWS_SRC = os.path.join(CSRC, "views.cpp")
-VIEWS_PATH = os.path.join(BUILD_DIR, f"vsk_views_{platform.machine()}.so")
+VIEWS_PATH = os.path.join(BUILD_DIR, "vsk_views" + sysconfig.get_config_var("EXT_SUFFIX"))  # (names the Python and the machine)
 NVCC_ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [*NVCC_ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC"]
 
@@ -50,16 +50,28 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return path
 
 
+def _views_stamp() -> str:
+    """The torch that runs: what a views module built against another one is told by."""
+    import torch
+
+    return f"{torch.__version__}\n{os.path.dirname(torch.__file__)}\n"
+
+
+def _views_match() -> bool:
+    """Whether the views module is there and was built against this torch."""
+    try:
+        with open(VIEWS_PATH + ".torch") as f:
+            return f.read() == _views_stamp() and os.path.exists(VIEWS_PATH)
+    except OSError:
+        return False
+
+
 def _build_views(force: bool) -> None:
     """The views module, with the host compiler, against the torch that runs it."""
     import torch
 
-    stamp = VIEWS_PATH + ".torch"  # the version it was built against
-    if not force and os.path.exists(VIEWS_PATH) and os.path.exists(stamp):
-        with open(stamp) as f:
-            same = f.read() == torch.__version__
-        if same and os.path.getmtime(VIEWS_PATH) >= max(os.path.getmtime(VIEWS_SRC), os.path.getmtime(HEADER)):
-            return
+    if not force and _views_match() and os.path.getmtime(VIEWS_PATH) >= max(os.path.getmtime(VIEWS_SRC), os.path.getmtime(HEADER)):
+        return
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
@@ -72,8 +84,8 @@ def _build_views(force: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on views.cpp:\n{r.stderr}")
     os.replace(tmp, VIEWS_PATH)
-    with open(stamp, "w") as f:
-        f.write(torch.__version__)
+    with open(VIEWS_PATH + ".torch", "w") as f:
+        f.write(_views_stamp())
 
 
 def _build_lib(force: bool, verbose: bool) -> str:
@@ -236,13 +248,15 @@ _views = None
 
 
 def views():
-    """The function of the views module; raises if it was not built."""
+    """The function of the views module; raises if it was not built, or not for the
+    Python and torch that run."""
     global _views
     if _views is None:
         with _lock:
             if _views is None:
-                if not os.path.exists(VIEWS_PATH):
-                    raise RuntimeError(f"module {VIEWS_PATH} is missing: run __graft_entry__.build()")
+                if not _views_match():
+                    state = "was built against another torch" if os.path.exists(VIEWS_PATH) else "is missing"
+                    raise RuntimeError(f"module {VIEWS_PATH} {state}: run build()")
                 import torch  # noqa: F401  (its libraries, before the module that needs them)
                 from importlib.machinery import ExtensionFileLoader
                 from importlib.util import module_from_spec, spec_from_loader

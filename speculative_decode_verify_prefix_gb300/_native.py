@@ -3,9 +3,10 @@
 The library is compiled from ``csrc/*.cu`` with nvcc into ``_build/`` next to
 this file: every translation unit (the host side, and the kernels of each
 head_dim) in parallel, then linked into one shared library.  ``csrc/views.cpp``
-becomes the extension module that packs the views of a call's tensors.  Loading
-never falls back to anything: if the library or the module is missing or fails to
-load, callers get an exception.
+becomes the extension module that packs the views of a call's tensors.  Loading the
+library never falls back to anything: if it is missing or fails to load, callers get
+an exception.  The module only saves host time: where it cannot be built (no Python
+headers), build() warns and the calls pack their views in Python.
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import platform
 import subprocess
 import sysconfig
 import threading
+import warnings
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(_HERE, "csrc")
@@ -46,7 +48,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with ThreadPoolExecutor(1) as ex:
         views = ex.submit(_build_views, force)
         path = _build_lib(force, verbose)
-        views.result()
+        try:
+            views.result()
+        except (RuntimeError, OSError) as e:
+            warnings.warn(f"the views module was not built, calls will take longer on the host: {e}", RuntimeWarning, stacklevel=2)
     return path
 
 
@@ -72,6 +77,8 @@ def _build_views(force: bool) -> None:
 
     if not force and _views_match() and os.path.getmtime(VIEWS_PATH) >= max(os.path.getmtime(VIEWS_SRC), os.path.getmtime(HEADER)):
         return
+    if os.path.exists(VIEWS_PATH + ".torch"):  # a module that is not made anew is none
+        os.remove(VIEWS_PATH + ".torch")
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]

@@ -15,12 +15,53 @@ a call that is captured into a graph needs its own.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
+import warnings
 
 import torch
 
 from . import _native
-from .api import _SHARED_SIZE as _SIZES, _WS, _WS_LOCK, _coerce
+from .api import _SHARED_SIZE as _SIZES, _WS, _WS_LOCK, _coerce, as_vsk
+
+
+def _python_views(names, tensors):
+    """What the views module's function does, without the module: (device index, the
+    views, their addresses; None stays None)."""
+    device, views, args = -1, [], []
+    for name, t in zip(names, tensors):
+        if t is None:
+            args.append(None)
+            continue
+        dev = t.get_device() if isinstance(t, torch.Tensor) and t.is_cuda else -1
+        if dev < 0:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if device >= 0 and dev != device:
+            raise ValueError(f"{name} is on cuda:{dev}, the call's other tensors on cuda:{device}")
+        device = dev
+        try:
+            views.append(as_vsk(t))
+        except RuntimeError:  # a layout without memory or strides
+            raise ValueError(f"{name} must be a strided CUDA tensor") from None
+        args.append(ctypes.addressof(views[-1]))
+    if device < 0:
+        raise ValueError(f"{names[0]} must be a CUDA tensor")
+    return device, views, args
+
+
+_views = None
+
+
+def _load_views():
+    """The views module's function, or the one above where there is no module."""
+    global _views
+    try:
+        _views = _native.views()
+    except (RuntimeError, ImportError) as e:
+        warnings.warn(f"calls take longer on the host: {e}", RuntimeWarning, stacklevel=2)
+        _views = _python_views
+    return _views
+
 
 @functools.lru_cache(maxsize=None)
 def _device(index):
@@ -54,7 +95,7 @@ def _run(name, names, tensors, scalars, stream, workspace, need=None, scalars_at
     ``scalars_at`` tensors; None: after all), then workspace, its bytes and the
     stream, with the tensors' device current.  ``need``: workspace bytes (None:
     the error word; 0: the entry point takes none)."""
-    device, buf, args = (_native._views or _native.views())(names, tensors)  # buf: the views' memory
+    device, buf, args = (_views or _load_views())(names, tensors)  # buf: the views' memory
     if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _run(name, names, tensors, scalars, stream, workspace, need, scalars_at)

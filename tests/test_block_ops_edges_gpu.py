@@ -1,5 +1,7 @@
 """GPU tests of the rotary, append and block-scaled cache calls at corners that the
 tests of their formulas do not reach."""
+import ctypes
+
 import pytest
 import torch
 
@@ -100,3 +102,36 @@ def test_mask_offsets_near_the_largest(vsk, call):  # noqa: F811
             assert vsk.read_error_flags() == 16
     finally:
         vsk.set_tuning_split_launch(1)
+
+
+# ---------------------------------------------------------------- the binding
+
+def test_views_packed_in_python_are_the_modules(vsk, monkeypatch):  # noqa: F811
+    from speculative_decode_verify_prefix_gb300 import _native, cache_ops
+
+    x = torch.zeros(4, 6, 64, dtype=torch.bfloat16, device=DEV)
+    tensors = (x, None, x[:, 2:4], x.transpose(0, 1), x.view(torch.uint8), x[0, 0], x[0], x[..., 0, None, None, :], x.bool(), x.double(),
+               torch.zeros((), device=DEV), torch.zeros(0, 3, dtype=torch.int32, device=DEV), torch.arange(5, device=DEV))
+    names = tuple(f"t{i}" for i in range(len(tensors)))
+    size = ctypes.sizeof(_native.VskTensor)
+    packed = [pack(names, tensors) for pack in (_native.views(), cache_ops._python_views)]
+    (device, _, one), (other_device, _, other) = packed
+    assert device == other_device == x.get_device()
+    for a, b in zip(one, other):
+        assert (a is None) == (b is None) and (a is None or ctypes.string_at(a, size) == ctypes.string_at(b, size))
+    for pack in (_native.views(), cache_ops._python_views):
+        with pytest.raises(ValueError, match="b must be a strided CUDA tensor"):
+            pack(("a", "b"), (x, torch.ones(2, device=DEV).to_sparse()))
+    # a whole call without the module
+    c = block_case([40, 70], 16, 8, 2, 64, 4, seed=5)
+
+    def run():
+        o = torch.empty_like(c["q"])
+        vsk.verify_splitkv_block_fwd(c["q"], c["ke"], c["ve"], o, c["kc"], c["vc"], c["ks"], c["vs"], c["qo"], c["table"], c["lens"],
+                                     16, 4)
+        return o
+
+    want = run()
+    assert cache_ops._views is _native.views()
+    monkeypatch.setattr(cache_ops, "_views", cache_ops._python_views)
+    assert torch.equal(run(), want)

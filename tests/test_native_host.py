@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import speculative_decode_verify_prefix_gb300 as vsk
-from speculative_decode_verify_prefix_gb300 import _native
+from speculative_decode_verify_prefix_gb300 import _native, cache_ops
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -59,3 +59,30 @@ def test_build_makes_a_views_module_of_another_torch_anew(unloaded):
     before = os.stat(unloaded).st_ino
     _native._build_views(False)
     assert os.stat(unloaded).st_ino == before
+
+
+def test_without_python_headers_the_library_is_built_and_calls_run(unloaded, monkeypatch):
+    """Nothing but the views module needs Python.h: build() warns, and the calls pack their views in Python."""
+    paths = sysconfig.get_paths()
+    monkeypatch.setattr(sysconfig, "get_paths", lambda *a: {**paths, "include": "/nonexistent"})
+    monkeypatch.setattr(_native, "VIEWS_SRC", str(unloaded.with_name("views.cpp")))
+    unloaded.with_name("views.cpp").write_text("#error no headers\n")
+    with pytest.warns(RuntimeWarning, match="was not built"):
+        assert vsk.build() == _native.LIB_PATH
+    assert not _native._views_match()  # (the old one is not taken for the new source)
+    monkeypatch.setattr(cache_ops, "_views", None)
+    with pytest.warns(RuntimeWarning, match="longer on the host"):
+        with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+            vsk.rope_fwd(*[torch.zeros(1, 1, 64, dtype=torch.bfloat16)] * 4, torch.zeros(1), torch.zeros(32))
+    assert cache_ops._views is cache_ops._python_views
+
+
+@pytest.mark.parametrize("bad", [torch.zeros(1), [0, 1], torch.zeros(2).to_sparse()])
+def test_both_packers_refuse_alike(bad):
+    errors = []
+    for pack in (_native.views(), cache_ops._python_views):
+        for tensors in ((bad, None), (None, bad), (None, None)):
+            with pytest.raises(ValueError) as e:
+                pack(("a", "b"), tensors)
+            errors.append(str(e.value))
+    assert errors[:3] == errors[3:] and errors[0] == "a must be a CUDA tensor" and errors[1] == "b must be a CUDA tensor"

@@ -97,8 +97,8 @@ def get_workspace(device, max_bs, h_q, h_kv, head_dim, v_head_dim, l_ext, stream
     """Zero-filled workspace of ``stream`` (default: the device's current
     stream) on ``device``, grown (never shrunk) to fit max_bs.  One buffer per
     (device, stream): a buffer is never shared by calls that may overlap on the
-    GPU.  Growing allocates a new buffer; the old one is released by torch's
-    caching allocator on the current stream, after the calls queued on it."""
+    GPU.  Growing allocates a new buffer; both are memory of that stream, so the
+    new one is zero before, and the old one is reused after, the calls queued on it."""
     device = torch.device(device)
     if device.index is None:
         device = torch.device(device.type, torch.cuda.current_device())
@@ -114,7 +114,8 @@ def get_workspace(device, max_bs, h_q, h_kv, head_dim, v_head_dim, l_ext, stream
     with _WS_LOCK:
         ws = _WS.get(wkey)
         if ws is None or ws.numel() < need:
-            ws = torch.zeros(need, dtype=torch.uint8, device=device)
+            with torch.cuda.stream(stream):
+                ws = torch.zeros(need, dtype=torch.uint8, device=device)
             _WS[wkey] = ws
     return ws
 

@@ -1,13 +1,15 @@
 """What the package loads: the views module goes by the Python and the torch it was
 built for (no GPU needed)."""
+import contextlib
 import os
 import sysconfig
+import types
 
 import pytest
 import torch
 
 import speculative_decode_verify_prefix_gb300 as vsk
-from speculative_decode_verify_prefix_gb300 import _native, cache_ops
+from speculative_decode_verify_prefix_gb300 import _native, api, cache_ops
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -86,3 +88,35 @@ def test_both_packers_refuse_alike(bad):
                 pack(("a", "b"), tensors)
             errors.append(str(e.value))
     assert errors[:3] == errors[3:] and errors[0] == "a must be a CUDA tensor" and errors[1] == "b must be a CUDA tensor"
+
+
+# ------------------------------------------------------------------ workspaces
+
+@pytest.mark.parametrize("given", [True, False])
+def test_workspace_is_zeroed_on_the_stream_that_uses_it(monkeypatch, given):
+    current, zeroed = [], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    def zeros(n, **kw):
+        zeroed.append(current[-1] if current else None)
+        return torch.empty(n, dtype=torch.uint8)
+
+    one, other = types.SimpleNamespace(cuda_stream=0), types.SimpleNamespace(cuda_stream=7)
+    device = torch.device("cuda", 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: one)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch, "zeros", zeros)
+    monkeypatch.setattr(api, "_WS", {})
+    monkeypatch.setattr(api, "_WS_SIZE", {(device, b, 8, 2, 64, 64, 4): 1024 * b for b in (1, 2)})
+    at = (8, 2, 64, 64, 4, other if given else None)
+    small = vsk.get_workspace(device, 1, *at)
+    assert vsk.get_workspace(device, 1, *at) is small
+    large = vsk.get_workspace(device, 2, *at)
+    assert large.numel() == 2048 and vsk.get_workspace(device, 1, *at) is large
+    assert zeroed == [other if given else None] * 2
+    assert list(api._WS) == [(device, 7 if given else 0)]

@@ -62,6 +62,7 @@ constexpr int kSm = 128;     // softmax threads
 constexpr int kMeta = 8;     // tiles whose scales are kept (more than the ring holds)
 constexpr float kThr = 2.f;  // log2 headroom before a reference is raised
 constexpr int kUp = 6;       // y = 2^kUp x <= 2^(kUp + kThr) = 256
+constexpr float kMaxQsc = 1.5474250491067253e26f;  // 2^87
 constexpr float kMinScale = 9.094947017729282e-13f, kMaxScale = 1.099511627776e12f;  // 2^-40, 2^40
 
 struct BkParams {
@@ -354,7 +355,9 @@ __device__ __forceinline__ void put_rows(const BkParams& p, Rows<D, NR>& rows, u
     // the row's largest |q| 2^sh lies in [128, 256)
     const int sh = mx == 0 ? 0 : max(-120, min(120, 7 - (static_cast<int>(mx >> 7) - 127)));
     const float up = __int_as_float((127 + sh) << 23);
-    if (lane == 0) qsc[row] = p.scale2 * __int_as_float((127 - sh) << 23);
+    // capped, so that with the largest block scale it is still finite and a product of 0 a
+    // score of 0; where the cap holds, scores are equal or at least 2^29 apart all the same
+    if (lane == 0) qsc[row] = fminf(p.scale2 * __int_as_float((127 - sh) << 23), kMaxQsc);
     uint32_t hi[(W + 1) / 2] = {}, lo[(W + 1) / 2] = {};
 #pragma unroll
     for (int w = 0; w < W; ++w) {

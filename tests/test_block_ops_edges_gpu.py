@@ -135,3 +135,25 @@ def test_views_packed_in_python_are_the_modules(vsk, monkeypatch):  # noqa: F811
     assert cache_ops._views is _native.views()
     monkeypatch.setattr(cache_ops, "_views", cache_ops._python_views)
     assert torch.equal(run(), want)
+
+
+# ---------------------------------------------------------------- large queries
+
+@pytest.mark.parametrize("d,gq", [(64, 2), (128, 4), (256, 8)])
+@pytest.mark.parametrize("exponent", [-40, 0, 40])
+def test_block_largest_queries_against_zeros(vsk, d, gq, exponent):  # noqa: F811
+    """A query's largest elements meet zeros in every key: the scores are 0, whatever the scale of query and block."""
+    lens, l_ext = [70, 300], 4
+    c = block_case(lens, 16, 2 * gq, 2, d, l_ext, seed=6)
+    c["q"].zero_()
+    c["q"][:, :, 5] = 3e38
+    c["q"][1, :, 9] = -3e38
+    live = c["kc"].view(torch.uint8) != 0x7F
+    for col in (5, 9):
+        c["kc"].view(torch.uint8)[:, :, col] = torch.where(live[:, :, col], 0x80, 0x7F).to(torch.uint8)  # -0
+        c["ke"][:, :, col] = 0.0
+    c["ks"][c["ks"].isfinite()] = 2.0 ** exponent
+    o = torch.empty_like(c["q"])
+    vsk.verify_splitkv_block_fwd(c["q"], c["ke"], c["ve"], o, c["kc"], c["vc"], c["ks"], c["vs"], c["qo"], c["table"], c["lens"], 16,
+                                 l_ext)
+    check_block(o, *block_want(c["q"], c["ke"], c["ve"], c["kc"], c["vc"], c["ks"], c["vs"], c["table"], lens, 16, l_ext, d ** -0.5))

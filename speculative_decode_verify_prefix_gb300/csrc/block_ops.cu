@@ -200,10 +200,12 @@ static int allow_smem(const void* fn, size_t smem) {
 
 // Tokens and heads of a CTA that takes rows; the CTAs.  Few tokens: a row's heads
 // over several CTAs, a pass of the threads each at least.  More: one wave of CTAs (four an
-// SM), rounded up so that it is no more than one (4,082 rows, 16/2 heads of 256, rotated
-// 9.2 us, with a few CTAs left over 10.2; appended 10.3, 11.3).  Where that takes more than
-// kMaxTokens, `many` a CTA (7,000 rows, 16/2 heads of 256: with 8 27.7 us, with 4 24.9; the
-// queries beside 24,335 rows into blocks: with 8 103 us in all, with 4 107).
+// SM), rounded up so that it is no more than one (us, with a few CTAs left over in
+// brackets: 2,296 rows, 16/2 heads of 256, rotated 9.2 (10.2), appended to an e4m3 pool 10.3
+// (11.5), 4,082 rows 16.4 (16.0-16.4), 18.4 (22.4); 4,000 rows of 32/8 heads of 128, bf16
+// pool, 22.0 (25.7), but rotated 18.4 (17.7)).  Where that takes more than kMaxTokens,
+// `many` a CTA (7,000 rows, 16/2 heads of 256: with 8 27.7 us, with 4 25.0; the queries
+// beside 21,716 rows into blocks: with 8 103 us in all, with 4 107).
 static long long cut_rows(rp::RopeParams& p, long long heads, long long D, int sms, int threads, int many) {
   if (heads == 0) return 0;
   const long long slots = threads / (D / 16);
@@ -467,12 +469,14 @@ int rope_append_block_fwd(const vsk_tensor* q, const vsk_tensor* k, const vsk_te
   // a sequence adds to at most one block more than its rows fill, twice over, and to none without a row
   const long long units = std::min(p.n, p.n / block_size + 2 * B);
   // warps that hold the K or V rows of a block and head, 16 elements a thread
-  // (of the rows a block gets on the average)
+  // (of the rows a block gets on the average: a prompt beside many single rows gets few
+  // warps and reads most of its rows twice, 4,000 rows and 500 single ones in blocks of 64
+  // 44 us together, 28 and 14 apart; in blocks of 128 71, 37 and 16)
   const long long held = 32 * 16 / D, mean = std::min<long long>(block_size, (p.n + B - 1) / B);
   for (p.warps = 1; p.warps * held < mean && p.warps < rp::kBlockThreads / 32;) p.warps *= 2;
   const long long groups = rp::kBlockThreads / 32 / p.warps;
   p.units = static_cast<int>(units);
-  // CTAs that share a block's heads: some ten an SM (24,335 rows, 32/8 heads of 128, us: blocks of 64
+  // CTAs that share a block's heads: some ten an SM (21,716 rows, 32/8 heads of 128, us: blocks of 64
   // with 7, 10, 14 an SM 105.7, 102.7, 106.5; in blocks of 32 as many as four a block 107, so 99, of 16
   // 118, so 104), keys apart from values, which need no table of angles (8/1 heads together 37.9, apart
   // 35.3); two heads a CTA at least (16/2 of 256: one 102, two 94) and 16 at most (32/32, blocks of 32:

@@ -37,10 +37,11 @@
 // 420-428 us, 6.6-6.7 TB/s, memory; at head_dim 64 a tile's softmax outlasts its bytes
 // (189 us for 829 MB), with 32 rows the chain of scores, softmax and weights (313 us for
 // 1.66 GB).
-// Every wait is bounded (one second); in a CTA that gives up every role ends its
-// loop without copying, multiplying or arriving anywhere (the copies' barriers then
-// still tell when those under way are done), sets error bit 8, waits for copies and
-// MMAs in flight, frees the tensor memory and exits.  No barrier can run two phases
+// Every wait is bounded (one second); a CTA that gives up sets error bit 8.  Its loaders
+// end their loops, the other roles go through their tiles without waiting, multiplying
+// or arriving anywhere (the copies' barriers then still tell when those under way are
+// done; what such a CTA writes to its partials is no result), then it waits for copies
+// and MMAs in flight, frees the tensor memory and exits.  No barrier can run two phases
 // ahead of a wait for it: each phase needs an arrival that follows the wait for the
 // one before.
 #pragma once
@@ -55,7 +56,7 @@ enum : unsigned { kErrBadScale = 64u };
 namespace bk {
 
 constexpr int KT = 128;      // keys of a tile
-constexpr int GK = 16;       // keys of a group (one TMA box, one block's scale)
+constexpr int GK = 16;       // keys of a group (of one block, so under one scale; a TMA box takes 1, 2, 4 or 8)
 constexpr int GT = KT / GK;  // groups of a tile
 constexpr int kThreads = 224;
 constexpr int kSm = 128;     // softmax threads
@@ -81,7 +82,7 @@ struct BkParams {
   long long n_blocks, n_rows;
   int block, bgroups;   // keys, groups of a block
   int box;              // groups of a TMA box: a power of two that divides bgroups, GT at most
-  int B, L, gq, R, h_kv, rows;  // rows: of a partial (RT row tiles of 32)
+  int B, L, gq, R, h_kv, rows;  // rows: of a partial (whole row tiles: R rounded up to 8, 16 or a multiple of 32)
   float scale2;         // softmax scale in base 2
   int team, n_hg, n_team;  // KV heads of a team, h_kv / team, teams
   int tiles;               // row tiles: CTAs of a head in a team

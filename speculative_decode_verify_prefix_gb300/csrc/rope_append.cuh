@@ -14,8 +14,8 @@
 //
 // All of it but the blocks' keys and values is bound by memory: a thread takes 16
 // elements of one head of one row, the two 16-byte loads whose pairs belong together.
-// 24,335 rows of 32/8 heads of 128 take 71 us rotated (6.3 TB/s), 94 with K and V stored
-// to a pool (6.2); a plain copy of as many bytes 82.
+// 21,716 rows of 32/8 heads of 128 take 70 us rotated (445 MB, 6.3 TB/s), a plain copy of
+// as many bytes 68.5 (6.5); with K and V stored to a pool 93 (579 MB, 6.2).
 #pragma once
 #include "verify_kernel.cuh"
 
@@ -110,7 +110,7 @@ __device__ __forceinline__ long long index_at(const void* p, int wide, long long
 // Table of tokens [t0, t0 + n).  A thread reads the eight entries of pairs 8 c ..
 // 8 c + 7 in four pieces of two: piece k of all c lies together, so that the lanes
 // of a head read side by side (with a thread's entries together four lanes meet in a
-// bank: 24,335 rows, 32/8 heads of 128, 86 us, so 76).
+// bank: 21,716 rows, 32/8 heads of 128, 86 us, so 76).
 template <int NT>
 __device__ __forceinline__ void fill_table(const RopeParams& p, float2* cs, long long t0, int n) {
   const int pairs = p.rot >> 1;
@@ -329,7 +329,7 @@ __device__ __forceinline__ void rotate_rows(const rp::RopeParams& p, const float
 }
 
 // A CTA takes p.tokens tokens of p.heads heads (of the h_q + h_kv, or h_q + 2 h_kv,
-// of a row).  Without a pool five CTAs fit an SM (24,335 rows, 32/8 heads of 128: four
+// of a row).  Without a pool five CTAs fit an SM (21,716 rows, 32/8 heads of 128: four
 // 73.3 us, five 70.8, six 72.6); with one the fifth costs spills (94, so 96).
 template <int D, int POOL>
 __global__ void __launch_bounds__(rp::kThreads, POOL == 0 ? 5 : 4) rope_kernel(const __grid_constant__ rp::RopeParams p) {
@@ -355,8 +355,8 @@ __global__ void __launch_bounds__(rp::kThreads, POOL == 0 ? 5 : 4) rope_kernel(c
 // keys alone, some values alone: those need no table of angles.
 // The other CTAs take the queries as rope_kernel does: they are most of the bytes, and
 // need none of this.
-// 24,335 rows, 32/8 heads of 128, blocks of 64: 103 us, 5.2 TB/s, of which keys and
-// values alone 61 at 3.3: instructions and latency (without loads and stores 41, of
+// 21,716 rows, 32/8 heads of 128, blocks of 64: 103 us, 5.2 TB/s, of which keys and
+// values alone 60 at 3.0: instructions and latency (without loads and stores 41, of
 // which 10 to find the blocks and 14 for the tables).
 template <int D>
 __global__ void __launch_bounds__(rp::kBlockThreads, 4) rope_block_kernel(const __grid_constant__ rp::RopeParams p) {

@@ -93,6 +93,14 @@ def _stream_key(device, stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _made_current(stream, device):
+    """A context in which ``stream`` (None: the current one) is torch's current
+    stream.  As for the calls themselves, anything with a ``cuda_stream`` will do."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 def get_workspace(device, max_bs, h_q, h_kv, head_dim, v_head_dim, l_ext, stream=None) -> torch.Tensor:
     """Zero-filled workspace of ``stream`` (default: the device's current
     stream) on ``device``, grown (never shrunk) to fit max_bs.  One buffer per
@@ -114,7 +122,7 @@ def get_workspace(device, max_bs, h_q, h_kv, head_dim, v_head_dim, l_ext, stream
     with _WS_LOCK:
         ws = _WS.get(wkey)
         if ws is None or ws.numel() < need:
-            with torch.cuda.stream(stream):
+            with _made_current(stream, device):
                 ws = torch.zeros(need, dtype=torch.uint8, device=device)
             _WS[wkey] = ws
     return ws
@@ -134,7 +142,7 @@ def _flat_mask(mask, stream):
     after the call's kernels."""
     if stream is None or mask.is_contiguous():
         return mask.reshape(-1)
-    with torch.cuda.stream(stream):
+    with _made_current(stream, mask.device):
         return mask.reshape(-1)
 
 

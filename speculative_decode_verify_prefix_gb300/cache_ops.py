@@ -22,7 +22,7 @@ import warnings
 import torch
 
 from . import _native
-from .api import _SHARED_SIZE as _SIZES, _WS, _WS_LOCK, _coerce, as_vsk
+from .api import _SHARED_SIZE as _SIZES, _WS, _WS_LOCK, _coerce, _made_current, as_vsk
 
 
 def _python_views(names, tensors):
@@ -75,14 +75,14 @@ def _workspace_of(device, stream, raw_stream, need):
     if stream is None:
         capturing = torch.cuda.is_current_stream_capturing()
     else:
-        with torch.cuda.stream(stream):
+        with _made_current(stream, _device(device)):
             capturing = torch.cuda.is_current_stream_capturing()
     if capturing:
         raise ValueError("pass workspace= to a call that is captured into a graph")
     key = (_device(device), raw_stream)
     ws = _WS.get(key)
     if ws is None or ws.numel() < need:
-        with torch.cuda.stream(stream), _WS_LOCK:  # zeroed in the order of the stream that uses it
+        with _made_current(stream, _device(device)), _WS_LOCK:  # zeroed in the order of the stream that uses it
             ws = _WS.get(key)
             if ws is None or ws.numel() < need:
                 ws = torch.zeros(need, dtype=torch.uint8, device=key[0])

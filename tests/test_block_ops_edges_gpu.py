@@ -1,6 +1,7 @@
 """GPU tests of the rotary, append and block-scaled cache calls at corners that the
 tests of their formulas do not reach."""
 import ctypes
+import types
 
 import pytest
 import torch
@@ -23,7 +24,8 @@ def wide(mask):
 
 
 @pytest.mark.parametrize("call", ["blocks", "tree"])
-def test_mask_that_is_not_contiguous_on_another_stream(vsk, call):  # noqa: F811
+@pytest.mark.parametrize("given", [lambda s: s, lambda s: types.SimpleNamespace(cuda_stream=s.cuda_stream)], ids=["torch's", "another object"])
+def test_mask_that_is_not_contiguous_on_another_stream(vsk, call, given):  # noqa: F811
     """The copy is made on the call's stream, so it neither waits for the current one nor is overtaken by the kernels."""
     n, l_ext = 40, 4
     g = torch.Generator(device=DEV)
@@ -63,7 +65,7 @@ def test_mask_that_is_not_contiguous_on_another_stream(vsk, call):  # noqa: F811
     late = torch.cuda.Event()
     torch.cuda._sleep(200_000_000)  # the current stream is busy for some 0.1 s
     late.record()
-    run(mask, o, stream=side)
+    run(mask, o, stream=given(side))
     over = torch.ones(mask.shape, dtype=torch.bool, device=DEV)  # the copy's memory, if it were the current stream's
     side.synchronize()
     assert not late.query()

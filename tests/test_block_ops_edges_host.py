@@ -43,6 +43,7 @@ def streams(monkeypatch):
         current.pop()
 
     monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, device: types.SimpleNamespace(cuda_stream=raw))
     return current
 
 

@@ -110,6 +110,7 @@ def test_workspace_is_zeroed_on_the_stream_that_uses_it(monkeypatch, given):
     device = torch.device("cuda", 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: one)
     monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, device: other if raw == 7 else None)  # (any object with a cuda_stream)
     monkeypatch.setattr(torch, "zeros", zeros)
     monkeypatch.setattr(api, "_WS", {})
     monkeypatch.setattr(api, "_WS_SIZE", {(device, b, 8, 2, 64, 64, 4): 1024 * b for b in (1, 2)})

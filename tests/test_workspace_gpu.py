@@ -1,4 +1,6 @@
 """GPU test of the workspaces that the binding keeps for a stream."""
+import types
+
 import pytest
 import torch
 
@@ -10,7 +12,8 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("launches", [1, 2])
-def test_first_call_on_a_stream_does_not_wait_for_the_current_one(vsk, launches):  # noqa: F811
+@pytest.mark.parametrize("given", ["torch's", "another object"])
+def test_first_call_on_a_stream_does_not_wait_for_the_current_one(vsk, launches, given):  # noqa: F811
     """The workspace is zeroed on the stream that uses it: in time, although the current stream is busy."""
     p = gpu_problem(workloads.Spec("first", (900, 40), 4, 8, 2, 128, 128, perm=True, seed=211))
     vsk.set_tuning_split_launch(2 if launches == 2 else 0)
@@ -27,7 +30,7 @@ def test_first_call_on_a_stream_does_not_wait_for_the_current_one(vsk, launches)
         late.record()
         assert vsk.verify_splitkv_fwd(p["q"], p["k_ext"], p["v_ext"], o, p["k_buffer"], p["v_buffer"], p["qo_indptr"], p["kv_indptr"],
                                       p["kv_indices"], None, True, None, 4, p["k_scale"], p["v_scale"], sm_scale=p["sm_scale"],
-                                      stream=side)
+                                      stream=side if given == "torch's" else types.SimpleNamespace(cuda_stream=side.cuda_stream))
         side.synchronize()
         assert not late.query()
         torch.cuda.synchronize()
